@@ -44,7 +44,7 @@
 extern "C" {
 #endif
 
-#define SSD_ABI_VERSION 8
+#define SSD_ABI_VERSION 9
 
 /* Status codes: 0 is success, every error is negative. */
 enum {
@@ -372,6 +372,200 @@ int ssd_fwd_noalloc(const ssd_dims* dims, const ssd_layout* layout,
 
 /* Bytes of ssd_fwd_noalloc's fixed scratch array on each GPU. */
 size_t ssd_fwd_noalloc_max_bytes(void);
+
+/* ===========================================================================
+ * Operators around the scan: layer norm, the short causal convolution, the
+ * selective scan with a learned decay per channel and state entry, and the
+ * single-token forms.  The conventions above hold (host checks before any
+ * launch, no allocation, no synchronization, caller-owned workspaces), with
+ * these differences: pointers need their element's alignment only (16 bytes
+ * nowhere; workspaces 256), and strides are any element count up to 2^24.
+ * Weights, statistics, scan states and weight gradients are float32; sums
+ * run in float32 in a fixed order, so a call's result does not change from
+ * run to run.  Outputs must not overlap inputs except where said.
+ * ======================================================================== */
+
+/*
+ * Layer norm over the last dimension, per row of x [rows, width]:
+ *   mean = sum x / width,  rstd = 1 / sqrt(sum (x - mean)^2 / width + eps),
+ *   y = (x - mean) rstd weight + bias
+ * weight, bias [width] float32, each NULL for 1 / 0; mean, rstd [rows]
+ * float32 outputs, each NULL to skip.  y may be x itself.
+ */
+#define SSD_NORM_MAX_WIDTH 16384
+typedef struct ssd_norm_dims {
+    int64_t rows;     /* >= 0, < 2^31                                       */
+    int64_t x_row;    /* element stride of x's rows (and dx's), >= width    */
+    int64_t y_row;    /* of y's rows (ssd_norm_fwd)                         */
+    int64_t dy_row;   /* of dy's rows (ssd_norm_bwd)                        */
+    int32_t width;    /* 1 .. SSD_NORM_MAX_WIDTH                            */
+    int32_t dtype;    /* of x, y, dy, dx: SSD_F32 or SSD_BF16               */
+    float eps;        /* >= 0                                               */
+    int32_t reserved; /* 0                                                  */
+} ssd_norm_dims;
+
+int ssd_norm_fwd(const ssd_norm_dims* dims, const void* x, const float* weight, const float* bias,
+                 void* y, float* mean, float* rstd, void* stream);
+
+/*
+ * Its gradients, from the forward's mean and rstd: with xh = (x - mean) rstd
+ * and q = dy weight,
+ *   dx = rstd (q - mean(q) - xh mean(q xh)),
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy
+ * dweight, dbias [width] float32, each NULL to skip.  dx may be dy or x
+ * itself.  workspace: at least ssd_norm_bwd_workspace_bytes(dims) bytes (0
+ * for invalid dims), 256-byte aligned, no initialization.
+ */
+size_t ssd_norm_bwd_workspace_bytes(const ssd_norm_dims* dims);
+
+int ssd_norm_bwd(const ssd_norm_dims* dims, const void* x, const float* weight, const float* mean,
+                 const float* rstd, const void* dy, void* dx, float* dweight, float* dbias,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Short causal convolution over the tokens of each sequence, one filter of
+ * `width` taps per channel, with bias and SiLU:
+ *   v_t = bias + sum_k weight[k] x_{t - width + 1 + k},   y_t = v_t / (1 + e^{-v_t})
+ * x, y [b, L, E] of dtype (innermost dimension contiguous, token strides in
+ * the layout, batch rows L tokens apart); weight [width, E] and bias [E]
+ * float32 (bias NULL for 0).  x_{-1} of a sequence is row width - 2 of its
+ * init_state [S, width - 1, E] (dtype, contiguous; NULL for zeros), x_{-2}
+ * the row before, and so on; final_state (same shape, NULL to skip) receives
+ * the last width - 1 inputs of each sequence, init_state's rows among them
+ * where it is shorter.  cu_seqlens as ssd_fwd's; S is b or nseq.
+ * final_state must not overlap init_state (SSD_ERR_OVERLAP).
+ */
+typedef struct ssd_conv_dims {
+    int32_t batch;    /* b >= 1                                             */
+    int64_t seqlen;   /* L >= 0; b * L < 2^31                               */
+    int32_t channels; /* E >= 1, <= 2^24                                    */
+    int32_t width;    /* 2, 3 or 4 (others SSD_ERR_UNSUPPORTED)             */
+    int32_t nseq;     /* cu_seqlens segments (0 without them)               */
+    int32_t dtype;
+} ssd_conv_dims;
+
+typedef struct ssd_conv_layout {
+    int64_t x_token;  /* token strides in elements, E <= stride <= 2^24     */
+    int64_t y_token;
+    int64_t dy_token;
+} ssd_conv_layout;
+
+int ssd_conv_fwd(const ssd_conv_dims* dims, const ssd_conv_layout* layout,
+                 const void* x, const float* weight, const float* bias,
+                 const void* init_state, const int32_t* cu_seqlens,
+                 void* y, void* final_state, void* stream);
+
+/*
+ * Its gradients.  dy like y (layout->dy_token), d_final like final_state or
+ * NULL for zeros; dx is laid out like x; dweight [width, E], dbias [E]
+ * float32 and dinit_state (dtype, like init_state; also without one, the
+ * gradient at zeros), each NULL to skip.  dinit_state must not overlap
+ * d_final.  workspace: ssd_conv_bwd_workspace_bytes(dims), 256-byte aligned.
+ */
+size_t ssd_conv_bwd_workspace_bytes(const ssd_conv_dims* dims);
+
+int ssd_conv_bwd(const ssd_conv_dims* dims, const ssd_conv_layout* layout,
+                 const void* x, const float* weight, const float* bias,
+                 const void* init_state, const int32_t* cu_seqlens,
+                 const void* dy, const void* d_final,
+                 void* dx, float* dweight, float* dbias, void* dinit_state,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One new token for each of b sequences whose states lie in a pool:
+ * x, y [b, E] (row strides x_token, y_token; dims->seqlen 1, nseq 0), state
+ * [nslots, width - 1, E], slots [b] int32 the pool row of each (NULL: row i).
+ * Writes the state that includes the new token to the same rows of new_state,
+ * which may be state itself (in place) or another pool of its shape; other
+ * rows are left alone.  A slot outside [0, nslots) marks a padding row: its
+ * y is 0 and no state is touched.  Slots of one call must differ.
+ */
+int ssd_conv_step(const ssd_conv_dims* dims, const ssd_conv_layout* layout,
+                  const void* x, const float* weight, const float* bias,
+                  const void* state, const int32_t* slots, int32_t nslots,
+                  void* y, void* new_state, void* stream);
+
+/*
+ * Selective scan: per sequence, channel e and state entry n,
+ *   d_t = softplus(d_raw_t,e + d_init_e)
+ *   h_t = exp(d_t A_n,e) h_{t-1} + d_t B_t,n x_t,e
+ *   y_t,e = (sum_n C_t,n h_t + D_e x_t,e) * (z_t,e / (1 + e^{-z_t,e}))
+ * x, d_raw, z, y [b, L, E] and B, C [b, L, G, N] of dtype (channel e reads
+ * group e / (E / G)); d_init, D [E] and A [N, E] float32; D NULL for 0, z
+ * NULL for no gate; init_state [S, N, E] float32 or NULL for zeros,
+ * final_state likewise, NULL to skip, not overlapping init_state.
+ * exp(d A) is formed as exp2(d A log2(e)): A <= 0 is meant, and a positive A
+ * grows without a guard.  workspace: ssd_selscan_fwd_workspace_bytes(dims),
+ * 256-byte aligned, no initialization (may be NULL where that is 0).
+ */
+#define SSD_SELSCAN_MAX_STATE 64
+#define SSD_SELSCAN_MAX_CHANNELS (1 << 20)
+typedef struct ssd_selscan_dims {
+    int32_t batch;    /* b >= 1                                             */
+    int64_t seqlen;   /* L >= 0; b * L < 2^31                               */
+    int32_t channels; /* E >= 1, <= 2^20, a multiple of ngroups             */
+    int32_t d_state;  /* N: 1 .. 64                                         */
+    int32_t ngroups;  /* G >= 1                                             */
+    int32_t nseq;     /* cu_seqlens segments (0 without them)               */
+    int32_t dtype;
+    int32_t reserved; /* 0                                                  */
+} ssd_selscan_dims;
+
+typedef struct ssd_selscan_layout {
+    int64_t x_token, d_raw_token, z_token; /* elements, E <= stride <= 2^24 */
+    int64_t B_token, B_group, C_token, C_group;
+    int64_t y_token, dy_token;
+} ssd_selscan_layout;
+
+size_t ssd_selscan_fwd_workspace_bytes(const ssd_selscan_dims* dims);
+
+int ssd_selscan_fwd(const ssd_selscan_dims* dims, const ssd_selscan_layout* layout,
+                    const void* x, const void* d_raw, const float* d_init, const float* A,
+                    const void* B, const void* C, const float* D, const void* z,
+                    const float* init_state, const int32_t* cu_seqlens,
+                    void* y, float* final_state,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Its gradients: dy like y, d_final [S, N, E] float32 or NULL for zeros.
+ * dx, dd_raw, dz, dB, dC of dtype, laid out like their inputs (dz required
+ * with z); dA [N, E], dD, dd_init [E], dinit_state [S, N, E] float32, each
+ * NULL to skip (dinit_state not overlapping d_final).  workspace:
+ * ssd_selscan_bwd_workspace_bytes(dims), 256-byte aligned.
+ */
+size_t ssd_selscan_bwd_workspace_bytes(const ssd_selscan_dims* dims);
+
+int ssd_selscan_bwd(const ssd_selscan_dims* dims, const ssd_selscan_layout* layout,
+                    const void* x, const void* d_raw, const float* d_init, const float* A,
+                    const void* B, const void* C, const float* D, const void* z,
+                    const float* init_state, const int32_t* cu_seqlens,
+                    const void* dy, const float* d_final,
+                    void* dx, void* dd_raw, void* dB, void* dC, void* dz,
+                    float* dA, float* dD, float* dd_init, float* dinit_state,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One new token of the selective scan for each of b sequences (seqlen 1,
+ * nseq 0): x, d_raw, z, y [b, E], B, C [b, G, N], state and new_state
+ * [nslots, N, E] float32 with slots as ssd_conv_step's.
+ */
+int ssd_selscan_step(const ssd_selscan_dims* dims, const ssd_selscan_layout* layout,
+                     const void* x, const void* d_raw, const float* d_init, const float* A,
+                     const void* B, const void* C, const float* D, const void* z,
+                     const float* state, const int32_t* slots, int32_t nslots,
+                     void* y, float* new_state, void* stream);
+
+/*
+ * One new token of ssd_fwd's scan for each of dims->batch sequences (seqlen 1,
+ * nseq 0; sizes and dtypes as ssd_fwd, chunk_size unused): x, y [b, H, P],
+ * d_raw [b, H], B, C [b, G, N] with ssd_layout's strides (element alignment
+ * is enough here), state and new_state [nslots, H, N, P] float32 with slots
+ * as ssd_conv_step's.
+ */
+int ssd_step(const ssd_dims* dims, const ssd_layout* layout,
+             const void* x, const void* d_raw, float d_init, const void* B, const void* C,
+             const float* state, const int32_t* slots, int32_t nslots,
+             void* y, float* new_state, void* stream);
 
 /* Static description of a status code (never NULL). */
 const char* ssd_status_string(int status);

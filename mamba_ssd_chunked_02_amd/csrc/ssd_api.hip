@@ -416,6 +416,15 @@ void* scratch_address(int dev) {
 
 }  // namespace
 
+namespace ssd {
+bool check_cu_env(const int32_t* cu, int32_t nseq, int64_t T, hipStream_t s, int* status) {
+    const char* chk = getenv("SSD_CHECK");
+    if (!chk || chk[0] != '1') return false;
+    *status = check_cu(cu, nseq, T, s);
+    return *status != SSD_OK;
+}
+}  // namespace ssd
+
 extern "C" {
 
 int ssd_abi_version(void) { return SSD_ABI_VERSION; }

@@ -1,0 +1,374 @@
+// Layer norm, forward and backward, and the column sum behind every weight
+// gradient of the library.
+//
+//   mean = sum x / W, rstd = 1 / sqrt(sum (x - mean)^2 / W + eps)
+//   y = (x - mean) rstd w + b
+// and with xh = (x - mean) rstd, q = dy w:
+//   dx = rstd (q - mean(q) - xh mean(q xh)),  dw = sum_rows dy xh,  db = sum_rows dy.
+//
+// Both directions are bound by HBM: one pass, the row held in registers
+// between the sums and the output, so x (and dy) is read once.  A row belongs
+// to one wave where it fits (no barrier), else to one workgroup.
+#include "ssd_layer.h"
+
+namespace ssd {
+namespace {
+
+constexpr int kMaxWaves = 16;   // per row
+constexpr int kWavesPerWg = 4;  // rows of a workgroup where a row is one wave's
+
+struct NormParams {
+    const void* x;
+    const void* dy;
+    void* out;  // y or dx
+    const float* weight;
+    const float* bias;
+    float* mean;
+    float* rstd;
+    const float* mean_in;
+    const float* rstd_in;
+    float* part;  // [slots][2][width]
+    int64_t rows, x_row, out_row, dy_row;
+    int32_t width;
+    int32_t slots;  // row walkers (waves or workgroups) of the backward launch
+    float eps;
+};
+
+// Sums over the row's lanes of two values; `waves` waves share a row (1: no
+// barrier).  The exchange is double-buffered by `turn`, so one barrier a call
+// is enough: a wave can be at most one call ahead.
+__device__ __forceinline__ void row_sums(float& a, float& b, int waves, float (*ex)[kMaxWaves][2],
+                                         int& turn) {
+    a = wave_sum(a);
+    b = wave_sum(b);
+    if (waves == 1) return;
+    float (*e)[2] = ex[turn];
+    turn ^= 1;
+    const int w = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+        e[w][0] = a;
+        e[w][1] = b;
+    }
+    __syncthreads();
+    a = b = 0.f;
+    for (int i = 0; i < waves; ++i) {
+        a += e[i][0];
+        b += e[i][1];
+    }
+}
+
+// V elements a load, NV loads a thread.
+template <typename T, int V, int NV>
+__global__ __launch_bounds__(1024) void norm_fwd_kernel(NormParams p, int waves) {
+    __shared__ float ex[2][kMaxWaves][2];
+    const int lanes = waves * 64;
+    const int64_t row = waves == 1 ? (int64_t)blockIdx.x * kWavesPerWg + (threadIdx.x >> 6)
+                                   : (int64_t)blockIdx.x;
+    if (row >= p.rows) return;  // only where a row is one wave's: no barrier below
+    const int lane = waves == 1 ? threadIdx.x & 63 : threadIdx.x;
+    const T* x = (const T*)p.x + row * p.x_row;
+    T* y = (T*)p.out + row * p.out_row;
+    float v[NV][V];
+    float s = 0.f, zero = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * lanes + lane) * V;
+        load_vec<T, V>(x + c, p.width - c, v[i]);
+#pragma unroll
+        for (int j = 0; j < V; ++j) s += v[i][j];
+    }
+    int turn = 0;
+    row_sums(s, zero, waves, ex, turn);
+    const float mean = s / (float)p.width;
+    float q = 0.f;
+    zero = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * lanes + lane) * V;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            v[i][j] -= mean;
+            q += c + j < p.width ? v[i][j] * v[i][j] : 0.f;
+        }
+    }
+    row_sums(q, zero, waves, ex, turn);
+    const float rstd = 1.f / sqrtf(q / (float)p.width + p.eps);
+    if (lane == 0) {
+        if (p.mean) p.mean[row] = mean;
+        if (p.rstd) p.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * lanes + lane) * V, n = p.width - c;
+        if (n <= 0) break;
+        float w[V], b[V], o[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            w[j] = 1.f;
+            b[j] = 0.f;
+        }
+        if (p.weight) load_vec<float, V>(p.weight + c, n, w);
+        if (p.bias) load_vec<float, V>(p.bias + c, n, b);
+#pragma unroll
+        for (int j = 0; j < V; ++j) o[j] = v[i][j] * rstd * w[j] + b[j];
+        store_vec<T, V>(y + c, n, o);
+    }
+}
+
+// Each walker (wave or workgroup) takes the rows slot, slot + slots, ... and
+// keeps its share of dw and db in registers until its last row.
+template <typename T, int V, int NV>
+__global__ __launch_bounds__(1024) void norm_bwd_kernel(NormParams p, int waves) {
+    __shared__ float ex[2][kMaxWaves][2];
+    const int lanes = waves * 64;
+    const int slot = waves == 1 ? blockIdx.x * kWavesPerWg + (threadIdx.x >> 6) : blockIdx.x;
+    if (slot >= p.slots) return;  // only where a row is one wave's: no barrier below
+    const int lane = waves == 1 ? threadIdx.x & 63 : threadIdx.x;
+    float w[NV][V], dw[NV][V], db[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * lanes + lane) * V;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            w[i][j] = 1.f;
+            dw[i][j] = db[i][j] = 0.f;
+        }
+        if (p.weight) load_vec<float, V>(p.weight + c, p.width - c, w[i]);
+    }
+    int turn = 0;
+    const float inv = 1.f / (float)p.width;
+    for (int64_t row = slot; row < p.rows; row += p.slots) {
+        const T* x = (const T*)p.x + row * p.x_row;
+        const T* dy = (const T*)p.dy + row * p.dy_row;
+        const float mean = p.mean_in[row], rstd = p.rstd_in[row];
+        float v[NV][V], g[NV][V];
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * lanes + lane) * V;
+            load_vec<T, V>(x + c, p.width - c, v[i]);
+            load_vec<T, V>(dy + c, p.width - c, g[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                v[i][j] = (v[i][j] - mean) * rstd;  // past the row g is 0: nothing is summed
+                dw[i][j] += g[i][j] * v[i][j];
+                db[i][j] += g[i][j];
+                g[i][j] *= w[i][j];
+                s0 += g[i][j];
+                s1 += g[i][j] * v[i][j];
+            }
+        }
+        row_sums(s0, s1, waves, ex, turn);
+        s0 *= inv;
+        s1 *= inv;
+        T* dx = (T*)p.out + row * p.out_row;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * lanes + lane) * V, n = p.width - c;
+            float o[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) o[j] = rstd * (g[i][j] - s0 - v[i][j] * s1);
+            if (n > 0) store_vec<T, V>(dx + c, n, o);
+        }
+    }
+    float* pw = p.part + (int64_t)slot * 2 * p.width;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * lanes + lane) * V, n = p.width - c;
+        if (n > 0) {
+            store_vec<float, V>(pw + c, n, dw[i]);
+            store_vec<float, V>(pw + p.width + c, n, db[i]);
+        }
+    }
+}
+
+// Sixteen waves a workgroup, each adding every sixteenth row of 64 columns;
+// the waves' sums are joined in LDS.
+__global__ __launch_bounds__(1024) void colsum_kernel(ColSum p) {
+    __shared__ float ex[16][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+    float s = 0.f;
+    if (c < p.cols) {
+        const float* q = p.part + c;
+        int64_t r = w;
+        for (; r + 7 * 16 < p.rows; r += 8 * 16) {
+            float t[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) t[k] = q[(r + k * 16) * p.cols];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += t[k];
+        }
+        for (; r < p.rows; r += 16) s += q[r * p.cols];
+    }
+    ex[w][lane] = s;
+    __syncthreads();
+    if (w || c >= p.cols) return;
+    s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) s += ex[k][lane];
+    if (c < p.c0) {
+        if (p.out0) p.out0[c] = s;
+    } else if (c < p.c0 + p.c1) {
+        if (p.out1) p.out1[c - p.c0] = s;
+    } else if (p.out2) {
+        p.out2[c - p.c0 - p.c1] = s;
+    }
+}
+
+// Waves a row and loads a thread: the fewest waves that hold the row with at
+// most `most` loads a thread.
+struct NormPlan {
+    int waves, nv;
+};
+NormPlan norm_plan(const ssd_norm_dims& d, int most) {
+    const int V = d.dtype == SSD_BF16 ? 8 : 4;
+    const int64_t vecs = cdiv(d.width, V);
+    NormPlan pl;
+    const int64_t w = cdiv(vecs, 64 * most);
+    pl.waves = (int)w;
+    pl.nv = (int)cdiv(vecs, 64 * w);
+    return pl;
+}
+constexpr int kMostFwd = 8;
+// backward: five row vectors a load are live, so 128 registers hold two loads
+// of 8 or four of 4
+inline int most_bwd(const ssd_norm_dims& d) { return d.dtype == SSD_BF16 ? 2 : 4; }
+
+int32_t norm_slots(const ssd_norm_dims& d) {
+    // two workgroups a CU; a walker's share of dw and db is written once, so
+    // more walkers than rows / 4 would write more than they read
+    const NormPlan pl = norm_plan(d, most_bwd(d));
+    const int64_t most = pl.waves == 1 ? 2048 : (pl.waves <= 4 ? 1024 : 512);
+    const int64_t s = imax(1, cdiv(d.rows, 4));
+    return (int32_t)(s < most ? s : most);
+}
+
+int norm_check(const ssd_norm_dims* d) {
+    if (!d) return SSD_ERR_NULL_ARG;
+    if (d->dtype != SSD_F32 && d->dtype != SSD_BF16) return SSD_ERR_DTYPE;
+    if (d->rows < 0 || d->rows > kMaxTokens || d->width < 1) return SSD_ERR_SHAPE;
+    if (d->width > SSD_NORM_MAX_WIDTH) return SSD_ERR_UNSUPPORTED;
+    if (!(d->eps >= 0.f)) return SSD_ERR_SHAPE;
+    for (int64_t s : {d->x_row, d->y_row, d->dy_row})
+        if (s < d->width || s > kMaxStride) return SSD_ERR_SHAPE;
+    return SSD_OK;
+}
+
+template <typename T, int V, bool BWD>
+void launch_norm(const NormParams& p, NormPlan pl, hipStream_t s) {
+    const int64_t walkers = BWD ? p.slots : p.rows;
+    const dim3 grid((unsigned)(pl.waves == 1 ? cdiv(walkers, kWavesPerWg) : walkers));
+    const dim3 block(pl.waves == 1 ? 64 * kWavesPerWg : 64 * pl.waves);
+#define SSD_NORM_CASE(NV)                                                       \
+    case NV:                                                                    \
+        if constexpr (!BWD) norm_fwd_kernel<T, V, NV><<<grid, block, 0, s>>>(p, pl.waves); \
+        else if constexpr (NV * V <= 16) norm_bwd_kernel<T, V, NV><<<grid, block, 0, s>>>(p, pl.waves); \
+        break
+    switch (pl.nv) {
+        SSD_NORM_CASE(1);
+        SSD_NORM_CASE(2);
+        SSD_NORM_CASE(3);
+        SSD_NORM_CASE(4);
+        SSD_NORM_CASE(5);
+        SSD_NORM_CASE(6);
+        SSD_NORM_CASE(7);
+        SSD_NORM_CASE(8);
+    }
+#undef SSD_NORM_CASE
+}
+
+}  // namespace
+
+int launch_colsum(const ColSum& p, hipStream_t s) {
+    if (p.cols <= 0) return SSD_OK;
+    colsum_kernel<<<dim3((unsigned)cdiv(p.cols, 64)), dim3(1024), 0, s>>>(p);
+    return launched();
+}
+
+}  // namespace ssd
+
+using namespace ssd;
+
+extern "C" {
+
+int ssd_norm_fwd(const ssd_norm_dims* dims, const void* x, const float* weight, const float* bias,
+                 void* y, float* mean, float* rstd, void* stream) {
+    const int st = norm_check(dims);
+    if (st != SSD_OK) return st;
+    if (dims->rows == 0) return SSD_OK;
+    if (!x || !y) return SSD_ERR_NULL_ARG;
+    const size_t e = elem_size(dims->dtype);
+    if (!elem_aligned(x, e) || !elem_aligned(y, e) || !elem_aligned(weight, 4) ||
+        !elem_aligned(bias, 4) || !elem_aligned(mean, 4) || !elem_aligned(rstd, 4))
+        return SSD_ERR_ALIGN;
+    NormParams p = {};
+    p.x = x;
+    p.out = y;
+    p.weight = weight;
+    p.bias = bias;
+    p.mean = mean;
+    p.rstd = rstd;
+    p.rows = dims->rows;
+    p.x_row = dims->x_row;
+    p.out_row = dims->y_row;
+    p.width = dims->width;
+    p.eps = dims->eps;
+    const NormPlan pl = norm_plan(*dims, kMostFwd);
+    if (dims->dtype == SSD_BF16) launch_norm<bf16, 8, false>(p, pl, (hipStream_t)stream);
+    else launch_norm<float, 4, false>(p, pl, (hipStream_t)stream);
+    return launched();
+}
+
+size_t ssd_norm_bwd_workspace_bytes(const ssd_norm_dims* dims) {
+    if (norm_check(dims) != SSD_OK) return 0;
+    return up256((size_t)norm_slots(*dims) * 2 * dims->width * sizeof(float));
+}
+
+int ssd_norm_bwd(const ssd_norm_dims* dims, const void* x, const float* weight, const float* mean,
+                 const float* rstd, const void* dy, void* dx, float* dweight, float* dbias,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+    const int st = norm_check(dims);
+    if (st != SSD_OK) return st;
+    if (dims->rows > 0 && (!x || !mean || !rstd || !dy || !dx)) return SSD_ERR_NULL_ARG;
+    const size_t e = elem_size(dims->dtype);
+    if (!elem_aligned(x, e) || !elem_aligned(dy, e) || !elem_aligned(dx, e) ||
+        !elem_aligned(weight, 4) || !elem_aligned(mean, 4) || !elem_aligned(rstd, 4) ||
+        !elem_aligned(dweight, 4) || !elem_aligned(dbias, 4) || ((uintptr_t)workspace & 255))
+        return SSD_ERR_ALIGN;
+    if (!workspace || workspace_bytes < ssd_norm_bwd_workspace_bytes(dims))
+        return SSD_ERR_WORKSPACE;
+    NormParams p = {};
+    p.x = x;
+    p.dy = dy;
+    p.out = dx;
+    p.weight = weight;
+    p.mean_in = mean;
+    p.rstd_in = rstd;
+    p.part = (float*)workspace;
+    p.rows = dims->rows;
+    p.x_row = dims->x_row;
+    p.out_row = dims->x_row;
+    p.dy_row = dims->dy_row;
+    p.width = dims->width;
+    p.slots = norm_slots(*dims);  // with no rows one walker, which writes zeros
+    const NormPlan pl = norm_plan(*dims, most_bwd(*dims));
+    if (dims->dtype == SSD_BF16) launch_norm<bf16, 8, true>(p, pl, (hipStream_t)stream);
+    else launch_norm<float, 4, true>(p, pl, (hipStream_t)stream);
+    const int rc = launched();
+    if (rc != SSD_OK || (!dweight && !dbias)) return rc;
+    ColSum c = {};
+    c.part = p.part;
+    c.rows = p.slots;
+    c.cols = 2 * (int64_t)dims->width;
+    c.out0 = dweight;
+    c.c0 = dims->width;
+    c.out1 = dbias;
+    c.c1 = dims->width;
+    return launch_colsum(c, (hipStream_t)stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,888 @@
+// Selective scan with a decay per channel and state entry, forward and backward.
+//
+//   d_t = softplus(d_raw_t + d_init),  u_t = d_t x_t,  a_t,n = exp(d_t A_n)
+//   h_t,n = a_t,n h_{t-1},n + B_t,n u_t,   v_t = sum_n C_t,n h_t,n + D x_t,  y_t = v_t silu(z_t)
+// and with w_t = dy_t silu(z_t), q_t = a_{t+1} g_{t+1} (q after the last token: d_final):
+//   g_t,n = C_t,n w_t + q_t,n,                  dz_t = dy_t v_t silu'(z_t)
+//   dx_t = D w_t + d_t sum_n g_t,n B_t,n,       dB_t,n = sum_e g u,   dC_t,n = sum_e h w
+//   dd_t = x_t sum_n g B + sum_n A_n (a g h_{t-1}),   dd_raw_t = dd_t sigmoid(d_raw_t + d_init)
+//   dA_n = sum_t d_t (a g h_{t-1}),  dD = sum w x,  dd_init = sum dd_raw,  dinit_state = a_0 g_0
+//
+// Every token of every channel costs N exponentials and about 4 N products, so
+// both directions are bound by the vector units, not by memory; nothing here
+// has the shape of a matrix product (the decay differs in every lane).
+//
+// Mapping.  Four lanes of a wave hold one channel (a quad; N / 4 state entries
+// each), a wave 16 channels.  A workgroup owns 16 channels of one sequence;
+// its waves take consecutive chunks of TW tokens.  A segment of waves x TW
+// tokens goes: (1) every wave scans its chunk from a zero state, keeping all
+// a_t,n in registers; (2) the waves exchange (decay product, state) in LDS and
+// fold those before them; (3) every wave scans its chunk again from the state
+// that enters it, without forming an exponential.  The state that leaves the
+// segment enters the next one, so a sequence needs no other launch and no
+// global scratch.  Per-token values (d, u, y) live in the quad's lanes, token
+// 4 i + k in lane k, and reach the other three as DPP operands.
+#include "ssd_layer.h"
+
+namespace ssd {
+namespace {
+
+struct SelParams {
+    const void* x;
+    const void* d_raw;
+    const void* z;
+    const void* B;
+    const void* C;
+    const void* dy;
+    void* y;  // or dx
+    void* dd_raw;
+    void* dz;
+    const float* d_init;
+    const float* A;
+    const float* D;
+    const float* init;
+    const float* d_final;
+    const int32_t* cu;
+    float* final_state;  // or dinit_state
+    float* seg_states;   // backward: states entering the segments [slots][blocks][64][NR]
+    float* part_w;       // backward: [S][(N + 2) E] shares of dA, dD, dd_init
+    float* part_bc;      // backward: [blocks][T][2 NP] shares of dB, dC
+    int64_t xs, ds, zs, bs_t, bs_g, cs_t, cs_g, ys, gs;
+    int64_t L, T;
+    int32_t E, N, G, epg, S;
+    int32_t nblk;   // channel blocks in all
+    int32_t bpg;    // of one group
+    int32_t units;  // runs of kRun adjacent channel blocks, over all sequences
+    int32_t upr;    // of one sequence
+};
+
+constexpr int kChan = 16;  // channels of a wave
+constexpr int kRun = 8;    // adjacent channel blocks kept on one XCD
+
+template <int NR>
+struct Shape {
+    static constexpr int NP = 4 * NR;           // state entries held
+    static constexpr int kFwdTokens = 64 / NR;  // of a wave's chunk
+    static constexpr int kFwdWaves = NR <= 8 ? 16 : 8;
+    static constexpr int kBwdTokens = 64 / NR;
+    static constexpr int kBwdWaves = 8;
+};
+
+// ---- lane helpers -------------------------------------------------------------------------
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+// The value of the quad's lane k (constant once unrolled).
+__device__ __forceinline__ float quad_lane(float v, int k) {
+    switch (k) {
+        case 0: return dpp<0x00>(v);
+        case 1: return dpp<0x55>(v);
+        case 2: return dpp<0xaa>(v);
+        default: return dpp<0xff>(v);
+    }
+}
+// Lane k of each quad gets the quad's sum of v_k.
+__device__ __forceinline__ float quad_sums(float v0, float v1, float v2, float v3, bool b0, bool b1) {
+    const float r01 = (b0 ? v1 : v0) + dpp<0xb1>(b0 ? v0 : v1);
+    const float r23 = (b0 ? v3 : v2) + dpp<0xb1>(b0 ? v2 : v3);
+    return (b1 ? r23 : r01) + dpp<0x4e>(b1 ? r01 : r23);
+}
+__device__ __forceinline__ float quad_total(float v) {
+    v += dpp<0xb1>(v);
+    return v + dpp<0x4e>(v);
+}
+// Lower half: sum of a over lanes l and l + 32; upper half: of b.
+__device__ __forceinline__ float half_sums(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// Even rows of 16 lanes: sum of a over the row and the next; odd rows: of b.
+__device__ __forceinline__ float row_sums16(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Sum over the four lanes of a row of 16 that share bits 0 and 1.
+__device__ __forceinline__ float ring_sum(float v) {
+    v += dpp<0x128>(v);  // row_ror:8
+    return v + dpp<0x124>(v);  // row_ror:4
+}
+
+// Orders a wave's own LDS writes before its later reads of other lanes' data.
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+template <int NR>
+__device__ __forceinline__ void lds_get(const float* p, float (&o)[NR]) {
+    if constexpr (NR == 2) {
+        const f32x2 t = *(const f32x2*)p;
+        o[0] = t[0];
+        o[1] = t[1];
+    } else {
+#pragma unroll
+        for (int r = 0; r < NR; r += 4) {
+            const f32x4 t = *(const f32x4*)(p + r);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[r + j] = t[j];
+        }
+    }
+}
+template <int NR>
+__device__ __forceinline__ void lds_put(float* p, const float (&v)[NR]) {
+    if constexpr (NR == 2) {
+        *(f32x2*)p = f32x2{v[0], v[1]};
+    } else {
+#pragma unroll
+        for (int r = 0; r < NR; r += 4) *(f32x4*)(p + r) = f32x4{v[r], v[r + 1], v[r + 2], v[r + 3]};
+    }
+}
+
+// ---- the parts of a chunk -----------------------------------------------------------------
+
+// What a workgroup works on.
+struct Place {
+    int seq, group, blk;     // blk counts over all groups
+    int lane, wave, nl, e;   // nl: lane of the quad; e: channel of the wave
+    int ch;                  // channel
+    bool live;               // ch lies in the group
+    int64_t first, last;
+};
+
+// False where the workgroup has nothing to do.  Runs of kRun adjacent channel
+// blocks, which share the cache lines of x and the rows of B and C, go to one
+// XCD (workgroups are dealt to the eight XCDs in turn).
+__device__ __forceinline__ bool place_of(const SelParams& p, Place& o) {
+    const uint32_t id = blockIdx.x;
+    const uint32_t unit = id / (kXcds * kRun) * kXcds + id % kXcds;
+    if (unit >= (uint32_t)p.units) return false;
+    o.seq = (int)(unit / (uint32_t)p.upr);
+    o.blk = (int)(unit % (uint32_t)p.upr) * kRun + (int)(id / kXcds % kRun);
+    if (o.blk >= p.nblk) return false;
+    o.group = o.blk / p.bpg;
+    o.lane = threadIdx.x & 63;
+    o.wave = threadIdx.x >> 6;
+    o.nl = o.lane & 3;
+    o.e = o.lane >> 2;
+    const int off = (o.blk % p.bpg) * kChan + o.e;
+    o.live = off < p.epg;
+    o.ch = o.group * p.epg + off;
+    sequence_span(p.cu, o.seq, p.L, p.T, &o.first, &o.last);
+    return true;
+}
+
+// The chunk's rows of one per-token tensor: lane nl of a quad loads token
+// 4 i + nl; 0 past the sequence or the channels.
+template <typename T, int TW>
+__device__ __forceinline__ void load_tokens(const void* src, int64_t stride, const Place& o,
+                                            int64_t t0, T (&r)[TW / 4]) {
+    const T* q = (const T*)src + o.ch;
+#pragma unroll
+    for (int i = 0; i < TW / 4; ++i) {
+        const int64_t t = t0 + 4 * i + o.nl;
+        r[i] = (o.live && t < o.last) ? q[t * stride] : (T)0.f;
+    }
+}
+
+// The chunk's B or C rows, NP entries a token (0 past N and past the sequence).
+template <typename T, int NR, int TW>
+struct Rows {
+    static constexpr int K = TW * 4 * NR / 64;
+    T v[K];
+};
+template <typename T, int NR, int TW>
+__device__ __forceinline__ void load_rows(const void* src, int64_t stride, int64_t gstride,
+                                          const SelParams& p, const Place& o, int64_t t0,
+                                          Rows<T, NR, TW>& r) {
+    constexpr int NP = 4 * NR;
+    const T* q = (const T*)src + o.group * gstride;
+#pragma unroll
+    for (int k = 0; k < r.K; ++k) {
+        const int i = o.lane + 64 * k, n = i % NP;
+        const int64_t t = t0 + i / NP;
+        r.v[k] = (n < p.N && t < o.last) ? q[t * stride + n] : (T)0.f;
+    }
+}
+// Into LDS as float32: token row t at dst + t * 2 NP.
+template <typename T, int NR, int TW>
+__device__ __forceinline__ void put_rows(float* dst, const Place& o, const Rows<T, NR, TW>& r) {
+    constexpr int NP = 4 * NR;
+#pragma unroll
+    for (int k = 0; k < r.K; ++k) {
+        const int i = o.lane + 64 * k;
+        dst[i / NP * 2 * NP + i % NP] = (float)r.v[k];
+    }
+}
+
+// ---- forward ------------------------------------------------------------------------------
+
+template <typename T, int NR>
+__global__ __launch_bounds__(64 * Shape<NR>::kFwdWaves) void selscan_fwd_kernel(SelParams p) {
+    using S = Shape<NR>;
+    constexpr int TW = S::kFwdTokens, NP = S::NP, MW = S::kFwdWaves, Q = TW / 4;
+    __shared__ __align__(16) float bc[MW][TW][2][NP];
+    __shared__ __align__(16) float exP[MW][64][NR], exH[MW][64][NR];
+    Place o;
+    if (!place_of(p, o)) return;
+    const int waves = blockDim.x >> 6;
+    const int64_t seg = (int64_t)waves * TW;
+    const bool b0 = o.nl & 1, b1 = o.nl & 2;
+    float A2[NR], carry[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        const int n = o.nl * NR + r;
+        const bool ok = o.live && n < p.N;
+        A2[r] = ok ? fmaxf(p.A[(int64_t)n * p.E + o.ch] * kLog2e, -3e38f) : 0.f;
+        carry[r] = ok && p.init ? p.init[((int64_t)o.seq * p.N + n) * p.E + o.ch] : 0.f;
+    }
+    const float dinit = o.live ? p.d_init[o.ch] : 0.f;
+    const float Dv = o.live && p.D ? p.D[o.ch] : 0.f;
+    T* y = (T*)p.y + o.ch;
+
+    T xr[Q], dr[Q], zr[Q];
+    Rows<T, NR, TW> Br, Cr;
+    int64_t t0 = o.first + (int64_t)o.wave * TW;
+    auto fetch = [&](int64_t t) {
+        load_tokens<T, TW>(p.x, p.xs, o, t, xr);
+        load_tokens<T, TW>(p.d_raw, p.ds, o, t, dr);
+        if (p.z) load_tokens<T, TW>(p.z, p.zs, o, t, zr);
+        load_rows<T, NR, TW>(p.B, p.bs_t, p.bs_g, p, o, t, Br);
+        load_rows<T, NR, TW>(p.C, p.cs_t, p.cs_g, p, o, t, Cr);
+    };
+    if (o.first < o.last) fetch(t0);
+    for (int64_t base = o.first; base < o.last; base += seg, t0 += seg) {
+        float d[Q], u[Q], x[Q], gate[Q];
+        float sumd = 0.f;
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            // past the end d = 0: the state passes unchanged
+            const bool ok = o.live && t0 + 4 * i + o.nl < o.last;
+            x[i] = (float)xr[i];
+            d[i] = ok ? softplus((float)dr[i] + dinit) : 0.f;
+            u[i] = d[i] * x[i];
+            sumd += d[i];
+            gate[i] = 1.f;
+            if (p.z) gate[i] = (float)zr[i] * sigmoid((float)zr[i]);
+        }
+        sumd = quad_total(sumd);
+        put_rows<T, NR, TW>(&bc[o.wave][0][0][0], o, Br);
+        put_rows<T, NR, TW>(&bc[o.wave][0][1][0], o, Cr);
+        wave_lds_fence();
+        fetch(t0 + seg);
+
+        float a[TW][NR], h[NR], P[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            h[r] = 0.f;
+            P[r] = fexp2(sumd * A2[r]);
+        }
+#pragma unroll
+        for (int t = 0; t < TW; ++t) {
+            float b[NR];
+            lds_get<NR>(&bc[o.wave][t][0][o.nl * NR], b);
+            const float dt = quad_lane(d[t / 4], t % 4), ut = quad_lane(u[t / 4], t % 4);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                a[t][r] = fexp2(dt * A2[r]);
+                h[r] = a[t][r] * h[r] + b[r] * ut;
+            }
+        }
+        lds_put<NR>(exP[o.wave][o.lane], P);
+        lds_put<NR>(exH[o.wave][o.lane], h);
+        __syncthreads();
+        // the state entering this chunk, and the one leaving the segment
+        const int64_t left = cdiv(o.last - base, TW);
+        const int used = (int)imin(waves, left);
+#pragma unroll
+        for (int r = 0; r < NR; ++r) h[r] = carry[r];
+#pragma unroll 4
+        for (int j = 0; j < used; ++j) {
+            float Pj[NR], hj[NR];
+            lds_get<NR>(exP[j][o.lane], Pj);
+            lds_get<NR>(exH[j][o.lane], hj);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                if (j == o.wave) h[r] = carry[r];
+                carry[r] = Pj[r] * carry[r] + hj[r];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int t = 4 * i + k;
+                float b[NR], c[NR];
+                lds_get<NR>(&bc[o.wave][t][0][o.nl * NR], b);
+                lds_get<NR>(&bc[o.wave][t][1][o.nl * NR], c);
+                const float ut = quad_lane(u[i], k);
+                v[k] = 0.f;
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    h[r] = a[t][r] * h[r] + b[r] * ut;
+                    v[k] += c[r] * h[r];
+                }
+            }
+            const float out = (quad_sums(v[0], v[1], v[2], v[3], b0, b1) + Dv * x[i]) * gate[i];
+            const int64_t t = t0 + 4 * i + o.nl;
+            if (o.live && t < o.last) y[t * p.ys] = (T)out;
+        }
+        wave_lds_fence();  // the next segment's rows go where these were read
+    }
+    if (p.final_state && o.wave == 0) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const int n = o.nl * NR + r;
+            if (o.live && n < p.N) p.final_state[((int64_t)o.seq * p.N + n) * p.E + o.ch] = carry[r];
+        }
+    }
+}
+
+// ---- backward -----------------------------------------------------------------------------
+
+// First the segments forward, only to find the state that enters each (kept in
+// seg_states); then backward, where each wave holds a and h of its chunk in
+// registers and both directions' states are folded through LDS.
+template <typename T, int NR>
+__global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(SelParams p) {
+    using S = Shape<NR>;
+    constexpr int TW = S::kBwdTokens, NP = S::NP, MW = S::kBwdWaves, Q = TW / 4;
+    __shared__ __align__(16) float bc[MW][TW][2][NP];
+    __shared__ __align__(16) float exP[MW][64][NR], exH[MW][64][NR], exQ[MW][64][NR];
+    Place o;
+    if (!place_of(p, o)) return;
+    const int waves = blockDim.x >> 6;
+    const int64_t seg = (int64_t)waves * TW;
+    const bool b0 = o.nl & 1, b1 = o.nl & 2;
+    float A2[NR], carry[NR], dA[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        const int n = o.nl * NR + r;
+        const bool ok = o.live && n < p.N;
+        A2[r] = ok ? fmaxf(p.A[(int64_t)n * p.E + o.ch] * kLog2e, -3e38f) : 0.f;
+        carry[r] = ok && p.init ? p.init[((int64_t)o.seq * p.N + n) * p.E + o.ch] : 0.f;
+        dA[r] = 0.f;
+    }
+    const float dinit = o.live ? p.d_init[o.ch] : 0.f;
+    const float Dv = o.live && p.D ? p.D[o.ch] : 0.f;
+    const int64_t len = o.last - o.first;
+    const int64_t nseg = cdiv(len, seg);
+    // sequences' segments follow one another: this one's start at a slot that
+    // no earlier sequence reaches
+    float* segs = p.seg_states + (((o.first / seg + o.seq) * p.nblk + o.blk) * 64 + o.lane) * NR;
+    const int64_t seg_step = (int64_t)p.nblk * 64 * NR;
+
+    T xr[Q], dr[Q], zr[Q], gr[Q];
+    Rows<T, NR, TW> Br, Cr;
+    // -- forward over all segments but the last
+    for (int64_t k = 0; k < nseg; ++k) {
+        const int64_t base = o.first + k * seg, t0 = base + (int64_t)o.wave * TW;
+        if (o.wave == 0) {
+#pragma unroll
+            for (int r = 0; r < NR; ++r) segs[k * seg_step + r] = carry[r];
+        }
+        if (k == nseg - 1) break;
+        load_tokens<T, TW>(p.x, p.xs, o, t0, xr);
+        load_tokens<T, TW>(p.d_raw, p.ds, o, t0, dr);
+        load_rows<T, NR, TW>(p.B, p.bs_t, p.bs_g, p, o, t0, Br);
+        float d[Q], u[Q], h[NR], P[NR];
+        float sumd = 0.f;
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            d[i] = o.live ? softplus((float)dr[i] + dinit) : 0.f;
+            u[i] = d[i] * (float)xr[i];
+            sumd += d[i];
+        }
+        sumd = quad_total(sumd);
+        wave_lds_fence();
+        put_rows<T, NR, TW>(&bc[o.wave][0][0][0], o, Br);
+        wave_lds_fence();
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            h[r] = 0.f;
+            P[r] = fexp2(sumd * A2[r]);
+        }
+#pragma unroll
+        for (int t = 0; t < TW; ++t) {
+            float b[NR];
+            lds_get<NR>(&bc[o.wave][t][0][o.nl * NR], b);
+            const float dt = quad_lane(d[t / 4], t % 4), ut = quad_lane(u[t / 4], t % 4);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) h[r] = fexp2(dt * A2[r]) * h[r] + b[r] * ut;
+        }
+        __syncthreads();
+        lds_put<NR>(exP[o.wave][o.lane], P);
+        lds_put<NR>(exH[o.wave][o.lane], h);
+        __syncthreads();
+#pragma unroll 4
+        for (int j = 0; j < waves; ++j) {
+            float Pj[NR], hj[NR];
+            lds_get<NR>(exP[j][o.lane], Pj);
+            lds_get<NR>(exH[j][o.lane], hj);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) carry[r] = Pj[r] * carry[r] + hj[r];
+        }
+    }
+    // -- backward; carry is now q: what reaches a segment from behind
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        const int n = o.nl * NR + r;
+        carry[r] = o.live && n < p.N && p.d_final
+                       ? p.d_final[((int64_t)o.seq * p.N + n) * p.E + o.ch] : 0.f;
+    }
+    float dD = 0.f, dI = 0.f;
+    for (int64_t k = nseg - 1; k >= 0; --k) {
+        const int64_t base = o.first + k * seg, t0 = base + (int64_t)o.wave * TW;
+        load_tokens<T, TW>(p.x, p.xs, o, t0, xr);
+        load_tokens<T, TW>(p.d_raw, p.ds, o, t0, dr);
+        load_tokens<T, TW>(p.dy, p.gs, o, t0, gr);
+        if (p.z) load_tokens<T, TW>(p.z, p.zs, o, t0, zr);
+        load_rows<T, NR, TW>(p.B, p.bs_t, p.bs_g, p, o, t0, Br);
+        load_rows<T, NR, TW>(p.C, p.cs_t, p.cs_g, p, o, t0, Cr);
+        float hin[NR];
+        // every lane reads what wave 0's lane of its place wrote before a barrier
+#pragma unroll
+        for (int r = 0; r < NR; ++r) hin[r] = 0.f;
+        float d[Q], u[Q], w[Q];
+        float sumd = 0.f;
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            const bool ok = o.live && t0 + 4 * i + o.nl < o.last;
+            d[i] = ok ? softplus((float)dr[i] + dinit) : 0.f;
+            u[i] = d[i] * (float)xr[i];
+            sumd += d[i];
+            w[i] = (float)gr[i];
+            if (p.z) w[i] *= (float)zr[i] * sigmoid((float)zr[i]);
+        }
+        sumd = quad_total(sumd);
+        wave_lds_fence();
+        put_rows<T, NR, TW>(&bc[o.wave][0][0][0], o, Br);
+        put_rows<T, NR, TW>(&bc[o.wave][0][1][0], o, Cr);
+        wave_lds_fence();
+        // (1) the chunk from zero states, in both directions
+        float a[TW][NR], h[NR], q[NR], P[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            h[r] = q[r] = 0.f;
+            P[r] = fexp2(sumd * A2[r]);
+        }
+#pragma unroll
+        for (int t = 0; t < TW; ++t) {
+            float b[NR];
+            lds_get<NR>(&bc[o.wave][t][0][o.nl * NR], b);
+            const float dt = quad_lane(d[t / 4], t % 4), ut = quad_lane(u[t / 4], t % 4);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                a[t][r] = fexp2(dt * A2[r]);
+                h[r] = a[t][r] * h[r] + b[r] * ut;
+            }
+        }
+#pragma unroll
+        for (int t = TW - 1; t >= 0; --t) {
+            float c[NR];
+            lds_get<NR>(&bc[o.wave][t][1][o.nl * NR], c);
+            const float wt = quad_lane(w[t / 4], t % 4);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) q[r] = a[t][r] * (c[r] * wt + q[r]);
+        }
+        // (2) fold the chunks before this one (h) and behind it (q)
+        __syncthreads();
+        lds_put<NR>(exP[o.wave][o.lane], P);
+        lds_put<NR>(exH[o.wave][o.lane], h);
+        lds_put<NR>(exQ[o.wave][o.lane], q);
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < NR; ++r) hin[r] = segs[k * seg_step + r];
+        for (int j = 0; j < o.wave; ++j) {
+            float Pj[NR], hj[NR];
+            lds_get<NR>(exP[j][o.lane], Pj);
+            lds_get<NR>(exH[j][o.lane], hj);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) hin[r] = Pj[r] * hin[r] + hj[r];
+        }
+        for (int j = waves - 1; j >= 0; --j) {
+            float Pj[NR], qj[NR];
+            lds_get<NR>(exP[j][o.lane], Pj);
+            lds_get<NR>(exQ[j][o.lane], qj);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                if (j == o.wave) q[r] = carry[r];
+                carry[r] = Pj[r] * carry[r] + qj[r];
+            }
+        }
+        // (3) h of every token, then the gradients from the last token back
+        float hs[TW][NR];
+#pragma unroll
+        for (int t = 0; t < TW; ++t) {
+            float b[NR];
+            lds_get<NR>(&bc[o.wave][t][0][o.nl * NR], b);
+            const float ut = quad_lane(u[t / 4], t % 4);
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+                hs[t][r] = a[t][r] * (t ? hs[t - 1][r] : hin[r]) + b[r] * ut;
+        }
+#pragma unroll
+        for (int i = Q - 1; i >= 0; --i) {
+            float gB[4], sA[4], v[4];
+#pragma unroll
+            for (int kk = 3; kk >= 0; --kk) {
+                const int t = 4 * i + kk;
+                float b[NR], c[NR], db[NR], dc[NR];
+                lds_get<NR>(&bc[o.wave][t][0][o.nl * NR], b);
+                lds_get<NR>(&bc[o.wave][t][1][o.nl * NR], c);
+                const float dt = quad_lane(d[i], kk), ut = quad_lane(u[i], kk);
+                const float wt = quad_lane(w[i], kk);
+                gB[kk] = sA[kk] = v[kk] = 0.f;
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const float g = c[r] * wt + q[r];
+                    q[r] = a[t][r] * g;
+                    const float s = q[r] * (t ? hs[t - 1][r] : hin[r]);
+                    gB[kk] += g * b[r];
+                    sA[kk] += A2[r] * s;
+                    dA[r] += dt * s;
+                    v[kk] += c[r] * hs[t][r];
+                    db[r] = g * ut;
+                    dc[r] = hs[t][r] * wt;
+                }
+                // sums over the wave's 16 channels: lane bit 5 picks dB or dC,
+                // bits 4 and 3 the entry, bits 1 and 0 the quad's lane
+                constexpr int M = NR >= 4 ? NR / 4 : 1;
+                float f[M];
+                if constexpr (NR == 2) {
+                    f[0] = ring_sum(row_sums16(half_sums(db[0], dc[0]), half_sums(db[1], dc[1])));
+                } else {
+                    const bool b3 = o.lane & 8;
+#pragma unroll
+                    for (int m = 0; m < M; ++m) {
+                        const float f0 = row_sums16(half_sums(db[m], dc[m]),
+                                                    half_sums(db[m + NR / 2], dc[m + NR / 2]));
+                        const float f1 = row_sums16(
+                            half_sums(db[m + NR / 4], dc[m + NR / 4]),
+                            half_sums(db[m + 3 * NR / 4], dc[m + 3 * NR / 4]));
+                        const float s0 = ring_sum(f0), s1 = ring_sum(f1);
+                        f[m] = b3 ? s1 : s0;
+                    }
+                }
+                if (t0 + t < o.last && !(o.lane & 4) && (NR > 2 || !(o.lane & 8))) {
+                    const int r0 = (o.lane & 16 ? NR / 2 : 0) + (NR > 2 && (o.lane & 8) ? NR / 4 : 0);
+                    float* f_out = p.part_bc + ((int64_t)o.blk * p.T + t0 + t) * (2 * NP) +
+                                   (o.lane & 32 ? NP : 0) + o.nl * NR + r0;
+#pragma unroll
+                    for (int m = 0; m < M; ++m) f_out[m] = f[m];
+                }
+            }
+            const int64_t t = t0 + 4 * i + o.nl;
+            const float x = (float)xr[i];
+            const float gBt = quad_sums(gB[0], gB[1], gB[2], gB[3], b0, b1);
+            const float sAt = quad_sums(sA[0], sA[1], sA[2], sA[3], b0, b1) * 0.69314718055994531f;
+            const bool ok = o.live && t < o.last;
+            const float raw = (float)dr[i] + dinit;
+            const float ddr = ok ? (x * gBt + sAt) * sigmoid(raw) : 0.f;
+            dI += ddr;
+            dD += w[i] * x;
+            if (ok) {
+                ((T*)p.y)[t * p.xs + o.ch] = (T)(w[i] * Dv + d[i] * gBt);
+                ((T*)p.dd_raw)[t * p.ds + o.ch] = (T)ddr;
+            }
+            if (p.z) {
+                const float vt = quad_sums(v[0], v[1], v[2], v[3], b0, b1) + Dv * x;
+                const float zf = (float)zr[i];
+                if (ok) ((T*)p.dz)[t * p.zs + o.ch] = (T)((float)gr[i] * vt * silu_slope(zf, sigmoid(zf)));
+            }
+        }
+        wave_lds_fence();
+    }
+    if (p.final_state && o.wave == 0) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const int n = o.nl * NR + r;
+            if (o.live && n < p.N) p.final_state[((int64_t)o.seq * p.N + n) * p.E + o.ch] = carry[r];
+        }
+    }
+    // the waves' shares of dA, dD and dd_init
+    dD = quad_total(dD);
+    dI = quad_total(dI);
+    __syncthreads();
+    lds_put<NR>(exP[o.wave][o.lane], dA);
+    exH[o.wave][o.lane][0] = dD;
+    exH[o.wave][o.lane][1] = dI;
+    __syncthreads();
+    if (o.wave || !o.live) return;
+    for (int j = 1; j < waves; ++j) {
+        float t[NR];
+        lds_get<NR>(exP[j][o.lane], t);
+#pragma unroll
+        for (int r = 0; r < NR; ++r) dA[r] += t[r];
+        dD += exH[j][o.lane][0];
+        dI += exH[j][o.lane][1];
+    }
+    float* pw = p.part_w + (int64_t)o.seq * (p.N + 2) * p.E + o.ch;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        const int n = o.nl * NR + r;
+        if (n < p.N) pw[(int64_t)n * p.E] = dA[r];
+    }
+    if (o.nl == 0) {
+        pw[(int64_t)p.N * p.E] = dD;
+        pw[(int64_t)(p.N + 1) * p.E] = dI;
+    }
+}
+
+// dB and dC: the sum over a group's channel blocks, in order.
+template <typename T>
+__global__ __launch_bounds__(256) void selscan_bc_kernel(SelParams p, void* dB, void* dC, int NP) {
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int row = 2 * NP;
+    const int64_t tg = id / row;
+    const int j = (int)(id % row), n = j % NP;
+    const int64_t t = tg / p.G;
+    const int g = (int)(tg % p.G);
+    if (t >= p.T || n >= p.N) return;
+    const float* q = p.part_bc + ((int64_t)g * p.bpg * p.T + t) * row + j;
+    const int64_t step = p.T * row;
+    float s = 0.f;
+    int b = 0;
+    for (; b + 8 <= p.bpg; b += 8) {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = q[(b + k) * step];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s += v[k];
+    }
+    for (; b < p.bpg; ++b) s += q[b * step];
+    if (j < NP) ((T*)dB)[t * p.bs_t + g * p.bs_g + n] = (T)s;
+    else ((T*)dC)[t * p.cs_t + g * p.cs_g + n] = (T)s;
+}
+
+// ---- host ---------------------------------------------------------------------------------
+
+int32_t entries_per_lane(int32_t N) { return N <= 8 ? 2 : (N <= 16 ? 4 : (N <= 32 ? 8 : 16)); }
+
+int sel_check(const ssd_selscan_dims* d) {
+    if (!d) return SSD_ERR_NULL_ARG;
+    if (d->dtype != SSD_F32 && d->dtype != SSD_BF16) return SSD_ERR_DTYPE;
+    if (d->batch < 1 || d->seqlen < 0 || d->seqlen > kMaxTokens || d->channels < 1 ||
+        d->channels > SSD_SELSCAN_MAX_CHANNELS || d->ngroups < 1 || d->channels % d->ngroups ||
+        d->d_state < 1 || d->nseq < 0 || (d->nseq > 0 && d->batch != 1) ||
+        (int64_t)d->batch * d->seqlen > kMaxTokens)
+        return SSD_ERR_SHAPE;
+    if (d->d_state > SSD_SELSCAN_MAX_STATE) return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+struct SelPlan {
+    int32_t NR, S, bpg, nblk, upr;
+    int64_t units, grid, T;
+    int64_t slots;  // backward: segments of all sequences, at most
+    size_t off_seg, off_w, off_bc, total;
+};
+
+int sel_plan(const ssd_selscan_dims& d, SelPlan* pl) {
+    pl->NR = entries_per_lane(d.d_state);
+    pl->T = (int64_t)d.batch * d.seqlen;
+    pl->S = d.nseq > 0 ? d.nseq : d.batch;
+    pl->bpg = (int32_t)cdiv(d.channels / d.ngroups, kChan);
+    const int64_t nblk = (int64_t)pl->bpg * d.ngroups;
+    pl->nblk = (int32_t)nblk;
+    pl->upr = (int32_t)cdiv(nblk, kRun);
+    pl->units = (int64_t)pl->S * pl->upr;
+    pl->grid = cdiv(pl->units, kXcds) * kXcds * kRun;
+    if (pl->grid > INT32_MAX) return SSD_ERR_SHAPE;
+    const int64_t seg = 8 * (64 / pl->NR);
+    pl->slots = pl->T / seg + pl->S + 1;
+    size_t off = 0;
+    pl->off_seg = off;
+    off = up256(off + (size_t)pl->slots * nblk * 64 * pl->NR * sizeof(float));
+    pl->off_w = off;
+    off = up256(off + (size_t)pl->S * (d.d_state + 2) * d.channels * sizeof(float));
+    pl->off_bc = off;
+    off = up256(off + (size_t)nblk * pl->T * 8 * pl->NR * sizeof(float));
+    pl->total = off;
+    return SSD_OK;
+}
+
+// Shared checks and parameters of both directions.
+int sel_setup(const ssd_selscan_dims* dims, const ssd_selscan_layout* layout, const void* x,
+              const void* d_raw, const float* d_init, const float* A, const void* B, const void* C,
+              const float* D, const void* z, const float* init, const int32_t* cu, bool bwd,
+              SelParams* p, SelPlan* pl) {
+    int st = sel_check(dims);
+    if (st != SSD_OK) return st;
+    const ssd_selscan_dims& d = *dims;
+    const int64_t E = d.channels, N = d.d_state, G = d.ngroups;
+    ssd_selscan_layout l = {E, E, E, G * N, N, G * N, N, E, E};
+    if (layout) l = *layout;
+    if (!z) l.z_token = E;
+    for (int64_t s : {l.x_token, l.d_raw_token, l.z_token, bwd ? l.dy_token : l.y_token})
+        if (s < E || s > kMaxStride) return SSD_ERR_SHAPE;
+    for (int64_t s : {l.B_token, l.B_group, l.C_token, l.C_group})
+        if (s < 0 || s > kMaxStride) return SSD_ERR_SHAPE;
+    if ((d.nseq > 0) != (cu != nullptr)) return cu ? SSD_ERR_SHAPE : SSD_ERR_NULL_ARG;
+    if ((st = sel_plan(d, pl)) != SSD_OK) return st;
+    if (!d_init || !A || (pl->T > 0 && (!x || !d_raw || !B || !C))) return SSD_ERR_NULL_ARG;
+    const size_t e = elem_size(d.dtype);
+    for (const void* q : {x, d_raw, B, C, z})
+        if (!elem_aligned(q, e)) return SSD_ERR_ALIGN;
+    for (const void* q : {(const void*)d_init, (const void*)A, (const void*)D, (const void*)init,
+                          (const void*)cu})
+        if (!elem_aligned(q, 4)) return SSD_ERR_ALIGN;
+    *p = {};
+    p->x = x;
+    p->d_raw = d_raw;
+    p->z = z;
+    p->B = B;
+    p->C = C;
+    p->d_init = d_init;
+    p->A = A;
+    p->D = D;
+    p->init = init;
+    p->cu = cu;
+    p->xs = l.x_token;
+    p->ds = l.d_raw_token;
+    p->zs = l.z_token;
+    p->bs_t = l.B_token;
+    p->bs_g = l.B_group;
+    p->cs_t = l.C_token;
+    p->cs_g = l.C_group;
+    p->ys = l.y_token;
+    p->gs = l.dy_token;
+    p->L = d.seqlen;
+    p->T = pl->T;
+    p->E = d.channels;
+    p->N = d.d_state;
+    p->G = d.ngroups;
+    p->epg = d.channels / d.ngroups;
+    p->S = pl->S;
+    p->nblk = pl->nblk;
+    p->bpg = pl->bpg;
+    p->units = (int32_t)pl->units;
+    p->upr = pl->upr;
+    return SSD_OK;
+}
+
+template <typename T, int NR>
+void launch_sel(const SelParams& p, unsigned grid, bool bwd, hipStream_t s) {
+    if (bwd) selscan_bwd_kernel<T, NR><<<dim3(grid), dim3(64 * Shape<NR>::kBwdWaves), 0, s>>>(p);
+    else selscan_fwd_kernel<T, NR><<<dim3(grid), dim3(64 * Shape<NR>::kFwdWaves), 0, s>>>(p);
+}
+template <typename T>
+void launch_sel(const SelParams& p, int NR, unsigned grid, bool bwd, hipStream_t s) {
+    if (NR == 2) launch_sel<T, 2>(p, grid, bwd, s);
+    else if (NR == 4) launch_sel<T, 4>(p, grid, bwd, s);
+    else if (NR == 8) launch_sel<T, 8>(p, grid, bwd, s);
+    else launch_sel<T, 16>(p, grid, bwd, s);
+}
+
+}  // namespace
+}  // namespace ssd
+
+using namespace ssd;
+
+extern "C" {
+
+size_t ssd_selscan_fwd_workspace_bytes(const ssd_selscan_dims* dims) {
+    (void)dims;
+    return 0;
+}
+
+int ssd_selscan_fwd(const ssd_selscan_dims* dims, const ssd_selscan_layout* layout, const void* x,
+                    const void* d_raw, const float* d_init, const float* A, const void* B,
+                    const void* C, const float* D, const void* z, const float* init_state,
+                    const int32_t* cu_seqlens, void* y, float* final_state, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+    (void)workspace;
+    (void)workspace_bytes;
+    SelParams p;
+    SelPlan pl;
+    int st = sel_setup(dims, layout, x, d_raw, d_init, A, B, C, D, z, init_state, cu_seqlens, false,
+                       &p, &pl);
+    if (st != SSD_OK) return st;
+    if (pl.T > 0 && !y) return SSD_ERR_NULL_ARG;
+    if (!elem_aligned(y, elem_size(dims->dtype)) || !elem_aligned(final_state, 4))
+        return SSD_ERR_ALIGN;
+    const size_t sb = (size_t)pl.S * dims->d_state * dims->channels * sizeof(float);
+    if (overlaps(init_state, sb, final_state, sb)) return SSD_ERR_OVERLAP;
+    hipStream_t s = (hipStream_t)stream;
+    if (cu_seqlens && check_cu_env(cu_seqlens, dims->nseq, pl.T, s, &st)) return st;
+    if (pl.T == 0 && !final_state) return SSD_OK;
+    p.y = y;
+    p.final_state = final_state;
+    if (dims->dtype == SSD_BF16) launch_sel<bf16>(p, pl.NR, (unsigned)pl.grid, false, s);
+    else launch_sel<float>(p, pl.NR, (unsigned)pl.grid, false, s);
+    return launched();
+}
+
+size_t ssd_selscan_bwd_workspace_bytes(const ssd_selscan_dims* dims) {
+    SelPlan pl;
+    if (sel_check(dims) != SSD_OK || sel_plan(*dims, &pl) != SSD_OK) return 0;
+    return pl.total;
+}
+
+int ssd_selscan_bwd(const ssd_selscan_dims* dims, const ssd_selscan_layout* layout, const void* x,
+                    const void* d_raw, const float* d_init, const float* A, const void* B,
+                    const void* C, const float* D, const void* z, const float* init_state,
+                    const int32_t* cu_seqlens, const void* dy, const float* d_final, void* dx,
+                    void* dd_raw, void* dB, void* dC, void* dz, float* dA, float* dD,
+                    float* dd_init, float* dinit_state, void* workspace, size_t workspace_bytes,
+                    void* stream) {
+    SelParams p;
+    SelPlan pl;
+    int st = sel_setup(dims, layout, x, d_raw, d_init, A, B, C, D, z, init_state, cu_seqlens, true,
+                       &p, &pl);
+    if (st != SSD_OK) return st;
+    if (pl.T > 0 && (!dy || !dx || !dd_raw || !dB || !dC || (z && !dz))) return SSD_ERR_NULL_ARG;
+    const size_t e = elem_size(dims->dtype);
+    for (const void* q : {dy, (const void*)dx, (const void*)dd_raw, (const void*)dB,
+                          (const void*)dC, (const void*)dz})
+        if (!elem_aligned(q, e)) return SSD_ERR_ALIGN;
+    for (const void* q : {(const void*)d_final, (const void*)dA, (const void*)dD,
+                          (const void*)dd_init, (const void*)dinit_state})
+        if (!elem_aligned(q, 4)) return SSD_ERR_ALIGN;
+    if ((uintptr_t)workspace & 255) return SSD_ERR_ALIGN;
+    if (!workspace || workspace_bytes < pl.total) return SSD_ERR_WORKSPACE;
+    const size_t sb = (size_t)pl.S * dims->d_state * dims->channels * sizeof(float);
+    if (overlaps(d_final, sb, dinit_state, sb)) return SSD_ERR_OVERLAP;
+    hipStream_t s = (hipStream_t)stream;
+    if (cu_seqlens && check_cu_env(cu_seqlens, dims->nseq, pl.T, s, &st)) return st;
+    char* ws = (char*)workspace;
+    p.dy = dy;
+    p.d_final = d_final;
+    p.y = dx;
+    p.dd_raw = dd_raw;
+    p.dz = dz;
+    p.final_state = dinit_state;
+    p.seg_states = (float*)(ws + pl.off_seg);
+    p.part_w = (float*)(ws + pl.off_w);
+    p.part_bc = (float*)(ws + pl.off_bc);
+    if (dims->dtype == SSD_BF16) launch_sel<bf16>(p, pl.NR, (unsigned)pl.grid, true, s);
+    else launch_sel<float>(p, pl.NR, (unsigned)pl.grid, true, s);
+    if ((st = launched()) != SSD_OK) return st;
+    const int NP = 4 * pl.NR;
+    const int64_t items = pl.T * dims->ngroups * 2 * NP;
+    if (items > 0) {
+        const int64_t grid = cdiv(items, 256);
+        if (grid > INT32_MAX) return SSD_ERR_SHAPE;
+        const dim3 gd((unsigned)grid), bd(256);
+        if (dims->dtype == SSD_BF16) selscan_bc_kernel<bf16><<<gd, bd, 0, s>>>(p, dB, dC, NP);
+        else selscan_bc_kernel<float><<<gd, bd, 0, s>>>(p, dB, dC, NP);
+        if ((st = launched()) != SSD_OK) return st;
+    }
+    ColSum c = {};
+    c.part = p.part_w;
+    c.rows = pl.S;
+    c.cols = (int64_t)(dims->d_state + 2) * dims->channels;
+    c.out0 = dA;
+    c.c0 = (int64_t)dims->d_state * dims->channels;
+    c.out1 = dD;
+    c.c1 = dims->channels;
+    c.out2 = dd_init;
+    return launch_colsum(c, s);
+}
+
+}  // extern "C"
