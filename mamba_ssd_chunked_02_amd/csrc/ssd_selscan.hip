@@ -63,7 +63,7 @@ template <int NR>
 struct Shape {
     static constexpr int NP = 4 * NR;           // state entries held
     static constexpr int kFwdTokens = 64 / NR;  // of a wave's chunk
-    static constexpr int kFwdWaves = NR <= 8 ? 16 : 8;
+    static constexpr int kFwdWaves = NR <= 4 ? 16 : 8;
     static constexpr int kBwdTokens = 64 / NR;
     static constexpr int kBwdWaves = 8;
 };
@@ -148,9 +148,10 @@ __device__ __forceinline__ void lds_put(float* p, const float (&v)[NR]) {
 struct Place {
     int seq, group, blk;     // blk counts over all groups
     int lane, wave, nl, e;   // nl: lane of the quad; e: channel of the wave
-    int ch;                  // channel
-    bool live;               // ch lies in the group
-    int64_t first, last;
+    int ch0, ch;             // the workgroup's first channel; the lane's
+    int width;               // channels of the workgroup
+    bool live;               // ch is one of them
+    int first, last;
 };
 
 // False where the workgroup has nothing to do.  Runs of kRun adjacent channel
@@ -165,27 +166,72 @@ __device__ __forceinline__ bool place_of(const SelParams& p, Place& o) {
     if (o.blk >= p.nblk) return false;
     o.group = o.blk / p.bpg;
     o.lane = threadIdx.x & 63;
-    o.wave = threadIdx.x >> 6;
+    o.wave = wave_id();
     o.nl = o.lane & 3;
     o.e = o.lane >> 2;
     const int off = (o.blk % p.bpg) * kChan + o.e;
     o.live = off < p.epg;
-    o.ch = o.group * p.epg + off;
-    sequence_span(p.cu, o.seq, p.L, p.T, &o.first, &o.last);
+    o.ch0 = o.group * p.epg + (o.blk % p.bpg) * kChan;
+    o.ch = o.ch0 + o.e;
+    o.width = min(kChan, p.epg - (o.blk % p.bpg) * kChan);
+    int64_t first, last;
+    sequence_span(p.cu, o.seq, p.L, p.T, &first, &last);
+    o.first = __builtin_amdgcn_readfirstlane((int)first);
+    o.last = __builtin_amdgcn_readfirstlane((int)last);
     return true;
 }
 
-// The chunk's rows of one per-token tensor: lane nl of a quad loads token
-// 4 i + nl; 0 past the sequence or the channels.
-template <typename T, int TW>
-__device__ __forceinline__ void load_tokens(const void* src, int64_t stride, const Place& o,
-                                            int64_t t0, T (&r)[TW / 4]) {
-    const T* q = (const T*)src + o.ch;
-#pragma unroll
-    for (int i = 0; i < TW / 4; ++i) {
-        const int64_t t = t0 + 4 * i + o.nl;
-        r[i] = (o.live && t < o.last) ? q[t * stride] : (T)0.f;
+// The rows [tb, tb + have) of a per-token tensor as a buffer resource: lanes
+// give byte offsets from row tb, and an offset past the last row reads 0 and
+// stores nothing, so no access is predicated.  Everything in it is uniform.
+template <typename T>
+struct RowBuf {
+    __amdgpu_buffer_rsrc_t r;
+    __device__ __forceinline__ T get(uint32_t off) const {
+        if constexpr (sizeof(T) == 2)
+            return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
+        else
+            return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
     }
+    __device__ __forceinline__ void put(uint32_t off, float v) const {
+        if constexpr (sizeof(T) == 2)
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, (T)v), r, off, 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), r, off, 0, 0);
+    }
+};
+// An offset past every row of a chunk (at most 32 rows of 2^24 4-byte
+// elements): added to the largest row offset it still does not wrap.
+constexpr uint32_t kNowhere = 0x80000000u;
+// A value the compiler does not carry sums of across loop iterations: the
+// offsets off + i * step are formed anew in each segment (one add each) rather
+// than kept, which took 30 registers and spilled.
+__device__ __forceinline__ uint32_t fresh(uint32_t off) {
+    asm volatile("" : "+v"(off));
+    return off;
+}
+
+// width: elements of the last row that count.
+template <typename T>
+__device__ __forceinline__ RowBuf<T> row_buf(const void* src, int64_t stride, int64_t col, int tb,
+                                             int have, int width) {
+    const T* q = (const T*)src + (int64_t)tb * stride + col;
+    const uint32_t n = src && have > 0
+                           ? (uint32_t)(((have - 1) * stride + width) * (int64_t)sizeof(T)) : 0u;
+    return {__builtin_amdgcn_make_buffer_rsrc((void*)q, (short)0, (int)n, 0x00020000)};
+}
+
+// The chunk's rows of one per-token tensor: lane nl of a quad loads token
+// 4 i + nl from the lane's offset `off` (kNowhere in a lane without a channel).
+template <typename T, int TW>
+__device__ __forceinline__ void load_tokens(const void* src, int64_t stride, const Place& o, int tb,
+                                            T (&r)[TW / 4]) {
+    const RowBuf<T> q = row_buf<T>(src, stride, o.ch0, tb, min(o.last - tb, TW), o.width);
+    const uint32_t step = (uint32_t)(4 * stride) * (uint32_t)sizeof(T);
+    const uint32_t off =
+        fresh(o.live ? (uint32_t)(o.nl * stride + o.e) * (uint32_t)sizeof(T) : kNowhere);
+#pragma unroll
+    for (int i = 0; i < TW / 4; ++i) r[i] = q.get(off + i * step);
 }
 
 // The chunk's B or C rows, NP entries a token (0 past N and past the sequence).
@@ -196,26 +242,24 @@ struct Rows {
 };
 template <typename T, int NR, int TW>
 __device__ __forceinline__ void load_rows(const void* src, int64_t stride, int64_t gstride,
-                                          const SelParams& p, const Place& o, int64_t t0,
+                                          const SelParams& p, const Place& o, int tb,
                                           Rows<T, NR, TW>& r) {
-    constexpr int NP = 4 * NR;
-    const T* q = (const T*)src + o.group * gstride;
+    constexpr int NP = 4 * NR, TK = 64 / NP;  // tokens a load
+    const RowBuf<T> q = row_buf<T>(src, stride, o.group * gstride, tb, min(o.last - tb, TW), p.N);
+    const int n = o.lane % NP, t0 = o.lane / NP;
+    const uint32_t step = (uint32_t)(TK * stride) * (uint32_t)sizeof(T);
+    const uint32_t off =
+        fresh(n < p.N ? (uint32_t)(t0 * stride + n) * (uint32_t)sizeof(T) : kNowhere);
 #pragma unroll
-    for (int k = 0; k < r.K; ++k) {
-        const int i = o.lane + 64 * k, n = i % NP;
-        const int64_t t = t0 + i / NP;
-        r.v[k] = (n < p.N && t < o.last) ? q[t * stride + n] : (T)0.f;
-    }
+    for (int k = 0; k < r.K; ++k) r.v[k] = q.get(off + k * step);
 }
 // Into LDS as float32: token row t at dst + t * 2 NP.
 template <typename T, int NR, int TW>
 __device__ __forceinline__ void put_rows(float* dst, const Place& o, const Rows<T, NR, TW>& r) {
-    constexpr int NP = 4 * NR;
+    constexpr int NP = 4 * NR, TK = 64 / NP;
+    float* q = dst + o.lane / NP * 2 * NP + o.lane % NP;
 #pragma unroll
-    for (int k = 0; k < r.K; ++k) {
-        const int i = o.lane + 64 * k;
-        dst[i / NP * 2 * NP + i % NP] = (float)r.v[k];
-    }
+    for (int k = 0; k < r.K; ++k) q[k * TK * 2 * NP] = (float)r.v[k];
 }
 
 // ---- forward ------------------------------------------------------------------------------
@@ -225,11 +269,11 @@ __global__ __launch_bounds__(64 * Shape<NR>::kFwdWaves) void selscan_fwd_kernel(
     using S = Shape<NR>;
     constexpr int TW = S::kFwdTokens, NP = S::NP, MW = S::kFwdWaves, Q = TW / 4;
     __shared__ __align__(16) float bc[MW][TW][2][NP];
-    __shared__ __align__(16) float exP[MW][64][NR], exH[MW][64][NR];
+    __shared__ __align__(16) float exP[2][MW][64][NR], exH[2][MW][64][NR];
     Place o;
     if (!place_of(p, o)) return;
     const int waves = blockDim.x >> 6;
-    const int64_t seg = (int64_t)waves * TW;
+    const int seg = waves * TW;
     const bool b0 = o.nl & 1, b1 = o.nl & 2;
     float A2[NR], carry[NR];
 #pragma unroll
@@ -241,45 +285,46 @@ __global__ __launch_bounds__(64 * Shape<NR>::kFwdWaves) void selscan_fwd_kernel(
     }
     const float dinit = o.live ? p.d_init[o.ch] : 0.f;
     const float Dv = o.live && p.D ? p.D[o.ch] : 0.f;
-    T* y = (T*)p.y + o.ch;
+    const uint32_t ystep = (uint32_t)(4 * p.ys) * (uint32_t)sizeof(T);
+    const uint32_t yoff = o.live ? (uint32_t)(o.nl * p.ys + o.e) * (uint32_t)sizeof(T) : kNowhere;
+    const bool gated = p.z != nullptr;
 
     T xr[Q], dr[Q], zr[Q];
     Rows<T, NR, TW> Br, Cr;
-    int64_t t0 = o.first + (int64_t)o.wave * TW;
-    auto fetch = [&](int64_t t) {
+    int tb = o.first + o.wave * TW;
+    auto fetch = [&](int t) {
         load_tokens<T, TW>(p.x, p.xs, o, t, xr);
         load_tokens<T, TW>(p.d_raw, p.ds, o, t, dr);
-        if (p.z) load_tokens<T, TW>(p.z, p.zs, o, t, zr);
         load_rows<T, NR, TW>(p.B, p.bs_t, p.bs_g, p, o, t, Br);
         load_rows<T, NR, TW>(p.C, p.cs_t, p.cs_g, p, o, t, Cr);
     };
-    if (o.first < o.last) fetch(t0);
-    for (int64_t base = o.first; base < o.last; base += seg, t0 += seg) {
-        float d[Q], u[Q], x[Q], gate[Q];
+    fetch(tb);
+    int turn = 0;
+    for (int base = o.first; base < o.last; base += seg, tb += seg, turn ^= 1) {
+        load_tokens<T, TW>(p.z, p.zs, o, tb, zr);
+        float d[Q], u[Q], x[Q];
         float sumd = 0.f;
+        // tokens of this chunk that the sequence has (none or fewer: the rest
+        // take d = 0, which passes the state on unchanged)
+        const int have = min(o.last - tb, TW);
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
-            // past the end d = 0: the state passes unchanged
-            const bool ok = o.live && t0 + 4 * i + o.nl < o.last;
             x[i] = (float)xr[i];
-            d[i] = ok ? softplus((float)dr[i] + dinit) : 0.f;
+            d[i] = 4 * i + o.nl < have ? softplus((float)dr[i] + dinit) : 0.f;
             u[i] = d[i] * x[i];
             sumd += d[i];
-            gate[i] = 1.f;
-            if (p.z) gate[i] = (float)zr[i] * sigmoid((float)zr[i]);
         }
         sumd = quad_total(sumd);
         put_rows<T, NR, TW>(&bc[o.wave][0][0][0], o, Br);
         put_rows<T, NR, TW>(&bc[o.wave][0][1][0], o, Cr);
         wave_lds_fence();
-        fetch(t0 + seg);
 
-        float a[TW][NR], h[NR], P[NR];
+        float a[TW][NR], h[NR];
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            h[r] = 0.f;
-            P[r] = fexp2(sumd * A2[r]);
-        }
+        for (int r = 0; r < NR; ++r) h[r] = fexp2(sumd * A2[r]);
+        lds_put<NR>(exP[turn][o.wave][o.lane], h);
+#pragma unroll
+        for (int r = 0; r < NR; ++r) h[r] = 0.f;
 #pragma unroll
         for (int t = 0; t < TW; ++t) {
             float b[NR];
@@ -290,29 +335,32 @@ __global__ __launch_bounds__(64 * Shape<NR>::kFwdWaves) void selscan_fwd_kernel(
                 a[t][r] = fexp2(dt * A2[r]);
                 h[r] = a[t][r] * h[r] + b[r] * ut;
             }
+            if (t & 1) __builtin_amdgcn_sched_barrier(0);
         }
-        lds_put<NR>(exP[o.wave][o.lane], P);
-        lds_put<NR>(exH[o.wave][o.lane], h);
+        lds_put<NR>(exH[turn][o.wave][o.lane], h);
+        // the exchange is double-buffered: a wave is at most one barrier ahead
         __syncthreads();
         // the state entering this chunk, and the one leaving the segment
-        const int64_t left = cdiv(o.last - base, TW);
-        const int used = (int)imin(waves, left);
+        const int used = min(waves, (o.last - base + TW - 1) / TW);
 #pragma unroll
         for (int r = 0; r < NR; ++r) h[r] = carry[r];
-#pragma unroll 4
         for (int j = 0; j < used; ++j) {
             float Pj[NR], hj[NR];
-            lds_get<NR>(exP[j][o.lane], Pj);
-            lds_get<NR>(exH[j][o.lane], hj);
+            lds_get<NR>(exP[turn][j][o.lane], Pj);
+            lds_get<NR>(exH[turn][j][o.lane], hj);
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
                 if (j == o.wave) h[r] = carry[r];
                 carry[r] = Pj[r] * carry[r] + hj[r];
             }
         }
-        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+        const RowBuf<T> y = row_buf<T>(p.y, p.ys, o.ch0, tb, have, o.width);
+        const uint32_t yat = fresh(yoff);
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
+            // the next segment's rows, once half of a is used up
+            if (i == Q / 2) fetch(tb + seg);
             float v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -327,10 +375,13 @@ __global__ __launch_bounds__(64 * Shape<NR>::kFwdWaves) void selscan_fwd_kernel(
                     h[r] = a[t][r] * h[r] + b[r] * ut;
                     v[k] += c[r] * h[r];
                 }
+                if (k & 1) __builtin_amdgcn_sched_barrier(0);
             }
-            const float out = (quad_sums(v[0], v[1], v[2], v[3], b0, b1) + Dv * x[i]) * gate[i];
-            const int64_t t = t0 + 4 * i + o.nl;
-            if (o.live && t < o.last) y[t * p.ys] = (T)out;
+            float out = quad_sums(v[0], v[1], v[2], v[3], b0, b1) + Dv * x[i];
+            const float zf = (float)zr[i];
+            out *= gated ? zf * sigmoid(zf) : 1.f;
+            y.put(yat + i * ystep, out);
+            __builtin_amdgcn_sched_barrier(0);
         }
         wave_lds_fence();  // the next segment's rows go where these were read
     }
@@ -357,7 +408,7 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
     Place o;
     if (!place_of(p, o)) return;
     const int waves = blockDim.x >> 6;
-    const int64_t seg = (int64_t)waves * TW;
+    const int seg = waves * TW;
     const bool b0 = o.nl & 1, b1 = o.nl & 2;
     float A2[NR], carry[NR], dA[NR];
 #pragma unroll
@@ -370,31 +421,32 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
     }
     const float dinit = o.live ? p.d_init[o.ch] : 0.f;
     const float Dv = o.live && p.D ? p.D[o.ch] : 0.f;
-    const int64_t len = o.last - o.first;
-    const int64_t nseg = cdiv(len, seg);
+    const bool gated = p.z != nullptr;
+    const int nseg = (o.last - o.first + seg - 1) / seg;
     // sequences' segments follow one another: this one's start at a slot that
     // no earlier sequence reaches
-    float* segs = p.seg_states + (((o.first / seg + o.seq) * p.nblk + o.blk) * 64 + o.lane) * NR;
+    float* segs = p.seg_states +
+                  (((int64_t)(o.first / seg + o.seq) * p.nblk + o.blk) * 64 + o.lane) * NR;
     const int64_t seg_step = (int64_t)p.nblk * 64 * NR;
 
     T xr[Q], dr[Q], zr[Q], gr[Q];
     Rows<T, NR, TW> Br, Cr;
     // -- forward over all segments but the last
-    for (int64_t k = 0; k < nseg; ++k) {
-        const int64_t base = o.first + k * seg, t0 = base + (int64_t)o.wave * TW;
+    for (int k = 0; k < nseg; ++k) {
+        const int tb = o.first + k * seg + o.wave * TW;
         if (o.wave == 0) {
 #pragma unroll
             for (int r = 0; r < NR; ++r) segs[k * seg_step + r] = carry[r];
         }
         if (k == nseg - 1) break;
-        load_tokens<T, TW>(p.x, p.xs, o, t0, xr);
-        load_tokens<T, TW>(p.d_raw, p.ds, o, t0, dr);
-        load_rows<T, NR, TW>(p.B, p.bs_t, p.bs_g, p, o, t0, Br);
+        load_tokens<T, TW>(p.x, p.xs, o, tb, xr);
+        load_tokens<T, TW>(p.d_raw, p.ds, o, tb, dr);
+        load_rows<T, NR, TW>(p.B, p.bs_t, p.bs_g, p, o, tb, Br);
         float d[Q], u[Q], h[NR], P[NR];
         float sumd = 0.f;
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
-            d[i] = o.live ? softplus((float)dr[i] + dinit) : 0.f;
+            d[i] = softplus((float)dr[i] + dinit);
             u[i] = d[i] * (float)xr[i];
             sumd += d[i];
         }
@@ -419,7 +471,6 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
         lds_put<NR>(exP[o.wave][o.lane], P);
         lds_put<NR>(exH[o.wave][o.lane], h);
         __syncthreads();
-#pragma unroll 4
         for (int j = 0; j < waves; ++j) {
             float Pj[NR], hj[NR];
             lds_get<NR>(exP[j][o.lane], Pj);
@@ -436,28 +487,30 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
                        ? p.d_final[((int64_t)o.seq * p.N + n) * p.E + o.ch] : 0.f;
     }
     float dD = 0.f, dI = 0.f;
-    for (int64_t k = nseg - 1; k >= 0; --k) {
-        const int64_t base = o.first + k * seg, t0 = base + (int64_t)o.wave * TW;
-        load_tokens<T, TW>(p.x, p.xs, o, t0, xr);
-        load_tokens<T, TW>(p.d_raw, p.ds, o, t0, dr);
-        load_tokens<T, TW>(p.dy, p.gs, o, t0, gr);
-        if (p.z) load_tokens<T, TW>(p.z, p.zs, o, t0, zr);
-        load_rows<T, NR, TW>(p.B, p.bs_t, p.bs_g, p, o, t0, Br);
-        load_rows<T, NR, TW>(p.C, p.cs_t, p.cs_g, p, o, t0, Cr);
-        float hin[NR];
-        // every lane reads what wave 0's lane of its place wrote before a barrier
-#pragma unroll
-        for (int r = 0; r < NR; ++r) hin[r] = 0.f;
+    // where the lane's sums over channels go: see the reduction below
+    const int r_of = (o.lane & 16 ? NR / 2 : 0) + (NR > 2 && (o.lane & 8) ? NR / 4 : 0);
+    const uint32_t sum_off = !(o.lane & 4) && (NR > 2 || !(o.lane & 8))
+                                 ? (uint32_t)((o.lane & 32 ? NP : 0) + o.nl * NR + r_of) * 4u
+                                 : kNowhere;
+    for (int k = nseg - 1; k >= 0; --k) {
+        const int base = o.first + k * seg, tb = base + o.wave * TW;
+        const int have = min(o.last - tb, TW);
+        load_tokens<T, TW>(p.x, p.xs, o, tb, xr);
+        load_tokens<T, TW>(p.d_raw, p.ds, o, tb, dr);
+        load_tokens<T, TW>(p.dy, p.gs, o, tb, gr);
+        load_tokens<T, TW>(p.z, p.zs, o, tb, zr);
+        load_rows<T, NR, TW>(p.B, p.bs_t, p.bs_g, p, o, tb, Br);
+        load_rows<T, NR, TW>(p.C, p.cs_t, p.cs_g, p, o, tb, Cr);
         float d[Q], u[Q], w[Q];
         float sumd = 0.f;
+        // past the sequence and in lanes without a channel x and dy are 0
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
-            const bool ok = o.live && t0 + 4 * i + o.nl < o.last;
-            d[i] = ok ? softplus((float)dr[i] + dinit) : 0.f;
+            d[i] = 4 * i + o.nl < have ? softplus((float)dr[i] + dinit) : 0.f;
             u[i] = d[i] * (float)xr[i];
             sumd += d[i];
-            w[i] = (float)gr[i];
-            if (p.z) w[i] *= (float)zr[i] * sigmoid((float)zr[i]);
+            const float zf = (float)zr[i];
+            w[i] = (float)gr[i] * (gated ? zf * sigmoid(zf) : 1.f);
         }
         sumd = quad_total(sumd);
         wave_lds_fence();
@@ -481,6 +534,7 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
                 a[t][r] = fexp2(dt * A2[r]);
                 h[r] = a[t][r] * h[r] + b[r] * ut;
             }
+            if (t & 1) __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int t = TW - 1; t >= 0; --t) {
@@ -489,6 +543,7 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
             const float wt = quad_lane(w[t / 4], t % 4);
 #pragma unroll
             for (int r = 0; r < NR; ++r) q[r] = a[t][r] * (c[r] * wt + q[r]);
+            if (!(t & 1)) __builtin_amdgcn_sched_barrier(0);
         }
         // (2) fold the chunks before this one (h) and behind it (q)
         __syncthreads();
@@ -496,6 +551,7 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
         lds_put<NR>(exH[o.wave][o.lane], h);
         lds_put<NR>(exQ[o.wave][o.lane], q);
         __syncthreads();
+        float hin[NR];
 #pragma unroll
         for (int r = 0; r < NR; ++r) hin[r] = segs[k * seg_step + r];
         for (int j = 0; j < o.wave; ++j) {
@@ -525,7 +581,17 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
 #pragma unroll
             for (int r = 0; r < NR; ++r)
                 hs[t][r] = a[t][r] * (t ? hs[t - 1][r] : hin[r]) + b[r] * ut;
+            if (t & 1) __builtin_amdgcn_sched_barrier(0);
         }
+        const RowBuf<float> sums = row_buf<float>(p.part_bc + (int64_t)o.blk * p.T * (2 * NP),
+                                                  2 * NP, 0, tb, have, 2 * NP);
+        const RowBuf<T> dx = row_buf<T>(p.y, p.xs, o.ch0, tb, have, o.width);
+        const RowBuf<T> ddr = row_buf<T>(p.dd_raw, p.ds, o.ch0, tb, have, o.width);
+        const RowBuf<T> dz = row_buf<T>(p.dz, p.zs, o.ch0, tb, gated ? have : 0, o.width);
+        const auto lane_off = [&](int64_t stride) {
+            return fresh(o.live ? (uint32_t)(o.nl * stride + o.e) * (uint32_t)sizeof(T) : kNowhere);
+        };
+        const uint32_t xoff = lane_off(p.xs), doff = lane_off(p.ds), zoff = lane_off(p.zs);
 #pragma unroll
         for (int i = Q - 1; i >= 0; --i) {
             float gB[4], sA[4], v[4];
@@ -560,41 +626,34 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
                     const bool b3 = o.lane & 8;
 #pragma unroll
                     for (int m = 0; m < M; ++m) {
-                        const float f0 = row_sums16(half_sums(db[m], dc[m]),
-                                                    half_sums(db[m + NR / 2], dc[m + NR / 2]));
-                        const float f1 = row_sums16(
-                            half_sums(db[m + NR / 4], dc[m + NR / 4]),
-                            half_sums(db[m + 3 * NR / 4], dc[m + 3 * NR / 4]));
-                        const float s0 = ring_sum(f0), s1 = ring_sum(f1);
-                        f[m] = b3 ? s1 : s0;
+                        const float f0 = ring_sum(row_sums16(half_sums(db[m], dc[m]),
+                                                             half_sums(db[m + NR / 2], dc[m + NR / 2])));
+                        const float f1 = ring_sum(
+                            row_sums16(half_sums(db[m + NR / 4], dc[m + NR / 4]),
+                                       half_sums(db[m + 3 * NR / 4], dc[m + 3 * NR / 4])));
+                        f[m] = b3 ? f1 : f0;
                     }
                 }
-                if (t0 + t < o.last && !(o.lane & 4) && (NR > 2 || !(o.lane & 8))) {
-                    const int r0 = (o.lane & 16 ? NR / 2 : 0) + (NR > 2 && (o.lane & 8) ? NR / 4 : 0);
-                    float* f_out = p.part_bc + ((int64_t)o.blk * p.T + t0 + t) * (2 * NP) +
-                                   (o.lane & 32 ? NP : 0) + o.nl * NR + r0;
 #pragma unroll
-                    for (int m = 0; m < M; ++m) f_out[m] = f[m];
-                }
+                for (int m = 0; m < M; ++m) sums.put(sum_off + (uint32_t)(t * 2 * NP + m) * 4u, f[m]);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            const int64_t t = t0 + 4 * i + o.nl;
-            const float x = (float)xr[i];
+            const float x = (float)xr[i], zf = (float)zr[i];
             const float gBt = quad_sums(gB[0], gB[1], gB[2], gB[3], b0, b1);
+            // A2 is A log2(e)
             const float sAt = quad_sums(sA[0], sA[1], sA[2], sA[3], b0, b1) * 0.69314718055994531f;
-            const bool ok = o.live && t < o.last;
             const float raw = (float)dr[i] + dinit;
-            const float ddr = ok ? (x * gBt + sAt) * sigmoid(raw) : 0.f;
-            dI += ddr;
+            const float dd = 4 * i + o.nl < have && o.live ? (x * gBt + sAt) * sigmoid(raw) : 0.f;
+            dI += dd;
             dD += w[i] * x;
-            if (ok) {
-                ((T*)p.y)[t * p.xs + o.ch] = (T)(w[i] * Dv + d[i] * gBt);
-                ((T*)p.dd_raw)[t * p.ds + o.ch] = (T)ddr;
-            }
-            if (p.z) {
+            dx.put(xoff + i * (uint32_t)(4 * p.xs * sizeof(T)), w[i] * Dv + d[i] * gBt);
+            ddr.put(doff + i * (uint32_t)(4 * p.ds * sizeof(T)), dd);
+            if (gated) {
                 const float vt = quad_sums(v[0], v[1], v[2], v[3], b0, b1) + Dv * x;
-                const float zf = (float)zr[i];
-                if (ok) ((T*)p.dz)[t * p.zs + o.ch] = (T)((float)gr[i] * vt * silu_slope(zf, sigmoid(zf)));
+                dz.put(zoff + i * (uint32_t)(4 * p.zs * sizeof(T)),
+                       (float)gr[i] * vt * silu_slope(zf, sigmoid(zf)));
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
         wave_lds_fence();
     }
