@@ -85,18 +85,23 @@ def _entry(name):
     return f
 
 
-def _launch(name, like, *args):
-    """Call the entry point on the current stream of ``like``'s device."""
-    f = _entry(name)
-    dev = like.device
-    if dev.type != "cuda":
-        raise ValueError(f"{name} needs tensors on a GPU, got {dev}")
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if dev.index == torch.cuda.current_device():
-        rc = f(*args, stream)
+# The current stream of a device as an integer.  torch.cuda.current_stream
+# builds a Stream object first, 2 us of a call whose kernel takes 5.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(name, x, *args):
+    """Call the entry point on the current stream of x's device."""
+    f = _entries.get(name) or _entry(name)
+    index = x.get_device()
+    if index < 0:
+        raise ValueError(f"{name} needs tensors on a GPU, got {x.device}")
+    if index == torch.cuda.current_device():
+        rc = f(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            rc = f(*args, stream)
+        with torch.cuda.device(index):
+            rc = f(*args, _raw_stream(index))
     if rc != 0:
         raise SsdError(rc, name)
 
@@ -112,17 +117,22 @@ def _dtype_of(x, name):
     return code
 
 
-def _same(x, **others):
-    """Tensors of x's dtype on x's device."""
-    for name, t in others.items():
-        if t is not None and (t.dtype != x.dtype or t.device != x.device):
+def _same(x, *named):
+    """(tensor, name) pairs: tensors of x's dtype on x's device."""
+    dt, dev = x.dtype, x.get_device()
+    for t, name in named:
+        if t is not None and (t.dtype is not dt or t.get_device() != dev):
             raise ValueError(f"{name} must be on {x.device} with dtype {x.dtype}")
 
 
-def _floats(x, **others):
-    """(tensor, shape) pairs: contiguous float32 tensors on x's device."""
-    for name, (t, shape) in others.items():
-        if t is not None and (t.dtype != torch.float32 or t.device != x.device
+_FLOAT = torch.float32
+
+
+def _floats(x, *named):
+    """(tensor, shape, name): contiguous float32 tensors on x's device."""
+    dev = x.get_device()
+    for t, shape, name in named:
+        if t is not None and (t.dtype is not _FLOAT or t.get_device() != dev
                               or t.shape != shape or not t.is_contiguous()):
             raise ValueError(f"{name} must be contiguous float32 {list(shape)} on {x.device}")
 
@@ -174,6 +184,17 @@ def _rows(t, name, shape):
     return t.stride(0) if shape[0] > 1 else max(shape[1], t.stride(0))
 
 
+def _heads(t, name, shape):
+    """(row, head) strides of a [b, H, P] tensor with contiguous last dimension."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}")
+    if t.is_contiguous():
+        return shape[1] * shape[2], shape[2]
+    if shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} needs a contiguous last dimension")
+    return t.stride(0), t.stride(1)
+
+
 def _like(t):
     """An uninitialized tensor with t's shape and strides."""
     return torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device)
@@ -201,8 +222,9 @@ def _pools(x, state, new_state, row, dtype, slots):
     ``new_state`` (``state`` itself where not given)."""
     if new_state is None:
         new_state = state
+    dev = x.get_device()
     for name, t in (("state", state), ("new_state", new_state)):
-        if t.dtype != dtype or t.device != x.device or t.shape[1:] != row \
+        if t.dtype is not dtype or t.get_device() != dev or t.shape[1:] != row \
                 or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous {dtype} [nslots, "
                              f"{', '.join(map(str, row))}] on {x.device}")
@@ -211,7 +233,7 @@ def _pools(x, state, new_state, row, dtype, slots):
     if slots is None:
         if state.shape[0] < x.shape[0]:
             raise ValueError("without slots the pool needs a row for every sequence")
-    elif slots.dtype != torch.int32 or slots.device != x.device or slots.shape != x.shape[:1] \
+    elif slots.dtype is not torch.int32 or slots.get_device() != dev or slots.shape != x.shape[:1] \
             or not slots.is_contiguous():
         raise ValueError(f"slots must be contiguous int32 [{x.shape[0]}] on {x.device}")
     return new_state
@@ -240,12 +262,12 @@ def ssd_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None):
         raise ValueError("x [..., width] expected")
     width = x.shape[-1]
     code = _dtype_of(x, "x")
-    _floats(x, weight=(weight, (width,)), bias=(bias, (width,)))
+    _floats(x, (weight, (width,), "weight"), (bias, (width,), "bias"))
     rows, xs = _matrix(x, "x", width)
     if y is None:
-        y, ys = torch.empty(x.shape, dtype=x.dtype, device=x.device), width
+        y, ys = x.new_empty(x.shape), width
     else:
-        _same(x, y=y)
+        _same(x, (y, "y"))
         if y.shape != x.shape:
             raise ValueError("y must have x's shape")
         ys = _matrix(y, "y", width)[1]
@@ -262,10 +284,10 @@ def ssd_norm_bwd(x, weight, mean, rstd, dy, workspace=None):
         raise ValueError("x [..., width] expected")
     width = x.shape[-1]
     code = _dtype_of(x, "x")
-    _same(x, dy=dy)
+    _same(x, (dy, "dy"))
     if dy.shape != x.shape:
         raise ValueError("dy must have x's shape")
-    _floats(x, weight=(weight, (width,)), mean=(mean, x.shape[:-1]), rstd=(rstd, x.shape[:-1]))
+    _floats(x, (weight, (width,), "weight"), (mean, x.shape[:-1], "mean"), (rstd, x.shape[:-1], "rstd"))
     rows, xs = _matrix(x, "x", width)
     dx = _like(x)
     dweight, dbias = torch.empty((2, width), dtype=torch.float32, device=x.device).unbind(0)
@@ -284,10 +306,10 @@ def _conv_arguments(x, weight, bias, init_state, cu_seqlens, dims_of):
         raise ValueError("x [b, L, E] ([b, E] for one token) and weight [W, E] expected")
     W, E = weight.shape
     code = _dtype_of(x, "x")
-    _floats(x, weight=(weight, (W, E)), bias=(bias, (E,)))
+    _floats(x, (weight, (W, E), "weight"), (bias, (E,), "bias"))
     cu, S = _sequences(x, cu_seqlens, x.shape[0])
     if init_state is not None:
-        _same(x, init_state=init_state)
+        _same(x, (init_state, "init_state"))
         if init_state.shape != (S, W - 1, E) or not init_state.is_contiguous():
             raise ValueError(f"init_state must be contiguous [{S}, {W - 1}, {E}]")
     return W, E, code, cu, S
@@ -306,16 +328,16 @@ def ssd_conv_fwd(x, weight, bias=None, init_state=None, cu_seqlens=None, y=None,
     b, L, _ = x.shape
     xs = _tokens(x, "x", x.shape)
     if y is None:
-        y, ys = torch.empty(x.shape, dtype=x.dtype, device=x.device), E
+        y, ys = x.new_empty(x.shape), E
     else:
-        _same(x, y=y)
+        _same(x, (y, "y"))
         ys = _tokens(y, "y", x.shape)
     if final_state is True:
-        final_state = torch.empty((S, W - 1, E), dtype=x.dtype, device=x.device)
+        final_state = x.new_empty((S, W - 1, E))
     elif final_state is False:
         final_state = None
     elif final_state is not None:
-        _same(x, final_state=final_state)
+        _same(x, (final_state, "final_state"))
         if final_state.shape != (S, W - 1, E) or not final_state.is_contiguous():
             raise ValueError(f"final_state must be contiguous [{S}, {W - 1}, {E}]")
     dims = SsdConvDims(b, L, E, W, 0 if cu is None else S, code)
@@ -332,7 +354,7 @@ def ssd_conv_bwd(x, weight, bias, dy, init_state=None, cu_seqlens=None, d_final=
     final_state or None for zeros."""
     W, E, code, cu, S = _conv_arguments(x, weight, bias, init_state, cu_seqlens, 3)
     b, L, _ = x.shape
-    _same(x, dy=dy, d_final=d_final)
+    _same(x, (dy, "dy"), (d_final, "d_final"))
     if d_final is not None and (d_final.shape != (S, W - 1, E) or not d_final.is_contiguous()):
         raise ValueError(f"d_final must be contiguous [{S}, {W - 1}, {E}]")
     lay = SsdConvLayout(_tokens(x, "x", x.shape), E, _tokens(dy, "dy", x.shape))
@@ -359,9 +381,9 @@ def ssd_conv_step(x, state, weight, bias=None, slots=None, new_state=None, y=Non
     new_state = _pools(x, state, new_state, (W - 1, E), x.dtype, slots)
     xs = _rows(x, "x", x.shape)
     if y is None:
-        y, ys = torch.empty(x.shape, dtype=x.dtype, device=x.device), E
+        y, ys = x.new_empty(x.shape), E
     else:
-        _same(x, y=y)
+        _same(x, (y, "y"))
         ys = _rows(y, "y", x.shape)
     dims = SsdConvDims(x.shape[0], 1, E, W, 0, code)
     _launch("ssd_conv_step", x, dims, SsdConvLayout(xs, ys, E), _at(x), _at(weight), _at(bias),
@@ -377,17 +399,14 @@ def _selscan_arguments(x, d_raw, d_init, A, B, C, D, z, cu_seqlens):
     b, L, E = x.shape
     N, G = A.shape[0], B.shape[2]
     code = _dtype_of(x, "x")
-    _same(x, d_raw=d_raw, B=B, C=C, z=z)
-    _floats(x, d_init=(d_init, (E,)), A=(A, (N, E)), D=(D, (E,)))
+    _same(x, (d_raw, "d_raw"), (B, "B"), (C, "C"), (z, "z"))
+    _floats(x, (d_init, (E,), "d_init"), (A, (N, E), "A"), (D, (E,), "D"))
     cu, S = _sequences(x, cu_seqlens, b)
-    lay = SsdSelscanLayout()
-    lay.x_token = _tokens(x, "x", x.shape)
-    lay.d_raw_token = _tokens(d_raw, "d_raw", x.shape)
-    lay.z_token = E if z is None else _tokens(z, "z", x.shape)
     shape = (b, L, G, N)
-    lay.B_token, lay.B_group = _groups(B, "B", shape)
-    lay.C_token, lay.C_group = _groups(C, "C", shape)
-    lay.y_token = lay.dy_token = E
+    lay = SsdSelscanLayout(
+        _tokens(x, "x", x.shape), _tokens(d_raw, "d_raw", x.shape),
+        E if z is None else _tokens(z, "z", x.shape), *_groups(B, "B", shape),
+        *_groups(C, "C", shape), E, E)
     dims = SsdSelscanDims(b, L, E, N, G, 0 if cu is None else S, code, 0)
     return dims, lay, cu, (S, N, E)
 
@@ -405,18 +424,18 @@ def ssd_selscan_fwd(x, d_raw, d_init, A, B, C, D=None, z=None, init_state=None, 
     True, False or a [S, N, E] fp32 tensor to fill.  Returns (y, final_state or
     None)."""
     dims, lay, cu, state = _selscan_arguments(x, d_raw, d_init, A, B, C, D, z, cu_seqlens)
-    _floats(x, init_state=(init_state, state))
+    _floats(x, (init_state, state, "init_state"))
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = x.new_empty(x.shape)
     else:
-        _same(x, y=y)
+        _same(x, (y, "y"))
         lay.y_token = _tokens(y, "y", x.shape)
     if final_state is True:
         final_state = torch.empty(state, dtype=torch.float32, device=x.device)
     elif final_state is False:
         final_state = None
     else:
-        _floats(x, final_state=(final_state, state))
+        _floats(x, (final_state, state, "final_state"))
     if workspace is None:
         need = _entry("ssd_selscan_fwd_workspace_bytes")(ctypes.byref(dims))
         if need:
@@ -435,8 +454,8 @@ def ssd_selscan_bwd(x, d_raw, d_init, A, B, C, dy, D=None, z=None, init_state=No
     zeros without an init_state).  ``d_final`` is the gradient of final_state or
     None for zeros."""
     dims, lay, cu, state = _selscan_arguments(x, d_raw, d_init, A, B, C, D, z, cu_seqlens)
-    _floats(x, init_state=(init_state, state), d_final=(d_final, state))
-    _same(x, dy=dy)
+    _floats(x, (init_state, state, "init_state"), (d_final, state, "d_final"))
+    _same(x, (dy, "dy"))
     lay.dy_token = _tokens(dy, "dy", x.shape)
     N, E = A.shape
     g = {"dx": _like(x), "dd_raw": _like(d_raw), "dB": _like(B), "dC": _like(C)}
@@ -465,21 +484,18 @@ def ssd_selscan_step(x, d_raw, d_init, A, B, C, state, D=None, z=None, slots=Non
     b, E = x.shape
     N, G = A.shape[0], B.shape[1]
     code = _dtype_of(x, "x")
-    _same(x, d_raw=d_raw, B=B, C=C, z=z)
-    _floats(x, d_init=(d_init, (E,)), A=(A, (N, E)), D=(D, (E,)))
+    _same(x, (d_raw, "d_raw"), (B, "B"), (C, "C"), (z, "z"))
+    _floats(x, (d_init, (E,), "d_init"), (A, (N, E), "A"), (D, (E,), "D"))
     new_state = _pools(x, state, new_state, (N, E), torch.float32, slots)
-    lay = SsdSelscanLayout()
-    lay.x_token = _rows(x, "x", x.shape)
-    lay.d_raw_token = _rows(d_raw, "d_raw", x.shape)
-    lay.z_token = E if z is None else _rows(z, "z", x.shape)
-    lay.B_token, lay.B_group = _groups(B.unsqueeze(1), "B", (b, 1, G, N))
-    lay.C_token, lay.C_group = _groups(C.unsqueeze(1), "C", (b, 1, G, N))
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        lay.y_token = E
+        y, ys = x.new_empty((b, E)), E
     else:
-        _same(x, y=y)
-        lay.y_token = _rows(y, "y", x.shape)
+        _same(x, (y, "y"))
+        ys = _rows(y, "y", x.shape)
+    lay = SsdSelscanLayout(
+        _rows(x, "x", x.shape), _rows(d_raw, "d_raw", x.shape),
+        E if z is None else _rows(z, "z", x.shape), *_heads(B, "B", (b, G, N)),
+        *_heads(C, "C", (b, G, N)), ys, E)
     dims = SsdSelscanDims(b, 1, E, N, G, 0, code, 0)
     _launch("ssd_selscan_step", x, dims, lay, _at(x), _at(d_raw), _at(d_init), _at(A), _at(B),
             _at(C), _at(D), _at(z), _at(state), _at(slots), state.shape[0], _at(y),
@@ -488,17 +504,6 @@ def ssd_selscan_step(x, d_raw, d_init, A, B, C, state, D=None, z=None, slots=Non
 
 
 # ---- SSD, one token ------------------------------------------------------------------------
-
-def _heads(t, name, shape):
-    """(row, head) strides of a [b, H, P] tensor with contiguous last dimension."""
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}")
-    if t.is_contiguous():
-        return shape[1] * shape[2], shape[2]
-    if shape[2] > 1 and t.stride(2) != 1:
-        raise ValueError(f"{name} needs a contiguous last dimension")
-    return t.stride(0), t.stride(1)
-
 
 def ssd_step(x, d_raw, d_init, B, C, state, slots=None, new_state=None, y=None):
     """One new token of ``ssd_fwd``'s scan for each of b sequences: x [b, H, P],
@@ -510,20 +515,16 @@ def ssd_step(x, d_raw, d_init, B, C, state, slots=None, new_state=None, y=None):
     b, H, P = x.shape
     G, N = B.shape[1], B.shape[2]
     code = _dtype_of(x, "x")
-    _same(x, d_raw=d_raw, B=B, C=C)
+    _same(x, (d_raw, "d_raw"), (B, "B"), (C, "C"))
     if d_raw.shape != (b, H):
         raise ValueError(f"d_raw must have shape [{b}, {H}]")
     new_state = _pools(x, state, new_state, (H, N, P), torch.float32, slots)
-    lay = SsdLayout()
-    lay.x_token, lay.x_head = _heads(x, "x", x.shape)
-    lay.d_raw_token, lay.d_raw_head = d_raw.stride()
-    lay.B_token, lay.B_group = _heads(B, "B", (b, G, N))
-    lay.C_token, lay.C_group = _heads(C, "C", (b, G, N))
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = x.new_empty((b, H, P))
     else:
-        _same(x, y=y)
-    lay.y_token, lay.y_head = _heads(y, "y", x.shape)
+        _same(x, (y, "y"))
+    lay = SsdLayout(*_heads(x, "x", x.shape), *d_raw.stride(), *_heads(B, "B", (b, G, N)),
+                    *_heads(C, "C", (b, G, N)), *_heads(y, "y", x.shape))
     dims = SsdDims(b, 1, H, P, N, G, 64, 0, code)
     _launch("ssd_step", x, dims, lay, _at(x), _at(d_raw), float(d_init), _at(B), _at(C),
             _at(state), _at(slots), state.shape[0], _at(y), _at(new_state))
