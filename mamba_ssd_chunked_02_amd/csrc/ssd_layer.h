@@ -5,7 +5,7 @@
 #pragma once
 
 #include "ssd_device.h"
-#include "../../include/ssd.h"
+#include "ssd.h"
 
 namespace ssd {
 

@@ -56,6 +56,17 @@ struct SelParams {
     int32_t upr;    // of one sequence
 };
 
+// The kernel's argument block, read anew: what is loaded through the returned
+// pointer is not kept in scalar registers across the loops around it.  (Kept,
+// the pointers and strides of ten tensors did not fit and went through vector
+// lanes, 500 instructions a segment of the backward kernel.)
+typedef const __attribute__((address_space(4))) SelParams* ArgPtr;
+__device__ __forceinline__ ArgPtr fresh_args() {
+    ArgPtr k = (ArgPtr)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(k));
+    return k;
+}
+
 constexpr int kChan = 16;  // channels of a wave
 constexpr int kRun = 8;    // adjacent channel blocks kept on one XCD
 
@@ -64,8 +75,9 @@ struct Shape {
     static constexpr int NP = 4 * NR;           // state entries held
     static constexpr int kFwdTokens = 64 / NR;  // of a wave's chunk
     static constexpr int kFwdWaves = NR <= 4 ? 16 : 8;
-    static constexpr int kBwdTokens = 64 / NR;
-    static constexpr int kBwdWaves = 8;
+    static constexpr int kBwdTokens = NR == 2 ? 16 : 64 / NR;
+    static constexpr int kBwdWaves = NR <= 8 ? 8 : 4;
+    static constexpr int kBwdSegment = kBwdTokens * kBwdWaves;
 };
 
 // ---- lane helpers -------------------------------------------------------------------------
@@ -142,6 +154,14 @@ __device__ __forceinline__ void lds_put(float* p, const float (&v)[NR]) {
     }
 }
 
+// d of a token, 0 where it does not count.  The softplus is formed either way:
+// a branch around it costs more than its 20 operations.
+__device__ __forceinline__ float step_of(float raw, bool counts) {
+    float d = softplus(raw);
+    asm volatile("" : "+v"(d));
+    return counts ? d : 0.f;
+}
+
 // ---- the parts of a chunk -----------------------------------------------------------------
 
 // What a workgroup works on.
@@ -185,13 +205,18 @@ __device__ __forceinline__ bool place_of(const SelParams& p, Place& o) {
 // give byte offsets from row tb, and an offset past the last row reads 0 and
 // stores nothing, so no access is predicated.  Everything in it is uniform.
 template <typename T>
+__device__ __forceinline__ float value_of(uint32_t bits) {
+    return __uint_as_float(sizeof(T) == 2 ? bits << 16 : bits);
+}
+
+template <typename T>
 struct RowBuf {
     __amdgpu_buffer_rsrc_t r;
-    __device__ __forceinline__ T get(uint32_t off) const {
-        if constexpr (sizeof(T) == 2)
-            return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
-        else
-            return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+    // The element's bits, one register each: prefetched elements of 16 bits are
+    // not paired up (which would wait for them at once).
+    __device__ __forceinline__ uint32_t get(uint32_t off) const {
+        if constexpr (sizeof(T) == 2) return __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+        else return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
     }
     __device__ __forceinline__ void put(uint32_t off, float v) const {
         if constexpr (sizeof(T) == 2)
@@ -225,7 +250,7 @@ __device__ __forceinline__ RowBuf<T> row_buf(const void* src, int64_t stride, in
 // 4 i + nl from the lane's offset `off` (kNowhere in a lane without a channel).
 template <typename T, int TW>
 __device__ __forceinline__ void load_tokens(const void* src, int64_t stride, const Place& o, int tb,
-                                            T (&r)[TW / 4]) {
+                                            uint32_t (&r)[TW / 4]) {
     const RowBuf<T> q = row_buf<T>(src, stride, o.ch0, tb, min(o.last - tb, TW), o.width);
     const uint32_t step = (uint32_t)(4 * stride) * (uint32_t)sizeof(T);
     const uint32_t off =
@@ -238,18 +263,17 @@ __device__ __forceinline__ void load_tokens(const void* src, int64_t stride, con
 template <typename T, int NR, int TW>
 struct Rows {
     static constexpr int K = TW * 4 * NR / 64;
-    T v[K];
+    uint32_t v[K];
 };
 template <typename T, int NR, int TW>
-__device__ __forceinline__ void load_rows(const void* src, int64_t stride, int64_t gstride,
-                                          const SelParams& p, const Place& o, int tb,
-                                          Rows<T, NR, TW>& r) {
+__device__ __forceinline__ void load_rows(const void* src, int64_t stride, int64_t gstride, int N,
+                                          const Place& o, int tb, Rows<T, NR, TW>& r) {
     constexpr int NP = 4 * NR, TK = 64 / NP;  // tokens a load
-    const RowBuf<T> q = row_buf<T>(src, stride, o.group * gstride, tb, min(o.last - tb, TW), p.N);
+    const RowBuf<T> q = row_buf<T>(src, stride, o.group * gstride, tb, min(o.last - tb, TW), N);
     const int n = o.lane % NP, t0 = o.lane / NP;
     const uint32_t step = (uint32_t)(TK * stride) * (uint32_t)sizeof(T);
     const uint32_t off =
-        fresh(n < p.N ? (uint32_t)(t0 * stride + n) * (uint32_t)sizeof(T) : kNowhere);
+        fresh(n < N ? (uint32_t)(t0 * stride + n) * (uint32_t)sizeof(T) : kNowhere);
 #pragma unroll
     for (int k = 0; k < r.K; ++k) r.v[k] = q.get(off + k * step);
 }
@@ -259,7 +283,38 @@ __device__ __forceinline__ void put_rows(float* dst, const Place& o, const Rows<
     constexpr int NP = 4 * NR, TK = 64 / NP;
     float* q = dst + o.lane / NP * 2 * NP + o.lane % NP;
 #pragma unroll
-    for (int k = 0; k < r.K; ++k) q[k * TK * 2 * NP] = (float)r.v[k];
+    for (int k = 0; k < r.K; ++k) q[k * TK * 2 * NP] = value_of<T>(r.v[k]);
+}
+
+// A[n] log2(e) of the lane's channel and entries (0 where it has none).  A rate
+// of -inf is kept finite: times a step of 0 it would be NaN.
+template <int NR>
+__device__ __forceinline__ void load_rates(const SelParams& p, const Place& o, float (&A2)[NR]) {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        const int n = o.nl * NR + r;
+        A2[r] = o.live && n < p.N ? fmaxf(p.A[(int64_t)n * p.E + o.ch] * kLog2e, -3e38f) : 0.f;
+    }
+}
+// The lane's entries of its sequence's row of [S, N, E] (null reads 0, stores nothing).
+template <int NR>
+__device__ __forceinline__ void load_state(const float* src, const SelParams& p, const Place& o,
+                                           float (&h)[NR]) {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        const int n = o.nl * NR + r;
+        h[r] = src && o.live && n < p.N ? src[((int64_t)o.seq * p.N + n) * p.E + o.ch] : 0.f;
+    }
+}
+template <int NR>
+__device__ __forceinline__ void store_state(float* dst, const SelParams& p, const Place& o,
+                                            const float (&h)[NR]) {
+    if (!dst || !o.live) return;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        const int n = o.nl * NR + r;
+        if (n < p.N) dst[((int64_t)o.seq * p.N + n) * p.E + o.ch] = h[r];
+    }
 }
 
 // ---- forward ------------------------------------------------------------------------------
@@ -270,38 +325,39 @@ __global__ __launch_bounds__(64 * Shape<NR>::kFwdWaves) void selscan_fwd_kernel(
     constexpr int TW = S::kFwdTokens, NP = S::NP, MW = S::kFwdWaves, Q = TW / 4;
     __shared__ __align__(16) float bc[MW][TW][2][NP];
     __shared__ __align__(16) float exP[2][MW][64][NR], exH[2][MW][64][NR];
+    __shared__ __align__(16) float enter[2][64][NR];  // the state entering a segment
     Place o;
     if (!place_of(p, o)) return;
     const int waves = blockDim.x >> 6;
     const int seg = waves * TW;
     const bool b0 = o.nl & 1, b1 = o.nl & 2;
-    float A2[NR], carry[NR];
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-        const int n = o.nl * NR + r;
-        const bool ok = o.live && n < p.N;
-        A2[r] = ok ? fmaxf(p.A[(int64_t)n * p.E + o.ch] * kLog2e, -3e38f) : 0.f;
-        carry[r] = ok && p.init ? p.init[((int64_t)o.seq * p.N + n) * p.E + o.ch] : 0.f;
-    }
+    float A2[NR], h[NR];
+    load_rates<NR>(p, o, A2);
     const float dinit = o.live ? p.d_init[o.ch] : 0.f;
     const float Dv = o.live && p.D ? p.D[o.ch] : 0.f;
-    const uint32_t ystep = (uint32_t)(4 * p.ys) * (uint32_t)sizeof(T);
     const uint32_t yoff = o.live ? (uint32_t)(o.nl * p.ys + o.e) * (uint32_t)sizeof(T) : kNowhere;
     const bool gated = p.z != nullptr;
+    if (o.wave == 0) {
+        load_state<NR>(p.init, p, o, h);
+        lds_put<NR>(enter[0][o.lane], h);
+        if (o.first >= o.last) store_state<NR>(p.final_state, p, o, h);
+    }
 
-    T xr[Q], dr[Q], zr[Q];
+    uint32_t xr[Q], dr[Q], zr[Q];
     Rows<T, NR, TW> Br, Cr;
     int tb = o.first + o.wave * TW;
     auto fetch = [&](int t) {
-        load_tokens<T, TW>(p.x, p.xs, o, t, xr);
-        load_tokens<T, TW>(p.d_raw, p.ds, o, t, dr);
-        load_rows<T, NR, TW>(p.B, p.bs_t, p.bs_g, p, o, t, Br);
-        load_rows<T, NR, TW>(p.C, p.cs_t, p.cs_g, p, o, t, Cr);
+        const ArgPtr k = fresh_args();
+        load_tokens<T, TW>(k->x, k->xs, o, t, xr);
+        load_tokens<T, TW>(k->d_raw, k->ds, o, t, dr);
+        load_rows<T, NR, TW>(k->B, k->bs_t, k->bs_g, k->N, o, t, Br);
+        load_rows<T, NR, TW>(k->C, k->cs_t, k->cs_g, k->N, o, t, Cr);
     };
     fetch(tb);
     int turn = 0;
     for (int base = o.first; base < o.last; base += seg, tb += seg, turn ^= 1) {
-        load_tokens<T, TW>(p.z, p.zs, o, tb, zr);
+        const ArgPtr k = fresh_args();
+        load_tokens<T, TW>(k->z, k->zs, o, tb, zr);
         float d[Q], u[Q], x[Q];
         float sumd = 0.f;
         // tokens of this chunk that the sequence has (none or fewer: the rest
@@ -309,8 +365,8 @@ __global__ __launch_bounds__(64 * Shape<NR>::kFwdWaves) void selscan_fwd_kernel(
         const int have = min(o.last - tb, TW);
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
-            x[i] = (float)xr[i];
-            d[i] = 4 * i + o.nl < have ? softplus((float)dr[i] + dinit) : 0.f;
+            x[i] = value_of<T>(xr[i]);
+            d[i] = step_of(value_of<T>(dr[i]) + dinit, 4 * i + o.nl < have);
             u[i] = d[i] * x[i];
             sumd += d[i];
         }
@@ -319,12 +375,10 @@ __global__ __launch_bounds__(64 * Shape<NR>::kFwdWaves) void selscan_fwd_kernel(
         put_rows<T, NR, TW>(&bc[o.wave][0][1][0], o, Cr);
         wave_lds_fence();
 
-        float a[TW][NR], h[NR];
+        float a[TW][NR];
 #pragma unroll
         for (int r = 0; r < NR; ++r) h[r] = fexp2(sumd * A2[r]);
         lds_put<NR>(exP[turn][o.wave][o.lane], h);
-#pragma unroll
-        for (int r = 0; r < NR; ++r) h[r] = 0.f;
 #pragma unroll
         for (int t = 0; t < TW; ++t) {
             float b[NR];
@@ -333,29 +387,24 @@ __global__ __launch_bounds__(64 * Shape<NR>::kFwdWaves) void selscan_fwd_kernel(
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
                 a[t][r] = fexp2(dt * A2[r]);
-                h[r] = a[t][r] * h[r] + b[r] * ut;
+                h[r] = t ? a[t][r] * h[r] + b[r] * ut : b[r] * ut;
             }
             if (t & 1) __builtin_amdgcn_sched_barrier(0);
         }
         lds_put<NR>(exH[turn][o.wave][o.lane], h);
         // the exchange is double-buffered: a wave is at most one barrier ahead
         __syncthreads();
-        // the state entering this chunk, and the one leaving the segment
-        const int used = min(waves, (o.last - base + TW - 1) / TW);
-#pragma unroll
-        for (int r = 0; r < NR; ++r) h[r] = carry[r];
-        for (int j = 0; j < used; ++j) {
+        // the state entering this chunk
+        lds_get<NR>(enter[turn][o.lane], h);
+        for (int j = 0; j < o.wave; ++j) {
             float Pj[NR], hj[NR];
             lds_get<NR>(exP[turn][j][o.lane], Pj);
             lds_get<NR>(exH[turn][j][o.lane], hj);
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                if (j == o.wave) h[r] = carry[r];
-                carry[r] = Pj[r] * carry[r] + hj[r];
-            }
+            for (int r = 0; r < NR; ++r) h[r] = Pj[r] * h[r] + hj[r];
         }
         __builtin_amdgcn_sched_barrier(0);
-        const RowBuf<T> y = row_buf<T>(p.y, p.ys, o.ch0, tb, have, o.width);
+        const RowBuf<T> y = row_buf<T>(k->y, k->ys, o.ch0, tb, have, o.width);
         const uint32_t yat = fresh(yoff);
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
@@ -369,28 +418,27 @@ __global__ __launch_bounds__(64 * Shape<NR>::kFwdWaves) void selscan_fwd_kernel(
                 lds_get<NR>(&bc[o.wave][t][0][o.nl * NR], b);
                 lds_get<NR>(&bc[o.wave][t][1][o.nl * NR], c);
                 const float ut = quad_lane(u[i], k);
-                v[k] = 0.f;
 #pragma unroll
                 for (int r = 0; r < NR; ++r) {
                     h[r] = a[t][r] * h[r] + b[r] * ut;
-                    v[k] += c[r] * h[r];
+                    v[k] = r ? v[k] + c[r] * h[r] : c[r] * h[r];
                 }
                 if (k & 1) __builtin_amdgcn_sched_barrier(0);
             }
             float out = quad_sums(v[0], v[1], v[2], v[3], b0, b1) + Dv * x[i];
-            const float zf = (float)zr[i];
+            const float zf = value_of<T>(zr[i]);
             out *= gated ? zf * sigmoid(zf) : 1.f;
-            y.put(yat + i * ystep, out);
+            y.put(yat + i * (uint32_t)(4 * k->ys * sizeof(T)), out);
             __builtin_amdgcn_sched_barrier(0);
         }
-        wave_lds_fence();  // the next segment's rows go where these were read
-    }
-    if (p.final_state && o.wave == 0) {
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            const int n = o.nl * NR + r;
-            if (o.live && n < p.N) p.final_state[((int64_t)o.seq * p.N + n) * p.E + o.ch] = carry[r];
+        // the segment's last chunk leaves the state that enters the next one;
+        // its slot was last read before the barrier that this wave has passed
+        if (o.last - base <= seg) {
+            if (have > 0 && o.last - tb <= TW) store_state<NR>(p.final_state, p, o, h);
+        } else if (o.wave == waves - 1) {
+            lds_put<NR>(enter[turn ^ 1][o.lane], h);
         }
+        wave_lds_fence();  // the next segment's rows go where these were read
     }
 }
 
@@ -404,21 +452,15 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
     using S = Shape<NR>;
     constexpr int TW = S::kBwdTokens, NP = S::NP, MW = S::kBwdWaves, Q = TW / 4;
     __shared__ __align__(16) float bc[MW][TW][2][NP];
-    __shared__ __align__(16) float exP[MW][64][NR], exH[MW][64][NR], exQ[MW][64][NR];
+    __shared__ __align__(16) float exP[2][MW][64][NR], exH[2][MW][64][NR], exQ[2][MW][64][NR];
+    __shared__ __align__(16) float enter[2][64][NR];  // q entering a segment from behind
     Place o;
     if (!place_of(p, o)) return;
     const int waves = blockDim.x >> 6;
     const int seg = waves * TW;
     const bool b0 = o.nl & 1, b1 = o.nl & 2;
-    float A2[NR], carry[NR], dA[NR];
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-        const int n = o.nl * NR + r;
-        const bool ok = o.live && n < p.N;
-        A2[r] = ok ? fmaxf(p.A[(int64_t)n * p.E + o.ch] * kLog2e, -3e38f) : 0.f;
-        carry[r] = ok && p.init ? p.init[((int64_t)o.seq * p.N + n) * p.E + o.ch] : 0.f;
-        dA[r] = 0.f;
-    }
+    float A2[NR], dA[NR], h[NR], q[NR];
+    load_rates<NR>(p, o, A2);
     const float dinit = o.live ? p.d_init[o.ch] : 0.f;
     const float Dv = o.live && p.D ? p.D[o.ch] : 0.f;
     const bool gated = p.z != nullptr;
@@ -429,88 +471,112 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
                   (((int64_t)(o.first / seg + o.seq) * p.nblk + o.blk) * 64 + o.lane) * NR;
     const int64_t seg_step = (int64_t)p.nblk * 64 * NR;
 
-    T xr[Q], dr[Q], zr[Q], gr[Q];
+    uint32_t xr[Q], dr[Q], zr[Q], gr[Q];
     Rows<T, NR, TW> Br, Cr;
-    // -- forward over all segments but the last
-    for (int k = 0; k < nseg; ++k) {
-        const int tb = o.first + k * seg + o.wave * TW;
-        if (o.wave == 0) {
+    int turn = 0;
+    // -- forward over all segments but the last; wave 0 folds
+    float carry[NR];
+    load_state<NR>(p.init, p, o, carry);
+    int tb = o.first + o.wave * TW;
+    if (nseg > 0 && o.wave == 0) {
 #pragma unroll
-            for (int r = 0; r < NR; ++r) segs[k * seg_step + r] = carry[r];
-        }
-        if (k == nseg - 1) break;
-        load_tokens<T, TW>(p.x, p.xs, o, tb, xr);
-        load_tokens<T, TW>(p.d_raw, p.ds, o, tb, dr);
-        load_rows<T, NR, TW>(p.B, p.bs_t, p.bs_g, p, o, tb, Br);
-        float d[Q], u[Q], h[NR], P[NR];
+        for (int r = 0; r < NR; ++r) segs[r] = carry[r];
+    }
+    auto fetch_forward = [&](int t) {
+        const ArgPtr k = fresh_args();
+        load_tokens<T, TW>(k->x, k->xs, o, t, xr);
+        load_tokens<T, TW>(k->d_raw, k->ds, o, t, dr);
+        load_rows<T, NR, TW>(k->B, k->bs_t, k->bs_g, k->N, o, t, Br);
+    };
+    if (nseg > 1) fetch_forward(tb);
+    for (int k = 1; k < nseg; ++k, turn ^= 1) {
+        float d[Q], u[Q], P[NR];
         float sumd = 0.f;
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
-            d[i] = softplus((float)dr[i] + dinit);
-            u[i] = d[i] * (float)xr[i];
+            d[i] = softplus(value_of<T>(dr[i]) + dinit);
+            u[i] = d[i] * value_of<T>(xr[i]);
             sumd += d[i];
         }
         sumd = quad_total(sumd);
         wave_lds_fence();
         put_rows<T, NR, TW>(&bc[o.wave][0][0][0], o, Br);
         wave_lds_fence();
+        tb += seg;
+        if (k + 1 < nseg) fetch_forward(tb);
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            h[r] = 0.f;
-            P[r] = fexp2(sumd * A2[r]);
-        }
+        for (int r = 0; r < NR; ++r) P[r] = fexp2(sumd * A2[r]);
 #pragma unroll
         for (int t = 0; t < TW; ++t) {
             float b[NR];
             lds_get<NR>(&bc[o.wave][t][0][o.nl * NR], b);
             const float dt = quad_lane(d[t / 4], t % 4), ut = quad_lane(u[t / 4], t % 4);
 #pragma unroll
-            for (int r = 0; r < NR; ++r) h[r] = fexp2(dt * A2[r]) * h[r] + b[r] * ut;
+            for (int r = 0; r < NR; ++r)
+                h[r] = t ? fexp2(dt * A2[r]) * h[r] + b[r] * ut : b[r] * ut;
         }
+        lds_put<NR>(exP[turn][o.wave][o.lane], P);
+        lds_put<NR>(exH[turn][o.wave][o.lane], h);
         __syncthreads();
-        lds_put<NR>(exP[o.wave][o.lane], P);
-        lds_put<NR>(exH[o.wave][o.lane], h);
-        __syncthreads();
-        for (int j = 0; j < waves; ++j) {
-            float Pj[NR], hj[NR];
-            lds_get<NR>(exP[j][o.lane], Pj);
-            lds_get<NR>(exH[j][o.lane], hj);
+        if (o.wave == 0) {
+            for (int j = 0; j < waves; ++j) {
+                float hj[NR];
+                lds_get<NR>(exP[turn][j][o.lane], P);
+                lds_get<NR>(exH[turn][j][o.lane], hj);
 #pragma unroll
-            for (int r = 0; r < NR; ++r) carry[r] = Pj[r] * carry[r] + hj[r];
+                for (int r = 0; r < NR; ++r) carry[r] = P[r] * carry[r] + hj[r];
+            }
+#pragma unroll
+            for (int r = 0; r < NR; ++r) segs[k * seg_step + r] = carry[r];
         }
     }
-    // -- backward; carry is now q: what reaches a segment from behind
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-        const int n = o.nl * NR + r;
-        carry[r] = o.live && n < p.N && p.d_final
-                       ? p.d_final[((int64_t)o.seq * p.N + n) * p.E + o.ch] : 0.f;
+    // -- backward
+    if (o.wave == 0) {
+        load_state<NR>(p.d_final, p, o, q);
+        lds_put<NR>(enter[turn][o.lane], q);
     }
+    __syncthreads();  // wave 0's states and enter
     float dD = 0.f, dI = 0.f;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) dA[r] = 0.f;
     // where the lane's sums over channels go: see the reduction below
     const int r_of = (o.lane & 16 ? NR / 2 : 0) + (NR > 2 && (o.lane & 8) ? NR / 4 : 0);
     const uint32_t sum_off = !(o.lane & 4) && (NR > 2 || !(o.lane & 8))
                                  ? (uint32_t)((o.lane & 32 ? NP : 0) + o.nl * NR + r_of) * 4u
                                  : kNowhere;
-    for (int k = nseg - 1; k >= 0; --k) {
-        const int base = o.first + k * seg, tb = base + o.wave * TW;
+    auto fetch = [&](int t) {
+        const ArgPtr k = fresh_args();
+        load_tokens<T, TW>(k->x, k->xs, o, t, xr);
+        load_tokens<T, TW>(k->d_raw, k->ds, o, t, dr);
+        load_tokens<T, TW>(k->dy, k->gs, o, t, gr);
+        load_tokens<T, TW>(k->z, k->zs, o, t, zr);
+        load_rows<T, NR, TW>(k->B, k->bs_t, k->bs_g, k->N, o, t, Br);
+        load_rows<T, NR, TW>(k->C, k->cs_t, k->cs_g, k->N, o, t, Cr);
+    };
+    tb = o.first + (nseg - 1) * seg + o.wave * TW;
+    if (nseg > 0) fetch(tb);
+    for (int k = nseg - 1; k >= 0; --k, tb -= seg, turn ^= 1) {
         const int have = min(o.last - tb, TW);
-        load_tokens<T, TW>(p.x, p.xs, o, tb, xr);
-        load_tokens<T, TW>(p.d_raw, p.ds, o, tb, dr);
-        load_tokens<T, TW>(p.dy, p.gs, o, tb, gr);
-        load_tokens<T, TW>(p.z, p.zs, o, tb, zr);
-        load_rows<T, NR, TW>(p.B, p.bs_t, p.bs_g, p, o, tb, Br);
-        load_rows<T, NR, TW>(p.C, p.cs_t, p.cs_g, p, o, tb, Cr);
-        float d[Q], u[Q], w[Q];
-        float sumd = 0.f;
+        float hin[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) hin[r] = segs[k * seg_step + r];
         // past the sequence and in lanes without a channel x and dy are 0
+        float d[Q], u[Q], w[Q], x[Q], raw[Q], gz[Q];  // gz: what dz multiplies v by
+        float sumd = 0.f;
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
-            d[i] = 4 * i + o.nl < have ? softplus((float)dr[i] + dinit) : 0.f;
-            u[i] = d[i] * (float)xr[i];
+            x[i] = value_of<T>(xr[i]);
+            raw[i] = value_of<T>(dr[i]) + dinit;
+            d[i] = step_of(raw[i], 4 * i + o.nl < have);
+            u[i] = d[i] * x[i];
             sumd += d[i];
-            const float zf = (float)zr[i];
-            w[i] = (float)gr[i] * (gated ? zf * sigmoid(zf) : 1.f);
+            w[i] = gz[i] = value_of<T>(gr[i]);
+            if (gated) {
+                const float zf = value_of<T>(zr[i]), sz = sigmoid(zf);
+                w[i] *= zf * sz;
+                gz[i] *= silu_slope(zf, sz);
+            }
+            dD += w[i] * x[i];
         }
         sumd = quad_total(sumd);
         wave_lds_fence();
@@ -518,12 +584,10 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
         put_rows<T, NR, TW>(&bc[o.wave][0][1][0], o, Cr);
         wave_lds_fence();
         // (1) the chunk from zero states, in both directions
-        float a[TW][NR], h[NR], q[NR], P[NR];
+        float a[TW][NR];
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            h[r] = q[r] = 0.f;
-            P[r] = fexp2(sumd * A2[r]);
-        }
+        for (int r = 0; r < NR; ++r) h[r] = fexp2(sumd * A2[r]);
+        lds_put<NR>(exP[turn][o.wave][o.lane], h);
 #pragma unroll
         for (int t = 0; t < TW; ++t) {
             float b[NR];
@@ -532,44 +596,38 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
                 a[t][r] = fexp2(dt * A2[r]);
-                h[r] = a[t][r] * h[r] + b[r] * ut;
+                h[r] = t ? a[t][r] * h[r] + b[r] * ut : b[r] * ut;
             }
             if (t & 1) __builtin_amdgcn_sched_barrier(0);
         }
+        lds_put<NR>(exH[turn][o.wave][o.lane], h);
 #pragma unroll
         for (int t = TW - 1; t >= 0; --t) {
             float c[NR];
             lds_get<NR>(&bc[o.wave][t][1][o.nl * NR], c);
             const float wt = quad_lane(w[t / 4], t % 4);
 #pragma unroll
-            for (int r = 0; r < NR; ++r) q[r] = a[t][r] * (c[r] * wt + q[r]);
+            for (int r = 0; r < NR; ++r)
+                q[r] = t < TW - 1 ? a[t][r] * (c[r] * wt + q[r]) : a[t][r] * (c[r] * wt);
             if (!(t & 1)) __builtin_amdgcn_sched_barrier(0);
         }
+        lds_put<NR>(exQ[turn][o.wave][o.lane], q);
         // (2) fold the chunks before this one (h) and behind it (q)
         __syncthreads();
-        lds_put<NR>(exP[o.wave][o.lane], P);
-        lds_put<NR>(exH[o.wave][o.lane], h);
-        lds_put<NR>(exQ[o.wave][o.lane], q);
-        __syncthreads();
-        float hin[NR];
-#pragma unroll
-        for (int r = 0; r < NR; ++r) hin[r] = segs[k * seg_step + r];
         for (int j = 0; j < o.wave; ++j) {
             float Pj[NR], hj[NR];
-            lds_get<NR>(exP[j][o.lane], Pj);
-            lds_get<NR>(exH[j][o.lane], hj);
+            lds_get<NR>(exP[turn][j][o.lane], Pj);
+            lds_get<NR>(exH[turn][j][o.lane], hj);
 #pragma unroll
             for (int r = 0; r < NR; ++r) hin[r] = Pj[r] * hin[r] + hj[r];
         }
-        for (int j = waves - 1; j >= 0; --j) {
+        lds_get<NR>(enter[turn][o.lane], q);
+        for (int j = waves - 1; j > o.wave; --j) {
             float Pj[NR], qj[NR];
-            lds_get<NR>(exP[j][o.lane], Pj);
-            lds_get<NR>(exQ[j][o.lane], qj);
+            lds_get<NR>(exP[turn][j][o.lane], Pj);
+            lds_get<NR>(exQ[turn][j][o.lane], qj);
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                if (j == o.wave) q[r] = carry[r];
-                carry[r] = Pj[r] * carry[r] + qj[r];
-            }
+            for (int r = 0; r < NR; ++r) q[r] = Pj[r] * q[r] + qj[r];
         }
         // (3) h of every token, then the gradients from the last token back
         float hs[TW][NR];
@@ -583,17 +641,20 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
                 hs[t][r] = a[t][r] * (t ? hs[t - 1][r] : hin[r]) + b[r] * ut;
             if (t & 1) __builtin_amdgcn_sched_barrier(0);
         }
-        const RowBuf<float> sums = row_buf<float>(p.part_bc + (int64_t)o.blk * p.T * (2 * NP),
+        const ArgPtr out = fresh_args();
+        const RowBuf<float> sums = row_buf<float>(out->part_bc + (int64_t)o.blk * out->T * (2 * NP),
                                                   2 * NP, 0, tb, have, 2 * NP);
-        const RowBuf<T> dx = row_buf<T>(p.y, p.xs, o.ch0, tb, have, o.width);
-        const RowBuf<T> ddr = row_buf<T>(p.dd_raw, p.ds, o.ch0, tb, have, o.width);
-        const RowBuf<T> dz = row_buf<T>(p.dz, p.zs, o.ch0, tb, gated ? have : 0, o.width);
+        const RowBuf<T> dx = row_buf<T>(out->y, out->xs, o.ch0, tb, have, o.width);
+        const RowBuf<T> ddr = row_buf<T>(out->dd_raw, out->ds, o.ch0, tb, have, o.width);
+        const RowBuf<T> dz = row_buf<T>(out->dz, out->zs, o.ch0, tb, gated ? have : 0, o.width);
         const auto lane_off = [&](int64_t stride) {
             return fresh(o.live ? (uint32_t)(o.nl * stride + o.e) * (uint32_t)sizeof(T) : kNowhere);
         };
-        const uint32_t xoff = lane_off(p.xs), doff = lane_off(p.ds), zoff = lane_off(p.zs);
+        const uint32_t xoff = lane_off(out->xs), doff = lane_off(out->ds), zoff = lane_off(out->zs);
 #pragma unroll
         for (int i = Q - 1; i >= 0; --i) {
+            // the next segment's rows, once half of a and hs is used up
+            if (i == (Q - 1) / 2 && k > 0) fetch(tb - seg);
             float gB[4], sA[4], v[4];
 #pragma unroll
             for (int kk = 3; kk >= 0; --kk) {
@@ -638,48 +699,41 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
                 for (int m = 0; m < M; ++m) sums.put(sum_off + (uint32_t)(t * 2 * NP + m) * 4u, f[m]);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            const float x = (float)xr[i], zf = (float)zr[i];
             const float gBt = quad_sums(gB[0], gB[1], gB[2], gB[3], b0, b1);
             // A2 is A log2(e)
             const float sAt = quad_sums(sA[0], sA[1], sA[2], sA[3], b0, b1) * 0.69314718055994531f;
-            const float raw = (float)dr[i] + dinit;
-            const float dd = 4 * i + o.nl < have && o.live ? (x * gBt + sAt) * sigmoid(raw) : 0.f;
+            const float dd = 4 * i + o.nl < have && o.live ? (x[i] * gBt + sAt) * sigmoid(raw[i]) : 0.f;
             dI += dd;
-            dD += w[i] * x;
-            dx.put(xoff + i * (uint32_t)(4 * p.xs * sizeof(T)), w[i] * Dv + d[i] * gBt);
-            ddr.put(doff + i * (uint32_t)(4 * p.ds * sizeof(T)), dd);
+            dx.put(xoff + i * (uint32_t)(4 * out->xs * sizeof(T)), w[i] * Dv + d[i] * gBt);
+            ddr.put(doff + i * (uint32_t)(4 * out->ds * sizeof(T)), dd);
             if (gated) {
-                const float vt = quad_sums(v[0], v[1], v[2], v[3], b0, b1) + Dv * x;
-                dz.put(zoff + i * (uint32_t)(4 * p.zs * sizeof(T)),
-                       (float)gr[i] * vt * silu_slope(zf, sigmoid(zf)));
+                const float vt = quad_sums(v[0], v[1], v[2], v[3], b0, b1) + Dv * x[i];
+                dz.put(zoff + i * (uint32_t)(4 * out->zs * sizeof(T)), gz[i] * vt);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
+        // q leaving the segment's first chunk enters the segment before it; its
+        // slot was last read before the barrier that this wave has passed
+        if (o.wave == 0) lds_put<NR>(enter[turn ^ 1][o.lane], q);
         wave_lds_fence();
     }
-    if (p.final_state && o.wave == 0) {
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            const int n = o.nl * NR + r;
-            if (o.live && n < p.N) p.final_state[((int64_t)o.seq * p.N + n) * p.E + o.ch] = carry[r];
-        }
-    }
+    if (o.wave == 0) store_state<NR>(p.final_state, p, o, q);
     // the waves' shares of dA, dD and dd_init
     dD = quad_total(dD);
     dI = quad_total(dI);
     __syncthreads();
-    lds_put<NR>(exP[o.wave][o.lane], dA);
-    exH[o.wave][o.lane][0] = dD;
-    exH[o.wave][o.lane][1] = dI;
+    lds_put<NR>(exP[0][o.wave][o.lane], dA);
+    exH[0][o.wave][o.lane][0] = dD;
+    exH[0][o.wave][o.lane][1] = dI;
     __syncthreads();
     if (o.wave || !o.live) return;
     for (int j = 1; j < waves; ++j) {
         float t[NR];
-        lds_get<NR>(exP[j][o.lane], t);
+        lds_get<NR>(exP[0][j][o.lane], t);
 #pragma unroll
         for (int r = 0; r < NR; ++r) dA[r] += t[r];
-        dD += exH[j][o.lane][0];
-        dI += exH[j][o.lane][1];
+        dD += exH[0][j][o.lane][0];
+        dI += exH[0][j][o.lane][1];
     }
     float* pw = p.part_w + (int64_t)o.seq * (p.N + 2) * p.E + o.ch;
 #pragma unroll
@@ -753,7 +807,9 @@ int sel_plan(const ssd_selscan_dims& d, SelPlan* pl) {
     pl->units = (int64_t)pl->S * pl->upr;
     pl->grid = cdiv(pl->units, kXcds) * kXcds * kRun;
     if (pl->grid > INT32_MAX) return SSD_ERR_SHAPE;
-    const int64_t seg = 8 * (64 / pl->NR);
+    const int64_t seg = pl->NR == 2 ? Shape<2>::kBwdSegment
+                        : pl->NR == 4 ? Shape<4>::kBwdSegment
+                        : pl->NR == 8 ? Shape<8>::kBwdSegment : Shape<16>::kBwdSegment;
     pl->slots = pl->T / seg + pl->S + 1;
     size_t off = 0;
     pl->off_seg = off;
