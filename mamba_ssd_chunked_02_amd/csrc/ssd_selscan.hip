@@ -44,16 +44,21 @@ struct SelParams {
     const float* d_final;
     const int32_t* cu;
     float* final_state;  // or dinit_state
+    float* span_h;       // spans' states from zero [slots][blocks][64][NR]
+    float* span_q;       // backward: what their tokens pass on to the span before
+    float* span_d;       // their sums of d [slots][blocks][64]
     float* seg_states;   // backward: states entering the segments [slots][blocks][64][NR]
-    float* part_w;       // backward: [S][(N + 2) E] shares of dA, dD, dd_init
+    float* part_w;       // backward: [slots][(N + 2) E] shares of dA, dD, dd_init
     float* part_bc;      // backward: [blocks][T][2 NP] shares of dB, dC
     int64_t xs, ds, zs, bs_t, bs_g, cs_t, cs_g, ys, gs;
     int64_t L, T;
     int32_t E, N, G, epg, S;
     int32_t nblk;   // channel blocks in all
     int32_t bpg;    // of one group
-    int32_t units;  // runs of kRun adjacent channel blocks, over all sequences
-    int32_t upr;    // of one sequence
+    int32_t units;  // runs of kRun adjacent channel blocks, over all slots
+    int32_t upr;    // of one slot
+    int32_t span;   // tokens of a span (whole segments; 0: a sequence is one span)
+    int32_t per;    // without cu_seqlens: spans of a sequence
 };
 
 // The kernel's argument block, read anew: what is loaded through the returned
@@ -164,24 +169,48 @@ __device__ __forceinline__ float step_of(float raw, bool counts) {
 
 // ---- the parts of a chunk -----------------------------------------------------------------
 
-// What a workgroup works on.
+// What a workgroup works on: a channel block of one span.  Long sequences may
+// be cut into spans of whole segments so that few channels still fill the chip;
+// a first launch then forms what every span does to a state, and the scan of a
+// span begins by folding those before it.
 struct Place {
     int seq, group, blk;     // blk counts over all groups
+    int slot, k, nspan;      // the span's slot; it is span k of nspan (k >= nspan: nothing)
     int lane, wave, nl, e;   // nl: lane of the quad; e: channel of the wave
     int ch0, ch;             // the workgroup's first channel; the lane's
     int width;               // channels of the workgroup
     bool live;               // ch is one of them
-    int first, last;
+    int first, last;         // the span's tokens
 };
 
-// False where the workgroup has nothing to do.  Runs of kRun adjacent channel
-// blocks, which share the cache lines of x and the rows of B and C, go to one
-// XCD (workgroups are dealt to the eight XCDs in turn).
+// The sequence with the slot-th most tokens of at most 64 (equal ones in
+// order): the longest start first, so that none is left running alone.
+__device__ __forceinline__ int by_length(const int32_t* cu, int S, int slot) {
+    const int lane = threadIdx.x & 63;
+    const int len = lane < S ? cu[lane + 1] - cu[lane] : INT32_MIN;
+    int rank = 0;
+    for (int j = 0; j < S; ++j) {
+        const int other = __builtin_amdgcn_readlane(len, j);
+        rank += other > len || (other == len && j < lane);
+    }
+    const uint64_t hit = __ballot(lane < S && rank == slot);
+    return __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
+}
+
+// False where the grid's rounding left the workgroup without a channel block.
+// Runs of kRun adjacent channel blocks, which share the cache lines of x and
+// the rows of B and C, go to one XCD (workgroups are dealt to the eight XCDs
+// in turn).
+//
+// Slots of packed sequences: span k of sequence i, which starts at token f, has
+// slot f / span + i + k.  A sequence of n tokens takes at most
+// (f + n) / span - f / span + 1 of them, so no two sequences meet, some slots
+// stay empty, and the sequence of a slot is found by bisection.
 __device__ __forceinline__ bool place_of(const SelParams& p, Place& o) {
     const uint32_t id = blockIdx.x;
     const uint32_t unit = id / (kXcds * kRun) * kXcds + id % kXcds;
     if (unit >= (uint32_t)p.units) return false;
-    o.seq = (int)(unit / (uint32_t)p.upr);
+    o.slot = (int)(unit / (uint32_t)p.upr);
     o.blk = (int)(unit % (uint32_t)p.upr) * kRun + (int)(id / kXcds % kRun);
     if (o.blk >= p.nblk) return false;
     o.group = o.blk / p.bpg;
@@ -194,10 +223,36 @@ __device__ __forceinline__ bool place_of(const SelParams& p, Place& o) {
     o.ch0 = o.group * p.epg + (o.blk % p.bpg) * kChan;
     o.ch = o.ch0 + o.e;
     o.width = min(kChan, p.epg - (o.blk % p.bpg) * kChan);
+    o.seq = o.slot;
+    o.k = 0;
     int64_t first, last;
+    if (!p.cu) {
+        o.seq = o.slot / p.per;
+        o.k = o.slot % p.per;
+    } else if (p.span) {
+        int lo = 0, hi = p.S - 1;  // the last sequence whose slots start at or before this one
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            sequence_span(p.cu, mid, p.L, p.T, &first, &last);
+            if ((int)first / p.span + mid <= o.slot) lo = mid; else hi = mid - 1;
+        }
+        o.seq = __builtin_amdgcn_readfirstlane(lo);
+    } else if (p.S <= 64) {
+        o.seq = by_length(p.cu, p.S, o.slot);
+    }
     sequence_span(p.cu, o.seq, p.L, p.T, &first, &last);
     o.first = __builtin_amdgcn_readfirstlane((int)first);
     o.last = __builtin_amdgcn_readfirstlane((int)last);
+    o.nspan = 1;
+    if (p.span) {
+        if (p.cu) o.k = o.slot - (o.first / p.span + o.seq);
+        o.nspan = max(1, (o.last - o.first + p.span - 1) / p.span);
+        if (o.k < 0) o.k = o.nspan;  // only where cu_seqlens is not sorted
+        if (o.k < o.nspan) {
+            o.first += o.k * p.span;
+            if (o.last - o.first > p.span) o.last = o.first + p.span;
+        }
+    }
     return true;
 }
 
@@ -317,6 +372,135 @@ __device__ __forceinline__ void store_state(float* dst, const SelParams& p, cons
     }
 }
 
+// h = P h + (state of the span), over n spans of the sequence from span `from`
+// on (by = 1) or back (by = -1); P = exp of the span's sum of d times A.
+template <int NR>
+__device__ __forceinline__ void fold_spans(const float* states, const SelParams& p, const Place& o,
+                                           const float (&A2)[NR], int from, int n, int by,
+                                           float (&h)[NR]) {
+    const int64_t step = (int64_t)p.nblk * 64 * by;
+    int64_t at = ((int64_t)(o.slot - o.k + from) * p.nblk + o.blk) * 64 + o.lane;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j, at += step) {
+        const float d = p.span_d[at];
+        float v[NR];
+        __builtin_memcpy(v, states + at * NR, sizeof(v));
+#pragma unroll
+        for (int r = 0; r < NR; ++r) h[r] = fexp2(d * A2[r]) * h[r] + v[r];
+    }
+}
+
+// ---- what a span does to a state ------------------------------------------------------------
+
+// The wave takes a run of the span's chunks and keeps its state (and, for the
+// backward pass, Q and P: q before = P q behind + Q) in registers; the waves'
+// are joined once at the end.
+template <typename T, int NR, bool BWD>
+__global__ __launch_bounds__(512) void selscan_span_kernel(SelParams p) {
+    using S = Shape<NR>;
+    constexpr int TW = S::kBwdTokens, NP = S::NP, MW = 8, Q = TW / 4;
+    __shared__ __align__(16) float bc[MW][TW][2][NP];
+    __shared__ __align__(16) float exD[MW][64], exH[MW][64][NR], exQ[BWD ? MW : 1][64][NR];
+    Place o;
+    if (!place_of(p, o) || o.k >= o.nspan) return;
+    // nothing comes after a sequence's last span, and nothing before its first
+    if (!BWD && o.k == o.nspan - 1) return;
+    float A2[NR], h[NR], q[NR];
+    load_rates<NR>(p, o, A2);
+    const float dinit = o.live ? p.d_init[o.ch] : 0.f;
+    const bool gated = p.z != nullptr;
+    const int chunks = (o.last - o.first + TW - 1) / TW, run = (chunks + MW - 1) / MW;
+    const int c0 = min(o.wave * run, chunks), c1 = min(c0 + run, chunks);
+    float sum = 0.f;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) h[r] = q[r] = 0.f;
+    uint32_t xr[Q], dr[Q], gr[Q], zr[Q];
+    Rows<T, NR, TW> Br, Cr;
+    auto fetch = [&](int t) {
+        const ArgPtr k = fresh_args();
+        load_tokens<T, TW>(k->x, k->xs, o, t, xr);
+        load_tokens<T, TW>(k->d_raw, k->ds, o, t, dr);
+        load_rows<T, NR, TW>(k->B, k->bs_t, k->bs_g, k->N, o, t, Br);
+        if constexpr (BWD) {
+            load_tokens<T, TW>(k->dy, k->gs, o, t, gr);
+            load_tokens<T, TW>(k->z, k->zs, o, t, zr);
+            load_rows<T, NR, TW>(k->C, k->cs_t, k->cs_g, k->N, o, t, Cr);
+        }
+    };
+    int tb = o.first + c0 * TW;
+    if (c0 < c1) fetch(tb);
+    for (int c = c0; c < c1; ++c, tb += TW) {
+        const int have = min(o.last - tb, TW);
+        float d[Q], u[Q], w[Q], chunk_d = 0.f;
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            d[i] = step_of(value_of<T>(dr[i]) + dinit, 4 * i + o.nl < have);
+            u[i] = d[i] * value_of<T>(xr[i]);
+            chunk_d += d[i];
+            if constexpr (BWD) {
+                const float zf = value_of<T>(zr[i]);
+                w[i] = value_of<T>(gr[i]) * (gated ? zf * sigmoid(zf) : 1.f);
+            }
+        }
+        wave_lds_fence();
+        put_rows<T, NR, TW>(&bc[o.wave][0][0][0], o, Br);
+        if constexpr (BWD) put_rows<T, NR, TW>(&bc[o.wave][0][1][0], o, Cr);
+        wave_lds_fence();
+        if (c + 1 < c1) fetch(tb + TW);
+        float a[BWD ? TW : 1][NR];
+#pragma unroll
+        for (int t = 0; t < TW; ++t) {
+            float b[NR];
+            lds_get<NR>(&bc[o.wave][t][0][o.nl * NR], b);
+            const float dt = quad_lane(d[t / 4], t % 4), ut = quad_lane(u[t / 4], t % 4);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                const float at = fexp2(dt * A2[r]);
+                h[r] = at * h[r] + b[r] * ut;
+                if constexpr (BWD) a[t][r] = at;
+            }
+            if (t & 1) __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (BWD) {
+            float ql[NR];
+#pragma unroll
+            for (int t = TW - 1; t >= 0; --t) {
+                float cc[NR];
+                lds_get<NR>(&bc[o.wave][t][1][o.nl * NR], cc);
+                const float wt = quad_lane(w[t / 4], t % 4);
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+                    ql[r] = t < TW - 1 ? a[t][r] * (cc[r] * wt + ql[r]) : a[t][r] * (cc[r] * wt);
+                if (!(t & 1)) __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int r = 0; r < NR; ++r) q[r] += fexp2(sum * A2[r]) * ql[r];
+        }
+        sum += quad_total(chunk_d);
+    }
+    exD[o.wave][o.lane] = sum;
+    lds_put<NR>(exH[o.wave][o.lane], h);
+    if constexpr (BWD) lds_put<NR>(exQ[o.wave][o.lane], q);
+    __syncthreads();
+    if (o.wave) return;
+    for (int j = 1; j < MW; ++j) {
+        const float dj = exD[j][o.lane];
+        float hj[NR], qj[NR];
+        lds_get<NR>(exH[j][o.lane], hj);
+        if constexpr (BWD) lds_get<NR>(exQ[j][o.lane], qj);
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            h[r] = fexp2(dj * A2[r]) * h[r] + hj[r];
+            if constexpr (BWD) q[r] += fexp2(sum * A2[r]) * qj[r];
+        }
+        sum += dj;
+    }
+    const int64_t at = ((int64_t)o.slot * p.nblk + o.blk) * 64 + o.lane;
+    p.span_d[at] = sum;
+    __builtin_memcpy(p.span_h + at * NR, h, sizeof(h));
+    if constexpr (BWD) __builtin_memcpy(p.span_q + at * NR, q, sizeof(q));
+}
+
 // ---- forward ------------------------------------------------------------------------------
 
 template <typename T, int NR>
@@ -337,11 +521,14 @@ __global__ __launch_bounds__(64 * Shape<NR>::kFwdWaves) void selscan_fwd_kernel(
     const float Dv = o.live && p.D ? p.D[o.ch] : 0.f;
     const uint32_t yoff = o.live ? (uint32_t)(o.nl * p.ys + o.e) * (uint32_t)sizeof(T) : kNowhere;
     const bool gated = p.z != nullptr;
+    if (o.k >= o.nspan) return;
     if (o.wave == 0) {
         load_state<NR>(p.init, p, o, h);
+        if (p.span) fold_spans<NR>(p.span_h, p, o, A2, 0, o.k, 1, h);
         lds_put<NR>(enter[0][o.lane], h);
         if (o.first >= o.last) store_state<NR>(p.final_state, p, o, h);
     }
+    const bool ends = o.k == o.nspan - 1;  // the span's last state is the sequence's
 
     uint32_t xr[Q], dr[Q], zr[Q];
     Rows<T, NR, TW> Br, Cr;
@@ -434,7 +621,7 @@ __global__ __launch_bounds__(64 * Shape<NR>::kFwdWaves) void selscan_fwd_kernel(
         // the segment's last chunk leaves the state that enters the next one;
         // its slot was last read before the barrier that this wave has passed
         if (o.last - base <= seg) {
-            if (have > 0 && o.last - tb <= TW) store_state<NR>(p.final_state, p, o, h);
+            if (ends && have > 0 && o.last - tb <= TW) store_state<NR>(p.final_state, p, o, h);
         } else if (o.wave == waves - 1) {
             lds_put<NR>(enter[turn ^ 1][o.lane], h);
         }
@@ -464,7 +651,8 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
     const float dinit = o.live ? p.d_init[o.ch] : 0.f;
     const float Dv = o.live && p.D ? p.D[o.ch] : 0.f;
     const bool gated = p.z != nullptr;
-    const int nseg = (o.last - o.first + seg - 1) / seg;
+    // (a slot without a span has no tokens and still writes its share: zeros)
+    const int nseg = o.k < o.nspan ? (o.last - o.first + seg - 1) / seg : 0;
     // sequences' segments follow one another: this one's start at a slot that
     // no earlier sequence reaches
     float* segs = p.seg_states +
@@ -476,7 +664,10 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
     int turn = 0;
     // -- forward over all segments but the last; wave 0 folds
     float carry[NR];
-    load_state<NR>(p.init, p, o, carry);
+    if (o.wave == 0) {
+        load_state<NR>(p.init, p, o, carry);
+        if (p.span && nseg > 0) fold_spans<NR>(p.span_h, p, o, A2, 0, o.k, 1, carry);
+    }
     int tb = o.first + o.wave * TW;
     if (nseg > 0 && o.wave == 0) {
 #pragma unroll
@@ -533,6 +724,7 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
     // -- backward
     if (o.wave == 0) {
         load_state<NR>(p.d_final, p, o, q);
+        if (p.span) fold_spans<NR>(p.span_q, p, o, A2, o.nspan - 1, o.nspan - 1 - o.k, -1, q);
         lds_put<NR>(enter[turn][o.lane], q);
     }
     __syncthreads();  // wave 0's states and enter
@@ -717,7 +909,7 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
         if (o.wave == 0) lds_put<NR>(enter[turn ^ 1][o.lane], q);
         wave_lds_fence();
     }
-    if (o.wave == 0) store_state<NR>(p.final_state, p, o, q);
+    if (o.wave == 0 && o.k == 0) store_state<NR>(p.final_state, p, o, q);
     // the waves' shares of dA, dD and dd_init
     dD = quad_total(dD);
     dI = quad_total(dI);
@@ -735,7 +927,7 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
         dD += exH[0][j][o.lane][0];
         dI += exH[0][j][o.lane][1];
     }
-    float* pw = p.part_w + (int64_t)o.seq * (p.N + 2) * p.E + o.ch;
+    float* pw = p.part_w + (int64_t)o.slot * (p.N + 2) * p.E + o.ch;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
         const int n = o.nl * NR + r;
@@ -791,12 +983,20 @@ int sel_check(const ssd_selscan_dims* d) {
 
 struct SelPlan {
     int32_t NR, S, bpg, nblk, upr;
-    int64_t units, grid, T;
-    int64_t slots;  // backward: segments of all sequences, at most
-    size_t off_seg, off_w, off_bc, total;
+    int32_t span, per;  // tokens of a span (0: sequences are not cut), spans a sequence
+    int64_t slots, units, grid, T;
+    size_t off_h, off_q, off_d, off_seg, off_w, off_bc, total;
 };
 
-int sel_plan(const ssd_selscan_dims& d, SelPlan* pl) {
+template <typename F>
+auto with_shape(int NR, F f) {
+    if (NR == 2) return f(Shape<2>{});
+    if (NR == 4) return f(Shape<4>{});
+    if (NR == 8) return f(Shape<8>{});
+    return f(Shape<16>{});
+}
+
+int sel_plan(const ssd_selscan_dims& d, bool bwd, SelPlan* pl) {
     pl->NR = entries_per_lane(d.d_state);
     pl->T = (int64_t)d.batch * d.seqlen;
     pl->S = d.nseq > 0 ? d.nseq : d.batch;
@@ -804,20 +1004,51 @@ int sel_plan(const ssd_selscan_dims& d, SelPlan* pl) {
     const int64_t nblk = (int64_t)pl->bpg * d.ngroups;
     pl->nblk = (int32_t)nblk;
     pl->upr = (int32_t)cdiv(nblk, kRun);
-    pl->units = (int64_t)pl->S * pl->upr;
+    const int64_t seg = with_shape(pl->NR, [bwd](auto s) {
+        return bwd ? s.kBwdSegment : s.kFwdTokens * s.kFwdWaves;
+    });
+    // Cut sequences into spans where that shortens the longest chain of
+    // segments on a CU by more than the second launch costs.  A segment's cost
+    // is 1; with spans its tokens are walked once more for the spans' states
+    // (kAgain of a segment).  Packed sequences are taken as equally long.
+    const double kAgain = bwd ? 0.35 : 0.6, kLaunch = 1.5, kFold = 0.05;
+    const int64_t len = pl->S ? cdiv(pl->T, pl->S) : 0, nseg = cdiv(len, seg);
+    const int64_t whole = (int64_t)pl->S * nblk;
+    double best = (double)cdiv(whole, 256) * nseg;
+    int64_t best_segs = 0;
+    for (int64_t k = 2; k <= 64 && k <= nseg; ++k) {
+        const int64_t segs = cdiv(nseg, k), kk = cdiv(nseg, segs);
+        const double cost = (double)cdiv(whole * kk, 256) * segs * (1 + kAgain) + kLaunch + kFold * kk;
+        if (cost < best) {
+            best = cost;
+            best_segs = segs;
+        }
+    }
+    pl->span = (int32_t)(best_segs * seg);
+    pl->per = best_segs ? (int32_t)cdiv(nseg, best_segs) : 1;
+    pl->slots = d.nseq > 0 && pl->span ? pl->T / pl->span + pl->S : (int64_t)pl->S * pl->per;
+    pl->units = pl->slots * pl->upr;
     pl->grid = cdiv(pl->units, kXcds) * kXcds * kRun;
     if (pl->grid > INT32_MAX) return SSD_ERR_SHAPE;
-    const int64_t seg = pl->NR == 2 ? Shape<2>::kBwdSegment
-                        : pl->NR == 4 ? Shape<4>::kBwdSegment
-                        : pl->NR == 8 ? Shape<8>::kBwdSegment : Shape<16>::kBwdSegment;
-    pl->slots = pl->T / seg + pl->S + 1;
     size_t off = 0;
-    pl->off_seg = off;
-    off = up256(off + (size_t)pl->slots * nblk * 64 * pl->NR * sizeof(float));
-    pl->off_w = off;
-    off = up256(off + (size_t)pl->S * (d.d_state + 2) * d.channels * sizeof(float));
-    pl->off_bc = off;
-    off = up256(off + (size_t)nblk * pl->T * 8 * pl->NR * sizeof(float));
+    pl->off_h = pl->off_q = pl->off_d = 0;
+    if (pl->span) {
+        const size_t states = (size_t)pl->slots * nblk * 64 * pl->NR * sizeof(float);
+        pl->off_h = off;
+        off = up256(off + states);
+        pl->off_d = off;
+        off = up256(off + (size_t)pl->slots * nblk * 64 * sizeof(float));
+        pl->off_q = off;
+        if (bwd) off = up256(off + states);
+    }
+    pl->off_seg = pl->off_w = pl->off_bc = off;
+    if (bwd) {
+        off = up256(off + (size_t)(pl->T / seg + pl->S + 1) * nblk * 64 * pl->NR * sizeof(float));
+        pl->off_w = off;
+        off = up256(off + (size_t)pl->slots * (d.d_state + 2) * d.channels * sizeof(float));
+        pl->off_bc = off;
+        off = up256(off + (size_t)nblk * pl->T * 8 * pl->NR * sizeof(float));
+    }
     pl->total = off;
     return SSD_OK;
 }
@@ -839,7 +1070,7 @@ int sel_setup(const ssd_selscan_dims* dims, const ssd_selscan_layout* layout, co
     for (int64_t s : {l.B_token, l.B_group, l.C_token, l.C_group})
         if (s < 0 || s > kMaxStride) return SSD_ERR_SHAPE;
     if ((d.nseq > 0) != (cu != nullptr)) return cu ? SSD_ERR_SHAPE : SSD_ERR_NULL_ARG;
-    if ((st = sel_plan(d, pl)) != SSD_OK) return st;
+    if ((st = sel_plan(d, bwd, pl)) != SSD_OK) return st;
     if (!d_init || !A || (pl->T > 0 && (!x || !d_raw || !B || !C))) return SSD_ERR_NULL_ARG;
     const size_t e = elem_size(d.dtype);
     for (const void* q : {x, d_raw, B, C, z})
@@ -878,13 +1109,20 @@ int sel_setup(const ssd_selscan_dims* dims, const ssd_selscan_layout* layout, co
     p->bpg = pl->bpg;
     p->units = (int32_t)pl->units;
     p->upr = pl->upr;
+    p->span = pl->span;
+    p->per = pl->per;
     return SSD_OK;
 }
 
 template <typename T, int NR>
 void launch_sel(const SelParams& p, unsigned grid, bool bwd, hipStream_t s) {
-    if (bwd) selscan_bwd_kernel<T, NR><<<dim3(grid), dim3(64 * Shape<NR>::kBwdWaves), 0, s>>>(p);
-    else selscan_fwd_kernel<T, NR><<<dim3(grid), dim3(64 * Shape<NR>::kFwdWaves), 0, s>>>(p);
+    if (bwd) {
+        if (p.span) selscan_span_kernel<T, NR, true><<<dim3(grid), dim3(512), 0, s>>>(p);
+        selscan_bwd_kernel<T, NR><<<dim3(grid), dim3(64 * Shape<NR>::kBwdWaves), 0, s>>>(p);
+    } else {
+        if (p.span) selscan_span_kernel<T, NR, false><<<dim3(grid), dim3(512), 0, s>>>(p);
+        selscan_fwd_kernel<T, NR><<<dim3(grid), dim3(64 * Shape<NR>::kFwdWaves), 0, s>>>(p);
+    }
 }
 template <typename T>
 void launch_sel(const SelParams& p, int NR, unsigned grid, bool bwd, hipStream_t s) {
@@ -902,8 +1140,9 @@ using namespace ssd;
 extern "C" {
 
 size_t ssd_selscan_fwd_workspace_bytes(const ssd_selscan_dims* dims) {
-    (void)dims;
-    return 0;
+    SelPlan pl;
+    if (sel_check(dims) != SSD_OK || sel_plan(*dims, false, &pl) != SSD_OK) return 0;
+    return pl.total;
 }
 
 int ssd_selscan_fwd(const ssd_selscan_dims* dims, const ssd_selscan_layout* layout, const void* x,
@@ -911,8 +1150,6 @@ int ssd_selscan_fwd(const ssd_selscan_dims* dims, const ssd_selscan_layout* layo
                     const void* C, const float* D, const void* z, const float* init_state,
                     const int32_t* cu_seqlens, void* y, float* final_state, void* workspace,
                     size_t workspace_bytes, void* stream) {
-    (void)workspace;
-    (void)workspace_bytes;
     SelParams p;
     SelPlan pl;
     int st = sel_setup(dims, layout, x, d_raw, d_init, A, B, C, D, z, init_state, cu_seqlens, false,
@@ -921,6 +1158,10 @@ int ssd_selscan_fwd(const ssd_selscan_dims* dims, const ssd_selscan_layout* layo
     if (pl.T > 0 && !y) return SSD_ERR_NULL_ARG;
     if (!elem_aligned(y, elem_size(dims->dtype)) || !elem_aligned(final_state, 4))
         return SSD_ERR_ALIGN;
+    if (pl.total > 0) {
+        if ((uintptr_t)workspace & 255) return SSD_ERR_ALIGN;
+        if (!workspace || workspace_bytes < pl.total) return SSD_ERR_WORKSPACE;
+    }
     const size_t sb = (size_t)pl.S * dims->d_state * dims->channels * sizeof(float);
     if (overlaps(init_state, sb, final_state, sb)) return SSD_ERR_OVERLAP;
     hipStream_t s = (hipStream_t)stream;
@@ -928,6 +1169,8 @@ int ssd_selscan_fwd(const ssd_selscan_dims* dims, const ssd_selscan_layout* layo
     if (pl.T == 0 && !final_state) return SSD_OK;
     p.y = y;
     p.final_state = final_state;
+    p.span_h = (float*)((char*)workspace + pl.off_h);
+    p.span_d = (float*)((char*)workspace + pl.off_d);
     if (dims->dtype == SSD_BF16) launch_sel<bf16>(p, pl.NR, (unsigned)pl.grid, false, s);
     else launch_sel<float>(p, pl.NR, (unsigned)pl.grid, false, s);
     return launched();
@@ -935,7 +1178,7 @@ int ssd_selscan_fwd(const ssd_selscan_dims* dims, const ssd_selscan_layout* layo
 
 size_t ssd_selscan_bwd_workspace_bytes(const ssd_selscan_dims* dims) {
     SelPlan pl;
-    if (sel_check(dims) != SSD_OK || sel_plan(*dims, &pl) != SSD_OK) return 0;
+    if (sel_check(dims) != SSD_OK || sel_plan(*dims, true, &pl) != SSD_OK) return 0;
     return pl.total;
 }
 
@@ -972,6 +1215,9 @@ int ssd_selscan_bwd(const ssd_selscan_dims* dims, const ssd_selscan_layout* layo
     p.dd_raw = dd_raw;
     p.dz = dz;
     p.final_state = dinit_state;
+    p.span_h = (float*)(ws + pl.off_h);
+    p.span_q = (float*)(ws + pl.off_q);
+    p.span_d = (float*)(ws + pl.off_d);
     p.seg_states = (float*)(ws + pl.off_seg);
     p.part_w = (float*)(ws + pl.off_w);
     p.part_bc = (float*)(ws + pl.off_bc);
@@ -990,7 +1236,7 @@ int ssd_selscan_bwd(const ssd_selscan_dims* dims, const ssd_selscan_layout* layo
     }
     ColSum c = {};
     c.part = p.part_w;
-    c.rows = pl.S;
+    c.rows = pl.slots;
     c.cols = (int64_t)(dims->d_state + 2) * dims->channels;
     c.out0 = dA;
     c.c0 = (int64_t)dims->d_state * dims->channels;

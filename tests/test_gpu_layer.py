@@ -274,7 +274,11 @@ SCAN = [  # b, L, E, N, G, cu
     (1, 300, 33, 8, 1, None), (2, 70, 34, 32, 2, None), (1, 90, 10, 33, 1, None),
     (1, 40, 18, 64, 1, None), (1, 520, 5, 7, 1, None),
     (1, 9, 6, 16, 1, [0, 1, 1, 3, 9]), (1, 300, 24, 16, 1, [0, 0, 2, 19, 275, 300, 300]),
-    (1, 140, 12, 8, 2, [0, 128, 140]), (1, 0, 8, 16, 1, [0, 0, 0]), (2, 0, 8, 16, 1, None)]
+    (1, 140, 12, 8, 2, [0, 128, 140]),
+    # long with few channels: cut into spans
+    (1, 2600, 20, 16, 1, None), (2, 1500, 9, 8, 1, None), (1, 700, 6, 40, 1, None),
+    (1, 900, 34, 32, 2, None), (1, 2300, 18, 16, 1, [0, 0, 700, 701, 2300, 2300]),
+    (1, 0, 8, 16, 1, [0, 0, 0]), (2, 0, 8, 16, 1, None)]
 
 
 def scan_problem(dtype, case, gated=True, carry=True, seed=0):

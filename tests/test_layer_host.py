@@ -193,6 +193,22 @@ def test_workspaces_are_planned_from_the_sizes():
     assert need("ssd_norm_bwd_workspace_bytes", big) <= 2048 * 2 * 64 * 4
 
 
+@needs_no_gpu
+def test_selscan_cuts_long_sequences_of_few_channels():
+    """Spans (and a workspace for their states) only where whole sequences would
+    leave most of the chip idle."""
+    need = lambda **kw: ly._entry("ssd_selscan_fwd_workspace_bytes")(ctypes.byref(scan_dims(**kw)))
+    assert need(batch=1, seqlen=65536, channels=64) > 0
+    assert need(batch=1, seqlen=65536, channels=64, nseq=3) > 0
+    assert need(batch=1, seqlen=256, channels=64) == 0       # one segment
+    assert need(batch=8, seqlen=4096, channels=4096) == 0    # whole sequences fill the chip
+    assert need(batch=1, seqlen=0, channels=64) == 0
+    d = scan_dims(batch=1, seqlen=65536, channels=64)
+    assert call("ssd_selscan_fwd", d, ws=None) == WORKSPACE
+    assert call("ssd_selscan_fwd", d, wsb=256) == WORKSPACE
+    assert call("ssd_selscan_fwd", d, ws=FAKE + 16) == ALIGN
+
+
 def test_binding_refuses_mismatches():
     f, b = torch.float32, torch.bfloat16
     x = torch.zeros(2, 8, 16)
