@@ -9,7 +9,11 @@
 // every row of which it loads once and keeps in registers: the W - 1 rows
 // before the run (and, backwards, after it) are the only re-reads, and they
 // come from cache.  Threads of a wave lie along the channels, so every load
-// is a contiguous piece of a row.  The states (final_state, dinit_state)
+// is a contiguous piece of a row; where the channels are no multiple of the
+// vector, the last one is moved back to end with them (the channels it shares
+// with its neighbour are formed twice, to the same bits), so there is no
+// partial vector.  Runs that lie whole inside one sequence take an unrolled
+// path with all loads issued first; the others walk token by token.  The states (final_state, dinit_state)
 // come from work items of their own behind the tokens'.
 #include "ssd_layer.h"
 
@@ -51,12 +55,26 @@ __device__ __forceinline__ Walk walk_at(const ConvParams& p, int64_t t, int64_t 
     return w;
 }
 
+// First channel of vector i.
+template <int V>
+__device__ __forceinline__ int channel_of(const ConvParams& p, int i) {
+    return V == 1 ? i : min(i * V, p.E - V);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void load(const T* __restrict__ p, float (&o)[V]) {
+    load_vec<T, V>(p, V, o);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store(T* __restrict__ p, const float (&v)[V]) {
+    store_vec<T, V>(p, V, v);
+}
+
 // Row `row` of sequence seq's initial state (W - 2: the input before its first token).
 template <typename T, int W, int V>
-__device__ __forceinline__ void load_init(const ConvParams& p, int seq, int row, int e, int n,
-                                          float (&o)[V]) {
+__device__ __forceinline__ void load_init(const ConvParams& p, int seq, int row, int e, float (&o)[V]) {
     if (p.init) {
-        load_vec<T, V>((const T*)p.init + ((int64_t)seq * (W - 1) + row) * p.E + e, n, o);
+        load<T, V>((const T*)p.init + ((int64_t)seq * (W - 1) + row) * p.E + e, o);
     } else {
 #pragma unroll
         for (int j = 0; j < V; ++j) o[j] = 0.f;
@@ -66,12 +84,12 @@ __device__ __forceinline__ void load_init(const ConvParams& p, int seq, int row,
 // x at token t of the walk's sequence, or the state's row where t lies before it.
 template <typename T, int W, int V>
 __device__ __forceinline__ void load_line(const ConvParams& p, const Walk& w, int64_t t, int e,
-                                          int n, float (&o)[V]) {
+                                          float (&o)[V]) {
     if (t >= w.first) {
-        load_vec<T, V>((const T*)p.x + t * p.xs + e, n, o);
+        load<T, V>((const T*)p.x + t * p.xs + e, o);
     } else {
         const int64_t row = t - w.first + W - 1;  // < 0 only where cu_seqlens is not sorted
-        load_init<T, W, V>(p, w.seq, row < 0 ? 0 : (int)row, e, n, o);
+        load_init<T, W, V>(p, w.seq, row < 0 ? 0 : (int)row, e, o);
     }
 }
 
@@ -80,13 +98,37 @@ struct Raw {
     T v[V];
 };
 template <typename T, int V>
-__device__ __forceinline__ void load_raw(const T* p, int n, Raw<T, V>& r) {
-    if (n >= V) {
-        __builtin_memcpy(&r, p, sizeof(r));
-    } else {
+__device__ __forceinline__ Raw<T, V> load_raw(const T* __restrict__ p) {
+    Raw<T, V> r;
+    __builtin_memcpy(&r, p, sizeof(r));
+    return r;
+}
+
+template <int W, int V>
+__device__ __forceinline__ void load_taps(const ConvParams& p, int e, float (&w)[W][V], float (&b)[V]) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) r.v[j] = j < n ? p[j] : (T)0.f;
+    for (int k = 0; k < W; ++k) load<float, V>(p.weight + (int64_t)k * p.E + e, w[k]);
+#pragma unroll
+    for (int j = 0; j < V; ++j) b[j] = 0.f;
+    if (p.bias) load<float, V>(p.bias + e, b);
+}
+
+template <int W, int V>
+__device__ __forceinline__ void filter(const float (&win)[W][V], const float (&w)[W][V],
+                                       const float (&b)[V], float (&v)[V]) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        v[j] = b[j];
+#pragma unroll
+        for (int k = 0; k < W; ++k) v[j] += win[k][j] * w[k][j];
     }
+}
+template <int W, int V>
+__device__ __forceinline__ void shift(float (&win)[W][V]) {
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) win[k][j] = win[k + 1][j];
 }
 
 // ---- forward ------------------------------------------------------------------------------
@@ -99,61 +141,66 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p) {
         const int64_t id = ((int64_t)blockIdx.x - p.main_blocks) * 256 + threadIdx.x;
         if (id >= p.state_items) return;
         int64_t sr;
-        const int e = (int)divide(id, p.nvec, &sr) * V;
+        const int e = channel_of<V>(p, (int)divide(id, p.nvec, &sr));
         Walk w;
         w.seq = (int)(sr / (W - 1));
         const int r = (int)(sr % (W - 1));
         sequence_span(p.cu, w.seq, p.L, p.T, &w.first, &w.last);
         float o[V];
-        load_line<T, W, V>(p, w, w.last - (W - 1) + r, e, p.E - e, o);
-        store_vec<T, V>((T*)p.state_out + sr * p.E + e, p.E - e, o);
+        load_line<T, W, V>(p, w, w.last - (W - 1) + r, e, o);
+        store<T, V>((T*)p.state_out + sr * p.E + e, o);
         return;
     }
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
     int64_t tile, brow;
-    const int e = (int)divide(id, p.nvec, &tile) * V, left = p.E - e;
+    const int e = channel_of<V>(p, (int)divide(id, p.nvec, &tile));
     const int64_t len = p.cu ? p.T : p.L;
     const int64_t at0 = divide(tile, p.tiles_per_row, &brow) * TT;
     const int64_t t0 = brow * len + at0, t1 = imin(t0 + TT, (brow + 1) * len);
     if (t0 >= p.T || t0 >= t1) return;
-    Raw<T, V> rows[TT];
-#pragma unroll
-    for (int i = 0; i < TT; ++i)
-        if (t0 + i < t1) load_raw<T, V>(x + (t0 + i) * p.xs + e, left, rows[i]);
-    float w[W][V], b[V], win[W][V];
-#pragma unroll
-    for (int k = 0; k < W; ++k) load_vec<float, V>(p.weight + (int64_t)k * p.E + e, left, w[k]);
-#pragma unroll
-    for (int j = 0; j < V; ++j) b[j] = 0.f;
-    if (p.bias) load_vec<float, V>(p.bias + e, left, b);
     Walk at = walk_at(p, t0, brow);
+    float w[W][V], b[V], win[W][V], v[V];
+    const T* px = x + t0 * p.xs + e;
+    T* py = (T*)p.out + t0 * p.os + e;
+    if (t0 + TT <= t1 && t1 <= at.last) {
+        Raw<T, V> rows[TT];
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) load_line<T, W, V>(p, at, t0 - (W - 1) + k, e, left, win[k]);
-    T* y = (T*)p.out;
+        for (int i = 0; i < TT; ++i) rows[i] = load_raw<T, V>(px + i * p.xs);
+        load_taps<W, V>(p, e, w, b);
 #pragma unroll
-    for (int i = 0; i < TT; ++i) {
-        const int64_t t = t0 + i;
-        if (t >= t1) break;
+        for (int k = 0; k < W - 1; ++k) load_line<T, W, V>(p, at, t0 - (W - 1) + k, e, win[k]);
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) win[W - 1][j] = (float)rows[i].v[j];
+            filter<W, V>(win, w, b, v);
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] *= sigmoid(v[j]);
+            store<T, V>(py + i * p.os, v);
+            shift<W, V>(win);
+        }
+        return;
+    }
+    load_taps<W, V>(p, e, w, b);
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) load_line<T, W, V>(p, at, t0 - (W - 1) + k, e, win[k]);
+    Raw<T, V> next = load_raw<T, V>(px);
+#pragma unroll 1
+    for (int64_t t = t0; t < t1; ++t, px += p.xs, py += p.os) {
+        const Raw<T, V> now = next;
+        if (t + 1 < t1) next = load_raw<T, V>(px + p.xs);
         if (p.cu && t >= at.last && at.seq + 1 < p.nseq) {  // the next sequence that has tokens
             at = walk_at(p, t, 0);
 #pragma unroll
-            for (int k = 0; k < W - 1; ++k) load_init<T, W, V>(p, at.seq, k, e, left, win[k]);
+            for (int k = 0; k < W - 1; ++k) load_init<T, W, V>(p, at.seq, k, e, win[k]);
         }
 #pragma unroll
-        for (int j = 0; j < V; ++j) win[W - 1][j] = (float)rows[i].v[j];
-        float v[V];
+        for (int j = 0; j < V; ++j) win[W - 1][j] = (float)now.v[j];
+        filter<W, V>(win, w, b, v);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            v[j] = b[j];
-#pragma unroll
-            for (int k = 0; k < W; ++k) v[j] += win[k][j] * w[k][j];
-            v[j] *= sigmoid(v[j]);
-        }
-        store_vec<T, V>(y + t * p.os + e, left, v);
-#pragma unroll
-        for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-            for (int j = 0; j < V; ++j) win[k][j] = win[k + 1][j];
+        for (int j = 0; j < V; ++j) v[j] *= sigmoid(v[j]);
+        store<T, V>(py, v);
+        shift<W, V>(win);
     }
 }
 
@@ -173,32 +220,24 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
         const int64_t id = ((int64_t)blockIdx.x - p.main_blocks) * 256 + threadIdx.x;
         if (id >= p.state_items) return;
         int64_t sr;
-        const int e = (int)divide(id, p.nvec, &sr) * V, left = p.E - e;
+        const int e = channel_of<V>(p, (int)divide(id, p.nvec, &sr));
         Walk at;
         at.seq = (int)(sr / (W - 1));
         const int r = (int)(sr % (W - 1));
         sequence_span(p.cu, at.seq, p.L, p.T, &at.first, &at.last);
         const int64_t len = at.last - at.first;
         float acc[V], w[W][V], b[V];
+        load_taps<W, V>(p, e, w, b);
 #pragma unroll
-        for (int k = 0; k < W; ++k) load_vec<float, V>(p.weight + (int64_t)k * p.E + e, left, w[k]);
-#pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] = b[j] = 0.f;
-        if (p.bias) load_vec<float, V>(p.bias + e, left, b);
+        for (int j = 0; j < V; ++j) acc[j] = 0.f;
 #pragma unroll
         for (int q = 0; q < W - 1; ++q) {
             if (q > r || q >= len) break;
-            float v[V], g[V];
+            float v[V], g[V], win[W][V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) v[j] = b[j];
-#pragma unroll
-            for (int k = 0; k < W; ++k) {
-                float t[V];
-                load_line<T, W, V>(p, at, at.first + q - (W - 1) + k, e, left, t);
-#pragma unroll
-                for (int j = 0; j < V; ++j) v[j] += t[j] * w[k][j];
-            }
-            load_vec<T, V>(dy + (at.first + q) * p.gs + e, left, g);
+            for (int k = 0; k < W; ++k) load_line<T, W, V>(p, at, at.first + q - (W - 1) + k, e, win[k]);
+            filter<W, V>(win, w, b, v);
+            load<T, V>(dy + (at.first + q) * p.gs + e, g);
 #pragma unroll
             for (int k = 0; k < W; ++k)
                 if (k == r - q) {
@@ -209,11 +248,11 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
         }
         if (df && r >= len) {
             float g[V];
-            load_vec<T, V>(df + ((int64_t)at.seq * (W - 1) + r - len) * p.E + e, left, g);
+            load<T, V>(df + ((int64_t)at.seq * (W - 1) + r - len) * p.E + e, g);
 #pragma unroll
             for (int j = 0; j < V; ++j) acc[j] += g[j];
         }
-        store_vec<T, V>((T*)p.state_out + sr * p.E + e, left, acc);
+        store<T, V>((T*)p.state_out + sr * p.E + e, acc);
         return;
     }
     __shared__ float ex[3][W + 1][V][64];
@@ -221,62 +260,94 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
     const uint32_t groups = (uint32_t)(p.nvec + 63) / 64;
     const int64_t strip = blockIdx.x / groups;
     const int vec = (int)(blockIdx.x % groups) * 64 + lane;
-    const int e = vec * V, left = p.E - e;  // left <= 0 past the last channel: nothing is loaded
+    const bool live = vec < p.nvec;
+    const int e = channel_of<V>(p, live ? vec : 0);
     float w[W][V], b[V], dw[W][V], db[V];
-#pragma unroll
-    for (int k = 0; k < W; ++k) load_vec<float, V>(p.weight + (int64_t)k * p.E + e, left, w[k]);
+    load_taps<W, V>(p, e, w, b);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        b[j] = db[j] = 0.f;
+        db[j] = 0.f;
 #pragma unroll
         for (int k = 0; k < W; ++k) dw[k][j] = 0.f;
     }
-    if (p.bias) load_vec<float, V>(p.bias + e, left, b);
     T* dx = (T*)p.out;
     const int64_t len = p.cu ? p.T : p.L;
-    const int64_t tiles = p.tiles;
     for (int it = 0; it < p.iters; ++it) {
         const int64_t tile = (strip * 4 + wave) * p.iters + it;
-        if (tile >= tiles || left <= 0) break;
+        if (tile >= p.tiles || !live) break;
         int64_t brow;
         const int64_t at0 = divide(tile, p.tiles_per_row, &brow) * TT;
         const int64_t t0 = brow * len + at0;
         const int64_t t1 = imin(t0 + TT, (brow + 1) * len);
-        const int64_t te = imin(t1 + W - 1, (brow + 1) * len);  // tokens whose dv is formed
-        Raw<T, V> xr[TT + W - 1], gr[TT + W - 1];
-#pragma unroll
-        for (int i = 0; i < TT + W - 1; ++i)
-            if (t0 + i < te) {
-                load_raw<T, V>(x + (t0 + i) * p.xs + e, left, xr[i]);
-                load_raw<T, V>(dy + (t0 + i) * p.gs + e, left, gr[i]);
-            }
         Walk at = walk_at(p, t0, brow);
-        float win[W][V], acc[W][V];  // acc[j]: dx of token t - (W - 1) + j
-#pragma unroll
-        for (int k = 0; k < W - 1; ++k) load_line<T, W, V>(p, at, t0 - (W - 1) + k, e, left, win[k]);
+        float win[W][V], acc[W][V], v[V], dv[V];  // acc[j]: dx of token t - (W - 1) + j
 #pragma unroll
         for (int k = 0; k < W; ++k)
 #pragma unroll
             for (int j = 0; j < V; ++j) acc[k][j] = 0.f;
+        const T* px = x + t0 * p.xs + e;
+        const T* pg = dy + t0 * p.gs + e;
+        T* po = dx + t0 * p.xs + e;
+        if (t0 + TT <= t1 && t1 + W - 1 <= at.last) {
+            // every token whose dv reaches the run is of its sequence, and none
+            // of the run is a row of final_state
+            Raw<T, V> xr[TT + W - 1], gr[TT + W - 1];
 #pragma unroll
-        for (int i = 0; i < TT + W - 1; ++i) {
-            const int64_t t = t0 + i;
+            for (int i = 0; i < TT + W - 1; ++i) {
+                xr[i] = load_raw<T, V>(px + i * p.xs);
+                gr[i] = load_raw<T, V>(pg + i * p.gs);
+            }
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) load_line<T, W, V>(p, at, t0 - (W - 1) + k, e, win[k]);
+#pragma unroll
+            for (int i = 0; i < TT + W - 1; ++i) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) win[W - 1][j] = (float)xr[i].v[j];
+                filter<W, V>(win, w, b, v);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    dv[j] = (float)gr[i].v[j] * silu_slope(v[j], sigmoid(v[j]));
+                    if (i < TT) {
+                        db[j] += dv[j];
+#pragma unroll
+                        for (int k = 0; k < W; ++k) dw[k][j] += dv[j] * win[k][j];
+                    }
+                    // of the accumulators only those of the run's tokens count
+#pragma unroll
+                    for (int k = 0; k < W; ++k)
+                        if (i - (W - 1) + k >= 0 && i - (W - 1) + k < TT) acc[k][j] += dv[j] * w[k][j];
+                }
+                shift<W, V>(win);
+                if (i >= W - 1) store<T, V>(po + (i - (W - 1)) * p.xs, acc[0]);
+                shift<W, V>(acc);
+#pragma unroll
+                for (int j = 0; j < V; ++j) acc[W - 1][j] = 0.f;
+            }
+            continue;
+        }
+        const int64_t te = imin(t1 + W - 1, (brow + 1) * len);  // tokens whose dv is formed
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) load_line<T, W, V>(p, at, t0 - (W - 1) + k, e, win[k]);
+        Raw<T, V> xn = load_raw<T, V>(px), gn = load_raw<T, V>(pg);
+#pragma unroll 1
+        for (int64_t t = t0; t < t1 + W - 1; ++t) {
             if (t < te) {
+                const Raw<T, V> xt = xn, gt = gn;
+                if (t + 1 < te) {
+                    xn = load_raw<T, V>(x + (t + 1) * p.xs + e);
+                    gn = load_raw<T, V>(dy + (t + 1) * p.gs + e);
+                }
                 if (p.cu && t >= at.last && at.seq + 1 < p.nseq) {
                     at = walk_at(p, t, 0);
 #pragma unroll
-                    for (int k = 0; k < W - 1; ++k) load_init<T, W, V>(p, at.seq, k, e, left, win[k]);
+                    for (int k = 0; k < W - 1; ++k) load_init<T, W, V>(p, at.seq, k, e, win[k]);
                 }
                 const int64_t pos = t - at.first;
-                float dv[V];
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    win[W - 1][j] = (float)xr[i].v[j];
-                    float v = b[j];
+                for (int j = 0; j < V; ++j) win[W - 1][j] = (float)xt.v[j];
+                filter<W, V>(win, w, b, v);
 #pragma unroll
-                    for (int k = 0; k < W; ++k) v += win[k][j] * w[k][j];
-                    dv[j] = (float)gr[i].v[j] * silu_slope(v, sigmoid(v));
-                }
+                for (int j = 0; j < V; ++j) dv[j] = (float)gt.v[j] * silu_slope(v[j], sigmoid(v[j]));
                 if (t < t1) {
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
@@ -284,10 +355,9 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
 #pragma unroll
                         for (int k = 0; k < W; ++k) dw[k][j] += dv[j] * win[k][j];
                     }
-                    if (df && at.last > t && at.last - t <= W - 1) {  // the token is a row of final_state
+                    if (df && at.last > t && at.last - t <= W - 1) {  // a row of final_state
                         float g[V];
-                        load_vec<T, V>(df + ((int64_t)at.seq * (W - 1) + (W - 1) - (at.last - t)) * p.E + e,
-                                       left, g);
+                        load<T, V>(df + ((int64_t)at.seq * (W - 1) + (W - 1) - (at.last - t)) * p.E + e, g);
 #pragma unroll
                         for (int j = 0; j < V; ++j) acc[W - 1][j] += g[j];
                     }
@@ -299,17 +369,11 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
 #pragma unroll
                         for (int j = 0; j < V; ++j) acc[k][j] += dv[j] * w[k][j];
                     }
-#pragma unroll
-                for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-                    for (int j = 0; j < V; ++j) win[k][j] = win[k + 1][j];
+                shift<W, V>(win);
             }
             const int64_t done = t - (W - 1);
-            if (i >= W - 1 && done < t1) store_vec<T, V>(dx + done * p.xs + e, left, acc[0]);
-#pragma unroll
-            for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-                for (int j = 0; j < V; ++j) acc[k][j] = acc[k + 1][j];
+            if (done >= t0 && done < t1) store<T, V>(dx + done * p.xs + e, acc[0]);
+            shift<W, V>(acc);
 #pragma unroll
             for (int j = 0; j < V; ++j) acc[W - 1][j] = 0.f;
         }
@@ -323,7 +387,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
         }
     }
     __syncthreads();
-    if (wave || left <= 0) return;
+    if (wave || !live) return;
 #pragma unroll
     for (int o = 0; o < 3; ++o)
 #pragma unroll
@@ -334,28 +398,42 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
         }
     float* q = p.part + strip * (W + 1) * p.E + e;
 #pragma unroll
-    for (int k = 0; k < W; ++k) store_vec<float, V>(q + (int64_t)k * p.E, left, dw[k]);
-    store_vec<float, V>(q + (int64_t)W * p.E, left, db);
+    for (int k = 0; k < W; ++k) store<float, V>(q + (int64_t)k * p.E, dw[k]);
+    store<float, V>(q + (int64_t)W * p.E, db);
 }
 
 // ---- host ---------------------------------------------------------------------------------
 
-constexpr int kBwdTile = 8;
+// 65536 packed tokens x 1792 channels, bf16: runs of 16 tokens by vectors of 4
+// channels 98 us (4.8 TB/s); 8 by 4 104, 32 by 4 106, 16 by 8 115, 8 by 8 117
+// (fewer waves per SIMD to hide the loads).
+constexpr int kFwdTile = 16, kShortTile = 4;
+constexpr int kFwdVec = 4;
+constexpr int kBwdTile = 16, kBwdShortTile = 8;
 constexpr int kBwdVec = 4;
+
+// Channels a thread: fewer than a vector's are taken one by one.
+int vec_of(int32_t channels, int vec) { return channels >= vec ? vec : 1; }
 
 struct ConvBwdPlan {
     int64_t tiles, strips;
-    int32_t tiles_per_row, iters;
+    int32_t tile, tiles_per_row, iters;
 };
 
 ConvBwdPlan conv_bwd_plan(const ssd_conv_dims& d) {
     ConvBwdPlan pl;
     const int64_t len = d.seqlen, rows = d.batch;  // packed: one row
-    pl.tiles_per_row = (int32_t)imax(1, cdiv(len, kBwdTile));
+    const int64_t groups = cdiv(cdiv(d.channels, vec_of(d.channels, kBwdVec)), 64);
+    // Runs of 16 tokens re-read 2 (W - 1) / 16 of their rows, those of 8 twice
+    // that (32768 tokens x 1792 channels: 95 us against 110, bf16; 155 against
+    // 165, float32); the short ones fill the chip where there are few tokens
+    // (4096 tokens: 29.2 us against 30.0).
+    pl.tile = rows * cdiv(len, kBwdTile) * groups >= 4 * 1024 && vec_of(d.channels, kBwdVec) > 1
+                  ? kBwdTile : kBwdShortTile;
+    pl.tiles_per_row = (int32_t)imax(1, cdiv(len, pl.tile));
     pl.tiles = len == 0 ? 0 : rows * pl.tiles_per_row;
     // more tiles a wave (fewer partial rows) only while every CU keeps eight
     // workgroups
-    const int64_t groups = cdiv(cdiv(d.channels, kBwdVec), 64);
     const int64_t it = pl.tiles * groups / (4 * 256 * 8);
     pl.iters = (int32_t)(it < 1 ? 1 : (it > 8 ? 8 : it));
     pl.strips = imax(1, cdiv(pl.tiles, 4 * pl.iters));
@@ -407,12 +485,24 @@ void launch_conv_fwd(const ConvParams& p, int W, dim3 grid, hipStream_t s) {
     else if (W == 3) conv_fwd_kernel<T, 3, V, TT><<<grid, dim3(256), 0, s>>>(p);
     else conv_fwd_kernel<T, 4, V, TT><<<grid, dim3(256), 0, s>>>(p);
 }
-
 template <typename T>
+void launch_conv_fwd(const ConvParams& p, int W, int V, int tt, dim3 grid, hipStream_t s) {
+    if (V == 1) launch_conv_fwd<T, 1, kShortTile>(p, W, grid, s);
+    else if (tt == kFwdTile) launch_conv_fwd<T, kFwdVec, kFwdTile>(p, W, grid, s);
+    else launch_conv_fwd<T, kFwdVec, kShortTile>(p, W, grid, s);
+}
+
+template <typename T, int V, int TT>
 void launch_conv_bwd(const ConvParams& p, int W, dim3 grid, hipStream_t s) {
-    if (W == 2) conv_bwd_kernel<T, 2, kBwdVec, kBwdTile><<<grid, dim3(256), 0, s>>>(p);
-    else if (W == 3) conv_bwd_kernel<T, 3, kBwdVec, kBwdTile><<<grid, dim3(256), 0, s>>>(p);
-    else conv_bwd_kernel<T, 4, kBwdVec, kBwdTile><<<grid, dim3(256), 0, s>>>(p);
+    if (W == 2) conv_bwd_kernel<T, 2, V, TT><<<grid, dim3(256), 0, s>>>(p);
+    else if (W == 3) conv_bwd_kernel<T, 3, V, TT><<<grid, dim3(256), 0, s>>>(p);
+    else conv_bwd_kernel<T, 4, V, TT><<<grid, dim3(256), 0, s>>>(p);
+}
+template <typename T>
+void launch_conv_bwd(const ConvParams& p, int W, int V, int tile, dim3 grid, hipStream_t s) {
+    if (V == 1) launch_conv_bwd<T, 1, kBwdShortTile>(p, W, grid, s);
+    else if (tile == kBwdTile) launch_conv_bwd<T, kBwdVec, kBwdTile>(p, W, grid, s);
+    else launch_conv_bwd<T, kBwdVec, kBwdShortTile>(p, W, grid, s);
 }
 
 }  // namespace
@@ -442,7 +532,7 @@ int ssd_conv_fwd(const ssd_conv_dims* dims, const ssd_conv_layout* layout, const
     if (overlaps(init_state, sb, final_state, sb)) return SSD_ERR_OVERLAP;
     hipStream_t s = (hipStream_t)stream;
     if (cu_seqlens && check_cu_env(cu_seqlens, d.nseq, T, s, &st)) return st;
-    const int V = d.dtype == SSD_BF16 ? 8 : 4;
+    const int V = vec_of(d.channels, kFwdVec);
     ConvParams p = conv_params(d, l, cu_seqlens, V);
     p.x = x;
     p.weight = weight;
@@ -453,7 +543,8 @@ int ssd_conv_fwd(const ssd_conv_dims* dims, const ssd_conv_layout* layout, const
     p.state_out = final_state;
     // runs of 16 tokens where that still gives every SIMD a wave, else of 4
     const int64_t len = d.seqlen;
-    const int tt = (int64_t)d.batch * cdiv(len, 16) * p.nvec >= 4 * 256 * 64 ? 16 : 4;
+    const int tt = V > 1 && (int64_t)d.batch * cdiv(len, kFwdTile) * p.nvec >= 4 * 256 * 64
+                       ? kFwdTile : kShortTile;
     p.tiles_per_row = (int32_t)imax(1, cdiv(len, tt));
     p.main_blocks = len == 0 ? 0 : cdiv((int64_t)d.batch * p.tiles_per_row * p.nvec, 256);
     p.state_items = final_state ? (int64_t)p.S * (d.width - 1) * p.nvec : 0;
@@ -461,13 +552,8 @@ int ssd_conv_fwd(const ssd_conv_dims* dims, const ssd_conv_layout* layout, const
     if (grid == 0) return SSD_OK;
     if (grid > INT32_MAX) return SSD_ERR_SHAPE;
     const dim3 gd((unsigned)grid);
-    if (d.dtype == SSD_BF16) {
-        if (tt == 16) launch_conv_fwd<bf16, 8, 16>(p, d.width, gd, s);
-        else launch_conv_fwd<bf16, 8, 4>(p, d.width, gd, s);
-    } else {
-        if (tt == 16) launch_conv_fwd<float, 4, 16>(p, d.width, gd, s);
-        else launch_conv_fwd<float, 4, 4>(p, d.width, gd, s);
-    }
+    if (d.dtype == SSD_BF16) launch_conv_fwd<bf16>(p, d.width, V, tt, gd, s);
+    else launch_conv_fwd<float>(p, d.width, V, tt, gd, s);
     return launched();
 }
 
@@ -503,7 +589,8 @@ int ssd_conv_bwd(const ssd_conv_dims* dims, const ssd_conv_layout* layout, const
     hipStream_t s = (hipStream_t)stream;
     if (cu_seqlens && check_cu_env(cu_seqlens, d.nseq, T, s, &st)) return st;
     const ConvBwdPlan pl = conv_bwd_plan(d);
-    ConvParams p = conv_params(d, l, cu_seqlens, kBwdVec);
+    const int V = vec_of(d.channels, kBwdVec);
+    ConvParams p = conv_params(d, l, cu_seqlens, V);
     p.x = x;
     p.weight = weight;
     p.bias = bias;
@@ -523,8 +610,8 @@ int ssd_conv_bwd(const ssd_conv_dims* dims, const ssd_conv_layout* layout, const
     p.state_items = dinit_state ? (int64_t)p.S * (d.width - 1) * p.nvec : 0;
     const int64_t grid = p.main_blocks + cdiv(p.state_items, 256);
     if (grid > INT32_MAX) return SSD_ERR_SHAPE;
-    if (d.dtype == SSD_BF16) launch_conv_bwd<bf16>(p, d.width, dim3((unsigned)grid), s);
-    else launch_conv_bwd<float>(p, d.width, dim3((unsigned)grid), s);
+    if (d.dtype == SSD_BF16) launch_conv_bwd<bf16>(p, d.width, V, pl.tile, dim3((unsigned)grid), s);
+    else launch_conv_bwd<float>(p, d.width, V, pl.tile, dim3((unsigned)grid), s);
     if ((st = launched()) != SSD_OK || (!dweight && !dbias)) return st;
     ColSum c = {};
     c.part = p.part;

@@ -47,7 +47,7 @@ struct SelParams {
     float* span_h;       // spans' states from zero [slots][blocks][64][NR]
     float* span_q;       // backward: what their tokens pass on to the span before
     float* span_d;       // their sums of d [slots][blocks][64]
-    float* seg_states;   // backward: states entering the segments [slots][blocks][64][NR]
+    float* chunk_states; // backward: states entering the chunks [segments][waves][blocks][64][NR]
     float* part_w;       // backward: [slots][(N + 2) E] shares of dA, dD, dd_init
     float* part_bc;      // backward: [blocks][T][2 NP] shares of dB, dC
     int64_t xs, ds, zs, bs_t, bs_g, cs_t, cs_g, ys, gs;
@@ -84,6 +84,10 @@ struct Shape {
     static constexpr int kBwdWaves = NR <= 8 ? 8 : 4;
     static constexpr int kBwdSegment = kBwdTokens * kBwdWaves;
 };
+
+// Bounds what the scheduler moves together, so that the unrolled token loops
+// stay within the registers; LDS reads may still be started early.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0x100); }
 
 // ---- lane helpers -------------------------------------------------------------------------
 
@@ -459,7 +463,7 @@ __global__ __launch_bounds__(512) void selscan_span_kernel(SelParams p) {
                 h[r] = at * h[r] + b[r] * ut;
                 if constexpr (BWD) a[t][r] = at;
             }
-            if (t & 1) __builtin_amdgcn_sched_barrier(0);
+            if (t & 1) keep_order();
         }
         if constexpr (BWD) {
             float ql[NR];
@@ -471,7 +475,7 @@ __global__ __launch_bounds__(512) void selscan_span_kernel(SelParams p) {
 #pragma unroll
                 for (int r = 0; r < NR; ++r)
                     ql[r] = t < TW - 1 ? a[t][r] * (cc[r] * wt + ql[r]) : a[t][r] * (cc[r] * wt);
-                if (!(t & 1)) __builtin_amdgcn_sched_barrier(0);
+                if (!(t & 1)) keep_order();
             }
 #pragma unroll
             for (int r = 0; r < NR; ++r) q[r] += fexp2(sum * A2[r]) * ql[r];
@@ -576,7 +580,7 @@ __global__ __launch_bounds__(64 * Shape<NR>::kFwdWaves) void selscan_fwd_kernel(
                 a[t][r] = fexp2(dt * A2[r]);
                 h[r] = t ? a[t][r] * h[r] + b[r] * ut : b[r] * ut;
             }
-            if (t & 1) __builtin_amdgcn_sched_barrier(0);
+            if (t & 1) keep_order();
         }
         lds_put<NR>(exH[turn][o.wave][o.lane], h);
         // the exchange is double-buffered: a wave is at most one barrier ahead
@@ -590,7 +594,7 @@ __global__ __launch_bounds__(64 * Shape<NR>::kFwdWaves) void selscan_fwd_kernel(
 #pragma unroll
             for (int r = 0; r < NR; ++r) h[r] = Pj[r] * h[r] + hj[r];
         }
-        __builtin_amdgcn_sched_barrier(0);
+        keep_order();
         const RowBuf<T> y = row_buf<T>(k->y, k->ys, o.ch0, tb, have, o.width);
         const uint32_t yat = fresh(yoff);
 #pragma unroll
@@ -610,13 +614,13 @@ __global__ __launch_bounds__(64 * Shape<NR>::kFwdWaves) void selscan_fwd_kernel(
                     h[r] = a[t][r] * h[r] + b[r] * ut;
                     v[k] = r ? v[k] + c[r] * h[r] : c[r] * h[r];
                 }
-                if (k & 1) __builtin_amdgcn_sched_barrier(0);
+                if (k & 1) keep_order();
             }
             float out = quad_sums(v[0], v[1], v[2], v[3], b0, b1) + Dv * x[i];
             const float zf = value_of<T>(zr[i]);
             out *= gated ? zf * sigmoid(zf) : 1.f;
             y.put(yat + i * (uint32_t)(4 * k->ys * sizeof(T)), out);
-            __builtin_amdgcn_sched_barrier(0);
+            keep_order();
         }
         // the segment's last chunk leaves the state that enters the next one;
         // its slot was last read before the barrier that this wave has passed
@@ -631,16 +635,17 @@ __global__ __launch_bounds__(64 * Shape<NR>::kFwdWaves) void selscan_fwd_kernel(
 
 // ---- backward -----------------------------------------------------------------------------
 
-// First the segments forward, only to find the state that enters each (kept in
-// seg_states); then backward, where each wave holds a and h of its chunk in
-// registers and both directions' states are folded through LDS.
+// First the segments forward, only to find the state that enters each chunk
+// (kept in chunk_states); then backward, where each wave holds a and h of its
+// chunk in registers.  What enters the last segment's chunks is found there,
+// so a sequence of one segment is walked once.
 template <typename T, int NR>
 __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(SelParams p) {
     using S = Shape<NR>;
     constexpr int TW = S::kBwdTokens, NP = S::NP, MW = S::kBwdWaves, Q = TW / 4;
     __shared__ __align__(16) float bc[MW][TW][2][NP];
     __shared__ __align__(16) float exP[2][MW][64][NR], exH[2][MW][64][NR], exQ[2][MW][64][NR];
-    __shared__ __align__(16) float enter[2][64][NR];  // q entering a segment from behind
+    __shared__ __align__(16) float enter[3][64][NR];  // h or q entering a segment
     Place o;
     if (!place_of(p, o)) return;
     const int waves = blockDim.x >> 6;
@@ -655,23 +660,19 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
     const int nseg = o.k < o.nspan ? (o.last - o.first + seg - 1) / seg : 0;
     // sequences' segments follow one another: this one's start at a slot that
     // no earlier sequence reaches
-    float* segs = p.seg_states +
-                  (((int64_t)(o.first / seg + o.seq) * p.nblk + o.blk) * 64 + o.lane) * NR;
-    const int64_t seg_step = (int64_t)p.nblk * 64 * NR;
+    float* states = p.chunk_states +
+                    ((((int64_t)(o.first / seg + o.seq) * waves + o.wave) * p.nblk + o.blk) * 64 + o.lane) * NR;
+    const int64_t states_step = (int64_t)waves * p.nblk * 64 * NR;
 
     uint32_t xr[Q], dr[Q], zr[Q], gr[Q];
     Rows<T, NR, TW> Br, Cr;
     int turn = 0;
-    // -- forward over all segments but the last; wave 0 folds
-    float carry[NR];
-    if (o.wave == 0) {
-        load_state<NR>(p.init, p, o, carry);
-        if (p.span && nseg > 0) fold_spans<NR>(p.span_h, p, o, A2, 0, o.k, 1, carry);
-    }
+    // -- forward over all segments but the last
     int tb = o.first + o.wave * TW;
-    if (nseg > 0 && o.wave == 0) {
-#pragma unroll
-        for (int r = 0; r < NR; ++r) segs[r] = carry[r];
+    if (o.wave == 0) {
+        load_state<NR>(p.init, p, o, h);
+        if (p.span && nseg > 0) fold_spans<NR>(p.span_h, p, o, A2, 0, o.k, 1, h);
+        lds_put<NR>(enter[0][o.lane], h);
     }
     auto fetch_forward = [&](int t) {
         const ArgPtr k = fresh_args();
@@ -709,25 +710,32 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
         lds_put<NR>(exP[turn][o.wave][o.lane], P);
         lds_put<NR>(exH[turn][o.wave][o.lane], h);
         __syncthreads();
-        if (o.wave == 0) {
-            for (int j = 0; j < waves; ++j) {
-                float hj[NR];
-                lds_get<NR>(exP[turn][j][o.lane], P);
-                lds_get<NR>(exH[turn][j][o.lane], hj);
+        float hin[NR];
+        lds_get<NR>(enter[turn][o.lane], hin);
+        for (int j = 0; j < o.wave; ++j) {
+            float Pj[NR], hj[NR];
+            lds_get<NR>(exP[turn][j][o.lane], Pj);
+            lds_get<NR>(exH[turn][j][o.lane], hj);
 #pragma unroll
-                for (int r = 0; r < NR; ++r) carry[r] = P[r] * carry[r] + hj[r];
-            }
+            for (int r = 0; r < NR; ++r) hin[r] = Pj[r] * hin[r] + hj[r];
+        }
+        __builtin_memcpy(states + (k - 1) * states_step, hin, sizeof(hin));
+        if (o.wave == waves - 1) {
 #pragma unroll
-            for (int r = 0; r < NR; ++r) segs[k * seg_step + r] = carry[r];
+            for (int r = 0; r < NR; ++r) hin[r] = P[r] * hin[r] + h[r];
+            lds_put<NR>(enter[turn ^ 1][o.lane], hin);
         }
     }
-    // -- backward
+    // -- backward.  enter[turn] holds the state entering the last segment; q goes
+    // through the other two slots in turn, first through the one that no wave
+    // can still be reading.
+    const int last_slot = turn;
+    int q_slot = 2, q_next = turn ^ 1;
     if (o.wave == 0) {
         load_state<NR>(p.d_final, p, o, q);
         if (p.span) fold_spans<NR>(p.span_q, p, o, A2, o.nspan - 1, o.nspan - 1 - o.k, -1, q);
-        lds_put<NR>(enter[turn][o.lane], q);
+        lds_put<NR>(enter[q_slot][o.lane], q);
     }
-    __syncthreads();  // wave 0's states and enter
     float dD = 0.f, dI = 0.f;
 #pragma unroll
     for (int r = 0; r < NR; ++r) dA[r] = 0.f;
@@ -750,8 +758,7 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
     for (int k = nseg - 1; k >= 0; --k, tb -= seg, turn ^= 1) {
         const int have = min(o.last - tb, TW);
         float hin[NR];
-#pragma unroll
-        for (int r = 0; r < NR; ++r) hin[r] = segs[k * seg_step + r];
+        if (k < nseg - 1) __builtin_memcpy(hin, states + k * states_step, sizeof(hin));
         // past the sequence and in lanes without a channel x and dy are 0
         float d[Q], u[Q], w[Q], x[Q], raw[Q], gz[Q];  // gz: what dz multiplies v by
         float sumd = 0.f;
@@ -775,24 +782,29 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
         put_rows<T, NR, TW>(&bc[o.wave][0][0][0], o, Br);
         put_rows<T, NR, TW>(&bc[o.wave][0][1][0], o, Cr);
         wave_lds_fence();
-        // (1) the chunk from zero states, in both directions
+        // (1) every decay of the chunk, and q through it from zero
         float a[TW][NR];
 #pragma unroll
         for (int r = 0; r < NR; ++r) h[r] = fexp2(sumd * A2[r]);
         lds_put<NR>(exP[turn][o.wave][o.lane], h);
 #pragma unroll
         for (int t = 0; t < TW; ++t) {
-            float b[NR];
-            lds_get<NR>(&bc[o.wave][t][0][o.nl * NR], b);
-            const float dt = quad_lane(d[t / 4], t % 4), ut = quad_lane(u[t / 4], t % 4);
+            const float dt = quad_lane(d[t / 4], t % 4);
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                a[t][r] = fexp2(dt * A2[r]);
-                h[r] = t ? a[t][r] * h[r] + b[r] * ut : b[r] * ut;
-            }
-            if (t & 1) __builtin_amdgcn_sched_barrier(0);
+            for (int r = 0; r < NR; ++r) a[t][r] = fexp2(dt * A2[r]);
         }
-        lds_put<NR>(exH[turn][o.wave][o.lane], h);
+        if (k == nseg - 1) {
+#pragma unroll
+            for (int t = 0; t < TW; ++t) {
+                float b[NR];
+                lds_get<NR>(&bc[o.wave][t][0][o.nl * NR], b);
+                const float ut = quad_lane(u[t / 4], t % 4);
+#pragma unroll
+                for (int r = 0; r < NR; ++r) h[r] = t ? a[t][r] * h[r] + b[r] * ut : b[r] * ut;
+                if (t & 1) keep_order();
+            }
+            lds_put<NR>(exH[turn][o.wave][o.lane], h);
+        }
 #pragma unroll
         for (int t = TW - 1; t >= 0; --t) {
             float c[NR];
@@ -801,19 +813,23 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
 #pragma unroll
             for (int r = 0; r < NR; ++r)
                 q[r] = t < TW - 1 ? a[t][r] * (c[r] * wt + q[r]) : a[t][r] * (c[r] * wt);
-            if (!(t & 1)) __builtin_amdgcn_sched_barrier(0);
+            if (!(t & 1)) keep_order();
         }
         lds_put<NR>(exQ[turn][o.wave][o.lane], q);
-        // (2) fold the chunks before this one (h) and behind it (q)
+        // (2) fold the chunks behind this one (q), and in the last segment those
+        // before it (h)
         __syncthreads();
-        for (int j = 0; j < o.wave; ++j) {
-            float Pj[NR], hj[NR];
-            lds_get<NR>(exP[turn][j][o.lane], Pj);
-            lds_get<NR>(exH[turn][j][o.lane], hj);
+        if (k == nseg - 1) {
+            lds_get<NR>(enter[last_slot][o.lane], hin);
+            for (int j = 0; j < o.wave; ++j) {
+                float Pj[NR], hj[NR];
+                lds_get<NR>(exP[turn][j][o.lane], Pj);
+                lds_get<NR>(exH[turn][j][o.lane], hj);
 #pragma unroll
-            for (int r = 0; r < NR; ++r) hin[r] = Pj[r] * hin[r] + hj[r];
+                for (int r = 0; r < NR; ++r) hin[r] = Pj[r] * hin[r] + hj[r];
+            }
         }
-        lds_get<NR>(enter[turn][o.lane], q);
+        lds_get<NR>(enter[q_slot][o.lane], q);
         for (int j = waves - 1; j > o.wave; --j) {
             float Pj[NR], qj[NR];
             lds_get<NR>(exP[turn][j][o.lane], Pj);
@@ -831,7 +847,7 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
 #pragma unroll
             for (int r = 0; r < NR; ++r)
                 hs[t][r] = a[t][r] * (t ? hs[t - 1][r] : hin[r]) + b[r] * ut;
-            if (t & 1) __builtin_amdgcn_sched_barrier(0);
+            if (t & 1) keep_order();
         }
         const ArgPtr out = fresh_args();
         const RowBuf<float> sums = row_buf<float>(out->part_bc + (int64_t)o.blk * out->T * (2 * NP),
@@ -889,7 +905,7 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
                 }
 #pragma unroll
                 for (int m = 0; m < M; ++m) sums.put(sum_off + (uint32_t)(t * 2 * NP + m) * 4u, f[m]);
-                __builtin_amdgcn_sched_barrier(0);
+                keep_order();
             }
             const float gBt = quad_sums(gB[0], gB[1], gB[2], gB[3], b0, b1);
             // A2 is A log2(e)
@@ -902,11 +918,14 @@ __global__ __launch_bounds__(64 * Shape<NR>::kBwdWaves) void selscan_bwd_kernel(
                 const float vt = quad_sums(v[0], v[1], v[2], v[3], b0, b1) + Dv * x[i];
                 dz.put(zoff + i * (uint32_t)(4 * out->zs * sizeof(T)), gz[i] * vt);
             }
-            __builtin_amdgcn_sched_barrier(0);
+            keep_order();
         }
         // q leaving the segment's first chunk enters the segment before it; its
         // slot was last read before the barrier that this wave has passed
-        if (o.wave == 0) lds_put<NR>(enter[turn ^ 1][o.lane], q);
+        if (o.wave == 0) lds_put<NR>(enter[q_next][o.lane], q);
+        const int used = q_slot;
+        q_slot = q_next;
+        q_next = used;
         wave_lds_fence();
     }
     if (o.wave == 0 && o.k == 0) store_state<NR>(p.final_state, p, o, q);
@@ -1043,7 +1062,8 @@ int sel_plan(const ssd_selscan_dims& d, bool bwd, SelPlan* pl) {
     }
     pl->off_seg = pl->off_w = pl->off_bc = off;
     if (bwd) {
-        off = up256(off + (size_t)(pl->T / seg + pl->S + 1) * nblk * 64 * pl->NR * sizeof(float));
+        const int64_t waves = with_shape(pl->NR, [](auto s) { return s.kBwdWaves; });
+        off = up256(off + (size_t)(pl->T / seg + pl->S + 1) * waves * nblk * 64 * pl->NR * sizeof(float));
         pl->off_w = off;
         off = up256(off + (size_t)pl->slots * (d.d_state + 2) * d.channels * sizeof(float));
         pl->off_bc = off;
@@ -1218,7 +1238,7 @@ int ssd_selscan_bwd(const ssd_selscan_dims* dims, const ssd_selscan_layout* layo
     p.span_h = (float*)(ws + pl.off_h);
     p.span_q = (float*)(ws + pl.off_q);
     p.span_d = (float*)(ws + pl.off_d);
-    p.seg_states = (float*)(ws + pl.off_seg);
+    p.chunk_states = (float*)(ws + pl.off_seg);
     p.part_w = (float*)(ws + pl.off_w);
     p.part_bc = (float*)(ws + pl.off_bc);
     if (dims->dtype == SSD_BF16) launch_sel<bf16>(p, pl.NR, (unsigned)pl.grid, true, s);
