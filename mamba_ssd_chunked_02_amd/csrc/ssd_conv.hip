@@ -94,13 +94,11 @@ __device__ __forceinline__ void load_line(const ConvParams& p, const Walk& w, in
 }
 
 template <typename T, int V>
-struct Raw {
-    T v[V];
-};
+using Raw = RawVec<T, V>;
 template <typename T, int V>
 __device__ __forceinline__ Raw<T, V> load_raw(const T* __restrict__ p) {
     Raw<T, V> r;
-    __builtin_memcpy(&r, p, sizeof(r));
+    load_raw<T, V>(p, V, r);
     return r;
 }
 

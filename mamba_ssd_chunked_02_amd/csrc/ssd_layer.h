@@ -77,6 +77,22 @@ __device__ __forceinline__ void store_vec(T* __restrict__ p, int n, const float 
     }
 }
 
+// The same in two steps: the bits first (a load in flight holds no more than
+// them), their values later.
+template <typename T, int V>
+struct RawVec {
+    T v[V];
+};
+template <typename T, int V>
+__device__ __forceinline__ void load_raw(const T* __restrict__ p, int n, RawVec<T, V>& r) {
+    if (n >= V) {
+        __builtin_memcpy(&r, p, sizeof(r));
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) r.v[j] = j < n ? p[j] : (T)0.f;
+    }
+}
+
 // Sum over the 64 lanes, in every lane.
 __device__ __forceinline__ float wave_sum(float v) { return lane_value(wave_prefix_sum(v), 63); }
 

@@ -57,6 +57,21 @@ __device__ __forceinline__ void row_sums(float& a, float& b, int waves, float (*
     }
 }
 
+// Vector i of a row's thread: V elements from c, of which the first `skip`
+// belong to another vector too (the last one is moved back to end with the row,
+// a thread without elements takes the last vector and skips all of it).  They
+// are left out of the row's sums; what is written for them is the same twice.
+template <int V>
+struct Piece {
+    int c, skip;
+    __device__ __forceinline__ Piece(int i, int lanes, int lane, int width) {
+        const int at = (i * lanes + lane) * V;
+        c = min(at, width - V);
+        skip = min(at - c, V);
+    }
+    __device__ __forceinline__ bool any() const { return skip < V; }
+};
+
 // V elements a load, NV loads a thread.
 template <typename T, int V, int NV>
 __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormParams p, int waves) {
@@ -68,50 +83,55 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormParams p, int waves)
     const int lane = waves == 1 ? threadIdx.x & 63 : threadIdx.x;
     const T* x = (const T*)p.x + row * p.x_row;
     T* y = (T*)p.out + row * p.out_row;
+    RawVec<T, V> raw[NV];
     float v[NV][V];
     float s = 0.f, zero = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * lanes + lane) * V;
-        load_vec<T, V>(x + c, p.width - c, v[i]);
+    for (int i = 0; i < NV; ++i)
+        load_raw<T, V>(x + Piece<V>(i, lanes, lane, p.width).c, V, raw[i]);
 #pragma unroll
-        for (int j = 0; j < V; ++j) s += v[i][j];
+    for (int i = 0; i < NV; ++i) {
+        const Piece<V> q(i, lanes, lane, p.width);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            v[i][j] = (float)raw[i].v[j];
+            s += j >= q.skip ? v[i][j] : 0.f;
+        }
     }
     int turn = 0;
     row_sums(s, zero, waves, ex, turn);
     const float mean = s / (float)p.width;
-    float q = 0.f;
+    float sq = 0.f;
     zero = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * lanes + lane) * V;
+        const Piece<V> q(i, lanes, lane, p.width);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             v[i][j] -= mean;
-            q += c + j < p.width ? v[i][j] * v[i][j] : 0.f;
+            sq += j >= q.skip ? v[i][j] * v[i][j] : 0.f;
         }
     }
-    row_sums(q, zero, waves, ex, turn);
-    const float rstd = 1.f / sqrtf(q / (float)p.width + p.eps);
+    row_sums(sq, zero, waves, ex, turn);
+    const float rstd = 1.f / sqrtf(sq / (float)p.width + p.eps);
     if (lane == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * lanes + lane) * V, n = p.width - c;
-        if (n <= 0) break;
+        const Piece<V> q(i, lanes, lane, p.width);
         float w[V], b[V], o[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             w[j] = 1.f;
             b[j] = 0.f;
         }
-        if (p.weight) load_vec<float, V>(p.weight + c, n, w);
-        if (p.bias) load_vec<float, V>(p.bias + c, n, b);
+        if (p.weight) load_vec<float, V>(p.weight + q.c, V, w);
+        if (p.bias) load_vec<float, V>(p.bias + q.c, V, b);
 #pragma unroll
         for (int j = 0; j < V; ++j) o[j] = v[i][j] * rstd * w[j] + b[j];
-        store_vec<T, V>(y + c, n, o);
+        if (q.any()) store_vec<T, V>(y + q.c, V, o);
     }
 }
 
@@ -127,38 +147,58 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormParams p, int waves)
     float w[NV][V], dw[NV][V], db[NV][V];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * lanes + lane) * V;
+        const Piece<V> q(i, lanes, lane, p.width);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             w[i][j] = 1.f;
             dw[i][j] = db[i][j] = 0.f;
         }
-        if (p.weight) load_vec<float, V>(p.weight + c, p.width - c, w[i]);
+        if (p.weight) load_vec<float, V>(p.weight + q.c, V, w[i]);
     }
     int turn = 0;
     const float inv = 1.f / (float)p.width;
-    for (int64_t row = slot; row < p.rows; row += p.slots) {
+    // the next row is on its way while this one's sums are formed, where the
+    // registers of 16 waves hold both
+    constexpr bool kAhead = V * NV <= 8;
+    RawVec<T, V> xr[NV], gr[NV];
+    float mean_r = 0.f, rstd_r = 0.f;
+    auto fetch = [&](int64_t row) {
         const T* x = (const T*)p.x + row * p.x_row;
         const T* dy = (const T*)p.dy + row * p.dy_row;
-        const float mean = p.mean_in[row], rstd = p.rstd_in[row];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Piece<V> q(i, lanes, lane, p.width);
+            load_raw<T, V>(x + q.c, V, xr[i]);
+            load_raw<T, V>(dy + q.c, V, gr[i]);
+        }
+        mean_r = p.mean_in[row];
+        rstd_r = p.rstd_in[row];
+    };
+    if (kAhead && slot < p.rows) fetch(slot);
+    for (int64_t row = slot; row < p.rows; row += p.slots) {
+        if (!kAhead) fetch(row);
+        const float mean = mean_r, rstd = rstd_r;
         float v[NV][V], g[NV][V];
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * lanes + lane) * V;
-            load_vec<T, V>(x + c, p.width - c, v[i]);
-            load_vec<T, V>(dy + c, p.width - c, g[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                v[i][j] = (v[i][j] - mean) * rstd;  // past the row g is 0: nothing is summed
+                v[i][j] = (float)xr[i].v[j];
+                g[i][j] = (float)gr[i].v[j];
+            }
+        if (kAhead) fetch(row + p.slots < p.rows ? row + p.slots : row);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Piece<V> q(i, lanes, lane, p.width);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                v[i][j] = (v[i][j] - mean) * rstd;
                 dw[i][j] += g[i][j] * v[i][j];
                 db[i][j] += g[i][j];
                 g[i][j] *= w[i][j];
-                s0 += g[i][j];
-                s1 += g[i][j] * v[i][j];
+                s0 += j >= q.skip ? g[i][j] : 0.f;
+                s1 += j >= q.skip ? g[i][j] * v[i][j] : 0.f;
             }
         }
         row_sums(s0, s1, waves, ex, turn);
@@ -167,20 +207,20 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormParams p, int waves)
         T* dx = (T*)p.out + row * p.out_row;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * lanes + lane) * V, n = p.width - c;
+            const Piece<V> q(i, lanes, lane, p.width);
             float o[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) o[j] = rstd * (g[i][j] - s0 - v[i][j] * s1);
-            if (n > 0) store_vec<T, V>(dx + c, n, o);
+            if (q.any()) store_vec<T, V>(dx + q.c, V, o);
         }
     }
     float* pw = p.part + (int64_t)slot * 2 * p.width;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * lanes + lane) * V, n = p.width - c;
-        if (n > 0) {
-            store_vec<float, V>(pw + c, n, dw[i]);
-            store_vec<float, V>(pw + p.width + c, n, db[i]);
+        const Piece<V> q(i, lanes, lane, p.width);
+        if (q.any()) {
+            store_vec<float, V>(pw + q.c, V, dw[i]);
+            store_vec<float, V>(pw + p.width + q.c, V, db[i]);
         }
     }
 }
@@ -224,9 +264,13 @@ __global__ __launch_bounds__(1024) void colsum_kernel(ColSum p) {
 struct NormPlan {
     int waves, nv;
 };
-NormPlan norm_plan(const ssd_norm_dims& d, int most) {
+// Elements a load: 16 bytes, or one where a row is shorter.
+int norm_vec(const ssd_norm_dims& d) {
     const int V = d.dtype == SSD_BF16 ? 8 : 4;
-    const int64_t vecs = cdiv(d.width, V);
+    return d.width >= V ? V : 1;
+}
+NormPlan norm_plan(const ssd_norm_dims& d, int most) {
+    const int64_t vecs = cdiv(d.width, norm_vec(d));
     NormPlan pl;
     const int64_t w = cdiv(vecs, 64 * most);
     pl.waves = (int)w;
@@ -234,15 +278,21 @@ NormPlan norm_plan(const ssd_norm_dims& d, int most) {
     return pl;
 }
 constexpr int kMostFwd = 8;
-// backward: five row vectors a load are live, so 128 registers hold two loads
-// of 8 or four of 4
-inline int most_bwd(const ssd_norm_dims& d) { return d.dtype == SSD_BF16 ? 2 : 4; }
+// backward: one load of 8 or two of 4 elements of x and dy (then the next row is
+// loaded ahead); more where 16 waves do not span the row
+inline int most_bwd(const ssd_norm_dims& d) {
+    const int V = norm_vec(d), least = 8 / V;
+    const int64_t need = cdiv(d.width, (int64_t)V * 64 * kMaxWaves);
+    return need > least ? (int)need : least;
+}
 
 int32_t norm_slots(const ssd_norm_dims& d) {
-    // two workgroups a CU; a walker's share of dw and db is written once, so
-    // more walkers than rows / 4 would write more than they read
+    // Ten waves a CU.  Fewer walkers leave loads unhidden, more only write
+    // more shares (8192 x 2560 bf16, 5 waves: 256 walkers 38 us, 512 to 768
+    // 32, 1024 38; 2400 x 16384 float32, 16 waves: 256 walkers 114, 512 126,
+    // 1024 141); and none takes fewer than four rows.
     const NormPlan pl = norm_plan(d, most_bwd(d));
-    const int64_t most = pl.waves == 1 ? 2048 : (pl.waves <= 4 ? 1024 : 512);
+    const int64_t by_waves = imax(256, 2560 / pl.waves), most = by_waves < 2048 ? by_waves : 2048;
     const int64_t s = imax(1, cdiv(d.rows, 4));
     return (int32_t)(s < most ? s : most);
 }
@@ -263,6 +313,10 @@ void launch_norm(const NormParams& p, NormPlan pl, hipStream_t s) {
     const int64_t walkers = BWD ? p.slots : p.rows;
     const dim3 grid((unsigned)(pl.waves == 1 ? cdiv(walkers, kWavesPerWg) : walkers));
     const dim3 block(pl.waves == 1 ? 64 * kWavesPerWg : 64 * pl.waves);
+    if constexpr (V == 1) {  // rows of fewer elements than a vector: one load
+        if constexpr (BWD) norm_bwd_kernel<T, 1, 1><<<grid, block, 0, s>>>(p, pl.waves);
+        else norm_fwd_kernel<T, 1, 1><<<grid, block, 0, s>>>(p, pl.waves);
+    } else {
 #define SSD_NORM_CASE(NV)                                                       \
     case NV:                                                                    \
         if constexpr (!BWD) norm_fwd_kernel<T, V, NV><<<grid, block, 0, s>>>(p, pl.waves); \
@@ -278,7 +332,18 @@ void launch_norm(const NormParams& p, NormPlan pl, hipStream_t s) {
         SSD_NORM_CASE(7);
         SSD_NORM_CASE(8);
     }
+    }
 #undef SSD_NORM_CASE
+}
+template <bool BWD>
+void launch_norm(const ssd_norm_dims& d, const NormParams& p, NormPlan pl, hipStream_t s) {
+    if (d.dtype == SSD_BF16) {
+        if (norm_vec(d) == 1) launch_norm<bf16, 1, BWD>(p, pl, s);
+        else launch_norm<bf16, 8, BWD>(p, pl, s);
+    } else {
+        if (norm_vec(d) == 1) launch_norm<float, 1, BWD>(p, pl, s);
+        else launch_norm<float, 4, BWD>(p, pl, s);
+    }
 }
 
 }  // namespace
@@ -318,8 +383,7 @@ int ssd_norm_fwd(const ssd_norm_dims* dims, const void* x, const float* weight, 
     p.width = dims->width;
     p.eps = dims->eps;
     const NormPlan pl = norm_plan(*dims, kMostFwd);
-    if (dims->dtype == SSD_BF16) launch_norm<bf16, 8, false>(p, pl, (hipStream_t)stream);
-    else launch_norm<float, 4, false>(p, pl, (hipStream_t)stream);
+    launch_norm<false>(*dims, p, pl, (hipStream_t)stream);
     return launched();
 }
 
@@ -356,8 +420,7 @@ int ssd_norm_bwd(const ssd_norm_dims* dims, const void* x, const float* weight, 
     p.width = dims->width;
     p.slots = norm_slots(*dims);  // with no rows one walker, which writes zeros
     const NormPlan pl = norm_plan(*dims, most_bwd(*dims));
-    if (dims->dtype == SSD_BF16) launch_norm<bf16, 8, true>(p, pl, (hipStream_t)stream);
-    else launch_norm<float, 4, true>(p, pl, (hipStream_t)stream);
+    launch_norm<true>(*dims, p, pl, (hipStream_t)stream);
     const int rc = launched();
     if (rc != SSD_OK || (!dweight && !dbias)) return rc;
     ColSum c = {};
