@@ -7,6 +7,7 @@ workspaces are allocated with torch.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -43,6 +44,13 @@ class SsdSelscanLayout(ctypes.Structure):
     """Mirror of ``ssd_selscan_layout`` (element strides)."""
     _fields_ = [(n, _I64) for n in ("x_token", "d_raw_token", "z_token", "B_token", "B_group",
                                     "C_token", "C_group", "y_token", "dy_token")]
+
+
+@functools.lru_cache(maxsize=1024)
+def _struct(cls, *fields):
+    """The struct of these sizes; the library only reads it, so calls of the same
+    sizes share one."""
+    return cls(*fields)
 
 
 def _pointer(struct):
@@ -272,7 +280,7 @@ def ssd_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None):
             raise ValueError("y must have x's shape")
         ys = _matrix(y, "y", width)[1]
     mean, rstd = torch.empty((2,) + x.shape[:-1], dtype=torch.float32, device=x.device).unbind(0)
-    dims = SsdNormDims(rows, xs, ys, width, width, code, eps, 0)
+    dims = _struct(SsdNormDims, rows, xs, ys, width, width, code, eps, 0)
     _launch("ssd_norm_fwd", x, dims, _at(x), _at(weight), _at(bias), _at(y), _at(mean), _at(rstd))
     return y, mean, rstd
 
@@ -291,7 +299,7 @@ def ssd_norm_bwd(x, weight, mean, rstd, dy, workspace=None):
     rows, xs = _matrix(x, "x", width)
     dx = _like(x)
     dweight, dbias = torch.empty((2, width), dtype=torch.float32, device=x.device).unbind(0)
-    dims = SsdNormDims(rows, xs, width, _matrix(dy, "dy", width)[1], width, code, 0.0, 0)
+    dims = _struct(SsdNormDims, rows, xs, width, _matrix(dy, "dy", width)[1], width, code, 0.0, 0)
     if workspace is None:
         workspace = _workspace("ssd_norm_bwd_workspace_bytes", dims, x)
     _launch("ssd_norm_bwd", x, dims, _at(x), _at(weight), _at(mean), _at(rstd), _at(dy), _at(dx),
@@ -340,8 +348,8 @@ def ssd_conv_fwd(x, weight, bias=None, init_state=None, cu_seqlens=None, y=None,
         _same(x, (final_state, "final_state"))
         if final_state.shape != (S, W - 1, E) or not final_state.is_contiguous():
             raise ValueError(f"final_state must be contiguous [{S}, {W - 1}, {E}]")
-    dims = SsdConvDims(b, L, E, W, 0 if cu is None else S, code)
-    _launch("ssd_conv_fwd", x, dims, SsdConvLayout(xs, ys, E), _at(x), _at(weight), _at(bias),
+    dims = _struct(SsdConvDims, b, L, E, W, 0 if cu is None else S, code)
+    _launch("ssd_conv_fwd", x, dims, _struct(SsdConvLayout, xs, ys, E), _at(x), _at(weight), _at(bias),
             _at(init_state), _at(cu), _at(y), _at(final_state))
     return y, final_state
 
@@ -357,11 +365,11 @@ def ssd_conv_bwd(x, weight, bias, dy, init_state=None, cu_seqlens=None, d_final=
     _same(x, (dy, "dy"), (d_final, "d_final"))
     if d_final is not None and (d_final.shape != (S, W - 1, E) or not d_final.is_contiguous()):
         raise ValueError(f"d_final must be contiguous [{S}, {W - 1}, {E}]")
-    lay = SsdConvLayout(_tokens(x, "x", x.shape), E, _tokens(dy, "dy", x.shape))
+    lay = _struct(SsdConvLayout, _tokens(x, "x", x.shape), E, _tokens(dy, "dy", x.shape))
     dx = _like(x)
     sums = torch.empty((W + 1, E), dtype=torch.float32, device=x.device)
     dinit = torch.empty((S, W - 1, E), dtype=x.dtype, device=x.device)
-    dims = SsdConvDims(b, L, E, W, 0 if cu is None else S, code)
+    dims = _struct(SsdConvDims, b, L, E, W, 0 if cu is None else S, code)
     if workspace is None:
         workspace = _workspace("ssd_conv_bwd_workspace_bytes", dims, x)
     dweight, dbias = sums[:W], sums[W]
@@ -385,29 +393,30 @@ def ssd_conv_step(x, state, weight, bias=None, slots=None, new_state=None, y=Non
     else:
         _same(x, (y, "y"))
         ys = _rows(y, "y", x.shape)
-    dims = SsdConvDims(x.shape[0], 1, E, W, 0, code)
-    _launch("ssd_conv_step", x, dims, SsdConvLayout(xs, ys, E), _at(x), _at(weight), _at(bias),
+    dims = _struct(SsdConvDims, x.shape[0], 1, E, W, 0, code)
+    _launch("ssd_conv_step", x, dims, _struct(SsdConvLayout, xs, ys, E), _at(x), _at(weight), _at(bias),
             _at(state), _at(slots), state.shape[0], _at(y), _at(new_state))
     return y
 
 
 # ---- selective scan ------------------------------------------------------------------------
 
-def _selscan_arguments(x, d_raw, d_init, A, B, C, D, z, cu_seqlens):
+def _selscan_arguments(x, d_raw, d_init, A, B, C, D, z, cu_seqlens, y, dy):
     if x.dim() != 3 or A.dim() != 2 or B.dim() != 4:
         raise ValueError("x [b, L, E], A [N, E] and B, C [b, L, G, N] expected")
     b, L, E = x.shape
     N, G = A.shape[0], B.shape[2]
     code = _dtype_of(x, "x")
-    _same(x, (d_raw, "d_raw"), (B, "B"), (C, "C"), (z, "z"))
+    _same(x, (d_raw, "d_raw"), (B, "B"), (C, "C"), (z, "z"), (y, "y"), (dy, "dy"))
     _floats(x, (d_init, (E,), "d_init"), (A, (N, E), "A"), (D, (E,), "D"))
     cu, S = _sequences(x, cu_seqlens, b)
     shape = (b, L, G, N)
-    lay = SsdSelscanLayout(
-        _tokens(x, "x", x.shape), _tokens(d_raw, "d_raw", x.shape),
+    lay = _struct(
+        SsdSelscanLayout, _tokens(x, "x", x.shape), _tokens(d_raw, "d_raw", x.shape),
         E if z is None else _tokens(z, "z", x.shape), *_groups(B, "B", shape),
-        *_groups(C, "C", shape), E, E)
-    dims = SsdSelscanDims(b, L, E, N, G, 0 if cu is None else S, code, 0)
+        *_groups(C, "C", shape), E if y is None else _tokens(y, "y", x.shape),
+        E if dy is None else _tokens(dy, "dy", x.shape))
+    dims = _struct(SsdSelscanDims, b, L, E, N, G, 0 if cu is None else S, code, 0)
     return dims, lay, cu, (S, N, E)
 
 
@@ -423,13 +432,10 @@ def ssd_selscan_fwd(x, d_raw, d_init, A, B, C, D=None, z=None, init_state=None, 
     [nseq + 1] (b must be 1) or None.  ``y`` may be preallocated; ``final_state``:
     True, False or a [S, N, E] fp32 tensor to fill.  Returns (y, final_state or
     None)."""
-    dims, lay, cu, state = _selscan_arguments(x, d_raw, d_init, A, B, C, D, z, cu_seqlens)
+    dims, lay, cu, state = _selscan_arguments(x, d_raw, d_init, A, B, C, D, z, cu_seqlens, y, None)
     _floats(x, (init_state, state, "init_state"))
     if y is None:
         y = x.new_empty(x.shape)
-    else:
-        _same(x, (y, "y"))
-        lay.y_token = _tokens(y, "y", x.shape)
     if final_state is True:
         final_state = torch.empty(state, dtype=torch.float32, device=x.device)
     elif final_state is False:
@@ -453,10 +459,8 @@ def ssd_selscan_bwd(x, d_raw, d_init, A, B, C, dy, D=None, z=None, init_state=No
     dD [E] (the gradient at zeros without a D) and dinit_state [S, N, E] (at
     zeros without an init_state).  ``d_final`` is the gradient of final_state or
     None for zeros."""
-    dims, lay, cu, state = _selscan_arguments(x, d_raw, d_init, A, B, C, D, z, cu_seqlens)
+    dims, lay, cu, state = _selscan_arguments(x, d_raw, d_init, A, B, C, D, z, cu_seqlens, None, dy)
     _floats(x, (init_state, state, "init_state"), (d_final, state, "d_final"))
-    _same(x, (dy, "dy"))
-    lay.dy_token = _tokens(dy, "dy", x.shape)
     N, E = A.shape
     g = {"dx": _like(x), "dd_raw": _like(d_raw), "dB": _like(B), "dC": _like(C)}
     if z is not None:
@@ -492,11 +496,11 @@ def ssd_selscan_step(x, d_raw, d_init, A, B, C, state, D=None, z=None, slots=Non
     else:
         _same(x, (y, "y"))
         ys = _rows(y, "y", x.shape)
-    lay = SsdSelscanLayout(
-        _rows(x, "x", x.shape), _rows(d_raw, "d_raw", x.shape),
+    lay = _struct(
+        SsdSelscanLayout, _rows(x, "x", x.shape), _rows(d_raw, "d_raw", x.shape),
         E if z is None else _rows(z, "z", x.shape), *_heads(B, "B", (b, G, N)),
         *_heads(C, "C", (b, G, N)), ys, E)
-    dims = SsdSelscanDims(b, 1, E, N, G, 0, code, 0)
+    dims = _struct(SsdSelscanDims, b, 1, E, N, G, 0, code, 0)
     _launch("ssd_selscan_step", x, dims, lay, _at(x), _at(d_raw), _at(d_init), _at(A), _at(B),
             _at(C), _at(D), _at(z), _at(state), _at(slots), state.shape[0], _at(y),
             _at(new_state))
@@ -523,9 +527,9 @@ def ssd_step(x, d_raw, d_init, B, C, state, slots=None, new_state=None, y=None):
         y = x.new_empty((b, H, P))
     else:
         _same(x, (y, "y"))
-    lay = SsdLayout(*_heads(x, "x", x.shape), *d_raw.stride(), *_heads(B, "B", (b, G, N)),
+    lay = _struct(SsdLayout, *_heads(x, "x", x.shape), *d_raw.stride(), *_heads(B, "B", (b, G, N)),
                     *_heads(C, "C", (b, G, N)), *_heads(y, "y", x.shape))
-    dims = SsdDims(b, 1, H, P, N, G, 64, 0, code)
+    dims = _struct(SsdDims, b, 1, H, P, N, G, 64, 0, code)
     _launch("ssd_step", x, dims, lay, _at(x), _at(d_raw), float(d_init), _at(B), _at(C),
             _at(state), _at(slots), state.shape[0], _at(y), _at(new_state))
     return y

@@ -278,7 +278,16 @@ SCAN = [  # b, L, E, N, G, cu
     # long with few channels: cut into spans
     (1, 2600, 20, 16, 1, None), (2, 1500, 9, 8, 1, None), (1, 700, 6, 40, 1, None),
     (1, 900, 34, 32, 2, None), (1, 2300, 18, 16, 1, [0, 0, 700, 701, 2300, 2300]),
+    # the fewest waves a workgroup: few tokens, many sequences
+    (2, 7, 10, 33, 1, None), (2, 9, 10, 20, 1, None), (2, 20, 10, 16, 1, None),
+    (1, 1300, 8, 16, 1, list(range(0, 900)) + [1000, 1040, 1300] + [1300] * 200),
+    # many channels: workgroups of half and a quarter of the waves
+    (1, 100, 8320, 16, 1, None), (1, 70, 16480, 16, 1, None),
     (1, 0, 8, 16, 1, [0, 0, 0]), (2, 0, 8, 16, 1, None)]
+
+
+def scan_id(case):
+    return str(case if case[5] is None or len(case[5]) < 20 else case[:5] + ("many",))
 
 
 def scan_problem(dtype, case, gated=True, carry=True, seed=0):
@@ -302,7 +311,7 @@ def scan_call(p, cu, view=up):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("gated,carry", [(True, True), (False, False)])
-@pytest.mark.parametrize("case", SCAN, ids=str)
+@pytest.mark.parametrize("case", SCAN, ids=scan_id)
 def test_selscan(dtype, gated, carry, case):
     p, (dy, df), cu = scan_problem(dtype, case, gated, carry)
     b, L, E, N, G, _ = case
