@@ -49,10 +49,14 @@ struct SelParams {
     const float* d_final;
     const int32_t* cu;
     float* final_state;  // or dinit_state
-    float* span_h;       // spans' states from zero [slots][blocks][64][NR]
-    float* span_q;       // backward: what their tokens pass on to the span before
+    float* span_h;       // forward: spans' states from zero [slots][blocks][64][NR]
     float* span_d;       // their sums of d [slots][blocks][64]
-    float* chunk_states; // backward: states entering the chunks [segments][waves][blocks][64][NR]
+    float* run_h;        // backward: runs' states from zero, then entering them
+    float* run_q;        // q before them from zero, then q entering from behind
+                         // [runs][blocks][64][NR]
+    float* run_d;        // their sums of d [runs][blocks][64]
+    float* chunk_h;      // h before a run's chunks, from zero [chunks][blocks][64][NR]
+    float* chunk_d;      // the sum of d there [chunks][blocks][64]
     float* part_w;       // backward: [slots][(N + 2) E] shares of dA, dD, dd_init
     float* part_bc;      // backward: [blocks][T][2 NP] shares of dB, dC
     int64_t xs, ds, zs, bs_t, bs_g, cs_t, cs_g, ys, gs;
@@ -66,10 +70,10 @@ struct SelParams {
     int32_t per;    // without cu_seqlens: spans of a sequence
 };
 
-// The launches of the backward scan (its own translation unit): waves of a
-// workgroup, and with p.span the spans' states first.
-int launch_selscan_bwd(const SelParams& p, int32_t dtype, int NR, int waves, unsigned grid,
-                       hipStream_t s);
+// The launches of the backward scan up to the sums over channel blocks and
+// sequences (its own translation unit): waves of a workgroup, runs of a sequence.
+int launch_selscan_bwd(const SelParams& p, int32_t dtype, int NR, int waves, int64_t runs,
+                       unsigned grid, hipStream_t s);
 
 namespace {
 
@@ -93,10 +97,11 @@ struct Shape {
     static constexpr int NP = 4 * NR;           // state entries held
     static constexpr int kFwdTokens = 64 / NR;  // of a wave's chunk
     static constexpr int kFwdWaves = NR <= 4 ? 16 : 8;  // of a workgroup, at most
-    static constexpr int kBwdTokens = NR == 2 ? 16 : 64 / NR;
-    static constexpr int kBwdWaves = NR <= 8 ? 8 : 4;
-    // workgroups of fewer waves keep the registers of as many waves a SIMD
-    static constexpr int kFwdPerSimd = kFwdWaves / 4, kBwdPerSimd = kBwdWaves / 4;
+    static constexpr int kFwdPerSimd = kFwdWaves / 4;  // smaller workgroups as many
+    static constexpr int kBwdTokens = NR == 2 ? 16 : NR == 4 ? 8 : 4;
+    static constexpr int kRunTokens = 64;              // backward: of a wave
+    static constexpr int kBwdWaves = 4;
+    static constexpr int kBwdPerSimd = NR <= 4 ? 3 : NR == 8 ? 2 : 1;
 };
 
 // Bounds what the scheduler moves together, so that the unrolled token loops
@@ -390,135 +395,21 @@ __device__ __forceinline__ void store_state(float* dst, const SelParams& p, cons
     }
 }
 
-// h = P h + (state of the span), over n spans of the sequence from span `from`
-// on (by = 1) or back (by = -1); P = exp of the span's sum of d times A.
+// h through the n spans of the sequence before this one: h = P h + (state of the
+// span from zero), P = exp of the span's sum of d times A.
 template <int NR>
-__device__ __forceinline__ void fold_spans(const float* states, const SelParams& p, const Place& o,
-                                           const float (&A2)[NR], int from, int n, int by,
+__device__ __forceinline__ void fold_spans(const SelParams& p, const Place& o, const float (&A2)[NR],
                                            float (&h)[NR]) {
-    const int64_t step = (int64_t)p.nblk * 64 * by;
-    int64_t at = ((int64_t)(o.slot - o.k + from) * p.nblk + o.blk) * 64 + o.lane;
+    int64_t at = ((int64_t)(o.slot - o.k) * p.nblk + o.blk) * 64 + o.lane;
 #pragma unroll 4
-    for (int j = 0; j < n; ++j, at += step) {
+    for (int j = 0; j < o.k; ++j, at += (int64_t)p.nblk * 64) {
         const float d = p.span_d[at];
         float v[NR];
-        __builtin_memcpy(v, states + at * NR, sizeof(v));
+        __builtin_memcpy(v, p.span_h + at * NR, sizeof(v));
 #pragma unroll
         for (int r = 0; r < NR; ++r) h[r] = fexp2(d * A2[r]) * h[r] + v[r];
     }
 }
-
-// ---- what a span does to a state ------------------------------------------------------------
-
-// The wave takes a run of the span's chunks and keeps its state (and, for the
-// backward pass, Q and P: q before = P q behind + Q) in registers; the waves'
-// are joined once at the end.
-template <typename T, int NR, bool BWD>
-__global__ __launch_bounds__(512) void selscan_span_kernel(SelParams p) {
-    using S = Shape<NR>;
-    constexpr int TW = S::kBwdTokens, NP = S::NP, MW = 8, Q = TW / 4;
-    __shared__ __align__(16) float bc[MW][TW][2][NP];
-    __shared__ __align__(16) float exD[MW][64], exH[MW][64][NR], exQ[BWD ? MW : 1][64][NR];
-    Place o;
-    if (!place_of(p, o) || o.k >= o.nspan) return;
-    // nothing comes after a sequence's last span, and nothing before its first
-    if (!BWD && o.k == o.nspan - 1) return;
-    float A2[NR], h[NR], q[NR];
-    load_rates<NR>(p, o, A2);
-    const float dinit = o.live ? p.d_init[o.ch] : 0.f;
-    const bool gated = p.z != nullptr;
-    const int chunks = (o.last - o.first + TW - 1) / TW, run = (chunks + MW - 1) / MW;
-    const int c0 = min(o.wave * run, chunks), c1 = min(c0 + run, chunks);
-    float sum = 0.f;
-#pragma unroll
-    for (int r = 0; r < NR; ++r) h[r] = q[r] = 0.f;
-    uint32_t xr[Q], dr[Q], gr[Q], zr[Q];
-    Rows<T, NR, TW> Br, Cr;
-    auto fetch = [&](int t) {
-        const ArgPtr k = fresh_args();
-        load_tokens<T, TW>(k->x, k->xs, o, t, xr);
-        load_tokens<T, TW>(k->d_raw, k->ds, o, t, dr);
-        load_rows<T, NR, TW>(k->B, k->bs_t, k->bs_g, k->N, o, t, Br);
-        if constexpr (BWD) {
-            load_tokens<T, TW>(k->dy, k->gs, o, t, gr);
-            load_tokens<T, TW>(k->z, k->zs, o, t, zr);
-            load_rows<T, NR, TW>(k->C, k->cs_t, k->cs_g, k->N, o, t, Cr);
-        }
-    };
-    int tb = o.first + c0 * TW;
-    if (c0 < c1) fetch(tb);
-    for (int c = c0; c < c1; ++c, tb += TW) {
-        const int have = min(o.last - tb, TW);
-        float d[Q], u[Q], w[Q], chunk_d = 0.f;
-#pragma unroll
-        for (int i = 0; i < Q; ++i) {
-            d[i] = step_of(value_of<T>(dr[i]) + dinit, 4 * i + o.nl < have);
-            u[i] = d[i] * value_of<T>(xr[i]);
-            chunk_d += d[i];
-            if constexpr (BWD) {
-                const float zf = value_of<T>(zr[i]);
-                w[i] = value_of<T>(gr[i]) * (gated ? zf * sigmoid(zf) : 1.f);
-            }
-        }
-        wave_lds_fence();
-        put_rows<T, NR, TW>(&bc[o.wave][0][0][0], o, Br);
-        if constexpr (BWD) put_rows<T, NR, TW>(&bc[o.wave][0][1][0], o, Cr);
-        wave_lds_fence();
-        if (c + 1 < c1) fetch(tb + TW);
-        float a[BWD ? TW : 1][NR];
-#pragma unroll
-        for (int t = 0; t < TW; ++t) {
-            float b[NR];
-            lds_get<NR>(&bc[o.wave][t][0][o.nl * NR], b);
-            const float dt = quad_lane(d[t / 4], t % 4), ut = quad_lane(u[t / 4], t % 4);
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                const float at = fexp2(dt * A2[r]);
-                h[r] = at * h[r] + b[r] * ut;
-                if constexpr (BWD) a[t][r] = at;
-            }
-            if (t & 1) keep_order();
-        }
-        if constexpr (BWD) {
-            float ql[NR];
-#pragma unroll
-            for (int t = TW - 1; t >= 0; --t) {
-                float cc[NR];
-                lds_get<NR>(&bc[o.wave][t][1][o.nl * NR], cc);
-                const float wt = quad_lane(w[t / 4], t % 4);
-#pragma unroll
-                for (int r = 0; r < NR; ++r)
-                    ql[r] = t < TW - 1 ? a[t][r] * (cc[r] * wt + ql[r]) : a[t][r] * (cc[r] * wt);
-                if (!(t & 1)) keep_order();
-            }
-#pragma unroll
-            for (int r = 0; r < NR; ++r) q[r] += fexp2(sum * A2[r]) * ql[r];
-        }
-        sum += quad_total(chunk_d);
-    }
-    exD[o.wave][o.lane] = sum;
-    lds_put<NR>(exH[o.wave][o.lane], h);
-    if constexpr (BWD) lds_put<NR>(exQ[o.wave][o.lane], q);
-    __syncthreads();
-    if (o.wave) return;
-    for (int j = 1; j < MW; ++j) {
-        const float dj = exD[j][o.lane];
-        float hj[NR], qj[NR];
-        lds_get<NR>(exH[j][o.lane], hj);
-        if constexpr (BWD) lds_get<NR>(exQ[j][o.lane], qj);
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            h[r] = fexp2(dj * A2[r]) * h[r] + hj[r];
-            if constexpr (BWD) q[r] += fexp2(sum * A2[r]) * qj[r];
-        }
-        sum += dj;
-    }
-    const int64_t at = ((int64_t)o.slot * p.nblk + o.blk) * 64 + o.lane;
-    p.span_d[at] = sum;
-    __builtin_memcpy(p.span_h + at * NR, h, sizeof(h));
-    if constexpr (BWD) __builtin_memcpy(p.span_q + at * NR, q, sizeof(q));
-}
-
 
 }  // namespace
 }  // namespace ssd

@@ -5,6 +5,80 @@
 namespace ssd {
 namespace {
 
+// ---- what a span does to a state ------------------------------------------------------------
+
+// The wave takes a run of the span's chunks and keeps its state in registers;
+// the waves' are joined once at the end.
+template <typename T, int NR>
+__global__ __launch_bounds__(512) void selscan_span_kernel(SelParams p) {
+    using S = Shape<NR>;
+    constexpr int TW = S::kFwdTokens, NP = S::NP, MW = 8, Q = TW / 4;
+    __shared__ __align__(16) float bc[MW][TW][2][NP];
+    __shared__ __align__(16) float exD[MW][64], exH[MW][64][NR];
+    Place o;
+    if (!place_of(p, o) || o.k >= o.nspan) return;
+    if (o.k == o.nspan - 1) return;  // nothing comes after it
+    float A2[NR], h[NR];
+    load_rates<NR>(p, o, A2);
+    const float dinit = o.live ? p.d_init[o.ch] : 0.f;
+    const int chunks = (o.last - o.first + TW - 1) / TW, run = (chunks + MW - 1) / MW;
+    const int c0 = min(o.wave * run, chunks), c1 = min(c0 + run, chunks);
+    float sum = 0.f;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) h[r] = 0.f;
+    uint32_t xr[Q], dr[Q];
+    Rows<T, NR, TW> Br;
+    auto fetch = [&](int t) {
+        const ArgPtr k = fresh_args();
+        load_tokens<T, TW>(k->x, k->xs, o, t, xr);
+        load_tokens<T, TW>(k->d_raw, k->ds, o, t, dr);
+        load_rows<T, NR, TW>(k->B, k->bs_t, k->bs_g, k->N, o, t, Br);
+    };
+    int tb = o.first + c0 * TW;
+    if (c0 < c1) fetch(tb);
+    for (int c = c0; c < c1; ++c, tb += TW) {
+        const int have = min(o.last - tb, TW);
+        float d[Q], u[Q];
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            d[i] = step_of(value_of<T>(dr[i]) + dinit, 4 * i + o.nl < have);
+            u[i] = d[i] * value_of<T>(xr[i]);
+            sum += d[i];  // the lane's; the quad's at the end
+        }
+        wave_lds_fence();
+        put_rows<T, NR, TW>(&bc[o.wave][0][0][0], o, Br);
+        wave_lds_fence();
+        if (c + 1 < c1) fetch(tb + TW);
+#pragma unroll
+        for (int t = 0; t < TW; ++t) {
+            float b[NR];
+            lds_get<NR>(&bc[o.wave][t][0][o.nl * NR], b);
+            const float dt = quad_lane(d[t / 4], t % 4), ut = quad_lane(u[t / 4], t % 4);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                h[r] = fexp2(dt * A2[r]) * h[r] + b[r] * ut;
+            }
+            if (t & 1) keep_order();
+        }
+    }
+    sum = quad_total(sum);
+    exD[o.wave][o.lane] = sum;
+    lds_put<NR>(exH[o.wave][o.lane], h);
+    __syncthreads();
+    if (o.wave) return;
+    for (int j = 1; j < MW; ++j) {
+        const float dj = exD[j][o.lane];
+        float hj[NR];
+        lds_get<NR>(exH[j][o.lane], hj);
+#pragma unroll
+        for (int r = 0; r < NR; ++r) h[r] = fexp2(dj * A2[r]) * h[r] + hj[r];
+        sum += dj;
+    }
+    const int64_t at = ((int64_t)o.slot * p.nblk + o.blk) * 64 + o.lane;
+    p.span_d[at] = sum;
+    __builtin_memcpy(p.span_h + at * NR, h, sizeof(h));
+}
+
 // ---- forward ------------------------------------------------------------------------------
 
 template <typename T, int NR, int MW>
@@ -27,7 +101,7 @@ __global__ __launch_bounds__(64 * MW, Shape<NR>::kFwdPerSimd) void selscan_fwd_k
     if (o.k >= o.nspan) return;
     if (o.wave == 0) {
         load_state<NR>(p.init, p, o, h);
-        if (p.span) fold_spans<NR>(p.span_h, p, o, A2, 0, o.k, 1, h);
+        if (p.span) fold_spans<NR>(p, o, A2, h);
         lds_put<NR>(enter[0][o.lane], h);
         if (o.first >= o.last) store_state<NR>(p.final_state, p, o, h);
     }
@@ -181,9 +255,10 @@ int sel_check(const ssd_selscan_dims* d) {
 struct SelPlan {
     int32_t NR, S, bpg, nblk, upr;
     int32_t waves;      // of a workgroup
+    int64_t runs;       // backward: of a sequence
     int32_t span, per;  // tokens of a span (0: sequences are not cut), spans a sequence
     int64_t slots, units, grid, T;
-    size_t off_h, off_q, off_d, off_seg, off_w, off_bc, total;
+    size_t off_h, off_q, off_d, off_ch, off_cd, off_w, off_bc, total;
 };
 
 template <typename F>
@@ -194,30 +269,25 @@ auto with_shape(int NR, F f) {
     return f(Shape<16>{});
 }
 
-// Waves of a workgroup.  One workgroup of all the waves that a CU holds scans a
-// channel block's tokens the widest; where there are enough workgroups, smaller
-// ones do better, because several share a CU without waiting for each other and
-// because fewer waves stand idle in a sequence's last segment.  Measured with 16
-// states (us at 16 / 8 / 4 / 2 waves forward; 8 / 4 / 2 backward):
-//   192 workgroups, 2048 tokens:       51 / 60 / 89 / 177;   196 / 272 / 496
-//   576 workgroups, 2048 tokens:      156 / 151 / 157 / 223; 569 / 587 / 679
+// Waves of a forward workgroup.  One workgroup of all the waves that a CU holds
+// scans a channel block's tokens the widest; where there are enough workgroups,
+// smaller ones do better, because several share a CU without waiting for each
+// other and because fewer waves stand idle in a sequence's last segment.
+// Measured with 16 states (us at 16 / 8 / 4 / 2 waves):
+//   192 workgroups, 2048 tokens:        51 / 60 / 89 / 177
+//   576 workgroups, 2048 tokens:       156 / 151 / 157 / 223
 //   1536 workgroups, 256..8192 tokens: 640 / 576 / 550 / 687
-//   1536 workgroups, 2048 tokens:                            1221 / 1157 / 1414
-//   24576 workgroups, 20 tokens:      479 / 248 / 137 / 86;  1027 / 495 / 270
-int32_t waves_for(int NR, bool bwd, int64_t workgroups, int64_t chunks) {
-    const int32_t full = with_shape(NR, [bwd](auto s) { return bwd ? s.kBwdWaves : s.kFwdWaves; });
+//   24576 workgroups, 20 tokens:       479 / 248 / 137 / 86
+int32_t forward_waves(int NR, int64_t workgroups, int64_t chunks) {
+    const int32_t full = with_shape(NR, [](auto s) { return s.kFwdWaves; });
     if (NR != 4) return workgroups >= 1024 || chunks <= full / 4 ? full / 4 : full;
-    int32_t w = full;
-    if (bwd) {
-        if (workgroups >= 1024) w = 4;
-    } else if (workgroups >= 512) {
-        w = workgroups >= 1024 ? 4 : 8;
-    }
+    int32_t w = workgroups >= 1024 ? 4 : workgroups >= 512 ? 8 : 16;
     while (w > 2 && w / 2 >= chunks) w /= 2;
     return w;
 }
 
 int sel_plan(const ssd_selscan_dims& d, bool bwd, SelPlan* pl) {
+    *pl = {};
     pl->NR = entries_per_lane(d.d_state);
     pl->T = (int64_t)d.batch * d.seqlen;
     pl->S = d.nseq > 0 ? d.nseq : d.batch;
@@ -225,51 +295,61 @@ int sel_plan(const ssd_selscan_dims& d, bool bwd, SelPlan* pl) {
     const int64_t nblk = (int64_t)pl->bpg * d.ngroups;
     pl->nblk = (int32_t)nblk;
     pl->upr = (int32_t)cdiv(nblk, kRun);
-    const int64_t len = pl->S ? cdiv(pl->T, pl->S) : 0;
-    const int64_t whole = (int64_t)pl->S * nblk;
-    const int64_t tokens = with_shape(pl->NR, [bwd](auto s) { return bwd ? s.kBwdTokens : s.kFwdTokens; });
-    pl->waves = waves_for(pl->NR, bwd, whole, cdiv(len, tokens));
-    const int64_t waves = pl->waves, seg = waves * tokens;
-    // Cut sequences into spans where that shortens the longest chain of
-    // segments on a CU by more than the second launch costs.  A segment's cost
-    // is 1; with spans its tokens are walked once more for the spans' states
-    // (kAgain of a segment).  Packed sequences are taken as equally long.
-    const double kAgain = bwd ? 0.35 : 0.6, kLaunch = 1.5, kFold = 0.05;
-    const int64_t nseg = cdiv(len, seg);
-    double best = (double)cdiv(whole, 256) * nseg;
-    int64_t best_segs = 0;
-    for (int64_t k = 2; k <= 64 && k <= nseg; ++k) {
-        const int64_t segs = cdiv(nseg, k), kk = cdiv(nseg, segs);
-        const double cost = (double)cdiv(whole * kk, 256) * segs * (1 + kAgain) + kLaunch + kFold * kk;
-        if (cost < best) {
-            best = cost;
-            best_segs = segs;
+    // packed sequences are taken as equally long
+    const int64_t len = cdiv(pl->T, pl->S), whole = (int64_t)pl->S * nblk;
+    if (bwd) {
+        // sequences of one run take workgroups of one wave: the others would stand
+        // idle and hold their registers
+        const int64_t tokens = with_shape(pl->NR, [](auto s) { return s.kRunTokens; });
+        pl->waves = len > tokens ? with_shape(pl->NR, [](auto s) { return s.kBwdWaves; }) : 1;
+        pl->runs = cdiv(len, tokens);
+        pl->span = (int32_t)(pl->waves * tokens);
+        pl->per = (int32_t)imax(1, cdiv(d.seqlen, pl->span));
+    } else {
+        const int64_t tokens = with_shape(pl->NR, [](auto s) { return s.kFwdTokens; });
+        pl->waves = forward_waves(pl->NR, whole, cdiv(len, tokens));
+        // Cut sequences into spans where that shortens the longest chain of
+        // segments on a CU by more than the second launch costs.  A segment's
+        // cost is 1; with spans its tokens are walked once more for the spans'
+        // states (0.6 of a segment).
+        const int64_t seg = pl->waves * tokens, nseg = cdiv(len, seg);
+        double best = (double)cdiv(whole, 256) * nseg;
+        int64_t segs = 0;
+        for (int64_t k = 2; k <= 64 && k <= nseg; ++k) {
+            const int64_t each = cdiv(nseg, k), spans = cdiv(nseg, each);
+            const double cost = (double)cdiv(whole * spans, 256) * each * 1.6 + 1.5 + 0.05 * spans;
+            if (cost < best) {
+                best = cost;
+                segs = each;
+            }
         }
+        pl->span = (int32_t)(segs * seg);
+        pl->per = segs ? (int32_t)cdiv(nseg, segs) : 1;
     }
-    pl->span = (int32_t)(best_segs * seg);
-    pl->per = best_segs ? (int32_t)cdiv(nseg, best_segs) : 1;
     pl->slots = d.nseq > 0 && pl->span ? pl->T / pl->span + pl->S : (int64_t)pl->S * pl->per;
     pl->units = pl->slots * pl->upr;
     pl->grid = cdiv(pl->units, kXcds) * kXcds * kRun;
-    if (pl->grid > INT32_MAX) return SSD_ERR_SHAPE;
+    if (pl->grid > INT32_MAX || whole > INT32_MAX) return SSD_ERR_SHAPE;
     size_t off = 0;
-    pl->off_h = pl->off_q = pl->off_d = 0;
-    if (pl->span) {
-        const size_t states = (size_t)pl->slots * nblk * 64 * pl->NR * sizeof(float);
-        pl->off_h = off;
-        off = up256(off + states);
-        pl->off_d = off;
-        off = up256(off + (size_t)pl->slots * nblk * 64 * sizeof(float));
-        pl->off_q = off;
-        if (bwd) off = up256(off + states);
-    }
-    pl->off_seg = pl->off_w = pl->off_bc = off;
+    const auto take = [&off](int64_t floats) {
+        const size_t at = off;
+        off = up256(off + (size_t)floats * sizeof(float));
+        return at;
+    };
+    const int64_t lanes = nblk * 64;
     if (bwd) {
-        off = up256(off + (size_t)(pl->T / seg + pl->S + 1) * waves * nblk * 64 * pl->NR * sizeof(float));
-        pl->off_w = off;
-        off = up256(off + (size_t)pl->slots * (d.d_state + 2) * d.channels * sizeof(float));
-        pl->off_bc = off;
-        off = up256(off + (size_t)nblk * pl->T * 8 * pl->NR * sizeof(float));
+        const int64_t runs = pl->slots * pl->waves;
+        const int64_t chunks = pl->T / with_shape(pl->NR, [](auto s) { return s.kBwdTokens; }) + runs;
+        pl->off_h = take(runs * lanes * pl->NR);
+        pl->off_q = take(runs * lanes * pl->NR);
+        pl->off_d = take(runs * lanes);
+        pl->off_ch = take(chunks * lanes * pl->NR);
+        pl->off_cd = take(chunks * lanes);
+        pl->off_w = take(pl->slots * (d.d_state + 2) * d.channels);
+        pl->off_bc = take(nblk * pl->T * 8 * pl->NR);
+    } else if (pl->span) {
+        pl->off_h = take(pl->slots * lanes * pl->NR);
+        pl->off_d = take(pl->slots * lanes);
     }
     pl->total = off;
     return SSD_OK;
@@ -338,7 +418,7 @@ int sel_setup(const ssd_selscan_dims* dims, const ssd_selscan_layout* layout, co
 
 template <typename T, int NR, int MW>
 void launch(const SelParams& p, unsigned grid, hipStream_t s) {
-    if (p.span) selscan_span_kernel<T, NR, false><<<dim3(grid), dim3(512), 0, s>>>(p);
+    if (p.span) selscan_span_kernel<T, NR><<<dim3(grid), dim3(512), 0, s>>>(p);
     selscan_fwd_kernel<T, NR, MW><<<dim3(grid), dim3(64 * MW), 0, s>>>(p);
 }
 
@@ -444,13 +524,14 @@ int ssd_selscan_bwd(const ssd_selscan_dims* dims, const ssd_selscan_layout* layo
     p.dd_raw = dd_raw;
     p.dz = dz;
     p.final_state = dinit_state;
-    p.span_h = (float*)(ws + pl.off_h);
-    p.span_q = (float*)(ws + pl.off_q);
-    p.span_d = (float*)(ws + pl.off_d);
-    p.chunk_states = (float*)(ws + pl.off_seg);
+    p.run_h = (float*)(ws + pl.off_h);
+    p.run_q = (float*)(ws + pl.off_q);
+    p.run_d = (float*)(ws + pl.off_d);
+    p.chunk_h = (float*)(ws + pl.off_ch);
+    p.chunk_d = (float*)(ws + pl.off_cd);
     p.part_w = (float*)(ws + pl.off_w);
     p.part_bc = (float*)(ws + pl.off_bc);
-    if ((st = launch_selscan_bwd(p, dims->dtype, pl.NR, pl.waves, (unsigned)pl.grid, s)) != SSD_OK)
+    if ((st = launch_selscan_bwd(p, dims->dtype, pl.NR, pl.waves, pl.runs, (unsigned)pl.grid, s)) != SSD_OK)
         return st;
     const int NP = 4 * pl.NR;
     const int64_t items = pl.T * dims->ngroups * 2 * NP;

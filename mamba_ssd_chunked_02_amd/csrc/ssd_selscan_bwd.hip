@@ -1,117 +1,58 @@
 // Selective scan, backward (see ssd_selscan.h).
+//
+// Three launches.  A wave owns a run of 64 tokens of its 16 channels:
+//   runs   every run from zero, forward in time: its state, what it does to a q
+//          that enters from behind (q before = P q + Q, composed chunk by chunk),
+//          its sum of d, and the state before each of its chunks;
+//   links  along each sequence: the h that enters every run and the q that enters
+//          it from behind, in place;
+//   grads  every run again, its chunks from the last to the first, a and h of a
+//          chunk in registers.
+// The runs are independent of each other in both large launches: they fill the
+// chip whatever the number of sequences and channels, and no wave waits for
+// another.  (One launch that walked a sequence's segments forward and back, its
+// waves exchanging states in LDS, needed a workgroup per sequence and channel
+// block: 2 x 2048 tokens x 1536 channels kept 192 of 256 CUs busy, 193 us.)
 #include "ssd_selscan.h"
 
 namespace ssd {
 namespace {
 
-// First the segments forward, only to find the state that enters each chunk
-// (kept in chunk_states); then backward, where each wave holds a and h of its
-// chunk in registers.  What enters the last segment's chunks is found there,
-// so a sequence of one segment is walked once.
-template <typename T, int NR, int MW>
-__global__ __launch_bounds__(64 * MW, Shape<NR>::kBwdPerSimd) void selscan_bwd_kernel(SelParams p) {
+// Where a run's and its chunks' records lie.  Chunk c of run i, which starts at
+// token f, has record f / TW + i + c: no two runs meet.
+struct Run {
+    int first, chunks;
+    int64_t rec;     // of the run: [index][blk][lane]
+    int64_t chunk0;  // of its first chunk
+};
+template <int NR, int MW>
+__device__ __forceinline__ Run run_of(const SelParams& p, const Place& o) {
     using S = Shape<NR>;
-    constexpr int TW = S::kBwdTokens, NP = S::NP, Q = TW / 4, waves = MW;
+    Run r;
+    const int64_t index = (int64_t)o.slot * MW + o.wave;
+    r.first = o.first + o.wave * S::kRunTokens;
+    const int have = o.k < o.nspan ? min(o.last - r.first, S::kRunTokens) : 0;
+    r.chunks = have > 0 ? (have + S::kBwdTokens - 1) / S::kBwdTokens : 0;
+    r.rec = (index * p.nblk + o.blk) * 64 + o.lane;
+    r.chunk0 = ((r.first / S::kBwdTokens + index) * p.nblk + o.blk) * 64 + o.lane;
+    return r;
+}
+
+template <typename T, int NR, int MW>
+__global__ __launch_bounds__(64 * MW, NR <= 8 ? 4 : 2) void selscan_runs_kernel(SelParams p) {
+    using S = Shape<NR>;
+    constexpr int TW = S::kBwdTokens, NP = S::NP, Q = TW / 4;
     __shared__ __align__(16) float bc[MW][TW][2][NP];
-    __shared__ __align__(16) float exP[2][MW][64][NR], exH[2][MW][64][NR], exQ[2][MW][64][NR];
-    __shared__ __align__(16) float enter[3][64][NR];  // h or q entering a segment
     Place o;
     if (!place_of(p, o)) return;
-    const int seg = waves * TW;
-    const bool b0 = o.nl & 1, b1 = o.nl & 2;
-    float A2[NR], dA[NR], h[NR], q[NR];
+    const Run run = run_of<NR, MW>(p, o);
+    if (run.chunks == 0) return;
+    float A2[NR], h[NR], q[NR];
     load_rates<NR>(p, o, A2);
     const float dinit = o.live ? p.d_init[o.ch] : 0.f;
-    const float Dv = o.live && p.D ? p.D[o.ch] : 0.f;
     const bool gated = p.z != nullptr;
-    // (a slot without a span has no tokens and still writes its share: zeros)
-    const int nseg = o.k < o.nspan ? (o.last - o.first + seg - 1) / seg : 0;
-    // sequences' segments follow one another: this one's start at a slot that
-    // no earlier sequence reaches
-    float* states = p.chunk_states +
-                    ((((int64_t)(o.first / seg + o.seq) * waves + o.wave) * p.nblk + o.blk) * 64 + o.lane) * NR;
-    const int64_t states_step = (int64_t)waves * p.nblk * 64 * NR;
-
-    uint32_t xr[Q], dr[Q], zr[Q], gr[Q];
+    uint32_t xr[Q], dr[Q], gr[Q], zr[Q];
     Rows<T, NR, TW> Br, Cr;
-    int turn = 0;
-    // -- forward over all segments but the last
-    int tb = o.first + o.wave * TW;
-    if (o.wave == 0) {
-        load_state<NR>(p.init, p, o, h);
-        if (p.span && nseg > 0) fold_spans<NR>(p.span_h, p, o, A2, 0, o.k, 1, h);
-        lds_put<NR>(enter[0][o.lane], h);
-    }
-    auto fetch_forward = [&](int t) {
-        const ArgPtr k = fresh_args();
-        load_tokens<T, TW>(k->x, k->xs, o, t, xr);
-        load_tokens<T, TW>(k->d_raw, k->ds, o, t, dr);
-        load_rows<T, NR, TW>(k->B, k->bs_t, k->bs_g, k->N, o, t, Br);
-    };
-    if (nseg > 1) fetch_forward(tb);
-    for (int k = 1; k < nseg; ++k, turn ^= 1) {
-        float d[Q], u[Q], P[NR];
-        float sumd = 0.f;
-#pragma unroll
-        for (int i = 0; i < Q; ++i) {
-            d[i] = softplus(value_of<T>(dr[i]) + dinit);
-            u[i] = d[i] * value_of<T>(xr[i]);
-            sumd += d[i];
-        }
-        sumd = quad_total(sumd);
-        wave_lds_fence();
-        put_rows<T, NR, TW>(&bc[o.wave][0][0][0], o, Br);
-        wave_lds_fence();
-        tb += seg;
-        if (k + 1 < nseg) fetch_forward(tb);
-#pragma unroll
-        for (int r = 0; r < NR; ++r) P[r] = fexp2(sumd * A2[r]);
-#pragma unroll
-        for (int t = 0; t < TW; ++t) {
-            float b[NR];
-            lds_get<NR>(&bc[o.wave][t][0][o.nl * NR], b);
-            const float dt = quad_lane(d[t / 4], t % 4), ut = quad_lane(u[t / 4], t % 4);
-#pragma unroll
-            for (int r = 0; r < NR; ++r)
-                h[r] = t ? fexp2(dt * A2[r]) * h[r] + b[r] * ut : b[r] * ut;
-        }
-        lds_put<NR>(exP[turn][o.wave][o.lane], P);
-        lds_put<NR>(exH[turn][o.wave][o.lane], h);
-        __syncthreads();
-        float hin[NR];
-        lds_get<NR>(enter[turn][o.lane], hin);
-        for (int j = 0; j < o.wave; ++j) {
-            float Pj[NR], hj[NR];
-            lds_get<NR>(exP[turn][j][o.lane], Pj);
-            lds_get<NR>(exH[turn][j][o.lane], hj);
-#pragma unroll
-            for (int r = 0; r < NR; ++r) hin[r] = Pj[r] * hin[r] + hj[r];
-        }
-        __builtin_memcpy(states + (k - 1) * states_step, hin, sizeof(hin));
-        if (o.wave == waves - 1) {
-#pragma unroll
-            for (int r = 0; r < NR; ++r) hin[r] = P[r] * hin[r] + h[r];
-            lds_put<NR>(enter[turn ^ 1][o.lane], hin);
-        }
-    }
-    // -- backward.  enter[turn] holds the state entering the last segment; q goes
-    // through the other two slots in turn, first through the one that no wave
-    // can still be reading.
-    const int last_slot = turn;
-    int q_slot = 2, q_next = turn ^ 1;
-    if (o.wave == 0) {
-        load_state<NR>(p.d_final, p, o, q);
-        if (p.span) fold_spans<NR>(p.span_q, p, o, A2, o.nspan - 1, o.nspan - 1 - o.k, -1, q);
-        lds_put<NR>(enter[q_slot][o.lane], q);
-    }
-    float dD = 0.f, dI = 0.f;
-#pragma unroll
-    for (int r = 0; r < NR; ++r) dA[r] = 0.f;
-    // where the lane's sums over channels go: see the reduction below
-    const int r_of = (o.lane & 16 ? NR / 2 : 0) + (NR > 2 && (o.lane & 8) ? NR / 4 : 0);
-    const uint32_t sum_off = !(o.lane & 4) && (NR > 2 || !(o.lane & 8))
-                                 ? (uint32_t)((o.lane & 32 ? NP : 0) + o.nl * NR + r_of) * 4u
-                                 : kNowhere;
     auto fetch = [&](int t) {
         const ArgPtr k = fresh_args();
         load_tokens<T, TW>(k->x, k->xs, o, t, xr);
@@ -121,29 +62,198 @@ __global__ __launch_bounds__(64 * MW, Shape<NR>::kBwdPerSimd) void selscan_bwd_k
         load_rows<T, NR, TW>(k->B, k->bs_t, k->bs_g, k->N, o, t, Br);
         load_rows<T, NR, TW>(k->C, k->cs_t, k->cs_g, k->N, o, t, Cr);
     };
-    tb = o.first + (nseg - 1) * seg + o.wave * TW;
-    if (nseg > 0) fetch(tb);
-    for (int k = nseg - 1; k >= 0; --k, tb -= seg, turn ^= 1) {
-        if (tb >= o.last) {  // in the last segment, behind the sequence
-            __syncthreads();
-            if (k > 0) fetch(tb - seg);
-            q_slot = q_next;
-            q_next = 2;
-            continue;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) h[r] = q[r] = 0.f;
+    float sum = 0.f;
+    int tb = run.first;
+    fetch(tb);
+    for (int c = 0; c < run.chunks; ++c, tb += TW) {
+        if (c > 0) {  // before the first chunk both are 0
+            const int64_t rec = run.chunk0 + (int64_t)c * p.nblk * 64;
+            p.chunk_d[rec] = sum;
+            __builtin_memcpy(p.chunk_h + rec * NR, h, sizeof(h));
         }
         const int have = min(o.last - tb, TW);
+        float d[Q], u[Q], w[Q], chunk_d = 0.f;
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            d[i] = step_of(value_of<T>(dr[i]) + dinit, 4 * i + o.nl < have);
+            u[i] = d[i] * value_of<T>(xr[i]);
+            chunk_d += d[i];
+            const float zf = value_of<T>(zr[i]);
+            w[i] = value_of<T>(gr[i]) * (gated ? zf * sigmoid(zf) : 1.f);
+        }
+        wave_lds_fence();
+        put_rows<T, NR, TW>(&bc[o.wave][0][0][0], o, Br);
+        put_rows<T, NR, TW>(&bc[o.wave][0][1][0], o, Cr);
+        wave_lds_fence();
+        if (c + 1 < run.chunks) fetch(tb + TW);
+        float a[TW][NR], ql[NR];
+#pragma unroll
+        for (int t = 0; t < TW; ++t) {
+            float b[NR];
+            lds_get<NR>(&bc[o.wave][t][0][o.nl * NR], b);
+            const float dt = quad_lane(d[t / 4], t % 4), ut = quad_lane(u[t / 4], t % 4);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                a[t][r] = fexp2(dt * A2[r]);
+                h[r] = a[t][r] * h[r] + b[r] * ut;
+            }
+            if (t & 1) keep_order();
+        }
+#pragma unroll
+        for (int t = TW - 1; t >= 0; --t) {
+            float cc[NR];
+            lds_get<NR>(&bc[o.wave][t][1][o.nl * NR], cc);
+            const float wt = quad_lane(w[t / 4], t % 4);
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+                ql[r] = t < TW - 1 ? a[t][r] * (cc[r] * wt + ql[r]) : a[t][r] * (cc[r] * wt);
+            if (!(t & 1)) keep_order();
+        }
+#pragma unroll
+        for (int r = 0; r < NR; ++r) q[r] += fexp2(sum * A2[r]) * ql[r];
+        sum += quad_total(chunk_d);
+    }
+    p.run_d[run.rec] = sum;
+    __builtin_memcpy(p.run_h + run.rec * NR, h, sizeof(h));
+    __builtin_memcpy(p.run_q + run.rec * NR, q, sizeof(q));
+}
+
+// LW waves walk a sequence's runs forward (h), LW backward (q), each a piece of
+// them: first from zero, then, after the pieces before it are folded, from what
+// enters it.  Eight runs' records are loaded at a time.  MW runs a slot, as in the
+// other launches.
+template <int NR, int LW>
+__global__ __launch_bounds__(128 * LW) void selscan_links_kernel(SelParams p, int MW) {
+    constexpr int AHEAD = 8;
+    __shared__ __align__(16) float exV[2][LW][64][NR], exD[2][LW][64];
+    Place o = {};
+    o.seq = blockIdx.x / (uint32_t)p.nblk;
+    o.blk = blockIdx.x % (uint32_t)p.nblk;
+    o.group = o.blk / p.bpg;
+    o.lane = threadIdx.x & 63;
+    o.nl = o.lane & 3;
+    const int off = (o.blk % p.bpg) * kChan + (o.lane >> 2);
+    o.live = off < p.epg;
+    o.ch = o.group * p.epg + off;
+    int64_t first, last;
+    sequence_span(p.cu, o.seq, p.L, p.T, &first, &last);
+    const int slot = p.cu ? (int)first / p.span + o.seq : o.seq * p.per;
+    const int runs = (int)((last - first + Shape<NR>::kRunTokens - 1) / Shape<NR>::kRunTokens);
+    const int back = wave_id() / LW, piece = wave_id() % LW;
+    const int each = (runs + LW - 1) / LW, j0 = min(piece * each, runs), j1 = min(j0 + each, runs);
+    float A2[NR], v[NR];
+    load_rates<NR>(p, o, A2);
+    const int64_t step = (int64_t)p.nblk * 64 * (back ? -1 : 1);
+    const int64_t at0 = (((int64_t)slot * MW + (back ? runs - 1 - j0 : j0)) * p.nblk + o.blk) * 64 + o.lane;
+    float* state = back ? p.run_q : p.run_h;
+    float sum = 0.f;
+    const auto walk = [&](bool write) {
+        int64_t at = at0;
+        for (int j = j0; j < j1; j += AHEAD, at += AHEAD * step) {
+            float d[AHEAD], s[AHEAD][NR];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (j + i < j1) {
+                    d[i] = p.run_d[at + i * step];
+                    __builtin_memcpy(s[i], state + (at + i * step) * NR, sizeof(s[i]));
+                }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (j + i < j1) {
+                    if (write) __builtin_memcpy(state + (at + i * step) * NR, v, sizeof(v));
+                    sum += d[i];
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) v[r] = fexp2(d[i] * A2[r]) * v[r] + s[i][r];
+                }
+        }
+    };
+    if constexpr (LW > 1) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) v[r] = 0.f;
+        walk(false);
+        exD[back][piece][o.lane] = sum;
+        lds_put<NR>(exV[back][piece][o.lane], v);
+        __syncthreads();
+    }
+    load_state<NR>(back ? p.d_final : p.init, p, o, v);
+    if constexpr (LW > 1)
+        for (int i = 0; i < piece; ++i) {
+            const float d = exD[back][i][o.lane];
+            float s[NR];
+            lds_get<NR>(exV[back][i][o.lane], s);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) v[r] = fexp2(d * A2[r]) * v[r] + s[r];
+        }
+    walk(true);
+    if (back && piece == LW - 1) store_state<NR>(p.final_state, p, o, v);
+}
+
+template <typename T, int NR, int MW>
+__global__ __launch_bounds__(64 * MW, Shape<NR>::kBwdPerSimd) void selscan_grads_kernel(SelParams p) {
+    using S = Shape<NR>;
+    constexpr int TW = S::kBwdTokens, NP = S::NP, Q = TW / 4;
+    __shared__ __align__(16) float bc[MW][TW][2][NP];
+    __shared__ __align__(16) float exA[MW][64][NR], exD[MW][64][2];
+    Place o;
+    if (!place_of(p, o)) return;
+    const Run run = run_of<NR, MW>(p, o);
+    const bool b0 = o.nl & 1, b1 = o.nl & 2;
+    float A2[NR], dA[NR], q[NR], hrun[NR];
+    load_rates<NR>(p, o, A2);
+    const float dinit = o.live ? p.d_init[o.ch] : 0.f;
+    const float Dv = o.live && p.D ? p.D[o.ch] : 0.f;
+    const bool gated = p.z != nullptr;
+    uint32_t xr[Q], dr[Q], zr[Q], gr[Q];
+    Rows<T, NR, TW> Br, Cr;
+    float cd = 0.f, ch[NR];  // of the chunk's record
+    auto fetch = [&](int c) {
+        const ArgPtr k = fresh_args();
+        const int t = run.first + c * TW;
+        load_tokens<T, TW>(k->x, k->xs, o, t, xr);
+        load_tokens<T, TW>(k->d_raw, k->ds, o, t, dr);
+        load_tokens<T, TW>(k->dy, k->gs, o, t, gr);
+        load_tokens<T, TW>(k->z, k->zs, o, t, zr);
+        load_rows<T, NR, TW>(k->B, k->bs_t, k->bs_g, k->N, o, t, Br);
+        load_rows<T, NR, TW>(k->C, k->cs_t, k->cs_g, k->N, o, t, Cr);
+        if (c > 0) {
+            const int64_t rec = run.chunk0 + (int64_t)c * k->nblk * 64;
+            cd = k->chunk_d[rec];
+            __builtin_memcpy(ch, k->chunk_h + rec * NR, sizeof(ch));
+        } else {
+            cd = 0.f;
+#pragma unroll
+            for (int r = 0; r < NR; ++r) ch[r] = 0.f;
+        }
+    };
+    float dD = 0.f, dI = 0.f;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) dA[r] = 0.f;
+    // where the lane's sums over channels go: see the reduction below
+    const int r_of = (o.lane & 16 ? NR / 2 : 0) + (NR > 2 && (o.lane & 8) ? NR / 4 : 0);
+    const uint32_t sum_off = !(o.lane & 4) && (NR > 2 || !(o.lane & 8))
+                                 ? (uint32_t)((o.lane & 32 ? NP : 0) + o.nl * NR + r_of) * 4u
+                                 : kNowhere;
+    if (run.chunks > 0) {
+        fetch(run.chunks - 1);
+        __builtin_memcpy(q, p.run_q + run.rec * NR, sizeof(q));
+        __builtin_memcpy(hrun, p.run_h + run.rec * NR, sizeof(hrun));
+    }
+    for (int c = run.chunks - 1; c >= 0; --c) {
+        const int tb = run.first + c * TW;
+        const int have = min(o.last - tb, TW);
         float hin[NR];
-        if (k < nseg - 1) __builtin_memcpy(hin, states + k * states_step, sizeof(hin));
+#pragma unroll
+        for (int r = 0; r < NR; ++r) hin[r] = ch[r] + fexp2(cd * A2[r]) * hrun[r];
         // past the sequence and in lanes without a channel x and dy are 0
         float d[Q], u[Q], w[Q], x[Q], raw[Q], gz[Q];  // gz: what dz multiplies v by
-        float sumd = 0.f;
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
             x[i] = value_of<T>(xr[i]);
             raw[i] = value_of<T>(dr[i]) + dinit;
             d[i] = step_of(raw[i], 4 * i + o.nl < have);
             u[i] = d[i] * x[i];
-            sumd += d[i];
             w[i] = gz[i] = value_of<T>(gr[i]);
             if (gated) {
                 const float zf = value_of<T>(zr[i]), sz = sigmoid(zf);
@@ -152,77 +262,22 @@ __global__ __launch_bounds__(64 * MW, Shape<NR>::kBwdPerSimd) void selscan_bwd_k
             }
             dD += w[i] * x[i];
         }
-        sumd = quad_total(sumd);
         wave_lds_fence();
         put_rows<T, NR, TW>(&bc[o.wave][0][0][0], o, Br);
         put_rows<T, NR, TW>(&bc[o.wave][0][1][0], o, Cr);
         wave_lds_fence();
-        // (1) every decay of the chunk, and q through it from zero
-        float a[TW][NR];
-#pragma unroll
-        for (int r = 0; r < NR; ++r) h[r] = fexp2(sumd * A2[r]);
-        lds_put<NR>(exP[turn][o.wave][o.lane], h);
-#pragma unroll
-        for (int t = 0; t < TW; ++t) {
-            const float dt = quad_lane(d[t / 4], t % 4);
-#pragma unroll
-            for (int r = 0; r < NR; ++r) a[t][r] = fexp2(dt * A2[r]);
-        }
-        if (k == nseg - 1) {
-#pragma unroll
-            for (int t = 0; t < TW; ++t) {
-                float b[NR];
-                lds_get<NR>(&bc[o.wave][t][0][o.nl * NR], b);
-                const float ut = quad_lane(u[t / 4], t % 4);
-#pragma unroll
-                for (int r = 0; r < NR; ++r) h[r] = t ? a[t][r] * h[r] + b[r] * ut : b[r] * ut;
-                if (t & 1) keep_order();
-            }
-            lds_put<NR>(exH[turn][o.wave][o.lane], h);
-        }
-#pragma unroll
-        for (int t = TW - 1; t >= 0; --t) {
-            float c[NR];
-            lds_get<NR>(&bc[o.wave][t][1][o.nl * NR], c);
-            const float wt = quad_lane(w[t / 4], t % 4);
-#pragma unroll
-            for (int r = 0; r < NR; ++r)
-                q[r] = t < TW - 1 ? a[t][r] * (c[r] * wt + q[r]) : a[t][r] * (c[r] * wt);
-            if (!(t & 1)) keep_order();
-        }
-        lds_put<NR>(exQ[turn][o.wave][o.lane], q);
-        // (2) fold the chunks behind this one (q), and in the last segment those
-        // before it (h)
-        __syncthreads();
-        if (k == nseg - 1) {
-            lds_get<NR>(enter[last_slot][o.lane], hin);
-            for (int j = 0; j < o.wave; ++j) {
-                float Pj[NR], hj[NR];
-                lds_get<NR>(exP[turn][j][o.lane], Pj);
-                lds_get<NR>(exH[turn][j][o.lane], hj);
-#pragma unroll
-                for (int r = 0; r < NR; ++r) hin[r] = Pj[r] * hin[r] + hj[r];
-            }
-        }
-        lds_get<NR>(enter[q_slot][o.lane], q);
-        // the waves behind the sequence have left nothing
-        for (int j = min(waves, (o.last - o.first - k * seg + TW - 1) / TW) - 1; j > o.wave; --j) {
-            float Pj[NR], qj[NR];
-            lds_get<NR>(exP[turn][j][o.lane], Pj);
-            lds_get<NR>(exQ[turn][j][o.lane], qj);
-#pragma unroll
-            for (int r = 0; r < NR; ++r) q[r] = Pj[r] * q[r] + qj[r];
-        }
-        // (3) h of every token, then the gradients from the last token back
-        float hs[TW][NR];
+        // h of every token, then the gradients from the last token back
+        float a[TW][NR], hs[TW][NR];
 #pragma unroll
         for (int t = 0; t < TW; ++t) {
             float b[NR];
             lds_get<NR>(&bc[o.wave][t][0][o.nl * NR], b);
-            const float ut = quad_lane(u[t / 4], t % 4);
+            const float dt = quad_lane(d[t / 4], t % 4), ut = quad_lane(u[t / 4], t % 4);
 #pragma unroll
-            for (int r = 0; r < NR; ++r)
+            for (int r = 0; r < NR; ++r) {
+                a[t][r] = fexp2(dt * A2[r]);
                 hs[t][r] = a[t][r] * (t ? hs[t - 1][r] : hin[r]) + b[r] * ut;
+            }
             if (t & 1) keep_order();
         }
         const ArgPtr out = fresh_args();
@@ -237,27 +292,27 @@ __global__ __launch_bounds__(64 * MW, Shape<NR>::kBwdPerSimd) void selscan_bwd_k
         const uint32_t xoff = lane_off(out->xs), doff = lane_off(out->ds), zoff = lane_off(out->zs);
 #pragma unroll
         for (int i = Q - 1; i >= 0; --i) {
-            // the next segment's rows, once half of a and hs is used up
-            if (i == (Q - 1) / 2 && k > 0) fetch(tb - seg);
+            // the chunk before, once half of a and hs is used up
+            if (i == (Q - 1) / 2 && c > 0) fetch(c - 1);
             float gB[4], sA[4], v[4];
 #pragma unroll
             for (int kk = 3; kk >= 0; --kk) {
                 const int t = 4 * i + kk;
-                float b[NR], c[NR], db[NR], dc[NR];
+                float b[NR], cc[NR], db[NR], dc[NR];
                 lds_get<NR>(&bc[o.wave][t][0][o.nl * NR], b);
-                lds_get<NR>(&bc[o.wave][t][1][o.nl * NR], c);
+                lds_get<NR>(&bc[o.wave][t][1][o.nl * NR], cc);
                 const float dt = quad_lane(d[i], kk), ut = quad_lane(u[i], kk);
                 const float wt = quad_lane(w[i], kk);
                 gB[kk] = sA[kk] = v[kk] = 0.f;
 #pragma unroll
                 for (int r = 0; r < NR; ++r) {
-                    const float g = c[r] * wt + q[r];
+                    const float g = cc[r] * wt + q[r];
                     q[r] = a[t][r] * g;
                     const float s = q[r] * (t ? hs[t - 1][r] : hin[r]);
                     gB[kk] += g * b[r];
                     sA[kk] += A2[r] * s;
                     dA[r] += dt * s;
-                    v[kk] += c[r] * hs[t][r];
+                    v[kk] += cc[r] * hs[t][r];
                     db[r] = g * ut;
                     dc[r] = hs[t][r] * wt;
                 }
@@ -296,31 +351,22 @@ __global__ __launch_bounds__(64 * MW, Shape<NR>::kBwdPerSimd) void selscan_bwd_k
             }
             keep_order();
         }
-        // q leaving the segment's first chunk enters the segment before it; its
-        // slot was last read before the barrier that this wave has passed
-        if (o.wave == 0) lds_put<NR>(enter[q_next][o.lane], q);
-        const int used = q_slot;
-        q_slot = q_next;
-        q_next = used;
-        wave_lds_fence();
     }
-    if (o.wave == 0 && o.k == 0) store_state<NR>(p.final_state, p, o, q);
     // the waves' shares of dA, dD and dd_init
     dD = quad_total(dD);
     dI = quad_total(dI);
-    __syncthreads();
-    lds_put<NR>(exP[0][o.wave][o.lane], dA);
-    exH[0][o.wave][o.lane][0] = dD;
-    exH[0][o.wave][o.lane][1] = dI;
+    lds_put<NR>(exA[o.wave][o.lane], dA);
+    exD[o.wave][o.lane][0] = dD;
+    exD[o.wave][o.lane][1] = dI;
     __syncthreads();
     if (o.wave || !o.live) return;
-    for (int j = 1; j < waves; ++j) {
+    for (int j = 1; j < MW; ++j) {
         float t[NR];
-        lds_get<NR>(exP[0][j][o.lane], t);
+        lds_get<NR>(exA[j][o.lane], t);
 #pragma unroll
         for (int r = 0; r < NR; ++r) dA[r] += t[r];
-        dD += exH[0][j][o.lane][0];
-        dI += exH[0][j][o.lane][1];
+        dD += exD[j][o.lane][0];
+        dI += exD[j][o.lane][1];
     }
     float* pw = p.part_w + (int64_t)o.slot * (p.N + 2) * p.E + o.ch;
 #pragma unroll
@@ -336,35 +382,34 @@ __global__ __launch_bounds__(64 * MW, Shape<NR>::kBwdPerSimd) void selscan_bwd_k
 
 
 template <typename T, int NR, int MW>
-void launch(const SelParams& p, unsigned grid, hipStream_t s) {
-    if (p.span) selscan_span_kernel<T, NR, true><<<dim3(grid), dim3(512), 0, s>>>(p);
-    selscan_bwd_kernel<T, NR, MW><<<dim3(grid), dim3(64 * MW), 0, s>>>(p);
+void launch(const SelParams& p, int64_t runs, unsigned grid, hipStream_t s) {
+    const dim3 gd(grid), links((unsigned)p.S * (unsigned)p.nblk);
+    selscan_runs_kernel<T, NR, MW><<<gd, dim3(64 * MW), 0, s>>>(p);
+    if (runs <= 16) selscan_links_kernel<NR, 1><<<links, dim3(128), 0, s>>>(p, MW);
+    else selscan_links_kernel<NR, 4><<<links, dim3(512), 0, s>>>(p, MW);
+    selscan_grads_kernel<T, NR, MW><<<gd, dim3(64 * MW), 0, s>>>(p);
+}
+
+template <typename T, int NR>
+void launch(const SelParams& p, int waves, int64_t runs, unsigned grid, hipStream_t s) {
+    if (waves > 1) launch<T, NR, Shape<NR>::kBwdWaves>(p, runs, grid, s);
+    else launch<T, NR, 1>(p, runs, grid, s);
 }
 
 template <typename T>
-void launch(const SelParams& p, int NR, int waves, unsigned grid, hipStream_t s) {
-    if (NR == 2) {
-        if (waves == 8) launch<T, 2, 8>(p, grid, s);
-        else launch<T, 2, 2>(p, grid, s);
-    } else if (NR == 4) {
-        if (waves == 8) launch<T, 4, 8>(p, grid, s);
-        else if (waves == 4) launch<T, 4, 4>(p, grid, s);
-        else launch<T, 4, 2>(p, grid, s);
-    } else if (NR == 8) {
-        if (waves == 8) launch<T, 8, 8>(p, grid, s);
-        else launch<T, 8, 2>(p, grid, s);
-    } else {
-        if (waves == 4) launch<T, 16, 4>(p, grid, s);
-        else launch<T, 16, 1>(p, grid, s);
-    }
+void launch(const SelParams& p, int NR, int waves, int64_t runs, unsigned grid, hipStream_t s) {
+    if (NR == 2) launch<T, 2>(p, waves, runs, grid, s);
+    else if (NR == 4) launch<T, 4>(p, waves, runs, grid, s);
+    else if (NR == 8) launch<T, 8>(p, waves, runs, grid, s);
+    else launch<T, 16>(p, waves, runs, grid, s);
 }
 
 }  // namespace
 
-int launch_selscan_bwd(const SelParams& p, int32_t dtype, int NR, int waves, unsigned grid,
-                       hipStream_t s) {
-    if (dtype == SSD_BF16) launch<bf16>(p, NR, waves, grid, s);
-    else launch<float>(p, NR, waves, grid, s);
+int launch_selscan_bwd(const SelParams& p, int32_t dtype, int NR, int waves, int64_t runs,
+                       unsigned grid, hipStream_t s) {
+    if (dtype == SSD_BF16) launch<bf16>(p, NR, waves, runs, grid, s);
+    else launch<float>(p, NR, waves, runs, grid, s);
     return launched();
 }
 
