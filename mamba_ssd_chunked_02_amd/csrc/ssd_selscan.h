@@ -71,9 +71,9 @@ struct SelParams {
 };
 
 // The launches of the backward scan up to the sums over channel blocks and
-// sequences (its own translation unit): waves of a workgroup, runs of a sequence.
-int launch_selscan_bwd(const SelParams& p, int32_t dtype, int NR, int waves, int64_t runs,
-                       unsigned grid, hipStream_t s);
+// sequences (its own translation unit); runs: of a sequence.
+int launch_selscan_bwd(const SelParams& p, int32_t dtype, int NR, int64_t runs, unsigned grid,
+                       hipStream_t s);
 
 namespace {
 
@@ -100,7 +100,6 @@ struct Shape {
     static constexpr int kFwdPerSimd = kFwdWaves / 4;  // smaller workgroups as many
     static constexpr int kBwdTokens = NR == 2 ? 16 : NR == 4 ? 8 : 4;
     static constexpr int kRunTokens = 64;              // backward: of a wave
-    static constexpr int kBwdWaves = 4;
     static constexpr int kBwdPerSimd = NR <= 4 ? 3 : NR == 8 ? 2 : 1;
 };
 

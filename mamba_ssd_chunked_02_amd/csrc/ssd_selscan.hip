@@ -254,7 +254,7 @@ int sel_check(const ssd_selscan_dims* d) {
 
 struct SelPlan {
     int32_t NR, S, bpg, nblk, upr;
-    int32_t waves;      // of a workgroup
+    int32_t waves;      // forward: of a workgroup
     int64_t runs;       // backward: of a sequence
     int32_t span, per;  // tokens of a span (0: sequences are not cut), spans a sequence
     int64_t slots, units, grid, T;
@@ -298,12 +298,8 @@ int sel_plan(const ssd_selscan_dims& d, bool bwd, SelPlan* pl) {
     // packed sequences are taken as equally long
     const int64_t len = cdiv(pl->T, pl->S), whole = (int64_t)pl->S * nblk;
     if (bwd) {
-        // sequences of one run take workgroups of one wave: the others would stand
-        // idle and hold their registers
-        const int64_t tokens = with_shape(pl->NR, [](auto s) { return s.kRunTokens; });
-        pl->waves = len > tokens ? with_shape(pl->NR, [](auto s) { return s.kBwdWaves; }) : 1;
-        pl->runs = cdiv(len, tokens);
-        pl->span = (int32_t)(pl->waves * tokens);
+        pl->span = with_shape(pl->NR, [](auto s) { return s.kRunTokens; });
+        pl->runs = cdiv(len, pl->span);
         pl->per = (int32_t)imax(1, cdiv(d.seqlen, pl->span));
     } else {
         const int64_t tokens = with_shape(pl->NR, [](auto s) { return s.kFwdTokens; });
@@ -338,11 +334,10 @@ int sel_plan(const ssd_selscan_dims& d, bool bwd, SelPlan* pl) {
     };
     const int64_t lanes = nblk * 64;
     if (bwd) {
-        const int64_t runs = pl->slots * pl->waves;
-        const int64_t chunks = pl->T / with_shape(pl->NR, [](auto s) { return s.kBwdTokens; }) + runs;
-        pl->off_h = take(runs * lanes * pl->NR);
-        pl->off_q = take(runs * lanes * pl->NR);
-        pl->off_d = take(runs * lanes);
+        const int64_t chunks = pl->T / with_shape(pl->NR, [](auto s) { return s.kBwdTokens; }) + pl->slots;
+        pl->off_h = take(pl->slots * lanes * pl->NR);
+        pl->off_q = take(pl->slots * lanes * pl->NR);
+        pl->off_d = take(pl->slots * lanes);
         pl->off_ch = take(chunks * lanes * pl->NR);
         pl->off_cd = take(chunks * lanes);
         pl->off_w = take(pl->slots * (d.d_state + 2) * d.channels);
@@ -531,7 +526,7 @@ int ssd_selscan_bwd(const ssd_selscan_dims* dims, const ssd_selscan_layout* layo
     p.chunk_d = (float*)(ws + pl.off_cd);
     p.part_w = (float*)(ws + pl.off_w);
     p.part_bc = (float*)(ws + pl.off_bc);
-    if ((st = launch_selscan_bwd(p, dims->dtype, pl.NR, pl.waves, pl.runs, (unsigned)pl.grid, s)) != SSD_OK)
+    if ((st = launch_selscan_bwd(p, dims->dtype, pl.NR, pl.runs, (unsigned)pl.grid, s)) != SSD_OK)
         return st;
     const int NP = 4 * pl.NR;
     const int64_t items = pl.T * dims->ngroups * 2 * NP;

@@ -18,34 +18,35 @@
 namespace ssd {
 namespace {
 
-// Where a run's and its chunks' records lie.  Chunk c of run i, which starts at
-// token f, has record f / TW + i + c: no two runs meet.
+// A workgroup is one wave and its slot's span is one run.  (Workgroups of four
+// waves took as long where the runs were many, and kept the registers of idle
+// waves where they were few: 24 sequences of 170 tokens 230 us instead of 188.)
+// Where a run's and its chunks' records lie: chunk c of the run in slot i, which
+// starts at token f, has record f / TW + i + c, so no two runs meet.
 struct Run {
     int first, chunks;
-    int64_t rec;     // of the run: [index][blk][lane]
+    int64_t rec;     // of the run: [slot][blk][lane]
     int64_t chunk0;  // of its first chunk
 };
-template <int NR, int MW>
+template <int NR>
 __device__ __forceinline__ Run run_of(const SelParams& p, const Place& o) {
     using S = Shape<NR>;
     Run r;
-    const int64_t index = (int64_t)o.slot * MW + o.wave;
-    r.first = o.first + o.wave * S::kRunTokens;
-    const int have = o.k < o.nspan ? min(o.last - r.first, S::kRunTokens) : 0;
-    r.chunks = have > 0 ? (have + S::kBwdTokens - 1) / S::kBwdTokens : 0;
-    r.rec = (index * p.nblk + o.blk) * 64 + o.lane;
-    r.chunk0 = ((r.first / S::kBwdTokens + index) * p.nblk + o.blk) * 64 + o.lane;
+    r.first = o.first;
+    r.chunks = o.k < o.nspan ? (o.last - o.first + S::kBwdTokens - 1) / S::kBwdTokens : 0;
+    r.rec = ((int64_t)o.slot * p.nblk + o.blk) * 64 + o.lane;
+    r.chunk0 = ((int64_t)(r.first / S::kBwdTokens + o.slot) * p.nblk + o.blk) * 64 + o.lane;
     return r;
 }
 
-template <typename T, int NR, int MW>
-__global__ __launch_bounds__(64 * MW, NR <= 8 ? 4 : 2) void selscan_runs_kernel(SelParams p) {
+template <typename T, int NR>
+__global__ __launch_bounds__(64, NR <= 8 ? 4 : 2) void selscan_runs_kernel(SelParams p) {
     using S = Shape<NR>;
     constexpr int TW = S::kBwdTokens, NP = S::NP, Q = TW / 4;
-    __shared__ __align__(16) float bc[MW][TW][2][NP];
+    __shared__ __align__(16) float bc[TW][2][NP];
     Place o;
     if (!place_of(p, o)) return;
-    const Run run = run_of<NR, MW>(p, o);
+    const Run run = run_of<NR>(p, o);
     if (run.chunks == 0) return;
     float A2[NR], h[NR], q[NR];
     load_rates<NR>(p, o, A2);
@@ -84,15 +85,15 @@ __global__ __launch_bounds__(64 * MW, NR <= 8 ? 4 : 2) void selscan_runs_kernel(
             w[i] = value_of<T>(gr[i]) * (gated ? zf * sigmoid(zf) : 1.f);
         }
         wave_lds_fence();
-        put_rows<T, NR, TW>(&bc[o.wave][0][0][0], o, Br);
-        put_rows<T, NR, TW>(&bc[o.wave][0][1][0], o, Cr);
+        put_rows<T, NR, TW>(&bc[0][0][0], o, Br);
+        put_rows<T, NR, TW>(&bc[0][1][0], o, Cr);
         wave_lds_fence();
         if (c + 1 < run.chunks) fetch(tb + TW);
         float a[TW][NR], ql[NR];
 #pragma unroll
         for (int t = 0; t < TW; ++t) {
             float b[NR];
-            lds_get<NR>(&bc[o.wave][t][0][o.nl * NR], b);
+            lds_get<NR>(&bc[t][0][o.nl * NR], b);
             const float dt = quad_lane(d[t / 4], t % 4), ut = quad_lane(u[t / 4], t % 4);
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
@@ -104,7 +105,7 @@ __global__ __launch_bounds__(64 * MW, NR <= 8 ? 4 : 2) void selscan_runs_kernel(
 #pragma unroll
         for (int t = TW - 1; t >= 0; --t) {
             float cc[NR];
-            lds_get<NR>(&bc[o.wave][t][1][o.nl * NR], cc);
+            lds_get<NR>(&bc[t][1][o.nl * NR], cc);
             const float wt = quad_lane(w[t / 4], t % 4);
 #pragma unroll
             for (int r = 0; r < NR; ++r)
@@ -122,10 +123,9 @@ __global__ __launch_bounds__(64 * MW, NR <= 8 ? 4 : 2) void selscan_runs_kernel(
 
 // LW waves walk a sequence's runs forward (h), LW backward (q), each a piece of
 // them: first from zero, then, after the pieces before it are folded, from what
-// enters it.  Eight runs' records are loaded at a time.  MW runs a slot, as in the
-// other launches.
+// enters it.  Eight runs' records are loaded at a time.
 template <int NR, int LW>
-__global__ __launch_bounds__(128 * LW) void selscan_links_kernel(SelParams p, int MW) {
+__global__ __launch_bounds__(128 * LW) void selscan_links_kernel(SelParams p) {
     constexpr int AHEAD = 8;
     __shared__ __align__(16) float exV[2][LW][64][NR], exD[2][LW][64];
     Place o = {};
@@ -146,7 +146,7 @@ __global__ __launch_bounds__(128 * LW) void selscan_links_kernel(SelParams p, in
     float A2[NR], v[NR];
     load_rates<NR>(p, o, A2);
     const int64_t step = (int64_t)p.nblk * 64 * (back ? -1 : 1);
-    const int64_t at0 = (((int64_t)slot * MW + (back ? runs - 1 - j0 : j0)) * p.nblk + o.blk) * 64 + o.lane;
+    const int64_t at0 = ((int64_t)(slot + (back ? runs - 1 - j0 : j0)) * p.nblk + o.blk) * 64 + o.lane;
     float* state = back ? p.run_q : p.run_h;
     float sum = 0.f;
     const auto walk = [&](bool write) {
@@ -190,15 +190,14 @@ __global__ __launch_bounds__(128 * LW) void selscan_links_kernel(SelParams p, in
     if (back && piece == LW - 1) store_state<NR>(p.final_state, p, o, v);
 }
 
-template <typename T, int NR, int MW>
-__global__ __launch_bounds__(64 * MW, Shape<NR>::kBwdPerSimd) void selscan_grads_kernel(SelParams p) {
+template <typename T, int NR>
+__global__ __launch_bounds__(64, Shape<NR>::kBwdPerSimd) void selscan_grads_kernel(SelParams p) {
     using S = Shape<NR>;
     constexpr int TW = S::kBwdTokens, NP = S::NP, Q = TW / 4;
-    __shared__ __align__(16) float bc[MW][TW][2][NP];
-    __shared__ __align__(16) float exA[MW][64][NR], exD[MW][64][2];
+    __shared__ __align__(16) float bc[TW][2][NP];
     Place o;
     if (!place_of(p, o)) return;
-    const Run run = run_of<NR, MW>(p, o);
+    const Run run = run_of<NR>(p, o);
     const bool b0 = o.nl & 1, b1 = o.nl & 2;
     float A2[NR], dA[NR], q[NR], hrun[NR];
     load_rates<NR>(p, o, A2);
@@ -263,15 +262,15 @@ __global__ __launch_bounds__(64 * MW, Shape<NR>::kBwdPerSimd) void selscan_grads
             dD += w[i] * x[i];
         }
         wave_lds_fence();
-        put_rows<T, NR, TW>(&bc[o.wave][0][0][0], o, Br);
-        put_rows<T, NR, TW>(&bc[o.wave][0][1][0], o, Cr);
+        put_rows<T, NR, TW>(&bc[0][0][0], o, Br);
+        put_rows<T, NR, TW>(&bc[0][1][0], o, Cr);
         wave_lds_fence();
         // h of every token, then the gradients from the last token back
         float a[TW][NR], hs[TW][NR];
 #pragma unroll
         for (int t = 0; t < TW; ++t) {
             float b[NR];
-            lds_get<NR>(&bc[o.wave][t][0][o.nl * NR], b);
+            lds_get<NR>(&bc[t][0][o.nl * NR], b);
             const float dt = quad_lane(d[t / 4], t % 4), ut = quad_lane(u[t / 4], t % 4);
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
@@ -299,8 +298,8 @@ __global__ __launch_bounds__(64 * MW, Shape<NR>::kBwdPerSimd) void selscan_grads
             for (int kk = 3; kk >= 0; --kk) {
                 const int t = 4 * i + kk;
                 float b[NR], cc[NR], db[NR], dc[NR];
-                lds_get<NR>(&bc[o.wave][t][0][o.nl * NR], b);
-                lds_get<NR>(&bc[o.wave][t][1][o.nl * NR], cc);
+                lds_get<NR>(&bc[t][0][o.nl * NR], b);
+                lds_get<NR>(&bc[t][1][o.nl * NR], cc);
                 const float dt = quad_lane(d[i], kk), ut = quad_lane(u[i], kk);
                 const float wt = quad_lane(w[i], kk);
                 gB[kk] = sA[kk] = v[kk] = 0.f;
@@ -352,22 +351,10 @@ __global__ __launch_bounds__(64 * MW, Shape<NR>::kBwdPerSimd) void selscan_grads
             keep_order();
         }
     }
-    // the waves' shares of dA, dD and dd_init
+    // the run's share of dA, dD and dd_init
     dD = quad_total(dD);
     dI = quad_total(dI);
-    lds_put<NR>(exA[o.wave][o.lane], dA);
-    exD[o.wave][o.lane][0] = dD;
-    exD[o.wave][o.lane][1] = dI;
-    __syncthreads();
-    if (o.wave || !o.live) return;
-    for (int j = 1; j < MW; ++j) {
-        float t[NR];
-        lds_get<NR>(exA[j][o.lane], t);
-#pragma unroll
-        for (int r = 0; r < NR; ++r) dA[r] += t[r];
-        dD += exD[j][o.lane][0];
-        dI += exD[j][o.lane][1];
-    }
+    if (!o.live) return;
     float* pw = p.part_w + (int64_t)o.slot * (p.N + 2) * p.E + o.ch;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
@@ -381,35 +368,29 @@ __global__ __launch_bounds__(64 * MW, Shape<NR>::kBwdPerSimd) void selscan_grads
 }
 
 
-template <typename T, int NR, int MW>
-void launch(const SelParams& p, int64_t runs, unsigned grid, hipStream_t s) {
-    const dim3 gd(grid), links((unsigned)p.S * (unsigned)p.nblk);
-    selscan_runs_kernel<T, NR, MW><<<gd, dim3(64 * MW), 0, s>>>(p);
-    if (runs <= 16) selscan_links_kernel<NR, 1><<<links, dim3(128), 0, s>>>(p, MW);
-    else selscan_links_kernel<NR, 4><<<links, dim3(512), 0, s>>>(p, MW);
-    selscan_grads_kernel<T, NR, MW><<<gd, dim3(64 * MW), 0, s>>>(p);
-}
-
 template <typename T, int NR>
-void launch(const SelParams& p, int waves, int64_t runs, unsigned grid, hipStream_t s) {
-    if (waves > 1) launch<T, NR, Shape<NR>::kBwdWaves>(p, runs, grid, s);
-    else launch<T, NR, 1>(p, runs, grid, s);
+void launch(const SelParams& p, int64_t runs, unsigned grid, hipStream_t s) {
+    const dim3 links((unsigned)p.S * (unsigned)p.nblk);
+    selscan_runs_kernel<T, NR><<<dim3(grid), dim3(64), 0, s>>>(p);
+    if (runs <= 16) selscan_links_kernel<NR, 1><<<links, dim3(128), 0, s>>>(p);
+    else selscan_links_kernel<NR, 4><<<links, dim3(512), 0, s>>>(p);
+    selscan_grads_kernel<T, NR><<<dim3(grid), dim3(64), 0, s>>>(p);
 }
 
 template <typename T>
-void launch(const SelParams& p, int NR, int waves, int64_t runs, unsigned grid, hipStream_t s) {
-    if (NR == 2) launch<T, 2>(p, waves, runs, grid, s);
-    else if (NR == 4) launch<T, 4>(p, waves, runs, grid, s);
-    else if (NR == 8) launch<T, 8>(p, waves, runs, grid, s);
-    else launch<T, 16>(p, waves, runs, grid, s);
+void launch(const SelParams& p, int NR, int64_t runs, unsigned grid, hipStream_t s) {
+    if (NR == 2) launch<T, 2>(p, runs, grid, s);
+    else if (NR == 4) launch<T, 4>(p, runs, grid, s);
+    else if (NR == 8) launch<T, 8>(p, runs, grid, s);
+    else launch<T, 16>(p, runs, grid, s);
 }
 
 }  // namespace
 
-int launch_selscan_bwd(const SelParams& p, int32_t dtype, int NR, int waves, int64_t runs,
-                       unsigned grid, hipStream_t s) {
-    if (dtype == SSD_BF16) launch<bf16>(p, NR, waves, runs, grid, s);
-    else launch<float>(p, NR, waves, runs, grid, s);
+int launch_selscan_bwd(const SelParams& p, int32_t dtype, int NR, int64_t runs, unsigned grid,
+                       hipStream_t s) {
+    if (dtype == SSD_BF16) launch<bf16>(p, NR, runs, grid, s);
+    else launch<float>(p, NR, runs, grid, s);
     return launched();
 }
 
