@@ -502,7 +502,7 @@ int ssd_conv_step(const ssd_conv_dims* dims, const ssd_conv_layout* layout,
 #define SSD_SELSCAN_MAX_CHANNELS (1 << 20)
 typedef struct ssd_selscan_dims {
     int32_t batch;    /* b >= 1                                             */
-    int64_t seqlen;   /* L >= 0; b * L < 2^31                               */
+    int64_t seqlen;   /* L >= 0; b * L < 2^31 - 2^16                        */
     int32_t channels; /* E >= 1, <= 2^20, a multiple of ngroups             */
     int32_t d_state;  /* N: 1 .. 64                                         */
     int32_t ngroups;  /* G >= 1                                             */

@@ -548,7 +548,7 @@ int ssd_conv_fwd(const ssd_conv_dims* dims, const ssd_conv_layout* layout, const
     p.state_items = final_state ? (int64_t)p.S * (d.width - 1) * p.nvec : 0;
     const int64_t grid = p.main_blocks + cdiv(p.state_items, 256);
     if (grid == 0) return SSD_OK;
-    if (grid > INT32_MAX) return SSD_ERR_SHAPE;
+    if (grid * 256 > kMaxThreads) return SSD_ERR_SHAPE;
     const dim3 gd((unsigned)grid);
     if (d.dtype == SSD_BF16) launch_conv_fwd<bf16>(p, d.width, V, tt, gd, s);
     else launch_conv_fwd<float>(p, d.width, V, tt, gd, s);
@@ -607,7 +607,7 @@ int ssd_conv_bwd(const ssd_conv_dims* dims, const ssd_conv_layout* layout, const
     p.main_blocks = pl.strips * cdiv(p.nvec, 64);
     p.state_items = dinit_state ? (int64_t)p.S * (d.width - 1) * p.nvec : 0;
     const int64_t grid = p.main_blocks + cdiv(p.state_items, 256);
-    if (grid > INT32_MAX) return SSD_ERR_SHAPE;
+    if (grid * 256 > kMaxThreads) return SSD_ERR_SHAPE;
     if (d.dtype == SSD_BF16) launch_conv_bwd<bf16>(p, d.width, V, pl.tile, dim3((unsigned)grid), s);
     else launch_conv_bwd<float>(p, d.width, V, pl.tile, dim3((unsigned)grid), s);
     if ((st = launched()) != SSD_OK || (!dweight && !dbias)) return st;

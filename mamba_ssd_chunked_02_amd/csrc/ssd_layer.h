@@ -31,6 +31,8 @@ namespace {
 constexpr int64_t kMaxStride = (int64_t)1 << 24;
 constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - 1;
 
+constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 1;  // of a launch
+
 inline size_t elem_size(int32_t dtype) { return dtype == SSD_BF16 ? 2 : 4; }
 inline bool elem_aligned(const void* p, size_t e) { return ((uintptr_t)p & (e - 1)) == 0; }
 inline int64_t imax(int64_t a, int64_t b) { return a > b ? a : b; }

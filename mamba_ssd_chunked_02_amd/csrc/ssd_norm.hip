@@ -15,6 +15,7 @@ namespace ssd {
 namespace {
 
 constexpr int kMaxWaves = 16;   // per row
+constexpr int64_t kMaxGrid = ((int64_t)1 << 22) - 1;  // of 1024 threads
 constexpr int kWavesPerWg = 4;  // rows of a workgroup where a row is one wave's
 
 struct NormParams {
@@ -77,61 +78,63 @@ template <typename T, int V, int NV>
 __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormParams p, int waves) {
     __shared__ float ex[2][kMaxWaves][2];
     const int lanes = waves * 64;
-    const int64_t row = waves == 1 ? (int64_t)blockIdx.x * kWavesPerWg + (threadIdx.x >> 6)
-                                   : (int64_t)blockIdx.x;
-    if (row >= p.rows) return;  // only where a row is one wave's: no barrier below
+    const int per = waves == 1 ? kWavesPerWg : 1;
+    int64_t row = (int64_t)blockIdx.x * per + (waves == 1 ? threadIdx.x >> 6 : 0);
     const int lane = waves == 1 ? threadIdx.x & 63 : threadIdx.x;
-    const T* x = (const T*)p.x + row * p.x_row;
-    T* y = (T*)p.out + row * p.out_row;
-    RawVec<T, V> raw[NV];
-    float v[NV][V];
-    float s = 0.f, zero = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-        load_raw<T, V>(x + Piece<V>(i, lanes, lane, p.width).c, V, raw[i]);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const Piece<V> q(i, lanes, lane, p.width);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            v[i][j] = (float)raw[i].v[j];
-            s += j >= q.skip ? v[i][j] : 0.f;
-        }
-    }
     int turn = 0;
-    row_sums(s, zero, waves, ex, turn);
-    const float mean = s / (float)p.width;
-    float sq = 0.f;
-    zero = 0.f;
+    // one row, but for more rows than a launch may have threads
+    for (; row < p.rows; row += (int64_t)gridDim.x * per) {
+        const T* x = (const T*)p.x + row * p.x_row;
+        T* y = (T*)p.out + row * p.out_row;
+        RawVec<T, V> raw[NV];
+        float v[NV][V];
+        float s = 0.f, zero = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const Piece<V> q(i, lanes, lane, p.width);
+        for (int i = 0; i < NV; ++i)
+            load_raw<T, V>(x + Piece<V>(i, lanes, lane, p.width).c, V, raw[i]);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            v[i][j] -= mean;
-            sq += j >= q.skip ? v[i][j] * v[i][j] : 0.f;
+        for (int i = 0; i < NV; ++i) {
+            const Piece<V> q(i, lanes, lane, p.width);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                v[i][j] = (float)raw[i].v[j];
+                s += j >= q.skip ? v[i][j] : 0.f;
+            }
         }
-    }
-    row_sums(sq, zero, waves, ex, turn);
-    const float rstd = 1.f / sqrtf(sq / (float)p.width + p.eps);
-    if (lane == 0) {
-        if (p.mean) p.mean[row] = mean;
-        if (p.rstd) p.rstd[row] = rstd;
-    }
+        row_sums(s, zero, waves, ex, turn);
+        const float mean = s / (float)p.width;
+        float sq = 0.f;
+        zero = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const Piece<V> q(i, lanes, lane, p.width);
-        float w[V], b[V], o[V];
+        for (int i = 0; i < NV; ++i) {
+            const Piece<V> q(i, lanes, lane, p.width);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            w[j] = 1.f;
-            b[j] = 0.f;
+            for (int j = 0; j < V; ++j) {
+                v[i][j] -= mean;
+                sq += j >= q.skip ? v[i][j] * v[i][j] : 0.f;
+            }
         }
-        if (p.weight) load_vec<float, V>(p.weight + q.c, V, w);
-        if (p.bias) load_vec<float, V>(p.bias + q.c, V, b);
+        row_sums(sq, zero, waves, ex, turn);
+        const float rstd = 1.f / sqrtf(sq / (float)p.width + p.eps);
+        if (lane == 0) {
+            if (p.mean) p.mean[row] = mean;
+            if (p.rstd) p.rstd[row] = rstd;
+        }
 #pragma unroll
-        for (int j = 0; j < V; ++j) o[j] = v[i][j] * rstd * w[j] + b[j];
-        if (q.any()) store_vec<T, V>(y + q.c, V, o);
+        for (int i = 0; i < NV; ++i) {
+            const Piece<V> q(i, lanes, lane, p.width);
+            float w[V], b[V], o[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                w[j] = 1.f;
+                b[j] = 0.f;
+            }
+            if (p.weight) load_vec<float, V>(p.weight + q.c, V, w);
+            if (p.bias) load_vec<float, V>(p.bias + q.c, V, b);
+#pragma unroll
+            for (int j = 0; j < V; ++j) o[j] = v[i][j] * rstd * w[j] + b[j];
+            if (q.any()) store_vec<T, V>(y + q.c, V, o);
+        }
     }
 }
 
@@ -311,7 +314,8 @@ int norm_check(const ssd_norm_dims* d) {
 template <typename T, int V, bool BWD>
 void launch_norm(const NormParams& p, NormPlan pl, hipStream_t s) {
     const int64_t walkers = BWD ? p.slots : p.rows;
-    const dim3 grid((unsigned)(pl.waves == 1 ? cdiv(walkers, kWavesPerWg) : walkers));
+    const int64_t wgs = pl.waves == 1 ? cdiv(walkers, kWavesPerWg) : walkers;
+    const dim3 grid((unsigned)(wgs < kMaxGrid ? wgs : kMaxGrid));
     const dim3 block(pl.waves == 1 ? 64 * kWavesPerWg : 64 * pl.waves);
     if constexpr (V == 1) {  // rows of fewer elements than a vector: one load
         if constexpr (BWD) norm_bwd_kernel<T, 1, 1><<<grid, block, 0, s>>>(p, pl.waves);

@@ -12,19 +12,24 @@
 //   dd_t = x_t sum_n g B + sum_n A_n (a g h_{t-1}),   dd_raw_t = dd_t sigmoid(d_raw_t + d_init)
 //   dA_n = sum_t d_t (a g h_{t-1}),  dD = sum w x,  dd_init = sum dd_raw,  dinit_state = a_0 g_0
 //
-// Every token of every channel costs N exponentials and about 4 N products, so
-// both directions are bound by the vector units, not by memory; nothing here
-// has the shape of a matrix product (the decay differs in every lane).
+// Every token of every channel costs N exponentials and about 4 N products
+// (backward three times that), so both directions are bound by the vector units,
+// not by memory; nothing here has the shape of a matrix product (the decay
+// differs in every lane).
 //
 // Mapping.  Four lanes of a wave hold one channel (a quad; N / 4 state entries
-// each), a wave 16 channels.  A workgroup owns 16 channels of one sequence;
-// its waves take consecutive chunks of TW tokens.  A segment of waves x TW
-// tokens goes: (1) every wave scans its chunk from a zero state, keeping all
+// each), a wave 16 channels; chunks are TW tokens.  Forward, a workgroup owns 16
+// channels of one sequence and its waves take consecutive chunks.  A segment of
+// waves x TW tokens goes: (1) every wave scans its chunk from a zero state, keeping all
 // a_t,n in registers; (2) the waves exchange (decay product, state) in LDS and
 // fold those before them; (3) every wave scans its chunk again from the state
 // that enters it, without forming an exponential.  The state that leaves the
 // segment enters the next one, so a sequence needs no other launch and no
-// global scratch.  Per-token values (d, u, y) live in the quad's lanes, token
+// global scratch (scanning twice costs 8 issues a state entry and token where a
+// scan in order costs 6, but only this fills the chip).  The vector units are
+// busy 98 % of the time on the CUs that have a workgroup: 2 x 2048 tokens x 1536
+// channels x 16 states 49 us on 192 of the 256 CUs, 65536 packed tokens 548 us.
+// Per-token values (d, u, y) live in the quad's lanes, token
 // 4 i + k in lane k, and reach the other three as DPP operands.
 #pragma once
 
@@ -76,7 +81,6 @@ int launch_selscan_bwd(const SelParams& p, int32_t dtype, int NR, int64_t runs, 
                        hipStream_t s);
 
 namespace {
-
 
 // The kernel's argument block, read anew: what is loaded through the returned
 // pointer is not kept in scalar registers across the loops around it.  (Kept,

@@ -246,7 +246,7 @@ int sel_check(const ssd_selscan_dims* d) {
     if (d->batch < 1 || d->seqlen < 0 || d->seqlen > kMaxTokens || d->channels < 1 ||
         d->channels > SSD_SELSCAN_MAX_CHANNELS || d->ngroups < 1 || d->channels % d->ngroups ||
         d->d_state < 1 || d->nseq < 0 || (d->nseq > 0 && d->batch != 1) ||
-        (int64_t)d->batch * d->seqlen > kMaxTokens)
+        (int64_t)d->batch * d->seqlen > kMaxTokens - 65536)  // token sums stay in 32 bits
         return SSD_ERR_SHAPE;
     if (d->d_state > SSD_SELSCAN_MAX_STATE) return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
@@ -325,7 +325,8 @@ int sel_plan(const ssd_selscan_dims& d, bool bwd, SelPlan* pl) {
     pl->slots = d.nseq > 0 && pl->span ? pl->T / pl->span + pl->S : (int64_t)pl->S * pl->per;
     pl->units = pl->slots * pl->upr;
     pl->grid = cdiv(pl->units, kXcds) * kXcds * kRun;
-    if (pl->grid > INT32_MAX || whole > INT32_MAX) return SSD_ERR_SHAPE;
+    const int64_t threads = bwd ? 64 : imax(512, 64 * pl->waves);
+    if (pl->grid * threads > kMaxThreads || whole * 512 > kMaxThreads) return SSD_ERR_SHAPE;
     size_t off = 0;
     const auto take = [&off](int64_t floats) {
         const size_t at = off;
@@ -498,6 +499,7 @@ int ssd_selscan_bwd(const ssd_selscan_dims* dims, const ssd_selscan_layout* layo
     int st = sel_setup(dims, layout, x, d_raw, d_init, A, B, C, D, z, init_state, cu_seqlens, true,
                        &p, &pl);
     if (st != SSD_OK) return st;
+    if (pl.T * dims->ngroups * 8 * pl.NR + 256 > kMaxThreads) return SSD_ERR_SHAPE;
     if (pl.T > 0 && (!dy || !dx || !dd_raw || !dB || !dC || (z && !dz))) return SSD_ERR_NULL_ARG;
     const size_t e = elem_size(dims->dtype);
     for (const void* q : {dy, (const void*)dx, (const void*)dd_raw, (const void*)dB,
@@ -532,7 +534,6 @@ int ssd_selscan_bwd(const ssd_selscan_dims* dims, const ssd_selscan_layout* layo
     const int64_t items = pl.T * dims->ngroups * 2 * NP;
     if (items > 0) {
         const int64_t grid = cdiv(items, 256);
-        if (grid > INT32_MAX) return SSD_ERR_SHAPE;
         const dim3 gd((unsigned)grid), bd(256);
         if (dims->dtype == SSD_BF16) selscan_bc_kernel<bf16><<<gd, bd, 0, s>>>(p, dB, dC, NP);
         else selscan_bc_kernel<float><<<gd, bd, 0, s>>>(p, dB, dC, NP);

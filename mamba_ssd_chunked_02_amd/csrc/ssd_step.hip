@@ -323,7 +323,7 @@ int ssd_step(const ssd_dims* dims, const ssd_layout* layout, const void* x, cons
     p.hpg = d.nheads / d.ngroups;
     p.pieces = (int32_t)cdiv(d.headdim, cp);
     const int64_t grid = heads * p.pieces;
-    if (grid > INT32_MAX) return SSD_ERR_SHAPE;
+    if (grid * 256 > kMaxThreads) return SSD_ERR_SHAPE;
     const dim3 gd((unsigned)grid), bd(256);
     hipStream_t s = (hipStream_t)stream;
     if (d.dtype == SSD_BF16) {
