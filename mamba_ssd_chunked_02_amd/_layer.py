@@ -203,6 +203,12 @@ def _heads(t, name, shape):
     return t.stride(0), t.stride(1)
 
 
+def _output(x):
+    """An uninitialized contiguous tensor of x's shape and dtype (empty_like is the
+    cheapest way to one, but keeps a dense x's own order)."""
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+
+
 def _like(t):
     """An uninitialized tensor with t's shape and strides."""
     return torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device)
@@ -230,16 +236,16 @@ def _pools(x, state, new_state, row, dtype, slots):
     ``new_state`` (``state`` itself where not given)."""
     if new_state is None:
         new_state = state
-    dev = x.get_device()
-    for name, t in (("state", state), ("new_state", new_state)):
-        if t.dtype is not dtype or t.get_device() != dev or t.shape[1:] != row \
-                or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous {dtype} [nslots, "
-                             f"{', '.join(map(str, row))}] on {x.device}")
-    if new_state.shape[0] != state.shape[0]:
-        raise ValueError("state and new_state must have the same number of slots")
+    dev, shape = x.get_device(), state.shape
+    if new_state.shape != shape:
+        raise ValueError("state and new_state must have the same shape")
+    if shape[1:] != row or state.dtype is not dtype or new_state.dtype is not dtype \
+            or state.get_device() != dev or new_state.get_device() != dev \
+            or not state.is_contiguous() or not new_state.is_contiguous():
+        raise ValueError(f"state and new_state must be contiguous {dtype} [nslots, "
+                         f"{', '.join(map(str, row))}] on {x.device}")
     if slots is None:
-        if state.shape[0] < x.shape[0]:
+        if shape[0] < x.shape[0]:
             raise ValueError("without slots the pool needs a row for every sequence")
     elif slots.dtype is not torch.int32 or slots.get_device() != dev or slots.shape != x.shape[:1] \
             or not slots.is_contiguous():
@@ -273,7 +279,7 @@ def ssd_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None):
     _floats(x, (weight, (width,), "weight"), (bias, (width,), "bias"))
     rows, xs = _matrix(x, "x", width)
     if y is None:
-        y, ys = x.new_empty(x.shape), width
+        y, ys = _output(x), width
     else:
         _same(x, (y, "y"))
         if y.shape != x.shape:
@@ -281,7 +287,8 @@ def ssd_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None):
         ys = _matrix(y, "y", width)[1]
     mean, rstd = torch.empty((2,) + x.shape[:-1], dtype=torch.float32, device=x.device).unbind(0)
     dims = _struct(SsdNormDims, rows, xs, ys, width, width, code, eps, 0)
-    _launch("ssd_norm_fwd", x, dims, _at(x), _at(weight), _at(bias), _at(y), _at(mean), _at(rstd))
+    _launch("ssd_norm_fwd", x, dims, x.data_ptr(), _at(weight), _at(bias), y.data_ptr(),
+            mean.data_ptr(), rstd.data_ptr())
     return y, mean, rstd
 
 
@@ -302,8 +309,9 @@ def ssd_norm_bwd(x, weight, mean, rstd, dy, workspace=None):
     dims = _struct(SsdNormDims, rows, xs, width, _matrix(dy, "dy", width)[1], width, code, 0.0, 0)
     if workspace is None:
         workspace = _workspace("ssd_norm_bwd_workspace_bytes", dims, x)
-    _launch("ssd_norm_bwd", x, dims, _at(x), _at(weight), _at(mean), _at(rstd), _at(dy), _at(dx),
-            _at(dweight), _at(dbias), _at(workspace), workspace.numel())
+    _launch("ssd_norm_bwd", x, dims, x.data_ptr(), _at(weight), mean.data_ptr(), rstd.data_ptr(),
+            dy.data_ptr(), dx.data_ptr(), dweight.data_ptr(), dbias.data_ptr(),
+            workspace.data_ptr(), workspace.numel())
     return {"dx": dx, "dweight": dweight, "dbias": dbias}
 
 
@@ -336,7 +344,7 @@ def ssd_conv_fwd(x, weight, bias=None, init_state=None, cu_seqlens=None, y=None,
     b, L, _ = x.shape
     xs = _tokens(x, "x", x.shape)
     if y is None:
-        y, ys = x.new_empty(x.shape), E
+        y, ys = _output(x), E
     else:
         _same(x, (y, "y"))
         ys = _tokens(y, "y", x.shape)
@@ -349,8 +357,8 @@ def ssd_conv_fwd(x, weight, bias=None, init_state=None, cu_seqlens=None, y=None,
         if final_state.shape != (S, W - 1, E) or not final_state.is_contiguous():
             raise ValueError(f"final_state must be contiguous [{S}, {W - 1}, {E}]")
     dims = _struct(SsdConvDims, b, L, E, W, 0 if cu is None else S, code)
-    _launch("ssd_conv_fwd", x, dims, _struct(SsdConvLayout, xs, ys, E), _at(x), _at(weight), _at(bias),
-            _at(init_state), _at(cu), _at(y), _at(final_state))
+    _launch("ssd_conv_fwd", x, dims, _struct(SsdConvLayout, xs, ys, E), x.data_ptr(),
+            weight.data_ptr(), _at(bias), _at(init_state), _at(cu), y.data_ptr(), _at(final_state))
     return y, final_state
 
 
@@ -373,8 +381,9 @@ def ssd_conv_bwd(x, weight, bias, dy, init_state=None, cu_seqlens=None, d_final=
     if workspace is None:
         workspace = _workspace("ssd_conv_bwd_workspace_bytes", dims, x)
     dweight, dbias = sums[:W], sums[W]
-    _launch("ssd_conv_bwd", x, dims, lay, _at(x), _at(weight), _at(bias), _at(init_state), _at(cu),
-            _at(dy), _at(d_final), _at(dx), _at(dweight), _at(dbias), _at(dinit), _at(workspace),
+    _launch("ssd_conv_bwd", x, dims, lay, x.data_ptr(), weight.data_ptr(), _at(bias),
+            _at(init_state), _at(cu), dy.data_ptr(), _at(d_final), dx.data_ptr(),
+            dweight.data_ptr(), dbias.data_ptr(), dinit.data_ptr(), workspace.data_ptr(),
             workspace.numel())
     return {"dx": dx, "dweight": dweight, "dbias": dbias, "dinit_state": dinit}
 
@@ -389,13 +398,14 @@ def ssd_conv_step(x, state, weight, bias=None, slots=None, new_state=None, y=Non
     new_state = _pools(x, state, new_state, (W - 1, E), x.dtype, slots)
     xs = _rows(x, "x", x.shape)
     if y is None:
-        y, ys = x.new_empty(x.shape), E
+        y, ys = _output(x), E
     else:
         _same(x, (y, "y"))
         ys = _rows(y, "y", x.shape)
     dims = _struct(SsdConvDims, x.shape[0], 1, E, W, 0, code)
-    _launch("ssd_conv_step", x, dims, _struct(SsdConvLayout, xs, ys, E), _at(x), _at(weight), _at(bias),
-            _at(state), _at(slots), state.shape[0], _at(y), _at(new_state))
+    _launch("ssd_conv_step", x, dims, _struct(SsdConvLayout, xs, ys, E), x.data_ptr(),
+            weight.data_ptr(), _at(bias), state.data_ptr(), _at(slots), state.shape[0],
+            y.data_ptr(), new_state.data_ptr())
     return y
 
 
@@ -435,7 +445,7 @@ def ssd_selscan_fwd(x, d_raw, d_init, A, B, C, D=None, z=None, init_state=None, 
     dims, lay, cu, state = _selscan_arguments(x, d_raw, d_init, A, B, C, D, z, cu_seqlens, y, None)
     _floats(x, (init_state, state, "init_state"))
     if y is None:
-        y = x.new_empty(x.shape)
+        y = _output(x)
     if final_state is True:
         final_state = torch.empty(state, dtype=torch.float32, device=x.device)
     elif final_state is False:
@@ -446,8 +456,8 @@ def ssd_selscan_fwd(x, d_raw, d_init, A, B, C, D=None, z=None, init_state=None, 
         need = _entry("ssd_selscan_fwd_workspace_bytes")(ctypes.byref(dims))
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    _launch("ssd_selscan_fwd", x, dims, lay, _at(x), _at(d_raw), _at(d_init), _at(A), _at(B),
-            _at(C), _at(D), _at(z), _at(init_state), _at(cu), _at(y), _at(final_state),
+    _launch("ssd_selscan_fwd", x, dims, lay, x.data_ptr(), d_raw.data_ptr(), _at(d_init), _at(A), _at(B),
+            _at(C), _at(D), _at(z), _at(init_state), _at(cu), y.data_ptr(), _at(final_state),
             _at(workspace), 0 if workspace is None else workspace.numel())
     return y, final_state
 
@@ -470,8 +480,8 @@ def ssd_selscan_bwd(x, d_raw, d_init, A, B, C, dy, D=None, z=None, init_state=No
           "dinit_state": torch.empty(state, dtype=torch.float32, device=x.device)}
     if workspace is None:
         workspace = _workspace("ssd_selscan_bwd_workspace_bytes", dims, x)
-    _launch("ssd_selscan_bwd", x, dims, lay, _at(x), _at(d_raw), _at(d_init), _at(A), _at(B),
-            _at(C), _at(D), _at(z), _at(init_state), _at(cu), _at(dy), _at(d_final),
+    _launch("ssd_selscan_bwd", x, dims, lay, x.data_ptr(), d_raw.data_ptr(), _at(d_init), _at(A), _at(B),
+            _at(C), _at(D), _at(z), _at(init_state), _at(cu), dy.data_ptr(), _at(d_final),
             _at(g["dx"]), _at(g["dd_raw"]), _at(g["dB"]), _at(g["dC"]), _at(g.get("dz")),
             _at(g["dA"]), _at(g["dD"]), _at(g["dd_init"]), _at(g["dinit_state"]),
             _at(workspace), workspace.numel())
@@ -492,7 +502,7 @@ def ssd_selscan_step(x, d_raw, d_init, A, B, C, state, D=None, z=None, slots=Non
     _floats(x, (d_init, (E,), "d_init"), (A, (N, E), "A"), (D, (E,), "D"))
     new_state = _pools(x, state, new_state, (N, E), torch.float32, slots)
     if y is None:
-        y, ys = x.new_empty((b, E)), E
+        y, ys = _output(x), E
     else:
         _same(x, (y, "y"))
         ys = _rows(y, "y", x.shape)
@@ -501,9 +511,9 @@ def ssd_selscan_step(x, d_raw, d_init, A, B, C, state, D=None, z=None, slots=Non
         E if z is None else _rows(z, "z", x.shape), *_heads(B, "B", (b, G, N)),
         *_heads(C, "C", (b, G, N)), ys, E)
     dims = _struct(SsdSelscanDims, b, 1, E, N, G, 0, code, 0)
-    _launch("ssd_selscan_step", x, dims, lay, _at(x), _at(d_raw), _at(d_init), _at(A), _at(B),
-            _at(C), _at(D), _at(z), _at(state), _at(slots), state.shape[0], _at(y),
-            _at(new_state))
+    _launch("ssd_selscan_step", x, dims, lay, x.data_ptr(), d_raw.data_ptr(), _at(d_init), _at(A), _at(B),
+            _at(C), _at(D), _at(z), state.data_ptr(), _at(slots), state.shape[0], y.data_ptr(),
+            new_state.data_ptr())
     return y
 
 
@@ -524,12 +534,12 @@ def ssd_step(x, d_raw, d_init, B, C, state, slots=None, new_state=None, y=None):
         raise ValueError(f"d_raw must have shape [{b}, {H}]")
     new_state = _pools(x, state, new_state, (H, N, P), torch.float32, slots)
     if y is None:
-        y = x.new_empty((b, H, P))
+        y = _output(x)
     else:
         _same(x, (y, "y"))
     lay = _struct(SsdLayout, *_heads(x, "x", x.shape), *d_raw.stride(), *_heads(B, "B", (b, G, N)),
                     *_heads(C, "C", (b, G, N)), *_heads(y, "y", x.shape))
     dims = _struct(SsdDims, b, 1, H, P, N, G, 64, 0, code)
-    _launch("ssd_step", x, dims, lay, _at(x), _at(d_raw), float(d_init), _at(B), _at(C),
-            _at(state), _at(slots), state.shape[0], _at(y), _at(new_state))
+    _launch("ssd_step", x, dims, lay, x.data_ptr(), d_raw.data_ptr(), float(d_init), _at(B), _at(C),
+            state.data_ptr(), _at(slots), state.shape[0], y.data_ptr(), new_state.data_ptr())
     return y
