@@ -19,6 +19,19 @@ __device__ __forceinline__ int64_t pool_row(const int32_t* slots, int32_t nslots
     return s >= 0 && s < nslots ? s : -1;
 }
 
+// The elements from `skip` on of a vector: all of one store, or one by one where
+// the vector was moved back to end with its row.
+template <typename T, int V>
+__device__ __forceinline__ void store_own(T* p, int skip, const float (&v)[V]) {
+    if (skip == 0) {
+        store_vec<T, V>(p, V, v);
+    } else {
+#pragma unroll
+        for (int j = 1; j < V; ++j)
+            if (j >= skip) p[j] = (T)v[j];
+    }
+}
+
 // ---- SSD ----------------------------------------------------------------------------------
 
 struct StepParams {
@@ -35,6 +48,8 @@ struct StepParams {
     int32_t nslots, H, P, N, hpg, pieces;
 };
 
+// 64 sequences x 80 heads x 64 x 128 states: 67.3 us, 5.0 TB/s, what a copy of
+// this size reaches (75 with loads predicated by row).
 // A workgroup takes CP headdim columns of one head: CP / 4 lanes across, the
 // other threads down the state rows, at most UN rows each at a time (all
 // their loads in flight together).
@@ -49,13 +64,15 @@ __global__ __launch_bounds__(256) void step_kernel(StepParams p) {
     const int h = id % (uint32_t)p.H;
     const int64_t b = id / (uint32_t)p.H;
     const int g = h / p.hpg;
-    const int c = piece * CP + (tid % PL) * 4, n0 = tid / PL;
-    const int left = p.P - c;  // a multiple of 4 (P is one of 16); none past the last column
+    const int n0 = tid / PL;
+    int c = piece * CP + (tid % PL) * 4;
+    const bool own = c < p.P;  // P is a multiple of 16
+    c = own ? c : p.P - 4;
     const int64_t row = pool_row(p.slots, p.nslots, b);
     T* y = (T*)p.y + b * p.ys_t + h * p.ys_h;
     if (row < 0) {
         const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-        if (n0 == 0 && left > 0) store_vec<T, 4>(y + c, left, zero);
+        if (n0 == 0 && own) store_vec<T, 4>(y + c, 4, zero);
         return;
     }
     const int64_t at = (row * p.H + h) * (int64_t)p.N * p.P + c;
@@ -66,28 +83,28 @@ __global__ __launch_bounds__(256) void step_kernel(StepParams p) {
     const float d = softplus((float)((const T*)p.d_raw)[b * p.ds_t + h * p.ds_h] + p.d_init);
     const float decay = fexp2(-d * kLog2e);
     float u[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
-    load_vec<T, 4>((const T*)p.x + b * p.xs_t + h * p.xs_h + c, left, u);
+    load_vec<T, 4>((const T*)p.x + b * p.xs_t + h * p.xs_h + c, 4, u);
 #pragma unroll
     for (int j = 0; j < 4; ++j) u[j] *= d;
     for (int nb = 0; nb < p.N; nb += ROWS * UN) {
         float s[UN][4], bv[UN], cv[UN];
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
-            const int n = nb + i * ROWS + n0;
-            const bool ok = n < p.N && left > 0;
-            load_vec<float, 4>(in + (int64_t)n * p.P, ok ? 4 : 0, s[i]);
-            bv[i] = ok ? (float)B[n] : 0.f;
-            cv[i] = ok ? (float)C[n] : 0.f;
+            const int n = min(nb + i * ROWS + n0, p.N - 1);
+            load_vec<float, 4>(in + (int64_t)n * p.P, 4, s[i]);
+            bv[i] = (float)B[n];
+            cv[i] = (float)C[n];
         }
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
             const int n = nb + i * ROWS + n0;
+            if (n >= p.N) break;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 s[i][j] = decay * s[i][j] + bv[i] * u[j];
                 acc[j] += cv[i] * s[i][j];
             }
-            if (n < p.N && left > 0) store_vec<float, 4>(out + (int64_t)n * p.P, 4, s[i]);
+            if (own) store_vec<float, 4>(out + (int64_t)n * p.P, 4, s[i]);
         }
     }
     // rows of one wave, then the four waves
@@ -123,24 +140,29 @@ struct SelStepParams {
     int32_t nslots, E, N, epg, vpg, G;
 };
 
-// A thread takes V channels of one sequence, all their state entries.
+// A thread takes V channels of one sequence, all their state entries.  Small
+// workgroups even out over the CUs: 128 sequences x 5120 channels x 16 states 26.1
+// us with 64 or 128 threads (3.4 TB/s), 27.3 with 256, 32.4 with 512; two channels
+// a thread or all 16 entries at once are no faster (27.5 to 34).
+constexpr int kSelThreads = 128;
+
 template <typename T, int V>
-__global__ __launch_bounds__(256) void selscan_step_kernel(SelStepParams p) {
+__global__ __launch_bounds__(kSelThreads) void selscan_step_kernel(SelStepParams p) {
     constexpr int UN = 8;
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t id = (int64_t)blockIdx.x * kSelThreads + threadIdx.x;
     if (id >= p.items) return;
     const uint32_t per = (uint32_t)(p.vpg * p.G);
     const int64_t b = (uint32_t)id / per;
     const uint32_t v = (uint32_t)id % per;
-    const int g = v / (uint32_t)p.vpg, off = (v % (uint32_t)p.vpg) * V;
-    const int e = g * p.epg + off, left = p.epg - off;
+    const int g = v / (uint32_t)p.vpg, at = (v % (uint32_t)p.vpg) * V;
+    const int off = min(at, p.epg - V), skip = at - off, e = g * p.epg + off;
     T* y = (T*)p.y + b * p.ys + e;
     const int64_t row = pool_row(p.slots, p.nslots, b);
     float acc[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[j] = 0.f;
     if (row < 0) {
-        store_vec<T, V>(y, left, acc);
+        store_own<T, V>(y, skip, acc);
         return;
     }
     const float* in = p.state + row * (int64_t)p.N * p.E + e;
@@ -149,9 +171,9 @@ __global__ __launch_bounds__(256) void selscan_step_kernel(SelStepParams p) {
     const T* B = (const T*)p.B + b * p.bs_t + g * p.bs_g;
     const T* C = (const T*)p.C + b * p.cs_t + g * p.cs_g;
     float x[V], d[V], u[V], r[V];
-    load_vec<T, V>((const T*)p.x + b * p.xs + e, left, x);
-    load_vec<T, V>((const T*)p.d_raw + b * p.ds + e, left, d);
-    load_vec<float, V>(p.d_init + e, left, r);
+    load_vec<T, V>((const T*)p.x + b * p.xs + e, V, x);
+    load_vec<T, V>((const T*)p.d_raw + b * p.ds + e, V, d);
+    load_vec<float, V>(p.d_init + e, V, r);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         d[j] = softplus(d[j] + r[j]);
@@ -162,10 +184,9 @@ __global__ __launch_bounds__(256) void selscan_step_kernel(SelStepParams p) {
         float s[UN][V], a[UN][V];
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
-            const int n = n0 + i;
-            const int take = n < p.N ? left : 0;
-            load_vec<float, V>(in + (int64_t)n * p.E, take, s[i]);
-            load_vec<float, V>(A + (int64_t)n * p.E, take, a[i]);
+            const int n = min(n0 + i, p.N - 1);
+            load_vec<float, V>(in + (int64_t)n * p.E, V, s[i]);
+            load_vec<float, V>(A + (int64_t)n * p.E, V, a[i]);
         }
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
@@ -177,20 +198,20 @@ __global__ __launch_bounds__(256) void selscan_step_kernel(SelStepParams p) {
                 s[i][j] = fexp2(d[j] * a[i][j]) * s[i][j] + bn * u[j];
                 acc[j] += cn * s[i][j];
             }
-            store_vec<float, V>(out + (int64_t)n * p.E, left, s[i]);
+            store_own<float, V>(out + (int64_t)n * p.E, skip, s[i]);
         }
     }
     if (p.D) {
-        load_vec<float, V>(p.D + e, left, r);
+        load_vec<float, V>(p.D + e, V, r);
 #pragma unroll
         for (int j = 0; j < V; ++j) acc[j] += r[j] * x[j];
     }
     if (p.z) {
-        load_vec<T, V>((const T*)p.z + b * p.zs + e, left, r);
+        load_vec<T, V>((const T*)p.z + b * p.zs + e, V, r);
 #pragma unroll
         for (int j = 0; j < V; ++j) acc[j] *= r[j] * sigmoid(r[j]);
     }
-    store_vec<T, V>(y, left, acc);
+    store_own<T, V>(y, skip, acc);
 }
 
 // ---- convolution --------------------------------------------------------------------------
@@ -207,40 +228,39 @@ struct ConvStepParams {
     int32_t nslots, E, nvec;
 };
 
-template <typename T, int W>
+template <typename T, int W, int V>
 __global__ __launch_bounds__(256) void conv_step_kernel(ConvStepParams p) {
-    constexpr int V = 4;
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (id >= p.items) return;
     const int64_t b = (uint32_t)id / (uint32_t)p.nvec;
-    const int e = (uint32_t)id % (uint32_t)p.nvec * V, left = p.E - e;
+    const int at = (uint32_t)id % (uint32_t)p.nvec * V, e = min(at, p.E - V), skip = at - e;
     T* y = (T*)p.y + b * p.ys + e;
     const int64_t row = pool_row(p.slots, p.nslots, b);
     float v[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) v[j] = 0.f;
     if (row < 0) {
-        store_vec<T, V>(y, left, v);
+        store_own<T, V>(y, skip, v);
         return;
     }
     const T* in = (const T*)p.state + row * (int64_t)(W - 1) * p.E + e;
     T* out = (T*)p.new_state + row * (int64_t)(W - 1) * p.E + e;
     float t[W][V], w[W][V];
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) load_vec<T, V>(in + (int64_t)k * p.E, left, t[k]);
-    load_vec<T, V>((const T*)p.x + b * p.xs + e, left, t[W - 1]);
+    for (int k = 0; k < W - 1; ++k) load_vec<T, V>(in + (int64_t)k * p.E, V, t[k]);
+    load_vec<T, V>((const T*)p.x + b * p.xs + e, V, t[W - 1]);
 #pragma unroll
-    for (int k = 0; k < W; ++k) load_vec<float, V>(p.weight + (int64_t)k * p.E + e, left, w[k]);
-    if (p.bias) load_vec<float, V>(p.bias + e, left, v);
+    for (int k = 0; k < W; ++k) load_vec<float, V>(p.weight + (int64_t)k * p.E + e, V, w[k]);
+    if (p.bias) load_vec<float, V>(p.bias + e, V, v);
 #pragma unroll
     for (int k = 0; k < W; ++k)
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] += t[k][j] * w[k][j];
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) store_vec<T, V>(out + (int64_t)k * p.E, left, t[k + 1]);
+    for (int k = 0; k < W - 1; ++k) store_own<T, V>(out + (int64_t)k * p.E, skip, t[k + 1]);
 #pragma unroll
     for (int j = 0; j < V; ++j) v[j] *= sigmoid(v[j]);
-    store_vec<T, V>(y, left, v);
+    store_own<T, V>(y, skip, v);
 }
 
 // in place, or two pools that share nothing
@@ -395,11 +415,11 @@ int ssd_selscan_step(const ssd_selscan_dims* dims, const ssd_selscan_layout* lay
     p.epg = d.channels / d.ngroups;
     // four channels a thread (16-byte state rows) where that still gives every
     // CU a workgroup
-    const bool wide = (int64_t)d.batch * E >= (int64_t)4 * 256 * 256;
+    const bool wide = (int64_t)d.batch * E >= (int64_t)4 * 256 * 256 && p.epg >= 4;
     p.vpg = (int32_t)cdiv(p.epg, wide ? 4 : 1);
     p.items = (int64_t)d.batch * p.vpg * G;
     if (p.items > INT32_MAX) return SSD_ERR_SHAPE;
-    const dim3 gd((unsigned)cdiv(p.items, 256)), bd(256);
+    const dim3 gd((unsigned)cdiv(p.items, kSelThreads)), bd(kSelThreads);
     hipStream_t s = (hipStream_t)stream;
     if (d.dtype == SSD_BF16) {
         if (wide) selscan_step_kernel<bf16, 4><<<gd, bd, 0, s>>>(p);
@@ -447,19 +467,25 @@ int ssd_conv_step(const ssd_conv_dims* dims, const ssd_conv_layout* layout, cons
     p.ys = l.y_token;
     p.nslots = nslots;
     p.E = d.channels;
-    p.nvec = (int32_t)cdiv(E, 4);
+    const int V = E >= 4 ? 4 : 1;
+    p.nvec = (int32_t)cdiv(E, V);
     p.items = (int64_t)d.batch * p.nvec;
     if (p.items > INT32_MAX) return SSD_ERR_SHAPE;
     const dim3 gd((unsigned)cdiv(p.items, 256)), bd(256);
     hipStream_t s = (hipStream_t)stream;
-#define SSD_CONV_STEP(W)                                                            \
-    do {                                                                            \
-        if (d.dtype == SSD_BF16) conv_step_kernel<bf16, W><<<gd, bd, 0, s>>>(p);    \
-        else conv_step_kernel<float, W><<<gd, bd, 0, s>>>(p);                       \
+#define SSD_CONV_STEP(T, V)                                               \
+    do {                                                                  \
+        if (d.width == 2) conv_step_kernel<T, 2, V><<<gd, bd, 0, s>>>(p);      \
+        else if (d.width == 3) conv_step_kernel<T, 3, V><<<gd, bd, 0, s>>>(p); \
+        else conv_step_kernel<T, 4, V><<<gd, bd, 0, s>>>(p);                   \
     } while (0)
-    if (d.width == 2) SSD_CONV_STEP(2);
-    else if (d.width == 3) SSD_CONV_STEP(3);
-    else SSD_CONV_STEP(4);
+    if (d.dtype == SSD_BF16) {
+        if (V == 4) SSD_CONV_STEP(bf16, 4);
+        else SSD_CONV_STEP(bf16, 1);
+    } else {
+        if (V == 4) SSD_CONV_STEP(float, 4);
+        else SSD_CONV_STEP(float, 1);
+    }
 #undef SSD_CONV_STEP
     return launched();
 }
