@@ -387,6 +387,71 @@ def test_selscan_extremes():
     ry, rf = lo.selscan(**ins)
     within(y, ry, 64 + 160, "y")
     within(f, rf, 64 + 160, "final")
+    at = lambda t: t[:, 0]
+    st = kw["init_state"].clone()
+    y1 = m.ssd_selscan_step(*map(at, args[:2]), args[2], args[3], *map(at, args[4:]), st, D=kw["D"],
+                            z=at(kw["z"]))
+    within(y1, ry[:, 0], 64, "token")
+    assert torch.isfinite(st).all()
+
+
+def test_masked_places_do_not_spread():
+    """NaN in one sequence, in rows behind the sequences' and in padding rows'
+    states stays there."""
+    case = (1, 90, 20, 16, 1, [0, 40, 41, 90])
+    p, (dy, df), cu = scan_problem("f32", case)
+    args, kw = scan_call(p, cu)
+    g0 = m.ssd_selscan_bwd(*args, up(dy), **kw, d_final=up(df))
+    y0, f0 = m.ssd_selscan_fwd(*args, **kw)
+    w = up(torch.randn(4, 20))
+    c0, _ = m.ssd_conv_fwd(args[0], w, cu_seqlens=kw["cu_seqlens"])
+    args[0][0, 40] = float("nan")  # the sequence of one token
+    y, f = m.ssd_selscan_fwd(*args, **kw)
+    c, _ = m.ssd_conv_fwd(args[0], w, cu_seqlens=kw["cu_seqlens"])
+    g = m.ssd_selscan_bwd(*args, up(dy), **kw, d_final=up(df))
+    keep = [t for t in range(90) if t != 40]
+    assert torch.equal(y[0, keep], y0[0, keep]) and torch.equal(f[[0, 2]], f0[[0, 2]])
+    assert torch.equal(c[0, keep], c0[0, keep])
+    for k in ("dx", "dd_raw", "dz", "dB", "dC"):
+        assert torch.equal(g[k][0, keep], g0[k][0, keep]), k
+    assert torch.equal(g["dinit_state"][[0, 2]], g0["dinit_state"][[0, 2]])
+
+
+def test_offsets_past_32_bits():
+    """Pools and token strides whose far ends lie beyond 2^31 elements and 2^32
+    bytes: the same results as near ones."""
+    s = Source(21, "bf16")
+    H, N, P, far = 4, 128, 64, 66000
+    pool_ = torch.zeros((far, H, N, P), device=DEV)
+    near = up(s.f32(1, H, N, P))
+    pool_[far - 1] = near[0]
+    x, raw, B = up(s(1, H, P)), up(s(1, H)), up(s(1, 1, N))
+    slots = torch.tensor([far - 1], dtype=torch.int32, device=DEV)
+    y = m.ssd_step(x, raw, -1.0, B, B, pool_, slots=slots)
+    assert torch.equal(y, m.ssd_step(x, raw, -1.0, B, B, near)) and torch.equal(pool_[far - 1], near[0])
+    flat = pool_.view(far, 16, 2048)
+    a, x, d = up(-s.f32(16, 2048).exp()), up(s(1, 2048)), up(s.f32(2048))
+    near = flat[far - 1:].clone()
+    B = up(s(1, 1, 16))
+    y = m.ssd_selscan_step(x, x, d, a, B, B, flat, slots=slots)
+    assert torch.equal(y, m.ssd_selscan_step(x, x, d, a, B, B, near)) and torch.equal(flat[far - 1], near[0])
+    del pool_, flat
+    L, E, stride = 300, 40, (1 << 23) + 1
+    wide = torch.empty((1, L, stride), dtype=torch.bfloat16, device=DEV)
+    x = up(s(1, L, E))
+    xv = wide[..., 5:5 + E]
+    xv.copy_(x)
+    w, a, d = up(s.f32(4, E)), up(-s.f32(16, E).exp()), up(s.f32(E))
+    B = up(s(1, L, 1, 16))
+    assert torch.equal(m.ssd_conv_fwd(xv, w)[0], m.ssd_conv_fwd(x, w)[0])
+    assert torch.equal(m.ssd_norm_fwd(xv)[0], m.ssd_norm_fwd(x)[0])
+    assert torch.equal(m.ssd_selscan_fwd(xv, xv, d, a, B, B, z=xv)[0], m.ssd_selscan_fwd(x, x, d, a, B, B, z=x)[0])
+    dx = m.ssd_conv_bwd(xv, w, None, xv)["dx"]
+    assert torch.equal(dx, m.ssd_conv_bwd(x, w, None, x)["dx"])
+    del dx
+    g = m.ssd_selscan_bwd(xv, x, d, a, B, B, xv)
+    g0 = m.ssd_selscan_bwd(x, x, d, a, B, B, x)
+    assert all(torch.equal(g[k], g0[k]) for k in g)
 
 
 # ---- how calls run -------------------------------------------------------------------------
