@@ -408,26 +408,28 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
 constexpr int kFwdTile = 16, kShortTile = 4;
 constexpr int kFwdVec = 4;
 constexpr int kBwdTile = 16, kBwdShortTile = 8;
-constexpr int kBwdVec = 4;
+constexpr int kBwdVec = 4, kBwdShortVec = 2;
 
 // Channels a thread: fewer than a vector's are taken one by one.
 int vec_of(int32_t channels, int vec) { return channels >= vec ? vec : 1; }
 
 struct ConvBwdPlan {
     int64_t tiles, strips;
-    int32_t tile, tiles_per_row, iters;
+    int32_t tile, vec, tiles_per_row, iters;
 };
 
 ConvBwdPlan conv_bwd_plan(const ssd_conv_dims& d) {
     ConvBwdPlan pl;
     const int64_t len = d.seqlen, rows = d.batch;  // packed: one row
-    const int64_t groups = cdiv(cdiv(d.channels, vec_of(d.channels, kBwdVec)), 64);
-    // Runs of 16 tokens re-read 2 (W - 1) / 16 of their rows, those of 8 twice
-    // that (32768 tokens x 1792 channels: 95 us against 110, bf16; 155 against
-    // 165, float32); the short ones fill the chip where there are few tokens
-    // (4096 tokens: 29.2 us against 30.0).
-    pl.tile = rows * cdiv(len, kBwdTile) * groups >= 4 * 1024 && vec_of(d.channels, kBwdVec) > 1
-                  ? kBwdTile : kBwdShortTile;
+    // Runs of 16 tokens by 4 channels re-read 2 (W - 1) / 16 of their rows, those
+    // of 8 twice that (32768 tokens x 1792 channels: 95 us against 110, bf16; 155
+    // against 165, float32).  Where tokens are few, runs of 8 by 2 channels give
+    // enough waves to hide the loads (4096 tokens, float32: 25.7 us, by 4 channels
+    // 29.4, 16 by 4 30.0).
+    const bool many = rows * cdiv(len, kBwdTile) * cdiv(d.channels, 64 * kBwdVec) >= 4 * 1024;
+    pl.vec = vec_of(d.channels, many ? kBwdVec : kBwdShortVec);
+    pl.tile = pl.vec == kBwdVec ? kBwdTile : kBwdShortTile;
+    const int64_t groups = cdiv(cdiv(d.channels, pl.vec), 64);
     pl.tiles_per_row = (int32_t)imax(1, cdiv(len, pl.tile));
     pl.tiles = len == 0 ? 0 : rows * pl.tiles_per_row;
     // more tiles a wave (fewer partial rows) only while every CU keeps eight
@@ -497,10 +499,10 @@ void launch_conv_bwd(const ConvParams& p, int W, dim3 grid, hipStream_t s) {
     else conv_bwd_kernel<T, 4, V, TT><<<grid, dim3(256), 0, s>>>(p);
 }
 template <typename T>
-void launch_conv_bwd(const ConvParams& p, int W, int V, int tile, dim3 grid, hipStream_t s) {
+void launch_conv_bwd(const ConvParams& p, int W, int V, dim3 grid, hipStream_t s) {
     if (V == 1) launch_conv_bwd<T, 1, kBwdShortTile>(p, W, grid, s);
-    else if (tile == kBwdTile) launch_conv_bwd<T, kBwdVec, kBwdTile>(p, W, grid, s);
-    else launch_conv_bwd<T, kBwdVec, kBwdShortTile>(p, W, grid, s);
+    else if (V == kBwdVec) launch_conv_bwd<T, kBwdVec, kBwdTile>(p, W, grid, s);
+    else launch_conv_bwd<T, kBwdShortVec, kBwdShortTile>(p, W, grid, s);
 }
 
 }  // namespace
@@ -587,8 +589,7 @@ int ssd_conv_bwd(const ssd_conv_dims* dims, const ssd_conv_layout* layout, const
     hipStream_t s = (hipStream_t)stream;
     if (cu_seqlens && check_cu_env(cu_seqlens, d.nseq, T, s, &st)) return st;
     const ConvBwdPlan pl = conv_bwd_plan(d);
-    const int V = vec_of(d.channels, kBwdVec);
-    ConvParams p = conv_params(d, l, cu_seqlens, V);
+    ConvParams p = conv_params(d, l, cu_seqlens, pl.vec);
     p.x = x;
     p.weight = weight;
     p.bias = bias;
@@ -608,8 +609,8 @@ int ssd_conv_bwd(const ssd_conv_dims* dims, const ssd_conv_layout* layout, const
     p.state_items = dinit_state ? (int64_t)p.S * (d.width - 1) * p.nvec : 0;
     const int64_t grid = p.main_blocks + cdiv(p.state_items, 256);
     if (grid * 256 > kMaxThreads) return SSD_ERR_SHAPE;
-    if (d.dtype == SSD_BF16) launch_conv_bwd<bf16>(p, d.width, V, pl.tile, dim3((unsigned)grid), s);
-    else launch_conv_bwd<float>(p, d.width, V, pl.tile, dim3((unsigned)grid), s);
+    if (d.dtype == SSD_BF16) launch_conv_bwd<bf16>(p, d.width, pl.vec, dim3((unsigned)grid), s);
+    else launch_conv_bwd<float>(p, d.width, pl.vec, dim3((unsigned)grid), s);
     if ((st = launched()) != SSD_OK || (!dweight && !dbias)) return st;
     ColSum c = {};
     c.part = p.part;

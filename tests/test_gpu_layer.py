@@ -145,11 +145,12 @@ def test_conv(dtype, carry, case):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-def test_conv_long_runs(dtype):
+@pytest.mark.parametrize("L", [9000, 25000])
+def test_conv_long_runs(dtype, L):
     """Enough tokens that every tile and partial sum size is taken, against the
     same call in two shards chained through the state, and a sampled reference."""
     s = Source(3, dtype)
-    L, E, W = 9000, 520, 4
+    E, W = 520, 4
     x, w, bias, dy = s(1, L, E), s.f32(W, E, scale=0.5), s.f32(E), s(1, L, E)
     y, f = m.ssd_conv_fwd(up(x), up(w), up(bias))
     cut = 4097
