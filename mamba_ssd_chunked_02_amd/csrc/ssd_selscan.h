@@ -26,9 +26,9 @@
 // that enters it, without forming an exponential.  The state that leaves the
 // segment enters the next one, so a sequence needs no other launch and no
 // global scratch (scanning twice costs 8 issues a state entry and token where a
-// scan in order costs 6, but only this fills the chip).  The vector units are
-// busy 98 % of the time on the CUs that have a workgroup: 2 x 2048 tokens x 1536
-// channels x 16 states 49 us on 192 of the 256 CUs, 65536 packed tokens 548 us.
+// scan in order costs 6, but only this fills the chip).  The vector units bound
+// it: 2 x 2048 tokens x 1536 channels x 16 states 47 us on 192 of the 256 CUs,
+// 65536 packed tokens 538 us; their issue slots at 2.4 GHz are 94 % of that.
 // Per-token values (d, u, y) live in the quad's lanes, token
 // 4 i + k in lane k, and reach the other three as DPP operands.
 #pragma once

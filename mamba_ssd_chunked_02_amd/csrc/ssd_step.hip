@@ -48,7 +48,7 @@ struct StepParams {
     int32_t nslots, H, P, N, hpg, pieces;
 };
 
-// 64 sequences x 80 heads x 64 x 128 states: 67.3 us, 5.0 TB/s, what a copy of
+// 64 sequences x 80 heads x 64 x 128 states: 65.9 us, 5.1 TB/s, what a copy of
 // this size reaches (75 with loads predicated by row).
 // A workgroup takes CP headdim columns of one head: CP / 4 lanes across, the
 // other threads down the state rows, at most UN rows each at a time (all
@@ -142,8 +142,9 @@ struct SelStepParams {
 
 // A thread takes V channels of one sequence, all their state entries.  Small
 // workgroups even out over the CUs: 128 sequences x 5120 channels x 16 states 26.1
-// us with 64 or 128 threads (3.4 TB/s), 27.3 with 256, 32.4 with 512; two channels
-// a thread or all 16 entries at once are no faster (27.5 to 34).
+// us with 64 or 128 threads, 27.3 with 256, 32.4 with 512; two channels a thread or
+// all 16 entries at once are no faster (27.5 to 34).  As it stands now: 20.2 us,
+// 4.4 TB/s.
 constexpr int kSelThreads = 128;
 
 template <typename T, int V>
