@@ -529,8 +529,10 @@ int ssd_selscan_fwd(const ssd_selscan_dims* dims, const ssd_selscan_layout* layo
 /*
  * Its gradients: dy like y, d_final [S, N, E] float32 or NULL for zeros.
  * dx, dd_raw, dz, dB, dC of dtype, laid out like their inputs (dz required
- * with z); dA [N, E], dD, dd_init [E], dinit_state [S, N, E] float32, each
- * NULL to skip (dinit_state not overlapping d_final).  workspace:
+ * with z; SSD_ERR_SHAPE where the rows of B or C share elements, as those of
+ * a broadcast group or token do, since their gradients would too); dA [N, E],
+ * dD, dd_init [E], dinit_state [S, N, E] float32, each NULL to skip
+ * (dinit_state not overlapping d_final).  workspace:
  * ssd_selscan_bwd_workspace_bytes(dims), 256-byte aligned.
  */
 size_t ssd_selscan_bwd_workspace_bytes(const ssd_selscan_dims* dims);

@@ -214,6 +214,19 @@ def _like(t):
     return torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device)
 
 
+def _apart(t):
+    """t itself where each of its elements has a place of its own, else (an
+    expanded view) a dense copy: its gradient can then be laid out like it."""
+    if t.is_contiguous():
+        return t
+    extent = 1
+    for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n > 1):
+        if stride < extent:
+            return t.contiguous()
+        extent += stride * (size - 1)
+    return t
+
+
 def _workspace(name, dims, x):
     need = _entry(name)(ctypes.byref(dims))
     return torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
@@ -465,10 +478,12 @@ def ssd_selscan_fwd(x, d_raw, d_init, A, B, C, D=None, z=None, init_state=None, 
 def ssd_selscan_bwd(x, d_raw, d_init, A, B, C, dy, D=None, z=None, init_state=None,
                     cu_seqlens=None, d_final=None, workspace=None):
     """Gradients of ``ssd_selscan_fwd``: a dict with dx, dd_raw, dB, dC (and dz
-    with a gate), each laid out like its input, and in fp32 dA [N, E], dd_init,
-    dD [E] (the gradient at zeros without a D) and dinit_state [S, N, E] (at
-    zeros without an init_state).  ``d_final`` is the gradient of final_state or
-    None for zeros."""
+    with a gate), each laid out like its input (dB and dC dense where B or C is
+    an expanded view: every token and group has its own gradient), and in fp32
+    dA [N, E], dd_init, dD [E] (the gradient at zeros without a D) and
+    dinit_state [S, N, E] (at zeros without an init_state).  ``d_final`` is the
+    gradient of final_state or None for zeros."""
+    B, C = _apart(B), _apart(C)
     dims, lay, cu, state = _selscan_arguments(x, d_raw, d_init, A, B, C, D, z, cu_seqlens, None, dy)
     _floats(x, (init_state, state, "init_state"), (d_final, state, "d_final"))
     N, E = A.shape

@@ -35,6 +35,22 @@ __device__ __forceinline__ uint32_t fdiv(uint32_t n, FastDiv f) {
     return (__umulhi(n, f.m) + n) >> f.l;
 }
 
+// Whether the rows of n elements at i * t + j * g, 0 <= i < T, 0 <= j < G, have
+// no element in common: what a gradient that is laid out like its input needs
+// (strides >= 0; a stride over one index counts for nothing).
+inline bool rows_apart(int64_t T, int64_t t, int64_t G, int64_t g, int64_t n) {
+    if (T <= 1) return G <= 1 || g >= n;
+    if (G <= 1) return t >= n;
+    if (t < n || g < n) return false;
+    if (t >= (G - 1) * g + n || g >= (T - 1) * t + n) return true;  // one lies inside the other
+    for (int64_t j = 1; j < G; ++j)  // rows j apart in one index meet rows i or i + 1 apart in the other
+        for (int64_t i = j * g / t, k = i + 1; i <= k && i < T; ++i) {
+            const int64_t d = j * g - i * t;
+            if ((d < 0 ? -d : d) < n) return false;
+        }
+    return true;
+}
+
 // A span launch's grid decode, filled in by its launcher (set_decode) from
 // the sizes below and the launch's heads per workgroup.
 struct Decode {

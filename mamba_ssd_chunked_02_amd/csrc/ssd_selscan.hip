@@ -500,6 +500,10 @@ int ssd_selscan_bwd(const ssd_selscan_dims* dims, const ssd_selscan_layout* layo
                        &p, &pl);
     if (st != SSD_OK) return st;
     if (pl.T * dims->ngroups * 8 * pl.NR + 256 > kMaxThreads) return SSD_ERR_SHAPE;
+    // dB and dC take the places of B and C: no two of their rows may share one
+    if (pl.T > 0 && (!rows_apart(pl.T, p.bs_t, p.G, p.bs_g, p.N) ||
+                     !rows_apart(pl.T, p.cs_t, p.G, p.cs_g, p.N)))
+        return SSD_ERR_SHAPE;
     if (pl.T > 0 && (!dy || !dx || !dd_raw || !dB || !dC || (z && !dz))) return SSD_ERR_NULL_ARG;
     const size_t e = elem_size(dims->dtype);
     for (const void* q : {dy, (const void*)dx, (const void*)dd_raw, (const void*)dB,

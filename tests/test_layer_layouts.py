@@ -1,0 +1,76 @@
+"""Layouts the operators around the scan take or refuse (no GPU): rows that share
+elements, strides of dimensions of size 1, workspaces.  Made-up pointers are only
+passed where no GPU exists; the binding's calls run with the launch left out."""
+import ctypes
+
+import pytest
+import torch
+
+import mamba_ssd_chunked_02_amd as m
+from mamba_ssd_chunked_02_amd import _layer as ly
+from test_layer_host import FAKE, SHAPE, WORKSPACE, call, needs_no_gpu, scan_dims
+
+
+@pytest.fixture
+def launches(monkeypatch):
+    """The entry points' arguments instead of a launch."""
+    seen = []
+    monkeypatch.setattr(ly, "_launch", lambda name, x, *args: seen.append((name, args)))
+    return seen
+
+
+def scan_inputs(b, L, E, N):
+    z = lambda *s: torch.zeros(s)
+    return (z(b, L, E), z(b, L, E), z(E), z(N, E))
+
+
+# ---- gradients of inputs whose rows share elements -----------------------------------------
+
+def shares(T, t, G, g, n):
+    """By writing down every element."""
+    at = [i * t + j * g + k for i in range(T) for j in range(G) for k in range(n)]
+    return len(set(at)) < len(at)
+
+
+@needs_no_gpu
+def test_selscan_bwd_refuses_shared_rows():
+    """B and C whose rows share elements are refused where their gradients would be
+    written there, whatever way they do; layouts that keep them apart are not."""
+    N, seen = 4, set()
+    for b, L, G in ((1, 1, 1), (1, 1, 3), (2, 1, 1), (1, 3, 1), (2, 2, 3), (1, 5, 2)):
+        for t in (0, 3, 4, 5, 8, 11, 12, 13, 21):
+            for g in (0, 2, 4, 5, 9, 16, 20, 24):
+                bad = shares(b * L, t, G, g, N)
+                seen.add((b * L > 1, G > 1, bad))
+                d = scan_dims(batch=b, seqlen=L, ngroups=G, channels=6 * G, d_state=N)
+                for lay in ([t, g, G * N, N], [G * N, N, t, g]):
+                    full = m.SsdSelscanLayout(*[6 * G] * 3, *lay, *[6 * G] * 2)
+                    rc = call("ssd_selscan_bwd", d, layout=full, ws=None)  # else stopped here
+                    assert rc == (SHAPE if bad else WORKSPACE), (b, L, G, t, g, rc)
+    assert len(seen) == 7  # one row never shares, everything else both does and does not
+    # with no tokens nothing is written
+    d = scan_dims(seqlen=0, ngroups=2)
+    assert call("ssd_selscan_bwd", d, layout=m.SsdSelscanLayout(64, 64, 64, 0, 0, 0, 0, 64, 64),
+                ws=None) == WORKSPACE
+
+
+def test_selscan_bwd_gives_expanded_inputs_dense_gradients(launches):
+    """Where B or C is expanded over groups, tokens or the batch, each token and
+    group has a gradient of its own; other layouts are kept."""
+    b, L, E, N, G = 2, 3, 8, 4, 2
+    x, raw, dinit, A = scan_inputs(b, L, E, N)
+    dense = torch.zeros(b, L, G, N)
+    for B in (torch.zeros(b, L, 1, N).expand(b, L, G, N), torch.zeros(1, 1, G, N).expand(b, L, G, N),
+              torch.zeros(1, L, G, N).expand(b, L, G, N),
+              torch.zeros(100).as_strided((b, L, G, N), (3 * L, 3, 12, 1))):
+        for args in ((B, dense), (dense, B)):
+            g = m.ssd_selscan_bwd(x, raw, dinit, A, *args, x)
+            for k in ("dB", "dC"):
+                assert g[k].shape == dense.shape and g[k].is_contiguous()
+            lay = launches.pop()[1][1]
+            assert (lay.B_token, lay.B_group, lay.C_token, lay.C_group) == (G * N, N, G * N, N)
+    wide = torch.zeros(b, L, 5 + G * N)[..., 5:].unflatten(-1, (G, N))
+    swapped = torch.zeros(G, b, L, N).permute(1, 2, 0, 3)
+    for B in (wide, swapped):
+        g = m.ssd_selscan_bwd(x, raw, dinit, A, B, dense, x)
+        assert g["dB"].stride() == B.stride()
