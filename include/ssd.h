@@ -320,7 +320,9 @@ int ssd_fwd_bidir(const ssd_dims* dims, const ssd_tuning* tuning, const ssd_layo
  *   workspace   at least ssd_bwd_workspace_bytes(dims) bytes, 256-byte
  *               aligned, no initialization needed; calls that overlap in
  *               time need separate workspaces
- * x, B, C, dy, dx, dB and dC must be 16-byte aligned.  The gradients must
+ * x, B, C, dy, dx, dB and dC must be 16-byte aligned.  Rows of x, d_raw, B
+ * or C that share elements (a broadcast head, group or token) are refused
+ * with SSD_ERR_SHAPE: their gradients would too.  The gradients must
  * not overlap the inputs.  Outputs for tokens outside every cu_seqlens
  * segment are not written.  Returns SSD_OK once the work is queued.
  */

@@ -517,6 +517,24 @@ def _like(t):
     return torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device)
 
 
+def _is_apart(t):
+    """Whether each of t's elements has a place of its own (not so in an expanded
+    view), so that its gradient can be laid out like it."""
+    if t.is_contiguous():
+        return True
+    extent = 1
+    for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n > 1):
+        if stride < extent:
+            return False
+        extent += stride * (size - 1)
+    return True
+
+
+def _apart(t):
+    """t, or a dense copy where its elements share places."""
+    return t if _is_apart(t) else t.contiguous()
+
+
 def prepare_bwd(x, d_raw, d_init, B, C, y, dy, chunk_size=CHUNK, init_state=None,
                 cu_seqlens=None, reverse=False, d_final=None, workspace=None, tuning=None,
                 grads=None) -> PreparedBwd:
@@ -524,9 +542,11 @@ def prepare_bwd(x, d_raw, d_init, B, C, y, dy, chunk_size=CHUNK, init_state=None
     gradients (dict: dx, dd_raw, dB, dC, dinit_state, dd_init) and the
     workspace when not given.  dx, dd_raw, dB and dC are laid out like x,
     d_raw, B and C (the library writes each gradient with its input's
-    strides); ``grads`` may supply some or all of them, e.g. as views of one
-    projection-gradient buffer laid out like the inputs' projection.  ``y``
-    (the forward output) is optional: the library does not read it."""
+    strides, so inputs whose elements share places, as those of an expanded
+    view do, are refused); ``grads`` may supply some or all of them, e.g. as
+    views of one projection-gradient buffer laid out like the inputs'
+    projection.  ``y`` (the forward output) is optional: the library does not
+    read it."""
     if x.dim() != 4 or d_raw.dim() != 3 or B.dim() != 4 or C.dim() != 4:
         raise ValueError("x [b,L,H,P], d_raw [b,L,H], B/C [b,L,G,N] expected")
     b, L, H, P = x.shape
@@ -540,6 +560,10 @@ def prepare_bwd(x, d_raw, d_init, B, C, y, dy, chunk_size=CHUNK, init_state=None
         raise ValueError("shape mismatch between x, d_raw, B and C")
     if (y is not None and tuple(y.shape) != (b, L, H, P)) or tuple(dy.shape) != (b, L, H, P):
         raise ValueError("y and dy must have x's shape")
+    for name, t in (("x", x), ("d_raw", d_raw), ("B", B), ("C", C)):
+        if not _is_apart(t):
+            raise ValueError(f"{name}'s elements share places (an expanded view?): their gradients "
+                             "would too")
     G, N = B.shape[2], B.shape[3]
     if cu_seqlens is not None:
         if cu_seqlens.dtype != torch.int32 or cu_seqlens.device != dev or cu_seqlens.dim() != 1:
@@ -587,9 +611,10 @@ def ssd_bwd(x, d_raw, d_init, B, C, y, dy, chunk_size=CHUNK, init_state=None,
     the forward output, is accepted for the call's shape but not read; None
     is fine), dL/dy (``dy``, same layout rules as y) and
     optionally dL/d final_state (``d_final``), returns a dict with dx,
-    dd_raw, dB, dC (input dtype, each laid out like its input), dinit_state
-    [S,H,N,P] and dd_init [1] (fp32).  Launches on torch's current stream."""
-    call = prepare_bwd(x, d_raw, d_init, B, C, y, dy, chunk_size, init_state, cu_seqlens,
-                       reverse, d_final, workspace, tuning, grads)
+    dd_raw, dB, dC (input dtype, each laid out like its input, dense where
+    that is an expanded view), dinit_state [S,H,N,P] and dd_init [1] (fp32).
+    Launches on torch's current stream."""
+    call = prepare_bwd(_apart(x), _apart(d_raw), d_init, _apart(B), _apart(C), y, dy, chunk_size,
+                       init_state, cu_seqlens, reverse, d_final, workspace, tuning, grads)
     with torch.cuda.device(x.device):
         return call.run()

@@ -11,7 +11,7 @@ import functools
 
 import torch
 
-from ._binding import _DTYPES, SsdDims, SsdError, SsdLayout, library
+from ._binding import _DTYPES, SsdDims, SsdError, SsdLayout, _apart, library
 
 _P = ctypes.c_void_p
 _I32, _I64, _F32, _SIZE = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
@@ -212,19 +212,6 @@ def _output(x):
 def _like(t):
     """An uninitialized tensor with t's shape and strides."""
     return torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device)
-
-
-def _apart(t):
-    """t itself where each of its elements has a place of its own, else (an
-    expanded view) a dense copy: its gradient can then be laid out like it."""
-    if t.is_contiguous():
-        return t
-    extent = 1
-    for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n > 1):
-        if stride < extent:
-            return t.contiguous()
-        extent += stride * (size - 1)
-    return t
 
 
 def _workspace(name, dims, x):

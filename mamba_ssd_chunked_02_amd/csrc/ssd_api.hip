@@ -744,6 +744,12 @@ int ssd_bwd_ex(const ssd_dims* dims, const ssd_tuning* tuning, const ssd_layout*
     const ssd_layout lay = resolve_layout(d, layout);
     const int lc = check_layout(d, lay, true);
     if (lc != SSD_OK) return lc;
+    // each gradient takes the places of its input: no two rows may share one
+    if (T > 0 && (!ssd::rows_apart(T, lay.x_token, d.nheads, lay.x_head, d.headdim) ||
+                  !ssd::rows_apart(T, lay.d_raw_token, d.nheads, lay.d_raw_head, 1) ||
+                  !ssd::rows_apart(T, lay.B_token, d.ngroups, lay.B_group, d.d_state) ||
+                  !ssd::rows_apart(T, lay.C_token, d.ngroups, lay.C_group, d.d_state)))
+        return SSD_ERR_SHAPE;
     const int64_t esz = d.dtype == SSD_BF16 ? 2 : 4;
     if (!aligned16(x) || !aligned16(B) || !aligned16(C) || !aligned16(dy) || !aligned16(dx) ||
         !aligned16(dB) || !aligned16(dC))

@@ -5,7 +5,7 @@ import torch
 
 import mamba_ssd_chunked_02_amd as m
 from oracle import layer_ops as lo
-from test_gpu_layer import TYPES, dd, scan_call, scan_problem, up, within
+from test_gpu_layer import TYPES, Source, dd, scan_call, scan_problem, up, within
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +33,21 @@ def test_selscan_bwd_of_expanded_inputs(dtype, case, over):
     K = 4 * (64 + 4 * b * L) + 4 * E
     for k in "BC":
         within(got["d" + k], rg[k], K, "d" + k)
+
+
+@pytest.mark.parametrize("name,dim", [("B", 2), ("C", 2), ("B", 1), ("C", 0), ("x", 2), ("d_raw", 2)])
+def test_ssd_bwd_of_expanded_inputs(name, dim):
+    """The SSD scan's gradients of expanded views, as with dense copies."""
+    s = Source(31, "bf16")
+    b, L, H, P, G, N = 2, 130, 4, 32, 2, 32
+    ins = {"x": s(b, L, H, P), "d_raw": s(b, L, H), "B": s(b, L, G, N), "C": s(b, L, G, N)}
+    small = ins[name].narrow(dim, 0, 1)
+    ins[name] = small.expand_as(ins[name]).contiguous()
+    dy, ins = up(s(b, L, H, P)), {k: up(v) for k, v in ins.items()}
+
+    def grads(x, d_raw, B, C):
+        return m.ssd_bwd(x, d_raw, -2.0, B, C, None, dy)
+
+    want = grads(**ins)
+    got = grads(**(ins | {name: up(small).expand_as(ins[name])}))
+    assert got.keys() == want.keys() and all(torch.equal(got[k], want[k]) for k in want)

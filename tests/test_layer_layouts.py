@@ -1,13 +1,15 @@
-"""Layouts the operators around the scan take or refuse (no GPU): rows that share
-elements, strides of dimensions of size 1, workspaces.  Made-up pointers are only
+"""Layouts the operators take or refuse (no GPU): rows that share elements, strides of
+dimensions of size 1, workspaces.  Made-up pointers are only
 passed where no GPU exists; the binding's calls run with the launch left out."""
-import ctypes
+import contextlib
 
 import pytest
 import torch
 
 import mamba_ssd_chunked_02_amd as m
 from mamba_ssd_chunked_02_amd import _layer as ly
+from test_abi_host import call as ssd_call
+from test_abi_host import call_bwd, lay
 from test_layer_host import FAKE, SHAPE, WORKSPACE, call, needs_no_gpu, scan_dims
 
 
@@ -74,3 +76,43 @@ def test_selscan_bwd_gives_expanded_inputs_dense_gradients(launches):
     for B in (wide, swapped):
         g = m.ssd_selscan_bwd(x, raw, dinit, A, B, dense, x)
         assert g["dB"].stride() == B.stride()
+
+
+@needs_no_gpu
+@pytest.mark.parametrize("name,inner,row", [("x", "x_head", 16), ("d_raw", "d_raw_head", 1),
+                                            ("B", "B_group", 16), ("C", "C_group", 16)])
+def test_ssd_bwd_refuses_shared_rows(name, inner, row):
+    """The SSD scan's gradients are laid out like x, d_raw, B and C too."""
+    for b, L in ((1, 1), (1, 5), (2, 3)):
+        d = m.make_dims(b, L, 2, 16, 16, ngroups=2)
+        for t in (0, 8, 16, 24, 32, 40, 48):
+            for h in (0, 8, 16, 24, 80, 96):
+                l = lay(m, d, **{name + "_token": t, inner: h})
+                bad = shares(b * L, t, 2, h, row)
+                assert call_bwd(m, d, layout=l, ws=None) == (SHAPE if bad else WORKSPACE), (b, L, t, h)
+                assert ssd_call(m, d, layout=l, ws=None) == WORKSPACE  # the forward only reads them
+    l = lay(m, m.make_dims(1, 0, 2, 16, 16), **{name + "_token": 0, inner: 0})
+    assert call_bwd(m, m.make_dims(1, 0, 2, 16, 16), layout=l, ws=None) == WORKSPACE
+
+
+def test_ssd_bwd_binding_of_expanded_inputs(monkeypatch):
+    """A single call takes dense copies; a prepared one, which may run again after its
+    inputs have changed, refuses."""
+    import mamba_ssd_chunked_02_amd._binding as bind
+    b, L, H, P, G, N = 2, 3, 4, 16, 2, 16
+    full = {"x": torch.zeros(b, L, H, P), "d_raw": torch.zeros(b, L, H),
+            "B": torch.zeros(b, L, G, N), "C": torch.zeros(b, L, G, N)}
+    dy = torch.zeros(b, L, H, P)
+    seen = []
+    monkeypatch.setattr(bind.PreparedBwd, "run", lambda self: seen.append(self) or self.grads)
+    for k, t in full.items():
+        for dim in (0, 1, 2):
+            ins = full | {k: t.narrow(dim, 0, 1).expand_as(t)}
+            with pytest.raises(ValueError, match=k + ".*share"):
+                m.prepare_bwd(ins["x"], ins["d_raw"], -1.0, ins["B"], ins["C"], None, dy)
+            with monkeypatch.context() as c:
+                c.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+                g = m.ssd_bwd(ins["x"], ins["d_raw"], -1.0, ins["B"], ins["C"], None, dy)
+            assert g["d" + k].is_contiguous() and g["d" + k].shape == t.shape
+    l = seen[-1].layout
+    assert (l.B_token, l.B_group, l.C_token, l.C_group) == (G * N, N, G * N, N)
