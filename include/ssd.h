@@ -496,9 +496,10 @@ int ssd_conv_step(const ssd_conv_dims* dims, const ssd_conv_layout* layout,
  * group e / (E / G)); d_init, D [E] and A [N, E] float32; D NULL for 0, z
  * NULL for no gate; init_state [S, N, E] float32 or NULL for zeros,
  * final_state likewise, NULL to skip, not overlapping init_state.
- * exp(d A) is formed as exp2(d A log2(e)): A <= 0 is meant, and a positive A
- * grows without a guard.  workspace: ssd_selscan_fwd_workspace_bytes(dims),
- * 256-byte aligned, no initialization (may be NULL where that is 0).
+ * exp(d A) is formed as exp2(d A log2(e)): A <= 0 is meant (-inf too, which
+ * forgets), a positive A grows without a guard, a NaN stays one.  workspace:
+ * ssd_selscan_fwd_workspace_bytes(dims), 256-byte aligned, no initialization
+ * (may be NULL where that is 0).
  */
 #define SSD_SELSCAN_MAX_STATE 64
 #define SSD_SELSCAN_MAX_CHANNELS (1 << 20)

@@ -104,6 +104,10 @@ __device__ __forceinline__ float sigmoid(float v) {
     return __builtin_amdgcn_rcpf(1.f + fexp2(-v * kLog2e));
 }
 
+// A rate with -inf kept finite: times a step of 0 it would be NaN.  A comparison,
+// not a maximum, which would give the number where the rate is NaN.
+__device__ __forceinline__ float finite_rate(float a) { return a < -3e38f ? -3e38f : a; }
+
 // d/dv of v sigmoid(v)
 __device__ __forceinline__ float silu_slope(float v, float s) { return s * (1.f + v * (1.f - s)); }
 

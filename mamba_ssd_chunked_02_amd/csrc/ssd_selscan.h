@@ -367,14 +367,13 @@ __device__ __forceinline__ void put_rows(float* dst, const Place& o, const Rows<
     for (int k = 0; k < r.K; ++k) q[k * TK * 2 * NP] = value_of<T>(r.v[k]);
 }
 
-// A[n] log2(e) of the lane's channel and entries (0 where it has none).  A rate
-// of -inf is kept finite: times a step of 0 it would be NaN.
+// A[n] log2(e) of the lane's channel and entries (0 where it has none).
 template <int NR>
 __device__ __forceinline__ void load_rates(const SelParams& p, const Place& o, float (&A2)[NR]) {
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
         const int n = o.nl * NR + r;
-        A2[r] = o.live && n < p.N ? fmaxf(p.A[(int64_t)n * p.E + o.ch] * kLog2e, -3e38f) : 0.f;
+        A2[r] = o.live && n < p.N ? finite_rate(p.A[(int64_t)n * p.E + o.ch] * kLog2e) : 0.f;
     }
 }
 // The lane's entries of its sequence's row of [S, N, E] (null reads 0, stores nothing).

@@ -39,6 +39,15 @@ __device__ __forceinline__ Run run_of(const SelParams& p, const Place& o) {
     return r;
 }
 
+// A token's decay.  The product takes 0 times anything as 0: behind the sequence,
+// where d is 0, the decay is 1 also for a rate that is NaN, and q reaches the last
+// token unchanged.
+__device__ __forceinline__ float decay_of(float d, float A2) {
+    float p;
+    asm("v_mul_legacy_f32 %0, %1, %2" : "=v"(p) : "v"(d), "v"(A2));
+    return fexp2(p);
+}
+
 template <typename T, int NR>
 __global__ __launch_bounds__(64, NR <= 8 ? 4 : 2) void selscan_runs_kernel(SelParams p) {
     using S = Shape<NR>;
@@ -97,7 +106,7 @@ __global__ __launch_bounds__(64, NR <= 8 ? 4 : 2) void selscan_runs_kernel(SelPa
             const float dt = quad_lane(d[t / 4], t % 4), ut = quad_lane(u[t / 4], t % 4);
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
-                a[t][r] = fexp2(dt * A2[r]);
+                a[t][r] = decay_of(dt, A2[r]);
                 h[r] = a[t][r] * h[r] + b[r] * ut;
             }
             if (t & 1) keep_order();
@@ -274,7 +283,7 @@ __global__ __launch_bounds__(64, Shape<NR>::kBwdPerSimd) void selscan_grads_kern
             const float dt = quad_lane(d[t / 4], t % 4), ut = quad_lane(u[t / 4], t % 4);
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
-                a[t][r] = fexp2(dt * A2[r]);
+                a[t][r] = decay_of(dt, A2[r]);
                 hs[t][r] = a[t][r] * (t ? hs[t - 1][r] : hin[r]) + b[r] * ut;
             }
             if (t & 1) keep_order();

@@ -196,8 +196,7 @@ __global__ __launch_bounds__(kSelThreads) void selscan_step_kernel(SelStepParams
             const float bn = (float)B[n], cn = (float)C[n];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                // a rate of -inf times a step of 0 would be NaN
-                s[i][j] = fexp2(d[j] * fmaxf(a[i][j], -3e38f)) * s[i][j] + bn * u[j];
+                s[i][j] = fexp2(d[j] * finite_rate(a[i][j])) * s[i][j] + bn * u[j];
                 acc[j] += cn * s[i][j];
             }
             store_own<float, V>(out + (int64_t)n * p.E, skip, s[i]);
