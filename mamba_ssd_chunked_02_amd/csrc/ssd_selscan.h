@@ -188,7 +188,7 @@ __device__ __forceinline__ void lds_put(float* p, const float (&v)[NR]) {
 // d of a token, 0 where it does not count.  The softplus is formed either way:
 // a branch around it costs more than its 20 operations.
 __device__ __forceinline__ float step_of(float raw, bool counts) {
-    float d = softplus(raw);
+    float d = step_softplus(raw);
     asm volatile("" : "+v"(d));
     return counts ? d : 0.f;
 }

@@ -80,7 +80,7 @@ __global__ __launch_bounds__(256) void step_kernel(StepParams p) {
     float* out = p.new_state + at;
     const T* B = (const T*)p.B + b * p.bs_t + g * p.bs_g;
     const T* C = (const T*)p.C + b * p.cs_t + g * p.cs_g;
-    const float d = softplus((float)((const T*)p.d_raw)[b * p.ds_t + h * p.ds_h] + p.d_init);
+    const float d = step_softplus((float)((const T*)p.d_raw)[b * p.ds_t + h * p.ds_h] + p.d_init);
     const float decay = fexp2(-d * kLog2e);
     float u[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
     load_vec<T, 4>((const T*)p.x + b * p.xs_t + h * p.xs_h + c, 4, u);
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(kSelThreads) void selscan_step_kernel(SelStepParams
     load_vec<float, V>(p.d_init + e, V, r);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        d[j] = softplus(d[j] + r[j]);
+        d[j] = step_softplus(d[j] + r[j]);
         u[j] = d[j] * x[j];
         d[j] *= kLog2e;
     }

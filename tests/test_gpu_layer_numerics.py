@@ -59,3 +59,42 @@ def test_selscan_rates_of_minus_infinity_backward(dtype):
     rg = lo.gradients(lambda **k: lo.selscan(**k, cu=cu), ins, [dd(dy), dd(df)])
     for k, ref in rg.items():
         within(g[GRADS[k]], ref, 4 * (64 + 4 * 75) + (4 * 20 if k in "BC" else 0), k)
+
+
+def steps_and_values():
+    """Raw steps over the range that layers use and its ends, and softplus of them."""
+    z = torch.cat([torch.linspace(-4.2, -2, 3200), torch.linspace(-30, 30, 896)]).float()
+    return z, torch.log1p(torch.exp(-z.double().abs())) + z.double().clamp(min=0)
+
+
+def steps_right(got, z, exact):
+    """d = max(z, 0) + log(1 + v) with v = e^-|z|.  In units of 2^-24: |z| for the rounded
+    exponent and 0.25 |z| for its rounded factor log2(e), 2 each for the hardware's exp2
+    and reciprocal, and 4 more roundings."""
+    err = (got.double().cpu().flatten() / exact - 1).abs()
+    units = 8 + 1.25 * z.double().abs()
+    assert (err <= units * 2.0 ** -24).all(), (err / units * 2 ** 24).max().item()
+
+
+@pytest.mark.parametrize("form", ["scan", "gradient", "token", "ssd_token"])
+def test_step_sizes_keep_their_low_bits(form):
+    """With rates of 0 and ones for the rest one token's output is the step itself."""
+    z, exact = steps_and_values()
+    E = len(z)
+    one = lambda *s: torch.ones(s, device=DEV)
+    A, dinit = torch.zeros(1, E, device=DEV), torch.zeros(E, device=DEV)
+    if form == "ssd_token":
+        B = torch.zeros(64, 1, 16, device=DEV)
+        B[..., 0] = 1
+        y = m.ssd_step(one(64, E // 64, 16), up(z.view(64, -1)), 0.0, B, B,
+                       torch.zeros(64, E // 64, 16, 16, device=DEV))
+        assert (y == y[..., :1]).all()
+        got = y[..., 0]
+    elif form == "token":
+        got = m.ssd_selscan_step(one(1, E), up(z[None]), dinit, A, one(1, 1, 1), one(1, 1, 1),
+                                 torch.zeros(1, 1, E, device=DEV))
+    else:
+        args = (one(1, 1, E), up(z[None, None]), dinit, A, one(1, 1, 1, 1), one(1, 1, 1, 1))
+        got = m.ssd_selscan_fwd(*args)[0] if form == "scan" else m.ssd_selscan_bwd(
+            *args, one(1, 1, E))["dx"]
+    steps_right(got, z, exact)
