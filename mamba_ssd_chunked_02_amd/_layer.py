@@ -145,6 +145,8 @@ def _floats(x, *named):
             raise ValueError(f"{name} must be contiguous float32 {list(shape)} on {x.device}")
 
 
+# Of a dimension of size 1 torch keeps any stride; the helpers below give the dense one.
+
 def _tokens(t, name, shape):
     """Token stride of a [b, L, E] tensor whose rows are contiguous and whose
     batch rows are L tokens apart."""
@@ -158,7 +160,7 @@ def _tokens(t, name, shape):
         raise ValueError(f"{name} needs a contiguous last dimension")
     if L == 1:
         # one token a row: the batch stride is the token stride
-        return sb if b > 1 else max(E, st)
+        return sb if b > 1 else E
     if b > 1 and sb != L * st:
         raise ValueError(f"{name} needs batch stride L * token stride")
     return st
@@ -174,8 +176,10 @@ def _groups(t, name, shape):
     sb, st, sg, sn = t.stride()
     if N > 1 and sn != 1:
         raise ValueError(f"{name} needs a contiguous last dimension")
+    if G == 1:
+        sg = N
     if L == 1:
-        return (sb if b > 1 else st), sg
+        return (sb if b > 1 else G * N), sg
     if b > 1 and sb != L * st:
         raise ValueError(f"{name} needs batch stride L * token stride")
     return st, sg
@@ -189,18 +193,19 @@ def _rows(t, name, shape):
         return shape[1]
     if shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} needs a contiguous last dimension")
-    return t.stride(0) if shape[0] > 1 else max(shape[1], t.stride(0))
+    return t.stride(0) if shape[0] > 1 else shape[1]
 
 
 def _heads(t, name, shape):
     """(row, head) strides of a [b, H, P] tensor with contiguous last dimension."""
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}")
+    b, H, P = shape
     if t.is_contiguous():
-        return shape[1] * shape[2], shape[2]
-    if shape[2] > 1 and t.stride(2) != 1:
+        return H * P, P
+    if P > 1 and t.stride(2) != 1:
         raise ValueError(f"{name} needs a contiguous last dimension")
-    return t.stride(0), t.stride(1)
+    return t.stride(0) if b > 1 else H * P, t.stride(1) if H > 1 else P
 
 
 def _output(x):
@@ -264,7 +269,7 @@ def _matrix(t, name, width):
     m = t.view(-1, width)  # raises where the leading dimensions do not form one stride
     if width > 1 and m.stride(1) != 1:
         raise ValueError(f"{name} needs a contiguous last dimension")
-    return m.shape[0], (m.stride(0) if m.shape[0] > 1 else max(width, m.stride(0)))
+    return m.shape[0], (m.stride(0) if m.shape[0] > 1 else width)
 
 
 def ssd_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None):
@@ -539,7 +544,9 @@ def ssd_step(x, d_raw, d_init, B, C, state, slots=None, new_state=None, y=None):
         y = _output(x)
     else:
         _same(x, (y, "y"))
-    lay = _struct(SsdLayout, *_heads(x, "x", x.shape), *d_raw.stride(), *_heads(B, "B", (b, G, N)),
+    raw = (H, 1) if d_raw.is_contiguous() else (d_raw.stride(0) if b > 1 else H,
+                                                d_raw.stride(1) if H > 1 else 1)
+    lay = _struct(SsdLayout, *_heads(x, "x", x.shape), *raw, *_heads(B, "B", (b, G, N)),
                     *_heads(C, "C", (b, G, N)), *_heads(y, "y", x.shape))
     dims = _struct(SsdDims, b, 1, H, P, N, G, 64, 0, code)
     _launch("ssd_step", x, dims, lay, x.data_ptr(), d_raw.data_ptr(), float(d_init), _at(B), _at(C),

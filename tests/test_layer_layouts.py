@@ -2,6 +2,7 @@
 dimensions of size 1, workspaces.  Made-up pointers are only
 passed where no GPU exists; the binding's calls run with the launch left out."""
 import contextlib
+import ctypes
 
 import pytest
 import torch
@@ -116,3 +117,82 @@ def test_ssd_bwd_binding_of_expanded_inputs(monkeypatch):
             assert g["d" + k].is_contiguous() and g["d" + k].shape == t.shape
     l = seen[-1].layout
     assert (l.B_token, l.B_group, l.C_token, l.C_group) == (G * N, N, G * N, N)
+
+
+# ---- strides of dimensions of size 1 -------------------------------------------------------
+
+FAR = 1 << 25  # past the largest stride there is
+
+
+def apart(*shape, **far):
+    """A view of this shape whose dimensions dN of size 1 have the stride given: nothing is
+    that far apart."""
+    stride, step = [], 1
+    for n in reversed(shape):
+        stride.insert(0, step)
+        step *= n
+    for k, v in far.items():
+        assert shape[int(k[1:])] == 1
+        stride[int(k[1:])] = v
+    return torch.zeros(max(step, 1)).as_strided(shape, stride)
+
+
+def padded(*shape):
+    """Rows 3 elements further apart than dense ones."""
+    return torch.zeros(*shape[:-1], shape[-1] + 3)[..., :shape[-1]]
+
+
+def strides_passed(launches):
+    name, args = launches.pop()
+    return [getattr(s, f) for s in args[:2] if isinstance(s, ctypes.Structure) for f, t in s._fields_
+            if t is ctypes.c_int64 and f not in ("seqlen", "rows")]
+
+
+def test_strides_over_one_index_do_not_count(launches):
+    """One sequence, one token or one group: torch keeps any stride for such a dimension,
+    also one that the library refuses."""
+    for E in (8, 1):
+        for far in ({"d0": FAR}, {"d1": FAR}, {"d0": FAR, "d1": FAR}, {"d0": 0, "d1": 0}):
+            x = apart(1, 1, E, **far)
+            m.ssd_conv_fwd(x, torch.zeros(4, E), y=x)
+            assert max(strides_passed(launches)) <= E
+            m.ssd_norm_fwd(x, y=x)
+            assert max(strides_passed(launches)) <= E
+            m.ssd_selscan_fwd(x, x, torch.zeros(E), torch.zeros(4, E), apart(1, 1, 1, 4, **far),
+                              apart(1, 1, 1, 4, d2=FAR, **far), y=x, z=x)
+            assert max(strides_passed(launches)) <= max(E, 4)
+            m.ssd_selscan_bwd(x, x, torch.zeros(E), torch.zeros(4, E), apart(1, 1, 1, 4, **far),
+                              apart(1, 1, 1, 4, d2=FAR, **far), x, z=x)
+            assert max(strides_passed(launches)) <= max(E, 4)
+            m.ssd_conv_bwd(x, torch.zeros(4, E), None, x)
+            assert max(strides_passed(launches)) <= E
+            m.ssd_norm_bwd(x, None, torch.zeros(1, 1), torch.zeros(1, 1), x)
+            assert max(strides_passed(launches)) <= E
+        for far in (FAR, 0):
+            x = apart(1, E, d0=far)
+            m.ssd_conv_step(x, torch.zeros(1, 3, E), torch.zeros(4, E), y=x)
+            assert max(strides_passed(launches)) <= E
+            m.ssd_norm_fwd(x, y=x)
+            assert max(strides_passed(launches)) <= E
+            m.ssd_selscan_step(x, x, torch.zeros(E), torch.zeros(4, E), apart(1, 1, 4, d0=far, d1=far),
+                               apart(1, 1, 4, d0=far), torch.zeros(1, 4, E), y=x, z=x)
+            assert max(strides_passed(launches)) <= max(E, 4)
+    # a group of its own behind the tokens: [b, 1, L, N] transposed
+    B = torch.zeros(1, 1, 5, 4).transpose(1, 2)
+    B = B.as_strided(B.shape, (FAR, 4, FAR, 1))
+    x = torch.zeros(1, 5, 8)
+    m.ssd_selscan_fwd(x, x, torch.zeros(8), torch.zeros(4, 8), B, B)
+    assert max(strides_passed(launches)) <= 8
+    m.ssd_selscan_fwd(x, x, torch.zeros(8), torch.zeros(4, 8), padded(1, 5, 1, 4), B)
+    assert strides_passed(launches)[3:7] == [7, 4, 4, 4]
+    for far in (FAR, 0):
+        for H in (1, 3):
+            x = apart(1, H, 16, d0=far, **({"d1": far} if H == 1 else {}))
+            raw = apart(1, H, d0=far, **({"d1": far} if H == 1 else {}))
+            B = apart(1, 1, 16, d0=far, d1=far)
+            m.ssd_step(x, raw, -1.0, B, B, torch.zeros(1, H, 16, 16), y=x)
+            assert max(strides_passed(launches)) <= 16 * H
+    # the strides that count are passed on
+    m.ssd_step(padded(2, 3, 16), padded(2, 3), -1.0, padded(2, 1, 16), padded(2, 1, 16),
+               torch.zeros(2, 3, 16, 16))
+    assert strides_passed(launches)[:8] == [57, 19, 6, 1, 19, 16, 19, 16]
