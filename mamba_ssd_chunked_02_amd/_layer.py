@@ -219,9 +219,19 @@ def _like(t):
     return torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device)
 
 
-def _workspace(name, dims, x):
-    need = _entry(name)(ctypes.byref(dims))
-    return torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
+def _workspace(name, dims, x, given):
+    """(tensor to keep, address, bytes) of the workspace: the caller's, or one of the
+    size that the library names (none where that is 0)."""
+    if given is None:
+        need = _entry(name)(ctypes.byref(dims))
+        if need == 0:
+            return None, None, 0
+        given = torch.empty(need, dtype=torch.uint8, device=x.device)
+        return given, given.data_ptr(), need
+    if given.get_device() != x.get_device() or given.device.type != x.device.type \
+            or not given.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {x.device}")
+    return given, given.data_ptr(), given.nbytes
 
 
 def _sequences(x, cu_seqlens, b):
@@ -312,11 +322,10 @@ def ssd_norm_bwd(x, weight, mean, rstd, dy, workspace=None):
     dx = _like(x)
     dweight, dbias = torch.empty((2, width), dtype=torch.float32, device=x.device).unbind(0)
     dims = _struct(SsdNormDims, rows, xs, width, _matrix(dy, "dy", width)[1], width, code, 0.0, 0)
-    if workspace is None:
-        workspace = _workspace("ssd_norm_bwd_workspace_bytes", dims, x)
+    workspace, *ws = _workspace("ssd_norm_bwd_workspace_bytes", dims, x, workspace)
     _launch("ssd_norm_bwd", x, dims, x.data_ptr(), _at(weight), mean.data_ptr(), rstd.data_ptr(),
             dy.data_ptr(), dx.data_ptr(), dweight.data_ptr(), dbias.data_ptr(),
-            workspace.data_ptr(), workspace.numel())
+            *ws)
     return {"dx": dx, "dweight": dweight, "dbias": dbias}
 
 
@@ -383,13 +392,11 @@ def ssd_conv_bwd(x, weight, bias, dy, init_state=None, cu_seqlens=None, d_final=
     sums = torch.empty((W + 1, E), dtype=torch.float32, device=x.device)
     dinit = torch.empty((S, W - 1, E), dtype=x.dtype, device=x.device)
     dims = _struct(SsdConvDims, b, L, E, W, 0 if cu is None else S, code)
-    if workspace is None:
-        workspace = _workspace("ssd_conv_bwd_workspace_bytes", dims, x)
+    workspace, *ws = _workspace("ssd_conv_bwd_workspace_bytes", dims, x, workspace)
     dweight, dbias = sums[:W], sums[W]
     _launch("ssd_conv_bwd", x, dims, lay, x.data_ptr(), weight.data_ptr(), _at(bias),
             _at(init_state), _at(cu), dy.data_ptr(), _at(d_final), dx.data_ptr(),
-            dweight.data_ptr(), dbias.data_ptr(), dinit.data_ptr(), workspace.data_ptr(),
-            workspace.numel())
+            dweight.data_ptr(), dbias.data_ptr(), dinit.data_ptr(), *ws)
     return {"dx": dx, "dweight": dweight, "dbias": dbias, "dinit_state": dinit}
 
 
@@ -457,13 +464,10 @@ def ssd_selscan_fwd(x, d_raw, d_init, A, B, C, D=None, z=None, init_state=None, 
         final_state = None
     else:
         _floats(x, (final_state, state, "final_state"))
-    if workspace is None:
-        need = _entry("ssd_selscan_fwd_workspace_bytes")(ctypes.byref(dims))
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    workspace, *ws = _workspace("ssd_selscan_fwd_workspace_bytes", dims, x, workspace)
     _launch("ssd_selscan_fwd", x, dims, lay, x.data_ptr(), d_raw.data_ptr(), _at(d_init), _at(A), _at(B),
             _at(C), _at(D), _at(z), _at(init_state), _at(cu), y.data_ptr(), _at(final_state),
-            _at(workspace), 0 if workspace is None else workspace.numel())
+            *ws)
     return y, final_state
 
 
@@ -485,13 +489,12 @@ def ssd_selscan_bwd(x, d_raw, d_init, A, B, C, dy, D=None, z=None, init_state=No
     sums = torch.empty((N + 2, E), dtype=torch.float32, device=x.device)
     g |= {"dA": sums[:N], "dD": sums[N], "dd_init": sums[N + 1],
           "dinit_state": torch.empty(state, dtype=torch.float32, device=x.device)}
-    if workspace is None:
-        workspace = _workspace("ssd_selscan_bwd_workspace_bytes", dims, x)
+    workspace, *ws = _workspace("ssd_selscan_bwd_workspace_bytes", dims, x, workspace)
     _launch("ssd_selscan_bwd", x, dims, lay, x.data_ptr(), d_raw.data_ptr(), _at(d_init), _at(A), _at(B),
             _at(C), _at(D), _at(z), _at(init_state), _at(cu), dy.data_ptr(), _at(d_final),
             _at(g["dx"]), _at(g["dd_raw"]), _at(g["dB"]), _at(g["dC"]), _at(g.get("dz")),
             _at(g["dA"]), _at(g["dD"]), _at(g["dd_init"]), _at(g["dinit_state"]),
-            _at(workspace), workspace.numel())
+            *ws)
     return g
 
 

@@ -196,3 +196,35 @@ def test_strides_over_one_index_do_not_count(launches):
     m.ssd_step(padded(2, 3, 16), padded(2, 3), -1.0, padded(2, 1, 16), padded(2, 1, 16),
                torch.zeros(2, 3, 16, 16))
     assert strides_passed(launches)[:8] == [57, 19, 6, 1, 19, 16, 19, 16]
+
+
+# ---- workspaces ----------------------------------------------------------------------------
+
+def workspace_calls():
+    x, w = torch.zeros(2, 8, 16), torch.zeros(4, 16)
+    long = torch.zeros(1, 4096, 16)  # cut into spans: the forward scan wants a workspace
+    B = torch.zeros(1, 4096, 1, 4)
+    args = lambda t: (t, t, torch.zeros(16), torch.zeros(4, 16), B[:, :t.shape[1]].expand(len(t), -1, -1, -1),
+                      B[:, :t.shape[1]].expand(len(t), -1, -1, -1).contiguous())
+    mean = torch.zeros(2, 8)
+    return {"norm_bwd": lambda ws: m.ssd_norm_bwd(x, None, mean, mean, x, workspace=ws),
+            "conv_bwd": lambda ws: m.ssd_conv_bwd(x, w, None, x, workspace=ws),
+            "selscan_fwd": lambda ws: m.ssd_selscan_fwd(*args(long), workspace=ws),
+            "selscan_bwd": lambda ws: m.ssd_selscan_bwd(*args(long), long, workspace=ws)}
+
+
+@pytest.mark.parametrize("name", list(workspace_calls()))
+def test_workspaces_hold_the_bytes_that_are_passed(launches, name):
+    """A workspace of any type counts its bytes; one elsewhere, or whose elements are not
+    all there, is refused before a kernel writes into it."""
+    call = workspace_calls()[name]
+    call(torch.zeros(1000, dtype=torch.float64))
+    assert launches.pop()[1][-1] == 8000
+    call(None)
+    own = launches.pop()[1][-1]
+    assert own > 0
+    for bad in (torch.zeros(own, dtype=torch.uint8, device="meta"), torch.zeros(1, dtype=torch.uint8).expand(own),
+                torch.zeros(own, 2, dtype=torch.uint8)[:, 0]):
+        with pytest.raises(ValueError, match="workspace"):
+            call(bad)
+    assert not launches
