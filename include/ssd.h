@@ -564,8 +564,8 @@ int ssd_selscan_step(const ssd_selscan_dims* dims, const ssd_selscan_layout* lay
  * One new token of ssd_fwd's scan for each of dims->batch sequences (seqlen 1,
  * nseq 0; sizes and dtypes as ssd_fwd, chunk_size unused): x, y [b, H, P],
  * d_raw [b, H], B, C [b, G, N] with ssd_layout's strides (element alignment
- * is enough here), state and new_state [nslots, H, N, P] float32 with slots
- * as ssd_conv_step's.
+ * is enough here; SSD_ERR_SHAPE where y's rows share elements), state and
+ * new_state [nslots, H, N, P] float32 with slots as ssd_conv_step's.
  */
 int ssd_step(const ssd_dims* dims, const ssd_layout* layout,
              const void* x, const void* d_raw, float d_init, const void* B, const void* C,

@@ -306,6 +306,7 @@ int ssd_step(const ssd_dims* dims, const ssd_layout* layout, const void* x, cons
                       l.C_token, l.C_group, l.y_token, l.y_head})
         if (s < 0 || s > kMaxStride) return SSD_ERR_SHAPE;
     if (d.batch == 0) return SSD_OK;
+    if (!rows_apart(d.batch, l.y_token, d.nheads, l.y_head, d.headdim)) return SSD_ERR_SHAPE;
     if (!x || !d_raw || !B || !C || !y) return SSD_ERR_NULL_ARG;
     if (nslots > 0 && (!state || !new_state)) return SSD_ERR_NULL_ARG;
     const size_t e = elem_size(d.dtype);

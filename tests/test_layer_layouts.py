@@ -11,7 +11,7 @@ import mamba_ssd_chunked_02_amd as m
 from mamba_ssd_chunked_02_amd import _layer as ly
 from test_abi_host import call as ssd_call
 from test_abi_host import call_bwd, lay
-from test_layer_host import FAKE, SHAPE, WORKSPACE, call, needs_no_gpu, scan_dims
+from test_layer_host import FAKE, OVERLAP, SHAPE, WORKSPACE, call, needs_no_gpu, scan_dims
 
 
 @pytest.fixture
@@ -228,3 +228,19 @@ def test_workspaces_hold_the_bytes_that_are_passed(launches, name):
         with pytest.raises(ValueError, match="workspace"):
             call(bad)
     assert not launches
+
+
+# ---- outputs whose rows share elements -----------------------------------------------------
+
+@needs_no_gpu
+def test_ssd_step_refuses_shared_rows_of_y():
+    """y's strides, which no other tensor's bound, must keep its rows apart; the inputs
+    are only read and may share theirs."""
+    for b, H in ((1, 1), (1, 3), (4, 1), (4, 3)):
+        d = m.make_dims(b, 1, H, 16, 16)
+        for t in (0, 8, 15, 16, 32, 48, 64):
+            for h in (0, 8, 16, 17, 64, 80):
+                l = m.SsdLayout(*[0] * 8, t, h)
+                bad = shares(b, t, H, h, 16)
+                rc = call("ssd_step", d, layout=l, state=FAKE, new_state=FAKE + 4)  # else stopped here
+                assert rc == (SHAPE if bad else OVERLAP), (b, H, t, h, rc)
