@@ -7,8 +7,9 @@
 //   dx = rstd (q - mean(q) - xh mean(q xh)),  dw = sum_rows dy xh,  db = sum_rows dy.
 //
 // Both directions are bound by HBM: one pass, the row held in registers
-// between the sums and the output, so x (and dy) is read once.  A row belongs
-// to one wave where it fits (no barrier), else to one workgroup.
+// between the sums and the output (but for the widths named at kMostFwd), so x
+// (and dy) is read once.  A row belongs to one wave where it fits (no barrier),
+// else to one workgroup.
 #include "ssd_layer.h"
 
 namespace ssd {
@@ -280,6 +281,15 @@ NormPlan norm_plan(const ssd_norm_dims& d, int most) {
     pl.nv = (int)cdiv(vecs, 64 * w);
     return pl;
 }
+// Forward, at most 8 loads a lane against at most 4, us for 6e7 elements (at 5.0 TB/s
+// bf16 takes 48, float32 96):
+//   width            2560  3328  4096  6144  8192 12288 16384
+//   bf16, 8            47    62    81    50    83    85    84
+//   bf16, 4            53    54    52    51    51    57    57
+//   float32, 8         92    91    90    92    93    98    96
+//   float32, 4         88    88    86    88    88    94   110
+// The kernel is compiled for 1024 threads, 128 registers; 7 or 8 loads of 8 bf16 elements
+// do not fit, and 40 and 100 bytes a lane go through scratch memory.
 constexpr int kMostFwd = 8;
 // backward: one load of 8 or two of 4 elements of x and dy (then the next row is
 // loaded ahead); more where 16 waves do not span the row

@@ -28,7 +28,7 @@
 // global scratch (scanning twice costs 8 issues a state entry and token where a
 // scan in order costs 6, but only this fills the chip).  The vector units bound
 // it: 2 x 2048 tokens x 1536 channels x 16 states 47 us on 192 of the 256 CUs,
-// 65536 packed tokens 538 us; their issue slots at 2.4 GHz are 94 % of that.
+// 65536 packed tokens 538 to 566 us; their issue slots take 45 and 505 us at 2.4 GHz.
 // Per-token values (d, u, y) live in the quad's lanes, token
 // 4 i + k in lane k, and reach the other three as DPP operands.
 #pragma once

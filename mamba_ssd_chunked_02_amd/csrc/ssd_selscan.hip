@@ -278,6 +278,15 @@ auto with_shape(int NR, F f) {
 //   576 workgroups, 2048 tokens:       156 / 151 / 157 / 223
 //   1536 workgroups, 256..8192 tokens: 640 / 576 / 550 / 687
 //   24576 workgroups, 20 tokens:       479 / 248 / 137 / 86
+// With 8, 32 and 64 states there are all the waves or a quarter of them (us, all /
+// a quarter; 1536 channels, so 96 workgroups a sequence):
+//                                    8 states    32 states    64 states
+//   192 workgroups, 2048 tokens:      38 / 61    122 / 323     332 / 630
+//   576 workgroups, 2048 tokens:     111 / 104   344 / 388     946 / 800
+//   960 workgroups, 2048 tokens:     173 / 150   462 / 406    1268 / 1399
+//   1536 workgroups, 2048 tokens:    265 / 218   691 / 517    1902 / 1661
+//   6144 workgroups, 130 tokens:     160 / 70    273 / 147     606 / 448
+//   24576 workgroups, 20 tokens:     514 / 118   492 / 144     748 / 388
 int32_t forward_waves(int NR, int64_t workgroups, int64_t chunks) {
     const int32_t full = with_shape(NR, [](auto s) { return s.kFwdWaves; });
     if (NR != 4) return workgroups >= 1024 || chunks <= full / 4 ? full / 4 : full;
@@ -307,7 +316,7 @@ int sel_plan(const ssd_selscan_dims& d, bool bwd, SelPlan* pl) {
         // Cut sequences into spans where that shortens the longest chain of
         // segments on a CU by more than the second launch costs.  A segment's
         // cost is 1; with spans its tokens are walked once more for the spans'
-        // states (0.6 of a segment).
+        // states (0.6 of a segment).  Set for 16 states and applied to all.
         const int64_t seg = pl->waves * tokens, nseg = cdiv(len, seg);
         double best = (double)cdiv(whole, 256) * nseg;
         int64_t segs = 0;

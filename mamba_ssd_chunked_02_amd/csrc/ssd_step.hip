@@ -49,7 +49,9 @@ struct StepParams {
 };
 
 // 64 sequences x 80 heads x 64 x 128 states: 65.9 us, 5.1 TB/s, what a copy of
-// this size reaches (75 with loads predicated by row).
+// this size reaches (75 with loads predicated by row).  With 64 states (128
+// sequences) 63.3 us, 5.3 TB/s; with 32 (256) 91.7, 3.7, and with 16 (512) 151, 2.3:
+// there 6 and 7 of a thread's 8 loads repeat the state's last row.
 // A workgroup takes CP headdim columns of one head: CP / 4 lanes across, the
 // other threads down the state rows, at most UN rows each at a time (all
 // their loads in flight together).
