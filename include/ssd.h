@@ -574,6 +574,91 @@ int ssd_step(const ssd_dims* dims, const ssd_layout* layout,
              const float* state, const int32_t* slots, int32_t nslots,
              void* y, float* new_state, void* stream);
 
+/*
+ * Linear attention with a constant decay per head: for every sequence and
+ * head, in processing order t,
+ *     S_t = exp(decay) S_{t-1} + k_t^T v_t       (S: keydim x valuedim)
+ *     y_t = scale q_t S_t
+ * with S_{-1} = init_state (zeros when NULL) and final_state = S after the
+ * last processed token.  q [b, L, H, K], k [b, L, G, K], v [b, L, G, V],
+ * y [b, L, H, V] of dtype; head h reads keys and values of group h*G/H;
+ * decay [H] float32, the logarithm of the factor (<= 0; 0 forgets nothing,
+ * -inf keeps the current token alone), a constant of the head: it has no
+ * gradient.  States [S, H, K, V] float32 contiguous; final_state NULL to
+ * skip, or the same buffer as init_state.  cu_seqlens and reverse as
+ * ssd_fwd's.  Element alignment is enough for q, k, v and y; 16-byte aligned
+ * rows are faster.  SSD_ERR_SHAPE where y's rows share elements.
+ *
+ * bf16: scores and the states that q meets are rounded to bf16 once, as
+ * operands of their products (sums in float32); the states themselves and
+ * what is added to them keep 24 bits.  A NaN or infinity in a token may make
+ * NaN of its whole chunk of 64 tokens of the sequence, and of what follows.
+ */
+#define SSD_LINATTN_MAX_DIM 256
+typedef struct ssd_linattn_dims {
+    int32_t batch;     /* b >= 1                                            */
+    int64_t seqlen;    /* L >= 0; b * L < 2^31                              */
+    int32_t nheads;    /* H >= 1; sequences * H <= 2^21                     */
+    int32_t ngroups;   /* G >= 1, divides H                                 */
+    int32_t keydim;    /* K: 1 .. SSD_LINATTN_MAX_DIM                       */
+    int32_t valuedim;  /* V: 1 .. SSD_LINATTN_MAX_DIM                       */
+    int32_t nseq;      /* cu_seqlens segments (0 without them)              */
+    int32_t dtype;     /* SSD_F32 or SSD_BF16                               */
+    float scale;       /* not NaN                                           */
+    int32_t reserved;  /* 0                                                 */
+} ssd_linattn_dims;
+
+/* Element strides, 0 .. 2^24, as ssd_layout's (the innermost dimension is
+ * contiguous); a NULL layout means every tensor is contiguous. */
+typedef struct ssd_linattn_layout {
+    int64_t q_token, q_head;    /* q  [b, L, H, K] */
+    int64_t k_token, k_group;   /* k  [b, L, G, K] */
+    int64_t v_token, v_group;   /* v  [b, L, G, V] */
+    int64_t y_token, y_head;    /* y  [b, L, H, V] */
+    int64_t dy_token, dy_head;
+    int64_t dq_token, dq_head;
+    int64_t dk_token, dk_group;
+    int64_t dv_token, dv_group;
+} ssd_linattn_layout;
+
+/* workspace: ssd_linattn_fwd_workspace_bytes(dims) bytes (0 where sequences
+ * x heads fill the chip), 256-byte aligned, no initialization. */
+size_t ssd_linattn_fwd_workspace_bytes(const ssd_linattn_dims* dims);
+
+int ssd_linattn_fwd(const ssd_linattn_dims* dims, const ssd_linattn_layout* layout,
+                    const void* q, const void* k, const void* v, const float* decay,
+                    const float* init_state, const int32_t* cu_seqlens, int32_t reverse,
+                    void* y, float* final_state,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Its gradients: dy like y, d_final like final_state or NULL for zeros;
+ * dq, dk, dv of dtype like q, k, v (layout->dq_* and so on; SSD_ERR_SHAPE
+ * where their rows share elements), dk and dv summed over the heads of a
+ * group; dinit_state [S, H, K, V] float32 (the gradient at zeros without an
+ * init_state), NULL to skip, or d_final's own buffer; it must not overlap
+ * init_state.  workspace as above.
+ */
+size_t ssd_linattn_bwd_workspace_bytes(const ssd_linattn_dims* dims);
+
+int ssd_linattn_bwd(const ssd_linattn_dims* dims, const ssd_linattn_layout* layout,
+                    const void* q, const void* k, const void* v, const float* decay,
+                    const float* init_state, const int32_t* cu_seqlens, int32_t reverse,
+                    const void* dy, const float* d_final,
+                    void* dq, void* dk, void* dv, float* dinit_state,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One new token for each of dims->batch sequences (seqlen 1, nseq 0; batch
+ * may be 0): q [b, H, K], k [b, G, K], v [b, G, V], y [b, H, V], state and
+ * new_state [nslots, H, K, V] float32 with slots as ssd_conv_step's.  All in
+ * float32, y rounded once.
+ */
+int ssd_linattn_step(const ssd_linattn_dims* dims, const ssd_linattn_layout* layout,
+                     const void* q, const void* k, const void* v, const float* decay,
+                     const float* state, const int32_t* slots, int32_t nslots,
+                     void* y, float* new_state, void* stream);
+
 /* Static description of a status code (never NULL). */
 const char* ssd_status_string(int status);
 

@@ -46,6 +46,20 @@ class SsdSelscanLayout(ctypes.Structure):
                                     "C_token", "C_group", "y_token", "dy_token")]
 
 
+class SsdLinattnDims(ctypes.Structure):
+    """Mirror of ``ssd_linattn_dims``."""
+    _fields_ = [("batch", _I32), ("seqlen", _I64), ("nheads", _I32), ("ngroups", _I32),
+                ("keydim", _I32), ("valuedim", _I32), ("nseq", _I32), ("dtype", _I32),
+                ("scale", _F32), ("reserved", _I32)]
+
+
+class SsdLinattnLayout(ctypes.Structure):
+    """Mirror of ``ssd_linattn_layout`` (element strides)."""
+    _fields_ = [(n, _I64) for n in ("q_token", "q_head", "k_token", "k_group", "v_token", "v_group",
+                                    "y_token", "y_head", "dy_token", "dy_head", "dq_token",
+                                    "dq_head", "dk_token", "dk_group", "dv_token", "dv_group")]
+
+
 @functools.lru_cache(maxsize=1024)
 def _struct(cls, *fields):
     """The struct of these sizes; the library only reads it, so calls of the same
@@ -69,6 +83,12 @@ _SIGNATURES = {
                        + [_SIZE, _P],
     "ssd_selscan_step": [_pointer(SsdSelscanDims), _pointer(SsdSelscanLayout)] + [_P] * 10
                         + [_I32] + [_P] * 3,
+    "ssd_linattn_fwd": [_pointer(SsdLinattnDims), _pointer(SsdLinattnLayout)] + [_P] * 6
+                       + [_I32] + [_P] * 3 + [_SIZE, _P],
+    "ssd_linattn_bwd": [_pointer(SsdLinattnDims), _pointer(SsdLinattnLayout)] + [_P] * 6
+                       + [_I32] + [_P] * 7 + [_SIZE, _P],
+    "ssd_linattn_step": [_pointer(SsdLinattnDims), _pointer(SsdLinattnLayout)] + [_P] * 6
+                        + [_I32] + [_P] * 3,
     "ssd_step": [_pointer(SsdDims), _pointer(SsdLayout), _P, _P, _F32, _P, _P, _P, _P, _I32,
                  _P, _P, _P],
 }
@@ -77,6 +97,8 @@ _WORKSPACES = {
     "ssd_conv_bwd_workspace_bytes": SsdConvDims,
     "ssd_selscan_fwd_workspace_bytes": SsdSelscanDims,
     "ssd_selscan_bwd_workspace_bytes": SsdSelscanDims,
+    "ssd_linattn_fwd_workspace_bytes": SsdLinattnDims,
+    "ssd_linattn_bwd_workspace_bytes": SsdLinattnDims,
 }
 _entries = {}
 
@@ -554,4 +576,101 @@ def ssd_step(x, d_raw, d_init, B, C, state, slots=None, new_state=None, y=None):
     dims = _struct(SsdDims, b, 1, H, P, N, G, 64, 0, code)
     _launch("ssd_step", x, dims, lay, x.data_ptr(), d_raw.data_ptr(), float(d_init), _at(B), _at(C),
             state.data_ptr(), _at(slots), state.shape[0], y.data_ptr(), new_state.data_ptr())
+    return y
+
+
+# ---- linear attention ----------------------------------------------------------------------
+
+def _linattn_arguments(q, k, v, decay, scale, cu_seqlens, y, dy):
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q [b, L, H, K], k [b, L, G, K] and v [b, L, G, V] expected")
+    b, L, H, K = q.shape
+    G, V = v.shape[2], v.shape[3]
+    code = _dtype_of(q, "q")
+    _same(q, (k, "k"), (v, "v"), (y, "y"), (dy, "dy"))
+    _floats(q, (decay, (H,), "decay"))
+    if G < 1 or H % G:
+        raise ValueError(f"{H} heads do not divide into {G} groups")
+    cu, S = _sequences(q, cu_seqlens, b)
+    out = (b, L, H, V)
+    lay = _struct(
+        SsdLinattnLayout, *_groups(q, "q", (b, L, H, K)), *_groups(k, "k", (b, L, G, K)),
+        *_groups(v, "v", (b, L, G, V)), *((H * V, V) if y is None else _groups(y, "y", out)),
+        *((H * V, V) if dy is None else _groups(dy, "dy", out)), H * K, K, G * K, K, G * V, V)
+    dims = _struct(SsdLinattnDims, b, L, H, G, K, V, 0 if cu is None else S, code, float(scale), 0)
+    return dims, lay, cu, out, (S, H, K, V)
+
+
+def ssd_linattn_fwd(q, k, v, decay, scale=1.0, init_state=None, cu_seqlens=None, reverse=False,
+                    y=None, final_state=True, workspace=None):
+    """Linear attention with a constant decay per head:
+    ``S = exp(decay) S + k^T v``, ``y = scale q S``.
+
+    q [b, L, H, K], k [b, L, G, K], v [b, L, G, V] (bf16 or fp32, one dtype,
+    strided tokens and heads allowed; K and V up to 256; head h reads group
+    h G / H), decay [H] fp32 (logarithms, <= 0), init_state [S, H, K, V] fp32 or
+    None for zeros; cu_seqlens int32 [nseq + 1] (b must be 1) or None;
+    ``reverse`` runs every sequence from its last token.  ``y`` may be
+    preallocated; ``final_state``: True, False or a [S, H, K, V] fp32 tensor to
+    fill (init_state itself for in place).  Returns (y, final_state or None)."""
+    dims, lay, cu, out, state = _linattn_arguments(q, k, v, decay, scale, cu_seqlens, y, None)
+    _floats(q, (init_state, state, "init_state"))
+    if y is None:
+        y = torch.empty(out, dtype=q.dtype, device=q.device)
+    if final_state is True:
+        final_state = torch.empty(state, dtype=torch.float32, device=q.device)
+    elif final_state is False:
+        final_state = None
+    else:
+        _floats(q, (final_state, state, "final_state"))
+    workspace, *ws = _workspace("ssd_linattn_fwd_workspace_bytes", dims, q, workspace)
+    _launch("ssd_linattn_fwd", q, dims, lay, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            decay.data_ptr(), _at(init_state), _at(cu), int(bool(reverse)), y.data_ptr(),
+            _at(final_state), *ws)
+    return y, final_state
+
+
+def ssd_linattn_bwd(q, k, v, decay, dy, scale=1.0, init_state=None, cu_seqlens=None,
+                    reverse=False, d_final=None, workspace=None):
+    """Gradients of ``ssd_linattn_fwd``: a dict with contiguous dq, dk, dv (dk and
+    dv summed over the heads of a group) and dinit_state [S, H, K, V] fp32 (the
+    gradient at zeros without an init_state).  ``d_final`` is the gradient of
+    final_state or None for zeros.  The decay is a constant: it has none."""
+    dims, lay, cu, _, state = _linattn_arguments(q, k, v, decay, scale, cu_seqlens, None, dy)
+    _floats(q, (init_state, state, "init_state"), (d_final, state, "d_final"))
+    g = {"dq": _output(q), "dk": _output(k), "dv": _output(v),
+         "dinit_state": torch.empty(state, dtype=torch.float32, device=q.device)}
+    workspace, *ws = _workspace("ssd_linattn_bwd_workspace_bytes", dims, q, workspace)
+    _launch("ssd_linattn_bwd", q, dims, lay, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            decay.data_ptr(), _at(init_state), _at(cu), int(bool(reverse)), dy.data_ptr(),
+            _at(d_final), g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(),
+            g["dinit_state"].data_ptr(), *ws)
+    return g
+
+
+def ssd_linattn_step(q, k, v, decay, state, scale=1.0, slots=None, new_state=None, y=None):
+    """One new token of linear attention for each of b sequences: q [b, H, K],
+    k [b, G, K], v [b, G, V] (strided views allowed); state [nslots, H, K, V]
+    fp32, slots and new_state as ``ssd_conv_step``'s.  Returns y [b, H, V]."""
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q [b, H, K], k [b, G, K] and v [b, G, V] expected")
+    b, H, K = q.shape
+    G, V = v.shape[1], v.shape[2]
+    code = _dtype_of(q, "q")
+    _same(q, (k, "k"), (v, "v"))
+    _floats(q, (decay, (H,), "decay"))
+    if G < 1 or H % G:
+        raise ValueError(f"{H} heads do not divide into {G} groups")
+    new_state = _pools(q, state, new_state, (H, K, V), torch.float32, slots)
+    out = (b, H, V)
+    if y is None:
+        y = torch.empty(out, dtype=q.dtype, device=q.device)
+    else:
+        _same(q, (y, "y"))
+    lay = _struct(SsdLinattnLayout, *_heads(q, "q", q.shape), *_heads(k, "k", (b, G, K)),
+                  *_heads(v, "v", (b, G, V)), *_heads(y, "y", out), *([0] * 8))
+    dims = _struct(SsdLinattnDims, b, 1, H, G, K, V, 0, code, float(scale), 0)
+    _launch("ssd_linattn_step", q, dims, lay, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            decay.data_ptr(), state.data_ptr(), _at(slots), state.shape[0], y.data_ptr(),
+            new_state.data_ptr())
     return y

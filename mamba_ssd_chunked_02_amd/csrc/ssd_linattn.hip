@@ -1,0 +1,789 @@
+// Linear attention with a constant decay per head, forward and backward.
+//
+//   S_t = l S_{t-1} + k_t^T v_t,  y_t = scale q_t S_t        (l = exp(decay[h]); S: K x V)
+//
+// in chunks of C tokens.  With E the state that enters a chunk, decayed to its first token
+// (E = l S_{-1}), and i, j the tokens of the chunk:
+//   y_i = scale (l^i q_i E + sum_{j <= i} l^{i-j} (q_i . k_j) v_j)
+//   E'  = l^C E + sum_j l^{C-j} k_j^T v_j
+// The gradients are scans of the same form with other roles:
+//   dq = scan(q: dy, k: v,  v: k)           in the forward's order,   state S^T
+//   dk = scan(q: v,  k: dy, v: scale q)     in the opposite order,    state R^T
+//   dv = scan(q: k,  k: scale q, v: dy)     in the opposite order,    state R
+// with R_t = scale q_t^T dy_t + l R_{t+1} (R_{L-1} adds d_final, which therefore enters
+// undecayed) and dinit = l R_0: one kernel serves all four (LinPass::init_pow, final_pow).
+//
+// A workgroup walks the chunks of one span of a sequence for one head and VT columns of V,
+// the state in registers (each of its four waves holds all K rows of its own columns, so
+// no product needs a sum across waves).  Where sequences x heads do not fill the chip a
+// sequence is cut into spans: their states are formed first (STATE), joined along the
+// sequence (linattn_join) and then every span is walked from its own incoming state.
+#include <type_traits>
+
+#include "ssd_layer.h"
+
+namespace ssd {
+namespace {
+
+struct LinPass {
+    const void* q;
+    const void* k;
+    const void* v;
+    void* o;
+    int64_t q_t, q_h, k_t, k_h, v_t, v_h, o_t, o_h;
+    const float* decay;
+    const float* init;  // [S][H] states of K * V entries, entry (k, v) at k s_k + v s_v
+    float* final;
+    float* spans;       // [slots][H][vtiles] span states in register order
+    const int32_t* cu;
+    int64_t L, T, span; // tokens of a sequence without cu, of all, of a span
+    int32_t S, H, K, V, s_k, s_v;
+    int32_t qdiv, kdiv, vdiv;  // head h reads head h / div
+    int32_t slots, per;        // span slots; spans of a sequence without cu
+    int32_t vtiles, reverse, init_pow, final_pow;
+    float in_scale, out_scale;
+};
+
+// Sequence and span of a slot.  With cu sequence i owns the slots from cu[i] / span + i on:
+// one for every span it can have, and at least one.
+struct Span {
+    int64_t first, len;  // the sequence's tokens
+    int64_t t0;          // of the span, in processing order
+    int32_t seq, at;
+};
+__device__ __forceinline__ int64_t slot_base(const LinPass& p, int i) {
+    const int64_t c = p.cu[i];
+    return (c < 0 ? 0 : (c > p.T ? p.T : c)) / p.span + i;
+}
+__device__ __forceinline__ Span span_of(const LinPass& p, int slot) {
+    Span s;
+    if (!p.cu) {
+        s.seq = slot / p.per;
+        s.at = slot - s.seq * p.per;
+        s.first = s.seq * p.L;
+        s.len = p.L;
+    } else {
+        int lo = 0, hi = p.S - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (slot_base(p, mid) <= slot) lo = mid; else hi = mid - 1;
+        }
+        s.seq = lo;
+        s.at = slot - (int)slot_base(p, lo);
+        int64_t last;
+        sequence_span(p.cu, lo, 0, p.T, &s.first, &last);
+        s.len = last - s.first;
+    }
+    s.t0 = s.at * p.span;
+    return s;
+}
+
+// l^n in double (0^0 = 1): products of many chunks keep the rate's low bits.
+__device__ __forceinline__ double power(float decay, int64_t n) {
+    return n == 0 ? 1.0 : exp((double)n * (double)decay);
+}
+
+// Factors l^n, one for each of many steps of n tokens, as floats whose product stays the
+// power: what a float leaves out of l^n (`low`, relative) is gathered and put back whenever
+// it has grown to a unit of the last place.  Over 1000 steps of 32 tokens a fixed factor is
+// up to 3e-5 off.
+struct Rate {
+    float rate, low, unrate, owed;
+    __device__ __forceinline__ Rate(float decay, int64_t n) {
+        const double exact = power(decay, n);
+        rate = (float)exact;
+        low = rate > 0.f ? (float)((exact - (double)rate) / (double)rate) : 0.f;
+        unrate = rate > 0.f ? 1.f / rate : 0.f;
+        owed = 0.f;
+    }
+    __device__ __forceinline__ float next() {
+        owed += low;
+        const float f = fmaf(rate, owed, rate);
+        owed -= (f - rate) * unrate;
+        return f;
+    }
+};
+
+// A row-major LDS tile: rows 32 bytes apart from a multiple of 256, and the 16-byte units of
+// rows 8-15 of every 16 exchanged in pairs.  The reads below then touch every bank evenly:
+// 16 rows of one unit's half (row_frag) and 4 rows x 32 bytes (tok_frag).
+template <typename T, int COLS>
+struct Tile {
+    static constexpr int EPU = 16 / sizeof(T), ST = COLS + 32 / sizeof(T);
+    __device__ static __forceinline__ int off(int r, int c) {
+        return r * ST + (((c / EPU) ^ ((r >> 3) & 1)) * EPU) + c % EPU;
+    }
+};
+
+// MFMA operands over 32 entries of a contraction, in the order in which a pair of result
+// tiles holds them: a lane of group g has entries 4g..4g+3 and 16+4g..16+4g+3.
+template <typename T, int COLS>
+__device__ __forceinline__ typename Vec<T>::x8 row_frag(const T* t, int r, int c, int g) {
+    using X4 = typename Vec<T>::x4;
+    return cat<typename Vec<T>::x8, X4>(ld4(t + Tile<T, COLS>::off(r, c + 4 * g)),
+                                        ld4(t + Tile<T, COLS>::off(r, c + 16 + 4 * g)));
+}
+// over the tile's rows r0..r0+31: the lane's column is c0 + l16
+template <int COLS>
+__device__ __forceinline__ bf16x8 col_frag(const bf16* t, int r0, int c0, int lane) {
+    const int j = lane & 15, r = r0 + 4 * (lane >> 4) + (j >> 2), c = c0 + 4 * (j & 3);
+    return cat<bf16x8, bf16x4>(ldtr(t + Tile<bf16, COLS>::off(r, c)),
+                               ldtr(t + Tile<bf16, COLS>::off(r + 16, c)));
+}
+template <int COLS>
+__device__ __forceinline__ f32x8 col_frag(const float* t, int r0, int c0, int lane) {
+    const int r = r0 + 4 * (lane >> 4), c = c0 + (lane & 15);
+    f32x8 v;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        v[k] = t[Tile<float, COLS>::off(r + k, c)];
+        v[4 + k] = t[Tile<float, COLS>::off(r + 16 + k, c)];
+    }
+    return v;
+}
+
+// c + a (v w), v w in full: a float32 state that takes bfloat16 inputs would lose 16 bits
+// to one rounded product, so it is split into three bfloat16 values, whose sum is exact.
+__device__ __forceinline__ f32x4 mma_weighted(const bf16x8& a, const bf16x8 (&vw)[3], f32x4 c) {
+    c = mma(a, vw[2], c);
+    c = mma(a, vw[1], c);
+    return mma(a, vw[0], c);
+}
+__device__ __forceinline__ f32x4 mma_weighted(const f32x8& a, const f32x8 (&vw)[1], f32x4 c) {
+    return mma(a, vw[0], c);
+}
+__device__ __forceinline__ void weigh(const bf16x8& v, const f32x8& w, bf16x8 (&o)[3]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        float x = (float)v[j] * w[j];
+        o[0][j] = (bf16)x;
+        x -= (float)o[0][j];
+        o[1][j] = (bf16)x;
+        x -= (float)o[1][j];
+        o[2][j] = (bf16)x;
+    }
+}
+__device__ __forceinline__ void weigh(const f32x8& v, const f32x8& w, f32x8 (&o)[1]) { o[0] = v * w; }
+
+template <typename T> constexpr int kParts = sizeof(T) == 2 ? 3 : 1;
+
+// The 16-byte units of a C x COLS tile that one thread moves: loads for the next chunk stay
+// in registers until its LDS tile is free.
+template <typename T, int C, int COLS>
+struct Mover {
+    static constexpr int EPU = 16 / sizeof(T), UPR = COLS / EPU, N = C * UPR / 256;
+    typedef T unit __attribute__((ext_vector_type(16 / sizeof(T))));
+    unit u[N];
+    // rows at base + row * step (elements; negative against the order of memory); only
+    // rows < clen and columns < cols are read
+    __device__ __forceinline__ void load(const T* base, int64_t step, int clen, int cols) {
+        const int row = threadIdx.x / UPR, c = threadIdx.x % UPR * EPU;
+        if (cols % EPU == 0) {
+            const int cc = c < cols ? c : 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int r = row + i * (256 / UPR);
+                __builtin_memcpy(&u[i], base + (r < clen ? r : 0) * step + cc, 16);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int r = row + i * (256 / UPR);
+#pragma unroll
+                for (int j = 0; j < EPU; ++j)
+                    u[i][j] = r < clen && c + j < cols ? base[r * step + c + j] : (T)0.f;
+            }
+        }
+    }
+    __device__ __forceinline__ void put(T* tile, int clen, int cols) const {
+        const int row = threadIdx.x / UPR, c = threadIdx.x % UPR * EPU;
+        const bool whole = clen == C && cols == COLS;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int r = row + i * (256 / UPR);
+            unit x = u[i];
+            if (!whole && (r >= clen || c >= cols)) x = unit{};
+            *(unit*)(tile + Tile<T, COLS>::off(r, c)) = x;
+        }
+    }
+};
+
+template <typename T, int KD, int VT, int C>
+struct __attribute__((aligned(16))) Shared {
+    T q[C * Tile<T, KD>::ST];
+    T k[C * Tile<T, KD>::ST];
+    T v[C * Tile<T, VT>::ST];
+    T p[C * Tile<T, C>::ST];
+    float pw[C + 4];  // l^n
+    float w[C];       // weights of the chunk's tokens in the state behind it
+};
+template <typename T, int KD, int VT, int C>
+struct __attribute__((aligned(16))) SharedState {
+    T k[C * Tile<T, KD>::ST];
+    T v[C * Tile<T, VT>::ST];
+    float w[C];
+};
+
+// One span (or, STATE, only its state).  OT: the output's type.
+template <typename T, typename OT, int KD, int VT, int C, bool STATE>
+__global__ __launch_bounds__(256, KD * sizeof(T) > 512 ? 1 : 2) void linattn_kernel(LinPass p) {
+    using X8 = typename Vec<T>::x8;
+    using X4 = typename Vec<T>::x4;
+    constexpr int KB = KD / 16, KS = KD / 32, CB = VT / 64, IB = C / 16, TS = C / 32;
+    constexpr int NP = kParts<T>;
+    __shared__ std::conditional_t<STATE, SharedState<T, KD, VT, C>, Shared<T, KD, VT, C>> sh;
+    const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), l16 = lane & 15, g = lane >> 4;
+    uint32_t id = blockIdx.x;
+    const int vt = id % (uint32_t)p.vtiles;
+    id /= (uint32_t)p.vtiles;
+    const int h = id % (uint32_t)p.H, slot = id / (uint32_t)p.H;
+    const Span sp = span_of(p, slot);
+    if (sp.at < 0 || (sp.at > 0 && sp.t0 >= sp.len)) return;
+    const int64_t n = imin(p.span, sp.len - sp.t0);
+    const bool last = sp.t0 + n >= sp.len;
+    if (STATE && last) return;  // no span behind it
+    const int64_t block = ((int64_t)sp.seq * p.H + h) * ((int64_t)p.K * p.V);
+    const int v0 = vt * VT, vcols = min(VT, p.V - v0), mycol = wave * (16 * CB) + l16;
+    float* const mine = p.spans + (((int64_t)slot * p.H + h) * p.vtiles + vt) * (KD * VT) +
+                        wave * (CB * KB * 256) + lane * 4;
+
+    if (!STATE && n == 0) {  // an empty sequence hands on what came in
+        if (p.final)
+            for (int i = tid; i < p.K * vcols; i += 256) {
+                const int64_t e = block + (int64_t)(i / vcols) * p.s_k + (int64_t)(v0 + i % vcols) * p.s_v;
+                p.final[e] = p.init ? p.init[e] : 0.f;
+            }
+        return;
+    }
+
+    // the first chunk's tiles
+    const int64_t tok0 = p.reverse ? sp.first + sp.len - 1 - sp.t0 : sp.first + sp.t0;
+    const int64_t dir = p.reverse ? -1 : 1;
+    const T* qp = (const T*)p.q + tok0 * p.q_t + (h / p.qdiv) * p.q_h;
+    const T* kp = (const T*)p.k + tok0 * p.k_t + (h / p.kdiv) * p.k_h;
+    const T* vp = (const T*)p.v + tok0 * p.v_t + (h / p.vdiv) * p.v_h + v0;
+    OT* op = (OT*)p.o + tok0 * p.o_t + h * p.o_h + v0;
+    const int64_t qs = dir * p.q_t, ks = dir * p.k_t, vs = dir * p.v_t, os = dir * p.o_t;
+    Mover<T, C, KD> mq, mk;
+    Mover<T, C, VT> mv;
+    int clen = (int)imin(C, n);
+    if (!STATE) mq.load(qp, qs, clen, p.K);
+    mk.load(kp, ks, clen, p.K);
+    mv.load(vp, vs, clen, vcols);
+
+    const float decay = p.decay[h];
+    if constexpr (!STATE) {
+        if (tid <= C) sh.pw[tid] = (float)power(decay, tid);
+        // score tiles above the diagonal that a product over 32 tokens meets
+        for (int i = tid; i < C * Tile<T, C>::ST; i += 256) sh.p[i] = (T)0.f;
+    }
+    if (tid < C) sh.w[tid] = p.in_scale * (float)power(decay, C - tid);
+    Rate rate(decay, C);
+
+    f32x4 st[KB][CB];
+    const bool split = p.per != 1;  // states come in by way of the workspace
+    if (!STATE && split) {
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb) st[kb][cb] = *(const f32x4*)(mine + (cb * KB + kb) * 256);
+    } else {
+        const bool come = !STATE && p.init;
+        const float f = p.init_pow ? (float)power(decay, 1) : 1.f;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int kr = 16 * kb + 4 * g + r, vc = mycol + 16 * cb;
+                    const bool in = come && kr < p.K && vc < vcols;
+                    const int64_t e = block + (int64_t)kr * p.s_k + (int64_t)(v0 + vc) * p.s_v;
+                    st[kb][cb][r] = in ? f * p.init[in ? e : 0] : 0.f;
+                }
+    }
+
+    for (int64_t t = 0; t < n; t += C) {
+        const int cl = clen;
+        const bool end = t + C >= n;          // of the span
+        const bool close = last && end;       // of the sequence
+        if constexpr (!STATE) mq.put(sh.q, cl, p.K);
+        mk.put(sh.k, cl, p.K);
+        mv.put(sh.v, cl, vcols);
+        if (close && tid < C)
+            sh.w[tid] = tid < cl ? p.in_scale * (float)power(decay, cl - 1 - tid + p.final_pow) : 0.f;
+        __syncthreads();
+        if (!end) {
+            qp += C * qs;
+            kp += C * ks;
+            vp += C * vs;
+            clen = (int)imin(C, n - t - C);
+            if (!STATE) mq.load(qp, qs, clen, p.K);
+            mk.load(kp, ks, clen, p.K);
+            mv.load(vp, vs, clen, vcols);
+        }
+        f32x4 acc[IB][CB];
+        if constexpr (!STATE) {
+            // scores, transposed: a lane gets 4 tokens j of one row i
+            constexpr int NT = IB * (IB + 1) / 2;
+#pragma unroll
+            for (int x = 0; x < (NT + 3) / 4; ++x) {
+                const int tile = x * 4 + wave;
+                if (tile < NT) {
+                    int ib = 0, jb = tile;
+                    while (jb > ib) jb -= ++ib;
+                    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int kk = 0; kk < KS; ++kk)
+                        s = mma(row_frag<T, KD>(sh.k, 16 * jb + l16, 32 * kk, g),
+                                row_frag<T, KD>(sh.q, 16 * ib + l16, 32 * kk, g), s);
+                    const int d = 16 * (ib - jb) + l16 - 4 * g;
+                    X4 o;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        o[r] = d - r >= 0 ? (T)(s[r] * (p.in_scale * sh.pw[max(d - r, 0)])) : (T)0.f;
+                    *(X4*)(sh.p + Tile<T, C>::off(16 * ib + l16, 16 * jb + 4 * g)) = o;
+                }
+            }
+            // l^i q_i E
+#pragma unroll
+            for (int ib = 0; ib < IB; ++ib)
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb) acc[ib][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) {
+                X8 e[CB];
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        e[cb][r] = (T)st[2 * kk][cb][r];
+                        e[cb][4 + r] = (T)st[2 * kk + 1][cb][r];
+                    }
+#pragma unroll
+                for (int ib = 0; ib < IB; ++ib) {
+                    const X8 a = row_frag<T, KD>(sh.q, 16 * ib + l16, 32 * kk, g);
+#pragma unroll
+                    for (int cb = 0; cb < CB; ++cb) acc[ib][cb] = mma(a, e[cb], acc[ib][cb]);
+                }
+            }
+#pragma unroll
+            for (int ib = 0; ib < IB; ++ib) {
+                const f32x4 f = *(const f32x4*)(sh.pw + 16 * ib + 4 * g);
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb) acc[ib][cb] *= f;
+            }
+            __syncthreads();
+        }
+        // the chunk's values: scores times v, and the state behind the chunk
+        const bool update = STATE || !close || p.final;
+        if (update) {
+            const float f = close ? (float)power(decay, cl - 1 + p.final_pow) : rate.next();
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb) st[kb][cb] *= f;
+        }
+#pragma unroll
+        for (int ts = 0; ts < TS; ++ts) {
+            X8 vf[CB];
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb)
+                vf[cb] = col_frag<VT>(sh.v, 32 * ts, wave * (16 * CB) + 16 * cb, lane);
+            if constexpr (!STATE) {
+#pragma unroll
+                for (int ib = 2 * ts; ib < IB; ++ib) {
+                    const X8 a = row_frag<T, C>(sh.p, 16 * ib + l16, 32 * ts, g);
+#pragma unroll
+                    for (int cb = 0; cb < CB; ++cb) acc[ib][cb] = mma(a, vf[cb], acc[ib][cb]);
+                }
+            }
+            if (update) {
+                const f32x8 w = cat<f32x8, f32x4>(*(const f32x4*)(sh.w + 32 * ts + 4 * g),
+                                                  *(const f32x4*)(sh.w + 32 * ts + 16 + 4 * g));
+                X8 vw[CB][NP];
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb) weigh(vf[cb], w, vw[cb]);
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    const X8 a = col_frag<KD>(sh.k, 32 * ts, 16 * kb, lane);
+#pragma unroll
+                    for (int cb = 0; cb < CB; ++cb) st[kb][cb] = mma_weighted(a, vw[cb], st[kb][cb]);
+                }
+            }
+        }
+        if constexpr (!STATE) {
+#pragma unroll
+            for (int ib = 0; ib < IB; ++ib)
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int i = 16 * ib + 4 * g + r, c = mycol + 16 * cb;
+                        if (i < cl && c < vcols) op[i * os + c] = (OT)(p.out_scale * acc[ib][cb][r]);
+                    }
+            op += C * os;
+        }
+        __syncthreads();
+    }
+
+    if constexpr (STATE) {
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb) *(f32x4*)(mine + (cb * KB + kb) * 256) = st[kb][cb];
+    } else if (last && p.final) {
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int kr = 16 * kb + 4 * g + r, vc = mycol + 16 * cb;
+                    if (kr < p.K && vc < vcols)
+                        p.final[block + (int64_t)kr * p.s_k + (int64_t)(v0 + vc) * p.s_v] = st[kb][cb][r];
+                }
+    }
+}
+
+// Joins the span states of every sequence: slot s gets the state that enters span s.
+// A thread takes 4 entries (one lane's part of a result tile).
+__global__ __launch_bounds__(256) void linattn_join(LinPass p, int KD, int VT) {
+    uint32_t id = blockIdx.x;
+    const int vt = id % (uint32_t)p.vtiles;
+    id /= (uint32_t)p.vtiles;
+    const int h = id % (uint32_t)p.H, seq = id / (uint32_t)p.H;
+    const int slot0 = p.cu ? (int)slot_base(p, seq) : seq * p.per;
+    const Span sp = span_of(p, slot0);
+    const int64_t spans = cdiv(sp.len, p.span);
+    const int e = blockIdx.y * 256 + threadIdx.x, lane = e & 63, tile = e >> 6;
+    const int kb = tile % (KD / 16), vb = tile / (KD / 16);
+    const int kr = 16 * kb + 4 * (lane >> 4), vc = vt * VT + 16 * vb + (lane & 15);
+    const float decay = p.decay[h];
+    Rate rate(decay, p.span);
+    const float f = p.init_pow ? (float)power(decay, 1) : 1.f;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    if (p.init)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (kr + r < p.K && vc < p.V)
+                s[r] = f * p.init[((int64_t)seq * p.H + h) * ((int64_t)p.K * p.V) +
+                                  (int64_t)(kr + r) * p.s_k + (int64_t)vc * p.s_v];
+    float* at = p.spans + (((int64_t)slot0 * p.H + h) * p.vtiles + vt) * (KD * VT) + e * 4;
+    const int64_t step = (int64_t)p.H * p.vtiles * (KD * VT);
+    constexpr int UN = 8;  // spans in flight
+    for (int64_t i = 0; i < spans; i += UN, at += UN * step) {
+        f32x4 x[UN];
+#pragma unroll
+        for (int j = 0; j < UN; ++j)
+            if (i + j + 1 < spans) x[j] = *(const f32x4*)(at + j * step);
+#pragma unroll
+        for (int j = 0; j < UN; ++j)
+            if (i + j < spans) {
+                *(f32x4*)(at + j * step) = s;
+                if (i + j + 1 < spans) s = s * rate.next() + x[j];
+            }
+    }
+}
+
+// out[t][g] = the sum of part[t][g * R .. g * R + R - 1] (rows of D entries): gradients of
+// keys and values that R heads share.
+template <typename T>
+__global__ __launch_bounds__(256) void linattn_heads_sum(const float* part, T* out, int64_t items, int D,
+                                                         int G, int R, int64_t o_t, int64_t o_g) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < items; i += (int64_t)gridDim.x * 256) {
+        int64_t tg, t;
+        const int d = (int)divide(i, D, &tg);
+        const int g = (int)divide(tg, G, &t);
+        const float* q = part + (tg * R) * D + d;
+        float s = 0.f;
+        for (int r = 0; r < R; ++r) s += q[(int64_t)r * D];
+        out[t * o_t + g * o_g + d] = (T)s;
+    }
+}
+
+// ---- host ----------------------------------------------------------------------------------
+
+struct LinTiles {
+    int KD, VT, C;
+};
+// K is padded to 64, 128 or 256.  The state of a workgroup's columns is KD x VT / 256
+// registers a thread: 64 at most.
+LinTiles lin_tiles(int K, int V, int32_t dtype) {
+    LinTiles t;
+    t.KD = K <= 64 ? 64 : (K <= 128 ? 128 : 256);
+    t.VT = V <= 64 || t.KD == 256 ? 64 : 128;
+    t.C = dtype == SSD_F32 || t.KD == 256 ? 32 : 64;
+    return t;
+}
+
+struct LinPlan {
+    LinTiles t;
+    int64_t span;
+    int32_t slots, per, vtiles;
+    size_t bytes;  // of the span states (0: whole sequences)
+};
+constexpr int64_t kFill = 512;  // two workgroups a CU
+
+LinPlan lin_plan(const ssd_linattn_dims& d, int K, int V) {
+    LinPlan pl;
+    pl.t = lin_tiles(K, V, d.dtype);
+    pl.vtiles = (int)cdiv(V, pl.t.VT);
+    const int64_t S = d.nseq > 0 ? d.nseq : d.batch, T = (int64_t)d.batch * d.seqlen;
+    const int64_t wgs = S * d.nheads * pl.vtiles, C = pl.t.C;
+    // packed sequences are of any length: cut as if they were one
+    const int64_t want = d.nseq > 0 ? cdiv(kFill, (int64_t)d.nheads * pl.vtiles) : cdiv(kFill, wgs);
+    const int64_t tokens = d.nseq > 0 ? T : d.seqlen;
+    pl.span = cdiv(cdiv(tokens, want), C) * C;
+    if (pl.span < 2 * C) pl.span = 2 * C;
+    if (pl.span >= tokens) {
+        pl.span = (int64_t)1 << 40;  // whole sequences
+        pl.per = 1;
+        pl.slots = (int)S;
+        pl.bytes = 0;
+        return pl;
+    }
+    pl.per = d.nseq > 0 ? 0 : (int)cdiv(d.seqlen, pl.span);
+    pl.slots = (int)(d.nseq > 0 ? T / pl.span + S : S * pl.per);
+    pl.bytes = up256((size_t)pl.slots * d.nheads * pl.vtiles * pl.t.KD * pl.t.VT * 4);
+    return pl;
+}
+
+template <typename T, typename OT, int KD, int VT, int C>
+void launch_tiles(const LinPass& p, const LinPlan& pl, hipStream_t s) {
+    const dim3 grid((unsigned)((int64_t)pl.slots * p.H * pl.vtiles));
+    if (pl.bytes) {
+        linattn_kernel<T, OT, KD, VT, C, true><<<grid, 256, 0, s>>>(p);
+        const dim3 joins((unsigned)((int64_t)p.S * p.H * pl.vtiles), KD * VT / 1024);
+        linattn_join<<<joins, 256, 0, s>>>(p, KD, VT);
+    }
+    linattn_kernel<T, OT, KD, VT, C, false><<<grid, 256, 0, s>>>(p);
+}
+template <typename T, typename OT>
+void launch_pass(LinPass& p, const LinPlan& pl, hipStream_t s) {
+    constexpr int C = sizeof(T) == 2 ? 64 : 32;
+    p.span = pl.span;
+    p.slots = pl.slots;
+    p.per = pl.per;
+    p.vtiles = pl.vtiles;
+    if (pl.t.KD == 64) {
+        if (pl.t.VT == 64) launch_tiles<T, OT, 64, 64, C>(p, pl, s);
+        else launch_tiles<T, OT, 64, 128, C>(p, pl, s);
+    } else if (pl.t.KD == 128) {
+        if (pl.t.VT == 64) launch_tiles<T, OT, 128, 64, C>(p, pl, s);
+        else launch_tiles<T, OT, 128, 128, C>(p, pl, s);
+    } else {
+        launch_tiles<T, OT, 256, 64, 32>(p, pl, s);
+    }
+}
+
+int lin_check(const ssd_linattn_dims* d, const ssd_linattn_layout* l) {
+    if (!d) return SSD_ERR_NULL_ARG;
+    if (d->dtype != SSD_F32 && d->dtype != SSD_BF16) return SSD_ERR_DTYPE;
+    if (d->batch < 1 || d->seqlen < 0 || d->nheads < 1 || d->ngroups < 1 || d->nseq < 0 ||
+        d->nheads % d->ngroups != 0 || d->keydim < 1 ||
+        d->valuedim < 1 || d->reserved != 0 || d->seqlen > kMaxTokens / d->batch)
+        return SSD_ERR_SHAPE;
+    if (d->nseq > 0 && d->batch != 1) return SSD_ERR_SHAPE;
+    if (d->keydim > SSD_LINATTN_MAX_DIM || d->valuedim > SSD_LINATTN_MAX_DIM) return SSD_ERR_UNSUPPORTED;
+    if (!(d->scale == d->scale)) return SSD_ERR_SHAPE;
+    // workgroups of a launch; a sequence has at least one span
+    const int64_t S = d->nseq > 0 ? d->nseq : d->batch;
+    if (S * d->nheads > (int64_t)1 << 21) return SSD_ERR_SHAPE;
+    if (l)
+        for (int64_t s : {l->q_token, l->q_head, l->k_token, l->k_group, l->v_token, l->v_group,
+                          l->y_token, l->y_head, l->dy_token, l->dy_head, l->dq_token, l->dq_head,
+                          l->dk_token, l->dk_group, l->dv_token, l->dv_group})
+            if (s < 0 || s > kMaxStride) return SSD_ERR_SHAPE;
+    return SSD_OK;
+}
+
+ssd_linattn_layout lin_layout(const ssd_linattn_dims& d, const ssd_linattn_layout* l) {
+    if (l) return *l;
+    const int64_t H = d.nheads, G = d.ngroups, K = d.keydim, V = d.valuedim;
+    return ssd_linattn_layout{H * K, K, G * K, K, G * V, V, H * V, V, H * V, V, H * K, K, G * K, K, G * V, V};
+}
+
+LinPass lin_common(const ssd_linattn_dims& d, const float* decay, const int32_t* cu) {
+    LinPass p = {};
+    p.decay = decay;
+    p.cu = cu;
+    p.L = d.seqlen;
+    p.T = (int64_t)d.batch * d.seqlen;
+    p.S = d.nseq > 0 ? d.nseq : d.batch;
+    p.H = d.nheads;
+    p.qdiv = p.kdiv = p.vdiv = 1;
+    return p;
+}
+
+size_t state_bytes(const ssd_linattn_dims& d) {
+    return (size_t)(d.nseq > 0 ? d.nseq : d.batch) * d.nheads * d.keydim * d.valuedim * 4;
+}
+
+// The backward's workspace: span states of one pass at a time, and the shares of dk or dv.
+struct LinBwdPlan {
+    LinPlan dq, dk, dv;
+    size_t spans, shares;
+};
+LinBwdPlan lin_bwd_plan(const ssd_linattn_dims& d) {
+    LinBwdPlan b;
+    b.dq = lin_plan(d, d.valuedim, d.keydim);
+    b.dk = lin_plan(d, d.valuedim, d.keydim);
+    b.dv = lin_plan(d, d.keydim, d.valuedim);
+    b.spans = (size_t)imax(imax(b.dq.bytes, b.dk.bytes), b.dv.bytes);
+    b.shares = d.nheads == d.ngroups ? 0
+               : up256((size_t)d.batch * d.seqlen * d.nheads * imax(d.keydim, d.valuedim) * 4);
+    return b;
+}
+
+}  // namespace
+}  // namespace ssd
+
+using namespace ssd;
+
+extern "C" {
+
+size_t ssd_linattn_fwd_workspace_bytes(const ssd_linattn_dims* dims) {
+    if (lin_check(dims, nullptr) != SSD_OK) return 0;
+    return lin_plan(*dims, dims->keydim, dims->valuedim).bytes;
+}
+
+int ssd_linattn_fwd(const ssd_linattn_dims* dims, const ssd_linattn_layout* layout, const void* q,
+                    const void* k, const void* v, const float* decay, const float* init_state,
+                    const int32_t* cu_seqlens, int32_t reverse, void* y, float* final_state,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+    int st = lin_check(dims, layout);
+    if (st != SSD_OK) return st;
+    const ssd_linattn_dims& d = *dims;
+    if ((d.nseq > 0) != (cu_seqlens != nullptr)) return cu_seqlens ? SSD_ERR_SHAPE : SSD_ERR_NULL_ARG;
+    const ssd_linattn_layout l = lin_layout(d, layout);
+    const int64_t T = (int64_t)d.batch * d.seqlen;
+    if (!decay || (T > 0 && (!q || !k || !v || !y))) return SSD_ERR_NULL_ARG;
+    if (!rows_apart(T, l.y_token, d.nheads, l.y_head, d.valuedim)) return SSD_ERR_SHAPE;
+    const size_t e = elem_size(d.dtype);
+    if (!elem_aligned(q, e) || !elem_aligned(k, e) || !elem_aligned(v, e) || !elem_aligned(y, e) ||
+        !elem_aligned(decay, 4) || !elem_aligned(init_state, 4) || !elem_aligned(final_state, 4) ||
+        !elem_aligned(cu_seqlens, 4) || ((uintptr_t)workspace & 255))
+        return SSD_ERR_ALIGN;
+    if (init_state != final_state && overlaps(init_state, state_bytes(d), final_state, state_bytes(d)))
+        return SSD_ERR_OVERLAP;
+    const LinPlan pl = lin_plan(d, d.keydim, d.valuedim);
+    if (pl.bytes && (!workspace || workspace_bytes < pl.bytes)) return SSD_ERR_WORKSPACE;
+    if (cu_seqlens && check_cu_env(cu_seqlens, d.nseq, T, (hipStream_t)stream, &st)) return st;
+    LinPass p = lin_common(d, decay, cu_seqlens);
+    p.q = q, p.q_t = l.q_token, p.q_h = l.q_head;
+    p.k = k, p.k_t = l.k_token, p.k_h = l.k_group;
+    p.v = v, p.v_t = l.v_token, p.v_h = l.v_group;
+    p.o = y, p.o_t = l.y_token, p.o_h = l.y_head;
+    p.kdiv = p.vdiv = d.nheads / d.ngroups;
+    p.K = d.keydim, p.V = d.valuedim, p.s_k = d.valuedim, p.s_v = 1;
+    p.init = init_state, p.final = final_state, p.spans = (float*)workspace;
+    p.reverse = reverse != 0, p.init_pow = 1, p.final_pow = 0;
+    p.in_scale = 1.f, p.out_scale = d.scale;
+    if (d.dtype == SSD_BF16) launch_pass<bf16, bf16>(p, pl, (hipStream_t)stream);
+    else launch_pass<float, float>(p, pl, (hipStream_t)stream);
+    return launched();
+}
+
+size_t ssd_linattn_bwd_workspace_bytes(const ssd_linattn_dims* dims) {
+    if (lin_check(dims, nullptr) != SSD_OK) return 0;
+    const LinBwdPlan b = lin_bwd_plan(*dims);
+    return b.spans + b.shares;
+}
+
+int ssd_linattn_bwd(const ssd_linattn_dims* dims, const ssd_linattn_layout* layout, const void* q,
+                    const void* k, const void* v, const float* decay, const float* init_state,
+                    const int32_t* cu_seqlens, int32_t reverse, const void* dy,
+                    const float* d_final, void* dq, void* dk, void* dv, float* dinit_state,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+    int st = lin_check(dims, layout);
+    if (st != SSD_OK) return st;
+    const ssd_linattn_dims& d = *dims;
+    if ((d.nseq > 0) != (cu_seqlens != nullptr)) return cu_seqlens ? SSD_ERR_SHAPE : SSD_ERR_NULL_ARG;
+    const ssd_linattn_layout l = lin_layout(d, layout);
+    const int64_t T = (int64_t)d.batch * d.seqlen;
+    if (!decay || (T > 0 && (!q || !k || !v || !dy || !dq || !dk || !dv))) return SSD_ERR_NULL_ARG;
+    if (!rows_apart(T, l.dq_token, d.nheads, l.dq_head, d.keydim) ||
+        !rows_apart(T, l.dk_token, d.ngroups, l.dk_group, d.keydim) ||
+        !rows_apart(T, l.dv_token, d.ngroups, l.dv_group, d.valuedim))
+        return SSD_ERR_SHAPE;
+    const size_t e = elem_size(d.dtype);
+    for (const void* a : {q, k, v, dy, (const void*)dq, (const void*)dk, (const void*)dv})
+        if (!elem_aligned(a, e)) return SSD_ERR_ALIGN;
+    if (!elem_aligned(decay, 4) || !elem_aligned(init_state, 4) || !elem_aligned(d_final, 4) ||
+        !elem_aligned(dinit_state, 4) || !elem_aligned(cu_seqlens, 4) || ((uintptr_t)workspace & 255))
+        return SSD_ERR_ALIGN;
+    if (d_final != dinit_state && overlaps(d_final, state_bytes(d), dinit_state, state_bytes(d)))
+        return SSD_ERR_OVERLAP;
+    if (overlaps(init_state, state_bytes(d), dinit_state, state_bytes(d))) return SSD_ERR_OVERLAP;
+    const LinBwdPlan b = lin_bwd_plan(d);
+    if (b.spans + b.shares && (!workspace || workspace_bytes < b.spans + b.shares)) return SSD_ERR_WORKSPACE;
+    if (cu_seqlens && check_cu_env(cu_seqlens, d.nseq, T, (hipStream_t)stream, &st)) return st;
+    const hipStream_t s = (hipStream_t)stream;
+    const int R = d.nheads / d.ngroups;
+    float* const shares = (float*)((char*)workspace + b.spans);
+    const bool half = d.dtype == SSD_BF16;
+
+    LinPass p = lin_common(d, decay, cu_seqlens);
+    p.spans = (float*)workspace;
+    if (T > 0) {
+        p.q = dy, p.q_t = l.dy_token, p.q_h = l.dy_head;
+        p.k = v, p.k_t = l.v_token, p.k_h = l.v_group, p.kdiv = R;
+        p.v = k, p.v_t = l.k_token, p.v_h = l.k_group, p.vdiv = R;
+        p.o = dq, p.o_t = l.dq_token, p.o_h = l.dq_head;
+        p.K = d.valuedim, p.V = d.keydim, p.s_k = 1, p.s_v = d.valuedim;
+        p.init = init_state, p.final = nullptr;
+        p.reverse = reverse != 0, p.init_pow = 1, p.final_pow = 0;
+        p.in_scale = 1.f, p.out_scale = d.scale;
+        if (half) launch_pass<bf16, bf16>(p, b.dq, s);
+        else launch_pass<float, float>(p, b.dq, s);
+    }
+    // the passes in the opposite order, dk before dv: dinit may be d_final's buffer
+    p.init = d_final;
+    p.reverse = reverse == 0;
+    p.init_pow = 0, p.final_pow = 1;
+    p.in_scale = d.scale, p.out_scale = 1.f;
+    auto run = [&](const LinPlan& pl) {
+        if (R == 1) {
+            if (half) launch_pass<bf16, bf16>(p, pl, s);
+            else launch_pass<float, float>(p, pl, s);
+        } else {
+            if (half) launch_pass<bf16, float>(p, pl, s);
+            else launch_pass<float, float>(p, pl, s);
+        }
+    };
+    auto join = [&](void* out, int64_t o_t, int64_t o_g, int D) {
+        if (R == 1) return;
+        const int64_t items = T * d.ngroups * D;
+        const dim3 grid((unsigned)(items < (1 << 28) ? cdiv(items, 256) : 1 << 20));
+        if (half) linattn_heads_sum<bf16><<<grid, 256, 0, s>>>(shares, (bf16*)out, items, D, d.ngroups, R, o_t, o_g);
+        else linattn_heads_sum<float><<<grid, 256, 0, s>>>(shares, (float*)out, items, D, d.ngroups, R, o_t, o_g);
+    };
+    if (T > 0) {
+        p.q = v, p.q_t = l.v_token, p.q_h = l.v_group, p.qdiv = R;
+        p.k = dy, p.k_t = l.dy_token, p.k_h = l.dy_head, p.kdiv = 1;
+        p.v = q, p.v_t = l.q_token, p.v_h = l.q_head, p.vdiv = 1;
+        p.o = R == 1 ? dk : shares;
+        p.o_t = R == 1 ? l.dk_token : (int64_t)d.nheads * d.keydim;
+        p.o_h = R == 1 ? l.dk_group : d.keydim;
+        p.K = d.valuedim, p.V = d.keydim, p.s_k = 1, p.s_v = d.valuedim;
+        p.final = nullptr;
+        run(b.dk);
+        join(dk, l.dk_token, l.dk_group, d.keydim);
+    }
+    if (T > 0 || dinit_state) {
+        p.q = k, p.q_t = l.k_token, p.q_h = l.k_group, p.qdiv = R;
+        p.k = q, p.k_t = l.q_token, p.k_h = l.q_head, p.kdiv = 1;
+        p.v = dy, p.v_t = l.dy_token, p.v_h = l.dy_head, p.vdiv = 1;
+        p.o = R == 1 ? dv : shares;
+        p.o_t = R == 1 ? l.dv_token : (int64_t)d.nheads * d.valuedim;
+        p.o_h = R == 1 ? l.dv_group : d.valuedim;
+        p.K = d.keydim, p.V = d.valuedim, p.s_k = d.valuedim, p.s_v = 1;
+        p.final = dinit_state;
+        run(b.dv);
+        if (T > 0) join(dv, l.dv_token, l.dv_group, d.valuedim);
+    }
+    return launched();
+}
+
+}  // extern "C"

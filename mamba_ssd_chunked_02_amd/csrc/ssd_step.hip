@@ -4,8 +4,9 @@
 //   ssd_step          h = e^-d h + d B x^T,  y = C h        (h: N x P per head)
 //   ssd_selscan_step  h_n = e^(d A_n) h_n + d B_n x,  y = (C h + D x) silu(z)
 //   ssd_conv_step     y = silu(b + w . [state, x]), state shifted by one
+//   ssd_linattn_step  S = e^decay S + k v^T,  y = scale q S   (S: K x V per head)
 //
-// All three are bound by the state, read once and written once; every thread
+// All are bound by the state, read once and written once; every thread
 // holds its part of it in registers between the two, so the same buffer may
 // be updated in place.
 #include "ssd_layer.h"
@@ -266,6 +267,96 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvStepParams p) {
     store_own<T, V>(y, skip, v);
 }
 
+// ---- linear attention ---------------------------------------------------------------------
+
+struct LinStepParams {
+    const void* q;
+    const void* k;
+    const void* v;
+    void* y;
+    const float* decay;
+    const float* state;
+    float* new_state;
+    const int32_t* slots;
+    int64_t qs_t, qs_h, ks_t, ks_g, vs_t, vs_g, ys_t, ys_h;
+    float scale;
+    int32_t nslots, H, K, V, hpg, pieces;
+};
+
+// A workgroup takes CP value columns of one head: CP / VW lanes across (VW columns each,
+// the last vector moved back to end with the row), the other threads down the state's
+// rows, UN rows in flight each.
+template <typename T, int CP, int VW>
+__global__ __launch_bounds__(256) void linattn_step_kernel(LinStepParams p) {
+    constexpr int PL = CP / VW, ROWS = 256 / PL, UN = 8;
+    __shared__ float ex[4][CP];
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    uint32_t id = blockIdx.x;
+    const int piece = id % (uint32_t)p.pieces;
+    id /= (uint32_t)p.pieces;
+    const int h = id % (uint32_t)p.H;
+    const int64_t b = id / (uint32_t)p.H;
+    const int g = h / p.hpg, k0 = tid / PL, at = piece * CP + (tid % PL) * VW;
+    const bool own = at < p.V;
+    const int c = min(at, p.V - VW), skip = min(at - c, VW);
+    const int64_t row = pool_row(p.slots, p.nslots, b);
+    T* y = (T*)p.y + b * p.ys_t + h * p.ys_h;
+    float acc[VW];
+#pragma unroll
+    for (int j = 0; j < VW; ++j) acc[j] = 0.f;
+    if (row < 0) {
+        if (k0 == 0 && own) store_own<T, VW>(y + c, skip, acc);
+        return;
+    }
+    const int64_t base = (row * p.H + h) * ((int64_t)p.K * p.V) + c;
+    const float* in = p.state + base;
+    float* out = p.new_state + base;
+    const T* q = (const T*)p.q + b * p.qs_t + h * p.qs_h;
+    const T* k = (const T*)p.k + b * p.ks_t + g * p.ks_g;
+    const float rate = expf(p.decay[h]);
+    float v[VW];
+    load_vec<T, VW>((const T*)p.v + b * p.vs_t + g * p.vs_g + c, VW, v);
+    for (int kb = 0; kb < p.K; kb += ROWS * UN) {
+        float s[UN][VW], qv[UN], kv[UN];
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            const int n = min(kb + i * ROWS + k0, p.K - 1);
+            load_vec<float, VW>(in + n * p.V, VW, s[i]);
+            qv[i] = (float)q[n];
+            kv[i] = (float)k[n];
+        }
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            const int n = kb + i * ROWS + k0;
+            if (n >= p.K) break;
+#pragma unroll
+            for (int j = 0; j < VW; ++j) {
+                s[i][j] = rate * s[i][j] + kv[i] * v[j];
+                acc[j] += qv[i] * s[i][j];
+            }
+            if (own) store_own<float, VW>(out + n * p.V, skip, s[i]);
+        }
+    }
+    // rows of one wave, then the four waves
+#pragma unroll
+    for (int j = 0; j < VW; ++j)
+#pragma unroll
+        for (int o = PL; o < 64; o *= 2) acc[j] += __shfl_xor(acc[j], o);
+    if (lane < PL) {
+#pragma unroll
+        for (int j = 0; j < VW; ++j) ex[wave][lane * VW + j] = acc[j];
+    }
+    __syncthreads();
+    if (tid < PL && own) {
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+            const int x = tid * VW + j;
+            acc[j] = p.scale * (ex[0][x] + ex[1][x] + ex[2][x] + ex[3][x]);
+        }
+        store_own<T, VW>(y + c, skip, acc);
+    }
+}
+
 // in place, or two pools that share nothing
 bool pools_ok(const void* a, const void* b, size_t bytes) {
     return a == b || !overlaps(a, bytes, b, bytes);
@@ -491,6 +582,73 @@ int ssd_conv_step(const ssd_conv_dims* dims, const ssd_conv_layout* layout, cons
         else SSD_CONV_STEP(float, 1);
     }
 #undef SSD_CONV_STEP
+    return launched();
+}
+
+int ssd_linattn_step(const ssd_linattn_dims* dims, const ssd_linattn_layout* layout, const void* q,
+                     const void* k, const void* v, const float* decay, const float* state,
+                     const int32_t* slots, int32_t nslots, void* y, float* new_state, void* stream) {
+    if (!dims) return SSD_ERR_NULL_ARG;
+    const ssd_linattn_dims& d = *dims;
+    if (d.dtype != SSD_F32 && d.dtype != SSD_BF16) return SSD_ERR_DTYPE;
+    if (d.batch < 0 || d.seqlen != 1 || d.nseq != 0 || d.nheads < 1 || d.ngroups < 1 ||
+        d.nheads % d.ngroups || d.keydim < 1 || d.valuedim < 1 || d.reserved != 0 || nslots < 0 ||
+        (!slots && nslots < d.batch) || !(d.scale == d.scale) ||
+        (int64_t)d.batch * d.nheads > (int64_t)1 << 21)
+        return SSD_ERR_SHAPE;
+    if (d.keydim > SSD_LINATTN_MAX_DIM || d.valuedim > SSD_LINATTN_MAX_DIM) return SSD_ERR_UNSUPPORTED;
+    const int64_t H = d.nheads, G = d.ngroups, K = d.keydim, V = d.valuedim;
+    ssd_linattn_layout l = {H * K, K, G * K, K, G * V, V, H * V, V};
+    if (layout) l = *layout;
+    for (int64_t s : {l.q_token, l.q_head, l.k_token, l.k_group, l.v_token, l.v_group, l.y_token, l.y_head})
+        if (s < 0 || s > kMaxStride) return SSD_ERR_SHAPE;
+    if (d.batch == 0) return SSD_OK;
+    if (!rows_apart(d.batch, l.y_token, H, l.y_head, V)) return SSD_ERR_SHAPE;
+    if (!q || !k || !v || !decay || !y) return SSD_ERR_NULL_ARG;
+    if (nslots > 0 && (!state || !new_state)) return SSD_ERR_NULL_ARG;
+    const size_t e = elem_size(d.dtype);
+    for (const void* a : {q, k, v, (const void*)y})
+        if (!elem_aligned(a, e)) return SSD_ERR_ALIGN;
+    for (const void* a : {(const void*)decay, (const void*)state, (const void*)new_state, (const void*)slots})
+        if (!elem_aligned(a, 4)) return SSD_ERR_ALIGN;
+    if (!pools_ok(state, new_state, (size_t)nslots * H * K * V * 4)) return SSD_ERR_OVERLAP;
+    LinStepParams p = {};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.y = y;
+    p.decay = decay;
+    p.state = state;
+    p.new_state = new_state;
+    p.slots = slots;
+    p.qs_t = l.q_token;
+    p.qs_h = l.q_head;
+    p.ks_t = l.k_token;
+    p.ks_g = l.k_group;
+    p.vs_t = l.v_token;
+    p.vs_g = l.v_group;
+    p.ys_t = l.y_token;
+    p.ys_h = l.y_head;
+    p.scale = d.scale;
+    p.nslots = nslots;
+    p.H = d.nheads;
+    p.K = d.keydim;
+    p.V = d.valuedim;
+    p.hpg = d.nheads / d.ngroups;
+    // 64 columns a workgroup; 16 where that leaves CUs without one
+    const bool wide = d.batch * H * cdiv(V, 64) >= 256 && V > 16;
+    p.pieces = (int)cdiv(V, wide ? 64 : 16);
+    const dim3 gd((unsigned)(d.batch * H * p.pieces));
+    hipStream_t s = (hipStream_t)stream;
+#define SSD_LINATTN_STEP(T)                                              \
+    do {                                                                 \
+        if (V < 4) linattn_step_kernel<T, 16, 1><<<gd, 256, 0, s>>>(p);  \
+        else if (wide) linattn_step_kernel<T, 64, 4><<<gd, 256, 0, s>>>(p); \
+        else linattn_step_kernel<T, 16, 4><<<gd, 256, 0, s>>>(p);        \
+    } while (0)
+    if (d.dtype == SSD_BF16) SSD_LINATTN_STEP(bf16);
+    else SSD_LINATTN_STEP(float);
+#undef SSD_LINATTN_STEP
     return launched();
 }
 
