@@ -659,6 +659,55 @@ int ssd_linattn_step(const ssd_linattn_dims* dims, const ssd_linattn_layout* lay
                      const float* state, const int32_t* slots, int32_t nslots,
                      void* y, float* new_state, void* stream);
 
+/*
+ * Group norm, channels last, with an activation: of x [n, P, C] (n samples
+ * of P positions), for each sample and each of G groups of D = C / G
+ * consecutive channels,
+ *   mean = sum x / (P D),  rstd = 1 / sqrt(sum (x - mean)^2 / (P D) + eps),
+ *   u = (x - mean) rstd weight + bias,
+ *   y = u,  u / (1 + e^-u) (SSD_ACT_SILU) or  u z / (1 + e^-z) (SSD_ACT_GATE)
+ * (with P = 1 the norm of every token's heads behind a scan).  weight, bias
+ * [C] float32, each NULL for 1 / 0; mean, rstd [n, G] float32 outputs, each
+ * NULL to skip.  y may be x itself.  z is read only with SSD_ACT_GATE.
+ * Element (i, p, c) of x is at x + i * x_sample + p * x_row + c, and so on.
+ * workspace: ssd_groupnorm_fwd_workspace_bytes(dims) bytes (0 where P is 1
+ * and a group has at most 1024 channels, 2048 in bf16), 256-byte aligned.
+ */
+enum { SSD_ACT_NONE = 0, SSD_ACT_SILU = 1, SSD_ACT_GATE = 2 };
+typedef struct ssd_groupnorm_dims {
+    int64_t samples;    /* n >= 0                                           */
+    int64_t positions;  /* P >= 1; n * P and n * G below 2^31               */
+    int64_t x_sample, x_row;    /* element strides, rows C .. 2^24 apart    */
+    int64_t y_sample, y_row;    /* of y (forward) or dx (backward)          */
+    int64_t z_sample, z_row;    /* of z and dz                              */
+    int64_t dy_sample, dy_row;
+    int32_t channels;   /* C: 1 .. 2^24                                     */
+    int32_t groups;     /* G >= 1, divides C                                */
+    int32_t dtype;      /* of x, y, z, dy, dx, dz: SSD_F32 or SSD_BF16      */
+    int32_t activation; /* SSD_ACT_*                                        */
+    float eps;          /* >= 0                                             */
+    int32_t reserved;   /* 0                                                */
+} ssd_groupnorm_dims;
+
+size_t ssd_groupnorm_fwd_workspace_bytes(const ssd_groupnorm_dims* dims);
+
+int ssd_groupnorm_fwd(const ssd_groupnorm_dims* dims, const void* x, const float* weight,
+                      const float* bias, const void* z, void* y, float* mean, float* rstd,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Its gradients, from the forward's mean and rstd: dx, with SSD_ACT_GATE dz
+ * (strides of z), and dweight, dbias [C] float32, each NULL to skip.  dx may
+ * be x's or dy's own buffer where the strides are the same; dz lies apart
+ * from every input.
+ */
+size_t ssd_groupnorm_bwd_workspace_bytes(const ssd_groupnorm_dims* dims);
+
+int ssd_groupnorm_bwd(const ssd_groupnorm_dims* dims, const void* x, const float* weight,
+                      const float* bias, const void* z, const float* mean, const float* rstd,
+                      const void* dy, void* dx, void* dz, float* dweight, float* dbias,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code (never NULL). */
 const char* ssd_status_string(int status);
 

@@ -15,7 +15,8 @@ SiLU), ``ssd_selscan_fwd`` / ``ssd_selscan_bwd`` (selective scan with a decay
 per channel and state entry), and for serving one token at a time
 ``ssd_step``, ``ssd_conv_step`` and ``ssd_selscan_step``.  Linear attention with
 a constant decay per head: ``ssd_linattn_fwd`` / ``ssd_linattn_bwd`` and
-``ssd_linattn_step`` for single tokens.
+``ssd_linattn_step`` for single tokens.  ``ssd_groupnorm_fwd`` /
+``ssd_groupnorm_bwd``: group norm, channels last, with SiLU or a gate.
 """
 from ._binding import (  # noqa: F401
     CHUNK, SSD_BF16, SSD_F32, STAGE_ALL, STAGE_PASS, STAGE_SCAN, STAGE_STATE, STAGE_TABLE,
@@ -26,8 +27,9 @@ from ._binding import (  # noqa: F401
     ssd_fwd_workspace_bytes, ssd_status_string,
 )
 from ._layer import (  # noqa: F401
-    SsdConvDims, SsdConvLayout, SsdLinattnDims, SsdLinattnLayout, SsdNormDims, SsdSelscanDims,
-    SsdSelscanLayout, ssd_conv_bwd, ssd_conv_fwd, ssd_conv_step, ssd_linattn_bwd, ssd_linattn_fwd,
+    SsdConvDims, SsdConvLayout, SsdGroupnormDims, SsdLinattnDims, SsdLinattnLayout, SsdNormDims, SsdSelscanDims,
+    SsdSelscanLayout, ssd_conv_bwd, ssd_conv_fwd, ssd_conv_step, ssd_groupnorm_bwd,
+    ssd_groupnorm_fwd, ssd_linattn_bwd, ssd_linattn_fwd,
     ssd_linattn_step, ssd_norm_bwd, ssd_norm_fwd, ssd_selscan_bwd, ssd_selscan_fwd,
     ssd_selscan_step, ssd_step,
 )

@@ -60,6 +60,14 @@ class SsdLinattnLayout(ctypes.Structure):
                                     "dq_head", "dk_token", "dk_group", "dv_token", "dv_group")]
 
 
+class SsdGroupnormDims(ctypes.Structure):
+    """Mirror of ``ssd_groupnorm_dims``."""
+    _fields_ = [(n, _I64) for n in ("samples", "positions", "x_sample", "x_row", "y_sample", "y_row",
+                                    "z_sample", "z_row", "dy_sample", "dy_row")] \
+        + [(n, _I32) for n in ("channels", "groups", "dtype", "activation")] \
+        + [("eps", _F32), ("reserved", _I32)]
+
+
 @functools.lru_cache(maxsize=1024)
 def _struct(cls, *fields):
     """The struct of these sizes; the library only reads it, so calls of the same
@@ -89,6 +97,8 @@ _SIGNATURES = {
                        + [_I32] + [_P] * 7 + [_SIZE, _P],
     "ssd_linattn_step": [_pointer(SsdLinattnDims), _pointer(SsdLinattnLayout)] + [_P] * 6
                         + [_I32] + [_P] * 3,
+    "ssd_groupnorm_fwd": [_pointer(SsdGroupnormDims)] + [_P] * 8 + [_SIZE, _P],
+    "ssd_groupnorm_bwd": [_pointer(SsdGroupnormDims)] + [_P] * 12 + [_SIZE, _P],
     "ssd_step": [_pointer(SsdDims), _pointer(SsdLayout), _P, _P, _F32, _P, _P, _P, _P, _I32,
                  _P, _P, _P],
 }
@@ -99,6 +109,8 @@ _WORKSPACES = {
     "ssd_selscan_bwd_workspace_bytes": SsdSelscanDims,
     "ssd_linattn_fwd_workspace_bytes": SsdLinattnDims,
     "ssd_linattn_bwd_workspace_bytes": SsdLinattnDims,
+    "ssd_groupnorm_fwd_workspace_bytes": SsdGroupnormDims,
+    "ssd_groupnorm_bwd_workspace_bytes": SsdGroupnormDims,
 }
 _entries = {}
 
@@ -674,3 +686,86 @@ def ssd_linattn_step(q, k, v, decay, state, scale=1.0, slots=None, new_state=Non
             decay.data_ptr(), state.data_ptr(), _at(slots), state.shape[0], y.data_ptr(),
             new_state.data_ptr())
     return y
+
+
+# ---- group norm ----------------------------------------------------------------------------
+
+def _maps(t, name, shape):
+    """(sample, position) strides of a [n, ..., C] tensor with contiguous channels whose
+    positions form one stride."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}")
+    n, C = shape[0], shape[-1]
+    P = shape[1:-1].numel()
+    if t.is_contiguous() or t.numel() == 0:
+        return P * C, C
+    m = t.view(n, P, C)  # raises where the positions do not form one stride
+    if C > 1 and m.stride(2) != 1:
+        raise ValueError(f"{name} needs contiguous channels")
+    row = m.stride(1) if P > 1 else C
+    return (m.stride(0) if n > 1 else P * row), row
+
+
+_ACTIVATIONS = {None: 0, "silu": 1}
+
+
+def _groupnorm_arguments(x, groups, weight, bias, z, activation, eps, out, dy, stats):
+    if x.dim() < 2 or x.shape[-1] < 1 or groups < 1 or x.shape[-1] % groups:
+        raise ValueError("x [n, ..., C] with C a multiple of groups expected")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be None or 'silu', not {activation!r}")
+    if z is not None and activation is not None:
+        raise ValueError("a gate z is the activation: give one of z and activation")
+    shape = x.shape
+    C = shape[-1]
+    code = _dtype_of(x, "x")
+    _same(x, (z, "z"), (out, "y"), (dy, "dy"))
+    _floats(x, (weight, (C,), "weight"), (bias, (C,), "bias"),
+            *((t, (shape[0], groups), name) for t, name in stats))
+    P = shape[1:-1].numel()
+    dense = (P * C, C)
+    act = 2 if z is not None else _ACTIVATIONS[activation]
+    return _struct(SsdGroupnormDims, shape[0], P, *_maps(x, "x", shape),
+                   *(dense if out is None else _maps(out, "y", shape)),
+                   *(dense if z is None else _maps(z, "z", shape)),
+                   *(dense if dy is None else _maps(dy, "dy", shape)), C, groups, code, act,
+                   float(eps), 0)
+
+
+def ssd_groupnorm_fwd(x, groups, weight=None, bias=None, z=None, activation=None, eps=1e-5, y=None,
+                      workspace=None):
+    """Group norm, channels last, with an activation: x [n, ..., C] (bf16 or fp32;
+    the dimensions between are positions, over which a sample's statistics run:
+    [tokens, C] norms every token's groups on their own), weight, bias [C] fp32 or
+    None.  ``activation``: None or "silu"; or ``z``, a gate like x:
+    ``y = norm(x) silu(z)``.  ``y`` may be preallocated (x itself for in place).
+    Returns (y, mean, rstd) with mean and rstd [n, groups] fp32, for
+    ``ssd_groupnorm_bwd``."""
+    dims = _groupnorm_arguments(x, groups, weight, bias, z, activation, eps, y, None, ())
+    if y is None:
+        y = _output(x)
+    mean, rstd = torch.empty((2, x.shape[0], groups), dtype=torch.float32, device=x.device).unbind(0)
+    workspace, *ws = _workspace("ssd_groupnorm_fwd_workspace_bytes", dims, x, workspace)
+    _launch("ssd_groupnorm_fwd", x, dims, x.data_ptr(), _at(weight), _at(bias), _at(z), y.data_ptr(),
+            mean.data_ptr(), rstd.data_ptr(), *ws)
+    return y, mean, rstd
+
+
+def ssd_groupnorm_bwd(x, groups, weight, bias, mean, rstd, dy, z=None, activation=None,
+                      workspace=None):
+    """Gradients of ``ssd_groupnorm_fwd`` from its arguments, mean and rstd: a dict
+    with dx (and dz with a gate), contiguous, and dweight, dbias [C] fp32."""
+    if z is not None:
+        z = z if z.is_contiguous() else z.contiguous()  # dz is laid out like it
+    dims = _groupnorm_arguments(x, groups, weight, bias, z, activation, 0.0, None, dy,
+                                ((mean, "mean"), (rstd, "rstd")))
+    g = {"dx": _output(x)}
+    if z is not None:
+        g["dz"] = torch.empty_like(z)
+    g["dweight"], g["dbias"] = torch.empty((2, x.shape[-1]), dtype=torch.float32,
+                                           device=x.device).unbind(0)
+    workspace, *ws = _workspace("ssd_groupnorm_bwd_workspace_bytes", dims, x, workspace)
+    _launch("ssd_groupnorm_bwd", x, dims, x.data_ptr(), _at(weight), _at(bias), _at(z), mean.data_ptr(),
+            rstd.data_ptr(), dy.data_ptr(), g["dx"].data_ptr(), _at(g.get("dz")),
+            g["dweight"].data_ptr(), g["dbias"].data_ptr(), *ws)
+    return g

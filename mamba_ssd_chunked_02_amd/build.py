@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libssd.so")
 SOURCES = ["ssd_api.hip", "ssd_kernels.hip", "ssd_hw_kernels.hip", "ssd_bwd_kernels.hip",
            "ssd_norm.hip", "ssd_conv.hip", "ssd_step.hip", "ssd_selscan.hip",
-           "ssd_selscan_bwd.hip", "ssd_linattn.hip"]
+           "ssd_selscan_bwd.hip", "ssd_linattn.hip",
+           "ssd_groupnorm.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # Packed-fp32 instructions are kept out of the device code (hipcc still

@@ -1,0 +1,816 @@
+// Group norm, channels last, with an activation; forward and backward.
+//
+// x [n, P, C]: a sample's statistics run over its P positions and the D = C / G channels of
+// each group (P = 1: every row's groups on their own, the norm of a layer's heads):
+//   mean = sum x / (P D),  rstd = 1 / sqrt(sum (x - mean)^2 / (P D) + eps)
+//   xh = (x - mean) rstd,  u = xh w + b,  y = u | silu(u) | u silu(z)
+// and with du = dL/du (from dy through the activation), g = du w:
+//   dx = rstd (g - mean(g) - xh mean(g xh)),  dw = sum du xh,  db = sum du,  dz = dy u silu'(z).
+//
+// Both are bound by memory.  P = 1: a group is D consecutive elements, LG lanes take it (64 /
+// LG groups a wave) and hold it in registers between the sums and the output: one pass.
+// P > 1: column statistics of runs of positions (one pass over x), joined per group, and a
+// second pass for the output, which the caches serve as far as they hold x.
+#include "ssd_layer.h"
+
+namespace ssd {
+namespace {
+
+enum { PLAIN = SSD_ACT_NONE, SILU = SSD_ACT_SILU, GATE = SSD_ACT_GATE };
+
+struct GnParams {
+    const void* x;
+    const void* z;
+    const void* dy;
+    void* out;  // y or dx
+    void* dz;
+    const float* weight;
+    const float* bias;
+    float* mean;
+    float* rstd;
+    const float* mean_in;
+    const float* rstd_in;
+    float* part;  // columns' sums of the runs [n][runs][2][C]
+    float* sums;  // backward, P > 1: mean(g), mean(g xh) [n][G][2]
+    int64_t n, P;
+    int64_t x_n, x_p, z_n, z_p, y_n, y_p, dy_n, dy_p;  // strides of samples and positions
+    int64_t runlen;
+    int32_t C, G, D, runs, walkers;
+    float eps;
+};
+
+// A launch's units of work lie along x, and along z where there are more than kAlong.
+constexpr int64_t kAlong = (int64_t)1 << 20;
+__device__ __forceinline__ int64_t unit() { return (int64_t)blockIdx.z * gridDim.x + blockIdx.x; }
+dim3 units(int64_t n, int64_t y = 1) {
+    const int64_t x = n < kAlong ? n : kAlong;
+    return dim3((unsigned)x, (unsigned)y, (unsigned)cdiv(n, x));
+}
+
+// u's value through the activation, z where it has a gate
+template <int ACT>
+__device__ __forceinline__ float activate(float u, float z) {
+    if (ACT == SILU) return u * sigmoid(u);
+    if (ACT == GATE) return u * (z * sigmoid(z));
+    return u;
+}
+// dL/du from dy, and dL/dz
+template <int ACT>
+__device__ __forceinline__ float slope(float dy, float u, float z, float& dz) {
+    if (ACT == SILU) return dy * silu_slope(u, sigmoid(u));
+    if (ACT == GATE) {
+        const float s = sigmoid(z);
+        dz = dy * u * silu_slope(z, s);
+        return dy * (z * s);
+    }
+    return dy;
+}
+
+// Sum over LG consecutive lanes (a power of two), in each of them.
+template <int LG>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int o = 1; o < LG; o *= 2) v += __shfl_xor(v, o);
+    return v;
+}
+
+// ---- P = 1 ---------------------------------------------------------------------------------
+
+// LG lanes x NV vectors of V elements hold one group of a row.  The last vector is moved back
+// to end with the group; the elements it shares (`skip`) are left out of the sums and stored
+// twice with the same value.
+template <int V>
+struct Cell {
+    int c, skip;
+    __device__ __forceinline__ Cell(int i, int lanes, int lane, int D) {
+        const int at = (i * lanes + lane) * V;
+        c = min(at, D - V);
+        skip = min(at - c, V);
+    }
+};
+
+template <typename T, int V, int NV, int LG, int ACT>
+__global__ __launch_bounds__(256) void gn_row_fwd(GnParams p) {
+    const int64_t id = (unit() * 256 + threadIdx.x) / LG;
+    const int lane = threadIdx.x % LG;
+    if (id >= p.n * p.G) return;  // whole groups of lanes
+    int64_t row;
+    const int g = (int)divide(id, p.G, &row);
+    const int c0 = g * p.D;
+    const T* x = (const T*)p.x + row * p.x_n + c0;
+    const T* z = (const T*)p.z + row * p.z_n + c0;
+    T* y = (T*)p.out + row * p.y_n + c0;
+    RawVec<T, V> xr[NV], zr[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const Cell<V> q(i, LG, lane, p.D);
+        load_raw<T, V>(x + q.c, V, xr[i]);
+        if (ACT == GATE) load_raw<T, V>(z + q.c, V, zr[i]);
+    }
+    float v[NV][V], s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const Cell<V> q(i, LG, lane, p.D);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            v[i][j] = (float)xr[i].v[j];
+            s += j >= q.skip ? v[i][j] : 0.f;
+        }
+    }
+    const float mean = lanes_sum<LG>(s) / (float)p.D;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const Cell<V> q(i, LG, lane, p.D);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            v[i][j] -= mean;
+            s += j >= q.skip ? v[i][j] * v[i][j] : 0.f;
+        }
+    }
+    const float rstd = 1.f / sqrtf(lanes_sum<LG>(s) / (float)p.D + p.eps);
+    if (lane == 0) {
+        if (p.mean) p.mean[id] = mean;
+        if (p.rstd) p.rstd[id] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const Cell<V> q(i, LG, lane, p.D);
+        float w[V], b[V], o[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            w[j] = 1.f;
+            b[j] = 0.f;
+        }
+        if (p.weight) load_vec<float, V>(p.weight + c0 + q.c, V, w);
+        if (p.bias) load_vec<float, V>(p.bias + c0 + q.c, V, b);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            o[j] = activate<ACT>(v[i][j] * rstd * w[j] + b[j], ACT == GATE ? (float)zr[i].v[j] : 0.f);
+        if (q.skip < V) store_vec<T, V>(y + q.c, V, o);
+    }
+}
+
+// A walker (LG lanes) keeps one group of channels and takes the rows walker, walker +
+// walkers, ...; its share of dw and db stays in registers until its last row.
+template <typename T, int V, int NV, int LG, int ACT>
+__global__ __launch_bounds__(256) void gn_row_bwd(GnParams p) {
+    const int64_t id = (unit() * 256 + threadIdx.x) / LG;
+    const int lane = threadIdx.x % LG;
+    if (id >= (int64_t)p.walkers * p.G) return;
+    int64_t walker;
+    const int g = (int)divide(id, p.G, &walker);
+    const int c0 = g * p.D;
+    float w[NV][V], b[NV][V], dw[NV][V], db[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const Cell<V> q(i, LG, lane, p.D);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            w[i][j] = 1.f;
+            b[i][j] = dw[i][j] = db[i][j] = 0.f;
+        }
+        if (p.weight) load_vec<float, V>(p.weight + c0 + q.c, V, w[i]);
+        if (ACT != PLAIN && p.bias) load_vec<float, V>(p.bias + c0 + q.c, V, b[i]);
+    }
+    const float inv = 1.f / (float)p.D;
+    for (int64_t row = walker; row < p.n; row += p.walkers) {
+        const T* x = (const T*)p.x + row * p.x_n + c0;
+        const T* z = (const T*)p.z + row * p.z_n + c0;
+        const T* dy = (const T*)p.dy + row * p.dy_n + c0;
+        T* dx = (T*)p.out + row * p.y_n + c0;
+        T* dz = (T*)p.dz + row * p.z_n + c0;
+        RawVec<T, V> xr[NV], zr[NV], gr[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Cell<V> q(i, LG, lane, p.D);
+            load_raw<T, V>(x + q.c, V, xr[i]);
+            load_raw<T, V>(dy + q.c, V, gr[i]);
+            if (ACT == GATE) load_raw<T, V>(z + q.c, V, zr[i]);
+        }
+        const float mean = p.mean_in[row * p.G + g], rstd = p.rstd_in[row * p.G + g];
+        float xh[NV][V], gw[NV][V], s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Cell<V> q(i, LG, lane, p.D);
+            float zo[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                xh[i][j] = ((float)xr[i].v[j] - mean) * rstd;
+                const float du = slope<ACT>((float)gr[i].v[j], xh[i][j] * w[i][j] + b[i][j],
+                                            ACT == GATE ? (float)zr[i].v[j] : 0.f, zo[j]);
+                dw[i][j] += du * xh[i][j];
+                db[i][j] += du;
+                gw[i][j] = du * w[i][j];
+                s0 += j >= q.skip ? gw[i][j] : 0.f;
+                s1 += j >= q.skip ? gw[i][j] * xh[i][j] : 0.f;
+            }
+            if (ACT == GATE && q.skip < V) store_vec<T, V>(dz + q.c, V, zo);
+        }
+        s0 = lanes_sum<LG>(s0) * inv;
+        s1 = lanes_sum<LG>(s1) * inv;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Cell<V> q(i, LG, lane, p.D);
+            float o[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) o[j] = rstd * (gw[i][j] - s0 - xh[i][j] * s1);
+            if (q.skip < V) store_vec<T, V>(dx + q.c, V, o);
+        }
+    }
+    float* part = p.part + walker * 2 * p.C + c0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const Cell<V> q(i, LG, lane, p.D);
+        if (q.skip < V) {
+            store_vec<float, V>(part + q.c, V, dw[i]);
+            store_vec<float, V>(part + p.C + q.c, V, db[i]);
+        }
+    }
+}
+
+// ---- P > 1 ---------------------------------------------------------------------------------
+
+// Threads of a workgroup: across CV vectors of V channels, down R rows.  The workgroup takes
+// one run of positions of one sample; R threads of a column are joined in LDS.
+template <int V>
+struct Grid {
+    int cl, r, R;  // this thread's vector and row, rows of the workgroup
+    int64_t c;     // first channel (moved back to end with the row), and those it shares
+    int skip;
+    __device__ __forceinline__ Grid(const GnParams& p, int across) {
+        cl = threadIdx.x % across;
+        r = threadIdx.x / across;
+        R = blockDim.x / across;
+        const int64_t at = ((int64_t)blockIdx.y * across + cl) * V;
+        c = at < p.C - V ? at : p.C - V;
+        skip = (int)(at - c < V ? at - c : V);
+    }
+};
+
+// Columns' means and squared deviations of a run, blocks of UN rows joined as they come
+// (Chan): no squares of values with a large mean are summed.
+template <typename T, int V>
+__global__ __launch_bounds__(256) void gn_stats(GnParams p, int across) {
+    constexpr int UN = 4;
+    __shared__ float ex[2][256][V];
+    const Grid<V> t(p, across);
+    int64_t n;
+    const int64_t run = divide(unit(), p.runs, &n);
+    if (n >= p.n) return;
+    const int64_t p0 = run * p.runlen, p1 = p0 + p.runlen < p.P ? p0 + p.runlen : p.P;
+    const T* x = (const T*)p.x + n * p.x_n + t.c;
+    float mean[V], m2[V], cnt = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) mean[j] = m2[j] = 0.f;
+    for (int64_t q = p0 + t.r; q < p1; q += UN * t.R) {
+        RawVec<T, V> raw[UN];
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            const int64_t at = q + i * t.R;
+            load_raw<T, V>(x + (at < p1 ? at : q) * p.x_p, V, raw[i]);
+        }
+        const int64_t rest = (p1 - q + t.R - 1) / t.R;
+        const float k = rest < UN ? (float)rest : (float)UN, all = cnt + k;
+        const float ik = 1.f / k, share = k / all, cross = cnt * share;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float v[UN], s = 0.f, d2 = 0.f;
+#pragma unroll
+            for (int i = 0; i < UN; ++i) {
+                v[i] = (float)raw[i].v[j];
+                s += i < rest ? v[i] : 0.f;
+            }
+            s *= ik;
+#pragma unroll
+            for (int i = 0; i < UN; ++i) {
+                const float d = v[i] - s;
+                d2 += i < rest ? d * d : 0.f;
+            }
+            const float d = s - mean[j];
+            mean[j] += d * share;
+            m2[j] += d2 + d * d * cross;
+        }
+        cnt = all;
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        ex[0][threadIdx.x][j] = mean[j];
+        ex[1][threadIdx.x][j] = m2[j];
+    }
+    __syncthreads();
+    if (t.r) return;
+    const int64_t len = p1 - p0;
+    cnt = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) mean[j] = m2[j] = 0.f;
+    for (int r = 0; r < t.R; ++r) {
+        const float k = (float)(len > r ? (len - r + t.R - 1) / t.R : 0);
+        if (k == 0.f) break;
+        const float share = k / (cnt + k), cross = cnt * share;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float d = ex[0][r * across + t.cl][j] - mean[j];
+            mean[j] += d * share;
+            m2[j] += ex[1][r * across + t.cl][j] + d * d * cross;
+        }
+        cnt += k;
+    }
+    if (t.skip < V) {
+        float* part = p.part + (n * p.runs + run) * 2 * p.C + t.c;
+        store_vec<float, V>(part, V, mean);
+        store_vec<float, V>(part + p.C, V, m2);
+    }
+}
+
+// Sum over a workgroup of 256, in every thread.
+__device__ __forceinline__ float group_sum(float v, float* ex) {
+    v = wave_sum(v);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) ex[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return ex[0] + ex[1] + ex[2] + ex[3];
+}
+
+// One workgroup a sample and group: mean and rstd from its columns' of every run.
+__global__ __launch_bounds__(256) void gn_stats_join(GnParams p) {
+    __shared__ float ex[4];
+    const int64_t id = unit();
+    if (id >= p.n * p.G) return;
+    int64_t n;
+    const int g = (int)divide(id, p.G, &n);
+    const float* part = p.part + n * p.runs * 2 * p.C + g * p.D;
+    const int64_t items = (int64_t)p.runs * p.D;
+    const float total = (float)p.P * (float)p.D;
+    float s = 0.f;
+    for (int64_t i = threadIdx.x; i < items; i += 256) {
+        int64_t run;
+        const int d = (int)divide(i, p.D, &run);
+        const int64_t len = run + 1 < p.runs ? p.runlen : p.P - run * p.runlen;
+        s += (float)len / (float)p.P * part[run * 2 * p.C + d];
+    }
+    const float mean = group_sum(s, ex) / (float)p.D;
+    s = 0.f;
+    for (int64_t i = threadIdx.x; i < items; i += 256) {
+        int64_t run;
+        const int d = (int)divide(i, p.D, &run);
+        const int64_t len = run + 1 < p.runs ? p.runlen : p.P - run * p.runlen;
+        const float e = part[run * 2 * p.C + d] - mean;
+        s += part[(run * 2 + 1) * p.C + d] + (float)len * e * e;
+    }
+    const float rstd = 1.f / sqrtf(group_sum(s, ex) / total + p.eps);
+    if (threadIdx.x == 0) {
+        p.mean[id] = mean;
+        p.rstd[id] = rstd;
+    }
+}
+
+// The output's pass.
+template <typename T, int V, int ACT>
+__global__ __launch_bounds__(256) void gn_apply(GnParams p, int across) {
+    constexpr int UN = 4;
+    const Grid<V> t(p, across);
+    int64_t n;
+    const int64_t run = divide(unit(), p.runs, &n);
+    if (n >= p.n) return;
+    const int64_t p0 = run * p.runlen, p1 = p0 + p.runlen < p.P ? p0 + p.runlen : p.P;
+    const T* x = (const T*)p.x + n * p.x_n + t.c;
+    const T* z = (const T*)p.z + n * p.z_n + t.c;
+    T* y = (T*)p.out + n * p.y_n + t.c;
+    float a[V], m[V], b[V], w[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        w[j] = 1.f;
+        b[j] = 0.f;
+    }
+    if (p.weight) load_vec<float, V>(p.weight + t.c, V, w);
+    if (p.bias) load_vec<float, V>(p.bias + t.c, V, b);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int64_t g = n * p.G + (t.c + j) / p.D;
+        m[j] = p.mean[g];
+        a[j] = p.rstd[g];
+    }
+    for (int64_t q = p0 + t.r; q < p1; q += UN * t.R) {
+        RawVec<T, V> xr[UN], zr[UN];
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            const int64_t at = q + i * t.R < p1 ? q + i * t.R : q;
+            load_raw<T, V>(x + at * p.x_p, V, xr[i]);
+            if (ACT == GATE) load_raw<T, V>(z + at * p.z_p, V, zr[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            const int64_t at = q + i * t.R;
+            float o[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                o[j] = activate<ACT>(((float)xr[i].v[j] - m[j]) * a[j] * w[j] + b[j],
+                                     ACT == GATE ? (float)zr[i].v[j] : 0.f);
+            if (at < p1) store_own<T, V>(y + at * p.y_p, t.skip, o);
+        }
+    }
+}
+
+// Backward.  DX false: columns' sums of du xh and du of a run (and dz); true: dx.
+template <typename T, int V, int ACT, bool DX>
+__global__ __launch_bounds__(256) void gn_bwd(GnParams p, int across) {
+    constexpr int UN = 2;
+    __shared__ float ex[DX ? 1 : 2][DX ? 1 : 256][V];
+    const Grid<V> t(p, across);
+    int64_t n;
+    const int64_t run = divide(unit(), p.runs, &n);
+    if (n >= p.n) return;
+    const int64_t p0 = run * p.runlen, p1 = p0 + p.runlen < p.P ? p0 + p.runlen : p.P;
+    const T* x = (const T*)p.x + n * p.x_n + t.c;
+    const T* z = (const T*)p.z + n * p.z_n + t.c;
+    const T* dy = (const T*)p.dy + n * p.dy_n + t.c;
+    T* dx = (T*)p.out + n * p.y_n + t.c;
+    T* dz = (T*)p.dz + n * p.z_n + t.c;
+    float m[V], a[V], b[V], w[V], s0[V], s1[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        w[j] = 1.f;
+        b[j] = 0.f;
+    }
+    if (p.weight) load_vec<float, V>(p.weight + t.c, V, w);
+    if (ACT != PLAIN && p.bias) load_vec<float, V>(p.bias + t.c, V, b);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int64_t g = n * p.G + (t.c + j) / p.D;
+        m[j] = p.mean_in[g];
+        a[j] = p.rstd_in[g];
+        s0[j] = DX ? p.sums[2 * g] : 0.f;
+        s1[j] = DX ? p.sums[2 * g + 1] : 0.f;
+    }
+    for (int64_t q = p0 + t.r; q < p1; q += UN * t.R) {
+        RawVec<T, V> xr[UN], zr[UN], gr[UN];
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            const int64_t at = q + i * t.R < p1 ? q + i * t.R : q;
+            load_raw<T, V>(x + at * p.x_p, V, xr[i]);
+            load_raw<T, V>(dy + at * p.dy_p, V, gr[i]);
+            if (ACT == GATE) load_raw<T, V>(z + at * p.z_p, V, zr[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            const int64_t at = q + i * t.R;
+            float o[V], zo[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float xh = ((float)xr[i].v[j] - m[j]) * a[j];
+                const float du = slope<ACT>((float)gr[i].v[j], xh * w[j] + b[j],
+                                            ACT == GATE ? (float)zr[i].v[j] : 0.f, zo[j]);
+                if (DX) {
+                    o[j] = a[j] * (du * w[j] - s0[j] - xh * s1[j]);
+                } else if (at < p1) {
+                    s0[j] += du * xh;
+                    s1[j] += du;
+                }
+            }
+            if (at < p1) {
+                if (DX) store_own<T, V>(dx + at * p.y_p, t.skip, o);
+                else if (ACT == GATE) store_own<T, V>(dz + at * p.z_p, t.skip, zo);
+            }
+        }
+    }
+    if constexpr (!DX) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            ex[0][threadIdx.x][j] = s0[j];
+            ex[1][threadIdx.x][j] = s1[j];
+        }
+        __syncthreads();
+        if (t.r || t.skip >= V) return;
+        for (int r = 1; r < t.R; ++r)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                s0[j] += ex[0][r * across + t.cl][j];
+                s1[j] += ex[1][r * across + t.cl][j];
+            }
+        float* part = p.part + (n * p.runs + run) * 2 * p.C + t.c;
+        store_vec<float, V>(part, V, s0);
+        store_vec<float, V>(part + p.C, V, s1);
+    }
+}
+
+// One workgroup a sample and group: mean(g) and mean(g xh) from the columns' sums.
+__global__ __launch_bounds__(256) void gn_bwd_join(GnParams p) {
+    __shared__ float ex[4];
+    const int64_t id = unit();
+    if (id >= p.n * p.G) return;
+    int64_t n;
+    const int g = (int)divide(id, p.G, &n);
+    const float* part = p.part + n * p.runs * 2 * p.C + g * p.D;
+    const float* w = p.weight ? p.weight + g * p.D : nullptr;
+    float s0 = 0.f, s1 = 0.f;
+    for (int64_t i = threadIdx.x; i < (int64_t)p.runs * p.D; i += 256) {
+        int64_t run;
+        const int d = (int)divide(i, p.D, &run);
+        const float f = w ? w[d] : 1.f;
+        s1 += f * part[run * 2 * p.C + d];
+        s0 += f * part[(run * 2 + 1) * p.C + d];
+    }
+    const float total = (float)p.P * (float)p.D;
+    s0 = group_sum(s0, ex) / total;
+    s1 = group_sum(s1, ex) / total;
+    if (threadIdx.x == 0) {
+        p.sums[2 * id] = s0;
+        p.sums[2 * id + 1] = s1;
+    }
+}
+
+// ---- host ----------------------------------------------------------------------------------
+
+int gn_vec(const ssd_groupnorm_dims& d, int64_t width) {
+    const int V = d.dtype == SSD_BF16 ? 8 : 4;
+    return width >= V ? V : 1;
+}
+
+// P = 1: lanes of a group and vectors of a lane
+struct RowPlan {
+    int V, LG, NV;
+};
+RowPlan row_plan(const ssd_groupnorm_dims& d) {
+    const int64_t D = d.channels / d.groups;
+    RowPlan r;
+    r.V = gn_vec(d, D);
+    const int64_t vecs = cdiv(D, r.V);
+    r.LG = 8;
+    while (r.LG < 64 && r.LG < vecs) r.LG *= 2;
+    r.NV = 1;
+    while (r.NV * r.LG < vecs) r.NV *= 2;
+    return r;
+}
+constexpr int kRowMost = 4;  // vectors of a lane: groups of up to 2048 (bf16) or 1024 channels
+
+// P > 1: runs of positions; threads across the channels
+struct RunPlan {
+    int V, across;
+    int64_t runlen;
+    int32_t runs, blocks;
+};
+RunPlan run_plan(const ssd_groupnorm_dims& d) {
+    RunPlan r;
+    r.V = gn_vec(d, d.channels);
+    const int64_t vecs = cdiv(d.channels, r.V);
+    r.blocks = (int)cdiv(vecs, 256);
+    r.across = (int)cdiv(vecs, r.blocks);
+    const int64_t R = 256 / r.across;
+    // four workgroups a CU, but no fewer than 8 rows a thread
+    const int64_t want = cdiv(1024, imax(1, d.samples) * r.blocks);
+    r.runlen = imax(cdiv(d.positions, want), 8 * R);
+    r.runs = (int)cdiv(d.positions, r.runlen);
+    return r;
+}
+
+bool by_rows(const ssd_groupnorm_dims& d) {
+    return d.positions == 1 && row_plan(d).NV <= kRowMost;
+}
+
+int32_t row_walkers(const ssd_groupnorm_dims& d) {
+    const RowPlan r = row_plan(d);
+    // 2048 workgroups' worth of lanes at most, and no fewer than four rows each
+    const int64_t per = cdiv((int64_t)d.groups * r.LG, 256);
+    int64_t w = imax(1, 2048 / per);
+    const int64_t most = imax(1, cdiv(d.samples, 4));
+    return (int32_t)(w < most ? w : most);
+}
+
+int gn_check(const ssd_groupnorm_dims* d) {
+    if (!d) return SSD_ERR_NULL_ARG;
+    if (d->dtype != SSD_F32 && d->dtype != SSD_BF16) return SSD_ERR_DTYPE;
+    if (d->samples < 0 || d->positions < 1 || d->groups < 1 || d->channels < 1 ||
+        d->channels % d->groups || d->channels > kMaxStride ||
+        d->samples > kMaxTokens / d->positions || !(d->eps >= 0.f))
+        return SSD_ERR_SHAPE;
+    if (d->activation < SSD_ACT_NONE || d->activation > SSD_ACT_GATE) return SSD_ERR_UNSUPPORTED;
+    if (d->samples * d->groups > kMaxTokens) return SSD_ERR_SHAPE;
+    for (int64_t s : {d->x_row, d->y_row, d->z_row, d->dy_row})
+        if (s < d->channels || s > kMaxStride) return SSD_ERR_SHAPE;
+    for (int64_t s : {d->x_sample, d->y_sample, d->z_sample, d->dy_sample})
+        if (s < 0 || s > (int64_t)1 << 40) return SSD_ERR_SHAPE;
+    return SSD_OK;
+}
+
+GnParams gn_params(const ssd_groupnorm_dims& d) {
+    GnParams p = {};
+    p.n = d.samples;
+    p.P = d.positions;
+    p.C = d.channels;
+    p.G = d.groups;
+    p.D = d.channels / d.groups;
+    p.eps = d.eps;
+    p.x_n = d.x_sample, p.x_p = d.x_row;
+    p.z_n = d.z_sample, p.z_p = d.z_row;
+    p.y_n = d.y_sample, p.y_p = d.y_row;
+    p.dy_n = d.dy_sample, p.dy_p = d.dy_row;
+    return p;
+}
+
+template <typename T, int V, int NV, int LG, bool BWD>
+void launch_row(const ssd_groupnorm_dims& d, const GnParams& p, hipStream_t s) {
+    const int64_t groups = BWD ? (int64_t)p.walkers * p.G : p.n * p.G;
+    const dim3 grid = units(cdiv(groups * LG, 256));
+#define SSD_GN_ACT(A)                                                        \
+    case A:                                                                  \
+        if constexpr (BWD) gn_row_bwd<T, V, NV, LG, A><<<grid, 256, 0, s>>>(p); \
+        else gn_row_fwd<T, V, NV, LG, A><<<grid, 256, 0, s>>>(p);            \
+        break
+    switch (d.activation) {
+        SSD_GN_ACT(PLAIN);
+        SSD_GN_ACT(SILU);
+        SSD_GN_ACT(GATE);
+    }
+#undef SSD_GN_ACT
+}
+template <typename T, int V, bool BWD>
+void launch_row(const ssd_groupnorm_dims& d, const GnParams& p, RowPlan r, hipStream_t s) {
+    if (r.V == 1) return launch_row<T, 1, 1, 8, BWD>(d, p, s);  // fewer channels than a vector
+    switch (r.NV * 64 + r.LG) {
+        case 64 + 8: return launch_row<T, V, 1, 8, BWD>(d, p, s);
+        case 64 + 16: return launch_row<T, V, 1, 16, BWD>(d, p, s);
+        case 64 + 32: return launch_row<T, V, 1, 32, BWD>(d, p, s);
+        case 128: return launch_row<T, V, 1, 64, BWD>(d, p, s);
+        case 192: return launch_row<T, V, 2, 64, BWD>(d, p, s);
+        default: return launch_row<T, V, 4, 64, BWD>(d, p, s);
+    }
+}
+
+template <typename T, int V>
+void launch_runs_fwd(const ssd_groupnorm_dims& d, const GnParams& p, RunPlan r, hipStream_t s) {
+    const dim3 grid = units(p.n * r.runs, r.blocks);
+    const dim3 block((unsigned)(256 / r.across * r.across));
+    gn_stats<T, V><<<grid, block, 0, s>>>(p, r.across);
+    gn_stats_join<<<units(p.n * p.G), 256, 0, s>>>(p);
+    if (d.activation == PLAIN) gn_apply<T, V, PLAIN><<<grid, block, 0, s>>>(p, r.across);
+    else if (d.activation == SILU) gn_apply<T, V, SILU><<<grid, block, 0, s>>>(p, r.across);
+    else gn_apply<T, V, GATE><<<grid, block, 0, s>>>(p, r.across);
+}
+template <typename T, int V, int ACT>
+void launch_runs_bwd(const GnParams& p, RunPlan r, hipStream_t s) {
+    const dim3 grid = units(p.n * r.runs, r.blocks);
+    const dim3 block((unsigned)(256 / r.across * r.across));
+    gn_bwd<T, V, ACT, false><<<grid, block, 0, s>>>(p, r.across);
+    gn_bwd_join<<<units(p.n * p.G), 256, 0, s>>>(p);
+    gn_bwd<T, V, ACT, true><<<grid, block, 0, s>>>(p, r.across);
+}
+template <typename T, int V>
+void launch_runs_bwd(const ssd_groupnorm_dims& d, const GnParams& p, RunPlan r, hipStream_t s) {
+    if (d.activation == PLAIN) launch_runs_bwd<T, V, PLAIN>(p, r, s);
+    else if (d.activation == SILU) launch_runs_bwd<T, V, SILU>(p, r, s);
+    else launch_runs_bwd<T, V, GATE>(p, r, s);
+}
+
+// Workspace: columns' sums of the runs (and what the backward's join leaves), and in the
+// forward the statistics where the caller does not take them.
+struct GnSpace {
+    size_t part, sums;
+};
+GnSpace gn_space(const ssd_groupnorm_dims& d, bool bwd) {
+    GnSpace w = {};
+    if (by_rows(d)) {
+        w.part = bwd ? up256((size_t)row_walkers(d) * 2 * d.channels * 4) : 0;
+        return w;
+    }
+    const RunPlan r = run_plan(d);
+    w.part = up256((size_t)imax(1, d.samples * r.runs) * 2 * d.channels * 4);
+    w.sums = up256((size_t)imax(1, d.samples * d.groups) * 2 * 4);
+    return w;
+}
+
+}  // namespace
+}  // namespace ssd
+
+using namespace ssd;
+
+extern "C" {
+
+size_t ssd_groupnorm_fwd_workspace_bytes(const ssd_groupnorm_dims* dims) {
+    if (gn_check(dims) != SSD_OK) return 0;
+    const GnSpace w = gn_space(*dims, false);
+    return w.part + w.sums;
+}
+
+int ssd_groupnorm_fwd(const ssd_groupnorm_dims* dims, const void* x, const float* weight,
+                      const float* bias, const void* z, void* y, float* mean, float* rstd,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+    const int st = gn_check(dims);
+    if (st != SSD_OK) return st;
+    const ssd_groupnorm_dims& d = *dims;
+    if (d.samples == 0) return SSD_OK;
+    if (!x || !y || (d.activation == SSD_ACT_GATE && !z)) return SSD_ERR_NULL_ARG;
+    if (!rows_apart(d.samples, d.y_sample, d.positions, d.y_row, d.channels)) return SSD_ERR_SHAPE;
+    const size_t e = elem_size(d.dtype);
+    if (!elem_aligned(x, e) || !elem_aligned(y, e) || !elem_aligned(z, e) || !elem_aligned(weight, 4) ||
+        !elem_aligned(bias, 4) || !elem_aligned(mean, 4) || !elem_aligned(rstd, 4) ||
+        ((uintptr_t)workspace & 255))
+        return SSD_ERR_ALIGN;
+    const GnSpace w = gn_space(d, false);
+    if (w.part + w.sums && (!workspace || workspace_bytes < w.part + w.sums)) return SSD_ERR_WORKSPACE;
+    GnParams p = gn_params(d);
+    p.x = x;
+    p.z = z;
+    p.out = y;
+    p.weight = weight;
+    p.bias = bias;
+    p.mean = mean;
+    p.rstd = rstd;
+    const hipStream_t s = (hipStream_t)stream;
+    if (by_rows(d)) {
+        const RowPlan r = row_plan(d);
+        if (d.dtype == SSD_BF16) launch_row<bf16, 8, false>(d, p, r, s);
+        else launch_row<float, 4, false>(d, p, r, s);
+        return launched();
+    }
+    const RunPlan r = run_plan(d);
+    p.part = (float*)workspace;
+    p.runs = r.runs;
+    p.runlen = r.runlen;
+    float* const stats = (float*)((char*)workspace + w.part);
+    if (!p.mean) p.mean = stats;
+    if (!p.rstd) p.rstd = stats + d.samples * d.groups;
+    if (d.dtype == SSD_BF16) {
+        if (r.V == 1) launch_runs_fwd<bf16, 1>(d, p, r, s);
+        else launch_runs_fwd<bf16, 8>(d, p, r, s);
+    } else {
+        if (r.V == 1) launch_runs_fwd<float, 1>(d, p, r, s);
+        else launch_runs_fwd<float, 4>(d, p, r, s);
+    }
+    return launched();
+}
+
+size_t ssd_groupnorm_bwd_workspace_bytes(const ssd_groupnorm_dims* dims) {
+    if (gn_check(dims) != SSD_OK) return 0;
+    const GnSpace w = gn_space(*dims, true);
+    return w.part + w.sums;
+}
+
+int ssd_groupnorm_bwd(const ssd_groupnorm_dims* dims, const void* x, const float* weight,
+                      const float* bias, const void* z, const float* mean, const float* rstd,
+                      const void* dy, void* dx, void* dz, float* dweight, float* dbias,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+    const int st = gn_check(dims);
+    if (st != SSD_OK) return st;
+    const ssd_groupnorm_dims& d = *dims;
+    const bool gate = d.activation == SSD_ACT_GATE;
+    if (d.samples > 0 && (!x || !mean || !rstd || !dy || !dx || (gate && (!z || !dz)))) return SSD_ERR_NULL_ARG;
+    if (d.samples > 0 && (!rows_apart(d.samples, d.y_sample, d.positions, d.y_row, d.channels) ||
+                          (gate && !rows_apart(d.samples, d.z_sample, d.positions, d.z_row, d.channels))))
+        return SSD_ERR_SHAPE;
+    const size_t e = elem_size(d.dtype);
+    for (const void* a : {x, z, dy, (const void*)dx, (const void*)dz})
+        if (!elem_aligned(a, e)) return SSD_ERR_ALIGN;
+    for (const void* a : {(const void*)weight, (const void*)bias, (const void*)mean, (const void*)rstd,
+                          (const void*)dweight, (const void*)dbias})
+        if (!elem_aligned(a, 4)) return SSD_ERR_ALIGN;
+    if ((uintptr_t)workspace & 255) return SSD_ERR_ALIGN;
+    const GnSpace w = gn_space(d, true);
+    if (!workspace || workspace_bytes < w.part + w.sums) return SSD_ERR_WORKSPACE;
+    GnParams p = gn_params(d);
+    p.x = x;
+    p.z = z;
+    p.dy = dy;
+    p.out = dx;
+    p.dz = dz;
+    p.weight = weight;
+    p.bias = bias;
+    p.mean_in = mean;
+    p.rstd_in = rstd;
+    p.part = (float*)workspace;
+    const hipStream_t s = (hipStream_t)stream;
+    ColSum c = {};
+    c.part = p.part;
+    c.cols = 2 * (int64_t)d.channels;
+    c.out0 = dweight;
+    c.c0 = d.channels;
+    c.out1 = dbias;
+    c.c1 = d.channels;
+    if (d.samples == 0) {
+        // no rows: sums of nothing
+        c.rows = 0;
+    } else if (by_rows(d)) {
+        const RowPlan r = row_plan(d);
+        c.rows = p.walkers = row_walkers(d);
+        if (d.dtype == SSD_BF16) launch_row<bf16, 8, true>(d, p, r, s);
+        else launch_row<float, 4, true>(d, p, r, s);
+    } else {
+        const RunPlan r = run_plan(d);
+        p.runs = r.runs;
+        p.runlen = r.runlen;
+        p.sums = (float*)((char*)workspace + w.part);
+        c.rows = d.samples * r.runs;
+        if (d.dtype == SSD_BF16) {
+            if (r.V == 1) launch_runs_bwd<bf16, 1>(d, p, r, s);
+            else launch_runs_bwd<bf16, 8>(d, p, r, s);
+        } else {
+            if (r.V == 1) launch_runs_bwd<float, 1>(d, p, r, s);
+            else launch_runs_bwd<float, 4>(d, p, r, s);
+        }
+    }
+    const int rc = launched();
+    if (rc != SSD_OK || (!dweight && !dbias)) return rc;
+    return launch_colsum(c, s);
+}
+
+}  // extern "C"

@@ -79,7 +79,20 @@ __device__ __forceinline__ void store_vec(T* __restrict__ p, int n, const float 
     }
 }
 
-// The same in two steps: the bits first (a load in flight holds no more than
+// The elements from `skip` on of a vector: all of one store, or one by one where
+// the vector was moved back to end with its row.
+template <typename T, int V>
+__device__ __forceinline__ void store_own(T* p, int skip, const float (&v)[V]) {
+    if (skip == 0) {
+        store_vec<T, V>(p, V, v);
+    } else {
+#pragma unroll
+        for (int j = 1; j < V; ++j)
+            if (j >= skip) p[j] = (T)v[j];
+    }
+}
+
+// load_vec in two steps: the bits first (a load in flight holds no more than
 // them), their values later.
 template <typename T, int V>
 struct RawVec {

@@ -20,19 +20,6 @@ __device__ __forceinline__ int64_t pool_row(const int32_t* slots, int32_t nslots
     return s >= 0 && s < nslots ? s : -1;
 }
 
-// The elements from `skip` on of a vector: all of one store, or one by one where
-// the vector was moved back to end with its row.
-template <typename T, int V>
-__device__ __forceinline__ void store_own(T* p, int skip, const float (&v)[V]) {
-    if (skip == 0) {
-        store_vec<T, V>(p, V, v);
-    } else {
-#pragma unroll
-        for (int j = 1; j < V; ++j)
-            if (j >= skip) p[j] = (T)v[j];
-    }
-}
-
 // ---- SSD ----------------------------------------------------------------------------------
 
 struct StepParams {
