@@ -14,8 +14,8 @@
 // undecayed) and dinit = l R_0: one kernel serves all four (LinPass::init_pow, final_pow).
 //
 // A workgroup walks the chunks of one span of a sequence for one head and VT columns of V,
-// the state in registers (each of its four waves holds all K rows of its own columns, so
-// no product needs a sum across waves).  Where sequences x heads do not fill the chip a
+// the state in registers: each of its VT / 16 waves holds all K rows of 16 columns, so no
+// product needs a sum across waves.  Where sequences x heads do not fill the chip a
 // sequence is cut into spans: their states are formed first (STATE), joined along the
 // sequence (linattn_join) and then every span is walked from its own incoming state.
 #include <type_traits>
@@ -40,7 +40,7 @@ struct LinPass {
     int32_t S, H, K, V, s_k, s_v;
     int32_t qdiv, kdiv, vdiv;  // head h reads head h / div
     int32_t slots, per;        // span slots; spans of a sequence without cu
-    int32_t vtiles, reverse, init_pow, final_pow;
+    int32_t vtiles, together, reverse, init_pow, final_pow;
     float in_scale, out_scale;
 };
 
@@ -116,28 +116,41 @@ struct Tile {
 };
 
 // MFMA operands over 32 entries of a contraction, in the order in which a pair of result
-// tiles holds them: a lane of group g has entries 4g..4g+3 and 16+4g..16+4g+3.
+// tiles holds them: a lane of group g has entries 4g..4g+3 and 16+4g..16+4g+3.  r0 and c0 are
+// multiples of 16, which leave the exchanged units where they are: all of a tile's operands
+// are at constants from one address a lane (row_base, col_base).
 template <typename T, int COLS>
-__device__ __forceinline__ typename Vec<T>::x8 row_frag(const T* t, int r, int c, int g) {
+__device__ __forceinline__ int row_base(int lane) {
+    return Tile<T, COLS>::off(lane & 15, 4 * (lane >> 4));
+}
+// tile[r0 + l16][c0 ..]
+template <typename T, int COLS>
+__device__ __forceinline__ typename Vec<T>::x8 row_frag(const T* t, int base, int r0, int c0) {
     using X4 = typename Vec<T>::x4;
-    return cat<typename Vec<T>::x8, X4>(ld4(t + Tile<T, COLS>::off(r, c + 4 * g)),
-                                        ld4(t + Tile<T, COLS>::off(r, c + 16 + 4 * g)));
+    const T* const q = t + base + (r0 * Tile<T, COLS>::ST + c0);
+    return cat<typename Vec<T>::x8, X4>(ld4(q), ld4(q + 16));
 }
-// over the tile's rows r0..r0+31: the lane's column is c0 + l16
-template <int COLS>
-__device__ __forceinline__ bf16x8 col_frag(const bf16* t, int r0, int c0, int lane) {
-    const int j = lane & 15, r = r0 + 4 * (lane >> 4) + (j >> 2), c = c0 + 4 * (j & 3);
-    return cat<bf16x8, bf16x4>(ldtr(t + Tile<bf16, COLS>::off(r, c)),
-                               ldtr(t + Tile<bf16, COLS>::off(r + 16, c)));
+// tile[r0 ..][c0 + l16]
+template <typename T, int COLS>
+__device__ __forceinline__ int col_base(int lane) {
+    const int j = lane & 15, r = 4 * (lane >> 4);
+    return sizeof(T) == 2 ? Tile<T, COLS>::off(r + (j >> 2), 4 * (j & 3)) : Tile<T, COLS>::off(r, j);
 }
 template <int COLS>
-__device__ __forceinline__ f32x8 col_frag(const float* t, int r0, int c0, int lane) {
-    const int r = r0 + 4 * (lane >> 4), c = c0 + (lane & 15);
+__device__ __forceinline__ bf16x8 col_frag(const bf16* t, int base, int r0, int c0) {
+    constexpr int ST = Tile<bf16, COLS>::ST;
+    const bf16* const q = t + base + (r0 * ST + c0);
+    return cat<bf16x8, bf16x4>(ldtr(q), ldtr(q + 16 * ST));
+}
+template <int COLS>
+__device__ __forceinline__ f32x8 col_frag(const float* t, int base, int r0, int c0) {
+    constexpr int ST = Tile<float, COLS>::ST;
+    const float* const q = t + base + (r0 * ST + c0);
     f32x8 v;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        v[k] = t[Tile<float, COLS>::off(r + k, c)];
-        v[4 + k] = t[Tile<float, COLS>::off(r + 16 + k, c)];
+        v[k] = q[k * ST];
+        v[4 + k] = q[(16 + k) * ST];
     }
     return v;
 }
@@ -165,30 +178,36 @@ __device__ __forceinline__ void weigh(const bf16x8& v, const f32x8& w, bf16x8 (&
 }
 __device__ __forceinline__ void weigh(const f32x8& v, const f32x8& w, f32x8 (&o)[1]) { o[0] = v * w; }
 
+// Waves a SIMD that the kernel is compiled for: two workgroups a CU.
+constexpr int lin_waves(int KD, int VT, int size) { return KD * size > 512 ? 1 : VT / 32; }
+
 template <typename T> constexpr int kParts = sizeof(T) == 2 ? 3 : 1;
 
-// The 16-byte units of a C x COLS tile that one thread moves: loads for the next chunk stay
-// in registers until its LDS tile is free.
-template <typename T, int C, int COLS>
+// The 16-byte units of a C x COLS tile that one of NT threads moves: loads for the next chunk
+// stay in registers until its LDS tile is free.
+template <typename T, int C, int COLS, int NT>
 struct Mover {
-    static constexpr int EPU = 16 / sizeof(T), UPR = COLS / EPU, N = C * UPR / 256;
+    static constexpr int EPU = 16 / sizeof(T), UPR = COLS / EPU, N = C * UPR / NT, STEP = NT / UPR;
+    static_assert(C * UPR % NT == 0 && NT % UPR == 0, "tile and threads");
     typedef T unit __attribute__((ext_vector_type(16 / sizeof(T))));
     unit u[N];
+    __device__ static __forceinline__ int row() { return threadIdx.x / UPR; }
+    __device__ static __forceinline__ int col() { return threadIdx.x % UPR * EPU; }
     // rows at base + row * step (elements; negative against the order of memory); only
     // rows < clen and columns < cols are read
     __device__ __forceinline__ void load(const T* base, int64_t step, int clen, int cols) {
-        const int row = threadIdx.x / UPR, c = threadIdx.x % UPR * EPU;
+        const int c = col();
         if (cols % EPU == 0) {
             const int cc = c < cols ? c : 0;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const int r = row + i * (256 / UPR);
+                const int r = row() + i * STEP;
                 __builtin_memcpy(&u[i], base + (r < clen ? r : 0) * step + cc, 16);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const int r = row + i * (256 / UPR);
+                const int r = row() + i * STEP;
 #pragma unroll
                 for (int j = 0; j < EPU; ++j)
                     u[i][j] = r < clen && c + j < cols ? base[r * step + c + j] : (T)0.f;
@@ -196,14 +215,32 @@ struct Mover {
         }
     }
     __device__ __forceinline__ void put(T* tile, int clen, int cols) const {
-        const int row = threadIdx.x / UPR, c = threadIdx.x % UPR * EPU;
         const bool whole = clen == C && cols == COLS;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int r = row + i * (256 / UPR);
+            const int r = row() + i * STEP;
             unit x = u[i];
-            if (!whole && (r >= clen || c >= cols)) x = unit{};
-            *(unit*)(tile + Tile<T, COLS>::off(r, c)) = x;
+            if (!whole && (r >= clen || col() >= cols)) x = unit{};
+            *(unit*)(tile + Tile<T, COLS>::off(r, col())) = x;
+        }
+    }
+    __device__ __forceinline__ void get(const T* tile) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) u[i] = *(const unit*)(tile + Tile<T, COLS>::off(row() + i * STEP, col()));
+    }
+    __device__ __forceinline__ void store(T* base, int64_t step, int clen, int cols) const {
+        const int c = col();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int r = row() + i * STEP;
+            if (r >= clen) continue;
+            if (c + EPU <= cols) {
+                __builtin_memcpy(base + r * step + c, &u[i], 16);
+            } else {
+#pragma unroll
+                for (int j = 0; j < EPU; ++j)
+                    if (c + j < cols) base[r * step + c + j] = u[i][j];
+            }
         }
     }
 };
@@ -215,25 +252,33 @@ struct __attribute__((aligned(16))) Shared {
     T v[C * Tile<T, VT>::ST];
     T p[C * Tile<T, C>::ST];
     float pw[C + 4];  // l^n
-    float w[C];       // weights of the chunk's tokens in the state behind it
+    float w[2][C];    // weights of a chunk's tokens in the state behind it; the last chunk's
 };
 template <typename T, int KD, int VT, int C>
 struct __attribute__((aligned(16))) SharedState {
     T k[C * Tile<T, KD>::ST];
     T v[C * Tile<T, VT>::ST];
-    float w[C];
+    float w[1][C];
 };
+
+// Workgroups that read the same rows (the V tiles of a head, the heads of a group) follow each
+// other on one XCD, whose L2 then serves all but the first: workgroups go to the 8 XCDs in turn.
+__device__ __forceinline__ uint32_t same_xcd(uint32_t id, uint32_t together, uint32_t n) {
+    const uint32_t whole = n / (8 * together) * (8 * together);
+    if (id >= whole) return id;
+    const uint32_t x = id % 8, i = id / 8;
+    return (i / together * 8 + x) * together + i % together;
+}
 
 // One span (or, STATE, only its state).  OT: the output's type.
 template <typename T, typename OT, int KD, int VT, int C, bool STATE>
-__global__ __launch_bounds__(256, KD * sizeof(T) > 512 ? 1 : 2) void linattn_kernel(LinPass p) {
+__global__ __launch_bounds__(VT * 4, lin_waves(KD, VT, sizeof(T))) void linattn_kernel(LinPass p) {
     using X8 = typename Vec<T>::x8;
     using X4 = typename Vec<T>::x4;
-    constexpr int KB = KD / 16, KS = KD / 32, CB = VT / 64, IB = C / 16, TS = C / 32;
-    constexpr int NP = kParts<T>;
+    constexpr int NT = VT * 4, KB = KD / 16, KS = KD / 32, IB = C / 16, TS = C / 32, NW = NT / 64;
     __shared__ std::conditional_t<STATE, SharedState<T, KD, VT, C>, Shared<T, KD, VT, C>> sh;
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), l16 = lane & 15, g = lane >> 4;
-    uint32_t id = blockIdx.x;
+    uint32_t id = same_xcd(blockIdx.x, p.together, gridDim.x);
     const int vt = id % (uint32_t)p.vtiles;
     id /= (uint32_t)p.vtiles;
     const int h = id % (uint32_t)p.H, slot = id / (uint32_t)p.H;
@@ -243,13 +288,13 @@ __global__ __launch_bounds__(256, KD * sizeof(T) > 512 ? 1 : 2) void linattn_ker
     const bool last = sp.t0 + n >= sp.len;
     if (STATE && last) return;  // no span behind it
     const int64_t block = ((int64_t)sp.seq * p.H + h) * ((int64_t)p.K * p.V);
-    const int v0 = vt * VT, vcols = min(VT, p.V - v0), mycol = wave * (16 * CB) + l16;
+    const int v0 = vt * VT, vcols = min(VT, p.V - v0), c0 = wave * 16, vc = c0 + l16;
     float* const mine = p.spans + (((int64_t)slot * p.H + h) * p.vtiles + vt) * (KD * VT) +
-                        wave * (CB * KB * 256) + lane * 4;
+                        wave * (KB * 256) + lane * 4;
 
     if (!STATE && n == 0) {  // an empty sequence hands on what came in
         if (p.final)
-            for (int i = tid; i < p.K * vcols; i += 256) {
+            for (int i = tid; i < p.K * vcols; i += NT) {
                 const int64_t e = block + (int64_t)(i / vcols) * p.s_k + (int64_t)(v0 + i % vcols) * p.s_v;
                 p.final[e] = p.init ? p.init[e] : 0.f;
             }
@@ -264,8 +309,11 @@ __global__ __launch_bounds__(256, KD * sizeof(T) > 512 ? 1 : 2) void linattn_ker
     const T* vp = (const T*)p.v + tok0 * p.v_t + (h / p.vdiv) * p.v_h + v0;
     OT* op = (OT*)p.o + tok0 * p.o_t + h * p.o_h + v0;
     const int64_t qs = dir * p.q_t, ks = dir * p.k_t, vs = dir * p.v_t, os = dir * p.o_t;
-    Mover<T, C, KD> mq, mk;
-    Mover<T, C, VT> mv;
+    Mover<T, C, KD, NT> mq, mk;
+    Mover<T, C, VT, NT> mv, mo;
+    const int kd = row_base<T, KD>(lane), cd = row_base<T, C>(lane);
+    const int kt = col_base<T, KD>(lane), vtb = col_base<T, VT>(lane), vd = row_base<T, VT>(lane);
+    constexpr bool kByTile = sizeof(OT) == sizeof(T);  // outputs leave through v's tile
     int clen = (int)imin(C, n);
     if (!STATE) mq.load(qp, qs, clen, p.K);
     mk.load(kp, ks, clen, p.K);
@@ -275,44 +323,52 @@ __global__ __launch_bounds__(256, KD * sizeof(T) > 512 ? 1 : 2) void linattn_ker
     if constexpr (!STATE) {
         if (tid <= C) sh.pw[tid] = (float)power(decay, tid);
         // score tiles above the diagonal that a product over 32 tokens meets
-        for (int i = tid; i < C * Tile<T, C>::ST; i += 256) sh.p[i] = (T)0.f;
+        for (int i = tid; i < C * Tile<T, C>::ST; i += NT) sh.p[i] = (T)0.f;
     }
-    if (tid < C) sh.w[tid] = p.in_scale * (float)power(decay, C - tid);
+    if (tid < C) sh.w[0][tid] = p.in_scale * (float)power(decay, C - tid);
     Rate rate(decay, C);
+    float closing = 0.f;  // the state's factor over the sequence's last chunk
+    if (!STATE && last && p.final) {
+        const int cl = (int)((n - 1) % C) + 1;
+        closing = (float)power(decay, cl - 1 + p.final_pow);
+        if (tid < C)
+            sh.w[STATE ? 0 : 1][tid] = tid < cl ? p.in_scale * (float)power(decay, cl - 1 - tid + p.final_pow) : 0.f;
+    }
 
-    f32x4 st[KB][CB];
+    f32x4 st[KB];
     const bool split = p.per != 1;  // states come in by way of the workspace
     if (!STATE && split) {
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-            for (int cb = 0; cb < CB; ++cb) st[kb][cb] = *(const f32x4*)(mine + (cb * KB + kb) * 256);
+        for (int kb = 0; kb < KB; ++kb) st[kb] = *(const f32x4*)(mine + kb * 256);
     } else {
-        const bool come = !STATE && p.init;
+        const bool come = !STATE && p.init && vc < vcols;
         const float f = p.init_pow ? (float)power(decay, 1) : 1.f;
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-            for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int kr = 16 * kb + 4 * g + r, vc = mycol + 16 * cb;
-                    const bool in = come && kr < p.K && vc < vcols;
-                    const int64_t e = block + (int64_t)kr * p.s_k + (int64_t)(v0 + vc) * p.s_v;
-                    st[kb][cb][r] = in ? f * p.init[in ? e : 0] : 0.f;
-                }
+            for (int r = 0; r < 4; ++r) {
+                const int kr = 16 * kb + 4 * g + r;
+                st[kb][r] = come && kr < p.K
+                                ? f * p.init[block + (int64_t)kr * p.s_k + (int64_t)(v0 + vc) * p.s_v] : 0.f;
+            }
     }
 
     for (int64_t t = 0; t < n; t += C) {
         const int cl = clen;
         const bool end = t + C >= n;          // of the span
         const bool close = last && end;       // of the sequence
+        // a thread's units of v's tile are those of the outputs that it takes from it
+        if constexpr (!STATE && kByTile)
+            if (t) mo.get((const T*)sh.v);
         if constexpr (!STATE) mq.put(sh.q, cl, p.K);
         mk.put(sh.k, cl, p.K);
         mv.put(sh.v, cl, vcols);
-        if (close && tid < C)
-            sh.w[tid] = tid < cl ? p.in_scale * (float)power(decay, cl - 1 - tid + p.final_pow) : 0.f;
-        __syncthreads();
+        if constexpr (!STATE && kByTile)
+            if (t) {
+                mo.store((T*)op, os, C, vcols);
+                op += C * os;
+            }
+        block_sync();
         if (!end) {
             qp += C * qs;
             kp += C * ks;
@@ -322,127 +378,113 @@ __global__ __launch_bounds__(256, KD * sizeof(T) > 512 ? 1 : 2) void linattn_ker
             mk.load(kp, ks, clen, p.K);
             mv.load(vp, vs, clen, vcols);
         }
-        f32x4 acc[IB][CB];
+        f32x4 acc[IB];  // transposed: a lane has 4 columns of token 16 ib + l16
         if constexpr (!STATE) {
-            // scores, transposed: a lane gets 4 tokens j of one row i
-            constexpr int NT = IB * (IB + 1) / 2;
+            // scores, transposed too: a lane gets 4 tokens j of one row i
+            constexpr int NS = IB * (IB + 1) / 2;
 #pragma unroll
-            for (int x = 0; x < (NT + 3) / 4; ++x) {
-                const int tile = x * 4 + wave;
-                if (tile < NT) {
+            for (int x = 0; x < (NS + NW - 1) / NW; ++x) {
+                const int tile = x * NW + wave;
+                if (tile < NS) {
                     int ib = 0, jb = tile;
                     while (jb > ib) jb -= ++ib;
                     f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int kk = 0; kk < KS; ++kk)
-                        s = mma(row_frag<T, KD>(sh.k, 16 * jb + l16, 32 * kk, g),
-                                row_frag<T, KD>(sh.q, 16 * ib + l16, 32 * kk, g), s);
+                        s = mma(row_frag<T, KD>(sh.k, kd, 16 * jb, 32 * kk),
+                                row_frag<T, KD>(sh.q, kd, 16 * ib, 32 * kk), s);
                     const int d = 16 * (ib - jb) + l16 - 4 * g;
                     X4 o;
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         o[r] = d - r >= 0 ? (T)(s[r] * (p.in_scale * sh.pw[max(d - r, 0)])) : (T)0.f;
-                    *(X4*)(sh.p + Tile<T, C>::off(16 * ib + l16, 16 * jb + 4 * g)) = o;
+                    *(X4*)(sh.p + cd + (16 * ib * Tile<T, C>::ST + 16 * jb)) = o;
                 }
             }
             // l^i q_i E
 #pragma unroll
-            for (int ib = 0; ib < IB; ++ib)
-#pragma unroll
-                for (int cb = 0; cb < CB; ++cb) acc[ib][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int ib = 0; ib < IB; ++ib) acc[ib] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
-                X8 e[CB];
+                X8 e;
 #pragma unroll
-                for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        e[cb][r] = (T)st[2 * kk][cb][r];
-                        e[cb][4 + r] = (T)st[2 * kk + 1][cb][r];
-                    }
-#pragma unroll
-                for (int ib = 0; ib < IB; ++ib) {
-                    const X8 a = row_frag<T, KD>(sh.q, 16 * ib + l16, 32 * kk, g);
-#pragma unroll
-                    for (int cb = 0; cb < CB; ++cb) acc[ib][cb] = mma(a, e[cb], acc[ib][cb]);
+                for (int r = 0; r < 4; ++r) {
+                    e[r] = (T)st[2 * kk][r];
+                    e[4 + r] = (T)st[2 * kk + 1][r];
                 }
+#pragma unroll
+                for (int ib = 0; ib < IB; ++ib)
+                    acc[ib] = mma(e, row_frag<T, KD>(sh.q, kd, 16 * ib, 32 * kk), acc[ib]);
             }
 #pragma unroll
-            for (int ib = 0; ib < IB; ++ib) {
-                const f32x4 f = *(const f32x4*)(sh.pw + 16 * ib + 4 * g);
-#pragma unroll
-                for (int cb = 0; cb < CB; ++cb) acc[ib][cb] *= f;
-            }
-            __syncthreads();
+            for (int ib = 0; ib < IB; ++ib) acc[ib] *= sh.pw[16 * ib + l16];
+            block_sync();
         }
         // the chunk's values: scores times v, and the state behind the chunk
         const bool update = STATE || !close || p.final;
         if (update) {
-            const float f = close ? (float)power(decay, cl - 1 + p.final_pow) : rate.next();
+            const float f = close ? closing : rate.next();
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                for (int cb = 0; cb < CB; ++cb) st[kb][cb] *= f;
+            for (int kb = 0; kb < KB; ++kb) st[kb] *= f;
         }
 #pragma unroll
         for (int ts = 0; ts < TS; ++ts) {
-            X8 vf[CB];
-#pragma unroll
-            for (int cb = 0; cb < CB; ++cb)
-                vf[cb] = col_frag<VT>(sh.v, 32 * ts, wave * (16 * CB) + 16 * cb, lane);
+            const X8 vf = col_frag<VT>(sh.v, vtb, 32 * ts, c0);
             if constexpr (!STATE) {
 #pragma unroll
-                for (int ib = 2 * ts; ib < IB; ++ib) {
-                    const X8 a = row_frag<T, C>(sh.p, 16 * ib + l16, 32 * ts, g);
-#pragma unroll
-                    for (int cb = 0; cb < CB; ++cb) acc[ib][cb] = mma(a, vf[cb], acc[ib][cb]);
-                }
+                for (int ib = 2 * ts; ib < IB; ++ib)
+                    acc[ib] = mma(vf, row_frag<T, C>(sh.p, cd, 16 * ib, 32 * ts), acc[ib]);
             }
             if (update) {
-                const f32x8 w = cat<f32x8, f32x4>(*(const f32x4*)(sh.w + 32 * ts + 4 * g),
-                                                  *(const f32x4*)(sh.w + 32 * ts + 16 + 4 * g));
-                X8 vw[CB][NP];
+                const float* const wt = sh.w[!STATE && close ? 1 : 0] + 32 * ts + 4 * g;
+                const f32x8 w = cat<f32x8, f32x4>(*(const f32x4*)wt, *(const f32x4*)(wt + 16));
+                X8 vw[kParts<T>];
+                weigh(vf, w, vw);
 #pragma unroll
-                for (int cb = 0; cb < CB; ++cb) weigh(vf[cb], w, vw[cb]);
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    const X8 a = col_frag<KD>(sh.k, 32 * ts, 16 * kb, lane);
-#pragma unroll
-                    for (int cb = 0; cb < CB; ++cb) st[kb][cb] = mma_weighted(a, vw[cb], st[kb][cb]);
-                }
+                for (int kb = 0; kb < KB; ++kb)
+                    st[kb] = mma_weighted(col_frag<KD>(sh.k, kt, 32 * ts, 16 * kb), vw, st[kb]);
             }
         }
         if constexpr (!STATE) {
+            if constexpr (kByTile) {
+                // this wave alone has read these columns of v
 #pragma unroll
-            for (int ib = 0; ib < IB; ++ib)
+                for (int ib = 0; ib < IB; ++ib) {
+                    X4 o;
 #pragma unroll
-                for (int cb = 0; cb < CB; ++cb)
+                    for (int r = 0; r < 4; ++r) o[r] = (T)(p.out_scale * acc[ib][r]);
+                    *(X4*)(sh.v + vd + (16 * ib * Tile<T, VT>::ST + c0)) = o;
+                }
+            } else {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int i = 16 * ib + 4 * g + r, c = mycol + 16 * cb;
-                        if (i < cl && c < vcols) op[i * os + c] = (OT)(p.out_scale * acc[ib][cb][r]);
-                    }
-            op += C * os;
+                for (int ib = 0; ib < IB; ++ib) {
+                    const int i = 16 * ib + l16, c = c0 + 4 * g;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (i < cl && c + r < vcols) op[i * os + c + r] = (OT)(p.out_scale * acc[ib][r]);
+                }
+                op += C * os;
+            }
         }
-        __syncthreads();
+        block_sync();
+        if constexpr (!STATE && kByTile)
+            if (end) {
+                mo.get((const T*)sh.v);
+                mo.store((T*)op, os, cl, vcols);
+            }
     }
 
     if constexpr (STATE) {
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-            for (int cb = 0; cb < CB; ++cb) *(f32x4*)(mine + (cb * KB + kb) * 256) = st[kb][cb];
-    } else if (last && p.final) {
+        for (int kb = 0; kb < KB; ++kb) *(f32x4*)(mine + kb * 256) = st[kb];
+    } else if (last && p.final && vc < vcols) {
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-            for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int kr = 16 * kb + 4 * g + r, vc = mycol + 16 * cb;
-                    if (kr < p.K && vc < vcols)
-                        p.final[block + (int64_t)kr * p.s_k + (int64_t)(v0 + vc) * p.s_v] = st[kb][cb][r];
-                }
+            for (int r = 0; r < 4; ++r) {
+                const int kr = 16 * kb + 4 * g + r;
+                if (kr < p.K) p.final[block + (int64_t)kr * p.s_k + (int64_t)(v0 + vc) * p.s_v] = st[kb][r];
+            }
     }
 }
 
@@ -553,11 +595,11 @@ template <typename T, typename OT, int KD, int VT, int C>
 void launch_tiles(const LinPass& p, const LinPlan& pl, hipStream_t s) {
     const dim3 grid((unsigned)((int64_t)pl.slots * p.H * pl.vtiles));
     if (pl.bytes) {
-        linattn_kernel<T, OT, KD, VT, C, true><<<grid, 256, 0, s>>>(p);
+        linattn_kernel<T, OT, KD, VT, C, true><<<grid, VT * 4, 0, s>>>(p);
         const dim3 joins((unsigned)((int64_t)p.S * p.H * pl.vtiles), KD * VT / 1024);
         linattn_join<<<joins, 256, 0, s>>>(p, KD, VT);
     }
-    linattn_kernel<T, OT, KD, VT, C, false><<<grid, 256, 0, s>>>(p);
+    linattn_kernel<T, OT, KD, VT, C, false><<<grid, VT * 4, 0, s>>>(p);
 }
 template <typename T, typename OT>
 void launch_pass(LinPass& p, const LinPlan& pl, hipStream_t s) {
@@ -566,6 +608,7 @@ void launch_pass(LinPass& p, const LinPlan& pl, hipStream_t s) {
     p.slots = pl.slots;
     p.per = pl.per;
     p.vtiles = pl.vtiles;
+    p.together = pl.vtiles * (p.qdiv > p.kdiv ? p.qdiv : p.kdiv);
     if (pl.t.KD == 64) {
         if (pl.t.VT == 64) launch_tiles<T, OT, 64, 64, C>(p, pl, s);
         else launch_tiles<T, OT, 64, 128, C>(p, pl, s);
