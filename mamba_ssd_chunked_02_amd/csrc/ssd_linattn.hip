@@ -13,9 +13,9 @@
 // with R_t = scale q_t^T dy_t + l R_{t+1} (R_{L-1} adds d_final, which therefore enters
 // undecayed) and dinit = l R_0: one kernel serves all four (LinPass::init_pow, final_pow).
 //
-// A workgroup walks the chunks of one span of a sequence for one head and VT columns of V,
-// the state in registers: each of its VT / 16 waves holds all K rows of 16 columns, so no
-// product needs a sum across waves.  Where sequences x heads do not fill the chip a
+// (C = 32.)  A workgroup walks the chunks of one span of a sequence for one head and VT columns of V,
+// the state in registers: each of its four waves holds all K rows of VT / 4 columns, so no
+// product needs a sum across waves, and what a wave reads from LDS meets all its columns.  Where sequences x heads do not fill the chip a
 // sequence is cut into spans: their states are formed first (STATE), joined along the
 // sequence (linattn_join) and then every span is walked from its own incoming state.
 #include <type_traits>
@@ -89,8 +89,7 @@ __device__ __forceinline__ double power(float decay, int64_t n) {
 // up to 3e-5 off.
 struct Rate {
     float rate, low, unrate, owed;
-    __device__ __forceinline__ Rate(float decay, int64_t n) {
-        const double exact = power(decay, n);
+    __device__ __forceinline__ explicit Rate(double exact) {
         rate = (float)exact;
         low = rate > 0.f ? (float)((exact - (double)rate) / (double)rate) : 0.f;
         unrate = rate > 0.f ? 1.f / rate : 0.f;
@@ -104,53 +103,65 @@ struct Rate {
     }
 };
 
-// A row-major LDS tile: rows 32 bytes apart from a multiple of 256, and the 16-byte units of
-// rows 8-15 of every 16 exchanged in pairs.  The reads below then touch every bank evenly:
-// 16 rows of one unit's half (row_frag) and 4 rows x 32 bytes (tok_frag).
+// An LDS tile of C tokens, row-major in 16-byte units, unit u of row r at place u ^ swap(r): a
+// tile is then filled by loads straight from memory, which put 64 lanes' units next to each
+// other, and every read below touches all banks evenly (16 rows of one half unit, 4 rows of
+// two or four units).
+constexpr int C = 32;  // tokens of a chunk
 template <typename T, int COLS>
 struct Tile {
-    static constexpr int EPU = 16 / sizeof(T), ST = COLS + 32 / sizeof(T);
-    __device__ static __forceinline__ int off(int r, int c) {
-        return r * ST + (((c / EPU) ^ ((r >> 3) & 1)) * EPU) + c % EPU;
+    static constexpr int EPU = 16 / sizeof(T), UPR = COLS / EPU, ROW = COLS * (int)sizeof(T);  // ROW: bytes
+    __device__ static __forceinline__ int swap(int r) {
+        return UPR == 8 ? ((r >> 1) & 3) << 1 | ((r >> 3) & 1) : (r & 7) << 1 | ((r >> 3) & 1);
+    }
+    // byte address of column c of row r
+    __device__ static __forceinline__ int at(int r, int c) {
+        return r * ROW + (((c / EPU) ^ swap(r)) * 16) + c % EPU * (int)sizeof(T);
     }
 };
 
+// Columns of a wave's 16 CB in the order of its result tiles: with two tiles a lane's 4 rows of
+// each are 8 neighbours in memory.
+template <int CB>
+__device__ __forceinline__ int tile_col(int cb, int m) {
+    return CB == 2 ? 8 * (m >> 2) + 4 * cb + (m & 3) : m;
+}
+
 // MFMA operands over 32 entries of a contraction, in the order in which a pair of result
-// tiles holds them: a lane of group g has entries 4g..4g+3 and 16+4g..16+4g+3.  r0 and c0 are
-// multiples of 16, which leave the exchanged units where they are: all of a tile's operands
-// are at constants from one address a lane (row_base, col_base).
+// tiles holds them: a lane of group g has entries 4g..4g+3 and 16+4g..16+4g+3.  Multiples of
+// 16 rows and columns move an address by a constant: + r0 ROW, ^ c0 sizeof(T).
 template <typename T, int COLS>
 __device__ __forceinline__ int row_base(int lane) {
-    return Tile<T, COLS>::off(lane & 15, 4 * (lane >> 4));
+    return Tile<T, COLS>::at(lane & 15, 4 * (lane >> 4));
 }
 // tile[r0 + l16][c0 ..]
 template <typename T, int COLS>
-__device__ __forceinline__ typename Vec<T>::x8 row_frag(const T* t, int base, int r0, int c0) {
+__device__ __forceinline__ typename Vec<T>::x8 row_frag(const char* t, int base, int r0, int c0) {
     using X4 = typename Vec<T>::x4;
-    const T* const q = t + base + (r0 * Tile<T, COLS>::ST + c0);
-    return cat<typename Vec<T>::x8, X4>(ld4(q), ld4(q + 16));
+    constexpr int E = sizeof(T);
+    return cat<typename Vec<T>::x8, X4>(*(const X4*)(t + (base ^ c0 * E) + r0 * Tile<T, COLS>::ROW),
+                                        *(const X4*)(t + (base ^ (c0 + 16) * E) + r0 * Tile<T, COLS>::ROW));
 }
-// tile[r0 ..][c0 + l16]
-template <typename T, int COLS>
+// tile[0 ..][c0 + the lane's column]: column m = l16 of result tile cb of CB
+template <typename T, int COLS, int CB>
 __device__ __forceinline__ int col_base(int lane) {
     const int j = lane & 15, r = 4 * (lane >> 4);
-    return sizeof(T) == 2 ? Tile<T, COLS>::off(r + (j >> 2), 4 * (j & 3)) : Tile<T, COLS>::off(r, j);
+    if (sizeof(T) == 2) return Tile<T, COLS>::at(r + (j >> 2), tile_col<CB>(0, 4 * (j & 3)));
+    return Tile<T, COLS>::at(r, tile_col<CB>(0, j));
 }
 template <int COLS>
-__device__ __forceinline__ bf16x8 col_frag(const bf16* t, int base, int r0, int c0) {
-    constexpr int ST = Tile<bf16, COLS>::ST;
-    const bf16* const q = t + base + (r0 * ST + c0);
-    return cat<bf16x8, bf16x4>(ldtr(q), ldtr(q + 16 * ST));
+__device__ __forceinline__ bf16x8 col_frag(const bf16*, const char* t, int base, int c0) {
+    const bf16* const q = (const bf16*)(t + (base ^ c0 * 2));
+    return cat<bf16x8, bf16x4>(ldtr(q), ldtr(q + 16 * COLS));
 }
 template <int COLS>
-__device__ __forceinline__ f32x8 col_frag(const float* t, int base, int r0, int c0) {
-    constexpr int ST = Tile<float, COLS>::ST;
-    const float* const q = t + base + (r0 * ST + c0);
+__device__ __forceinline__ f32x8 col_frag(const float*, const char* t, int base, int c0) {
     f32x8 v;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        v[k] = q[k * ST];
-        v[4 + k] = q[(16 + k) * ST];
+    for (int k = 0; k < 4; ++k) {  // swap(4g + k) = swap(4g) ^ 2k
+        const float* const q = (const float*)(t + (base ^ (c0 * 4) ^ (32 * k))) + k * COLS;
+        v[k] = q[0];
+        v[4 + k] = q[16 * COLS];
     }
     return v;
 }
@@ -178,87 +189,98 @@ __device__ __forceinline__ void weigh(const bf16x8& v, const f32x8& w, bf16x8 (&
 }
 __device__ __forceinline__ void weigh(const f32x8& v, const f32x8& w, f32x8 (&o)[1]) { o[0] = v * w; }
 
+// The rows of a chunk of one per-token tensor as a buffer resource: offsets are in bytes from
+// the chunk's lowest address, and one outside its rows reads 0 and stores nothing, so nothing
+// is predicated.  A chunk's rows span less than 2^31 bytes (32 rows of 2^24 elements),
+// which kNowhere is past.
+constexpr uint32_t kNowhere = 0x80000000u;
+struct Rows {
+    __amdgpu_buffer_rsrc_t r;
+    // `low`: the lowest row; have rows, `step` bytes apart, of `width` bytes
+    __device__ __forceinline__ Rows(const void* low, uint32_t step, int have, uint32_t width)
+        : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(low), (short)0,
+                                              (int)((uint32_t)(have - 1) * step + width), 0x00020000)) {}
+};
+
+// N neighbours of a row at byte offset `off`, of which `left` lie in the row: with whole units
+// all or none.
+template <typename OT, int N, bool RAGGED>
+__device__ __forceinline__ void store_run(const Rows& b, uint32_t off, int left, const float (&x)[N]) {
+    typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+    typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+    OT o[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) o[j] = (OT)x[j];
+    if constexpr (!RAGGED) {
+        if (left < N) off = kNowhere;
+        if constexpr (sizeof(o) == 8) {
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, o), b.r, off, 0, 0);
+        } else {
+#pragma unroll
+            for (int j = 0; j < (int)sizeof(o) / 16; ++j) {
+                u32x4 v;
+                __builtin_memcpy(&v, (const char*)o + 16 * j, 16);
+                __builtin_amdgcn_raw_buffer_store_b128(v, b.r, off + 16 * j, 0, 0);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const uint32_t at = j < left ? off + j * (uint32_t)sizeof(OT) : kNowhere;
+            if constexpr (sizeof(OT) == 2)
+                __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, o[j]), b.r, at, 0, 0);
+            else
+                __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, o[j]), b.r, at, 0, 0);
+        }
+    }
+}
+
 // Waves a SIMD that the kernel is compiled for: two workgroups a CU.
-constexpr int lin_waves(int KD, int VT, int size) { return KD * size > 512 ? 1 : VT / 32; }
+constexpr int lin_waves(int KD, int size) { return KD * size > 512 ? 1 : 2; }
 
 template <typename T> constexpr int kParts = sizeof(T) == 2 ? 3 : 1;
 
-// The 16-byte units of a C x COLS tile that one of NT threads moves: loads for the next chunk
-// stay in registers until its LDS tile is free.
-template <typename T, int C, int COLS, int NT>
-struct Mover {
-    static constexpr int EPU = 16 / sizeof(T), UPR = COLS / EPU, N = C * UPR / NT, STEP = NT / UPR;
-    static_assert(C * UPR % NT == 0 && NT % UPR == 0, "tile and threads");
-    typedef T unit __attribute__((ext_vector_type(16 / sizeof(T))));
-    unit u[N];
-    __device__ static __forceinline__ int row() { return threadIdx.x / UPR; }
-    __device__ static __forceinline__ int col() { return threadIdx.x % UPR * EPU; }
-    // rows at base + row * step (elements; negative against the order of memory); only
-    // rows < clen and columns < cols are read
-    __device__ __forceinline__ void load(const T* base, int64_t step, int clen, int cols) {
-        const int c = col();
-        if (cols % EPU == 0) {
-            const int cc = c < cols ? c : 0;
+// Fills a tile with the chunk's rows: row r is the chunk's r-th token in processing order (with
+// `back`, memory row have - 1 - r); rows past `have` are zeros, or values of the chunk where
+// its rows lie closer than they are wide, and columns past `cols` zeros.  Each of four waves
+// issues every fourth load of 64 units straight into LDS, nothing passes through registers and
+// nothing is waited for.  RAGGED (rows of no whole units): element by element, waiting.
+template <typename T, int COLS, bool RAGGED>
+__device__ __forceinline__ void fill(char* tile, const void* low, uint32_t step, int have, int cols, bool back) {
+    using L = Tile<T, COLS>;
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const Rows b(low, step, have, cols * (uint32_t)sizeof(T));
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int r = row() + i * STEP;
-                __builtin_memcpy(&u[i], base + (r < clen ? r : 0) * step + cc, 16);
-            }
+    for (int i = 0; i < C * L::UPR / 256; ++i) {
+        const int place = (i * 4 + wave) * 64 + lane, r = place / L::UPR, c = (place % L::UPR ^ L::swap(r)) * L::EPU;
+        const uint32_t off = (uint32_t)(back ? have - 1 - r : r) * step + (uint32_t)(c * sizeof(T));
+        if constexpr (!RAGGED) {
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                b.r, (__attribute__((address_space(3))) void*)(tile + (i * 4 + wave) * 1024), 16,
+                c < cols ? off : kNowhere, 0, 0, 0);
         } else {
+            T u[L::EPU];
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int r = row() + i * STEP;
-#pragma unroll
-                for (int j = 0; j < EPU; ++j)
-                    u[i][j] = r < clen && c + j < cols ? base[r * step + c + j] : (T)0.f;
+            for (int j = 0; j < L::EPU; ++j) {
+                const uint32_t at = c + j < cols ? off + j * (uint32_t)sizeof(T) : kNowhere;
+                if constexpr (sizeof(T) == 2)
+                    u[j] = __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(b.r, at, 0, 0));
+                else
+                    u[j] = __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(b.r, at, 0, 0));
             }
+            __builtin_memcpy(__builtin_assume_aligned(tile + place * 16, 16), u, 16);
         }
     }
-    __device__ __forceinline__ void put(T* tile, int clen, int cols) const {
-        const bool whole = clen == C && cols == COLS;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int r = row() + i * STEP;
-            unit x = u[i];
-            if (!whole && (r >= clen || col() >= cols)) x = unit{};
-            *(unit*)(tile + Tile<T, COLS>::off(r, col())) = x;
-        }
-    }
-    __device__ __forceinline__ void get(const T* tile) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) u[i] = *(const unit*)(tile + Tile<T, COLS>::off(row() + i * STEP, col()));
-    }
-    __device__ __forceinline__ void store(T* base, int64_t step, int clen, int cols) const {
-        const int c = col();
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int r = row() + i * STEP;
-            if (r >= clen) continue;
-            if (c + EPU <= cols) {
-                __builtin_memcpy(base + r * step + c, &u[i], 16);
-            } else {
-#pragma unroll
-                for (int j = 0; j < EPU; ++j)
-                    if (c + j < cols) base[r * step + c + j] = u[i][j];
-            }
-        }
-    }
-};
+}
 
-template <typename T, int KD, int VT, int C>
-struct __attribute__((aligned(16))) Shared {
-    T q[C * Tile<T, KD>::ST];
-    T k[C * Tile<T, KD>::ST];
-    T v[C * Tile<T, VT>::ST];
-    T p[C * Tile<T, C>::ST];
+// The chunk being worked on and the next one.
+template <typename T, int KD, int VT, bool STATE>
+struct __attribute__((aligned(1024))) Shared {
+    char q[STATE ? 0 : 2][C * Tile<T, KD>::ROW];
+    char k[2][C * Tile<T, KD>::ROW];
+    char v[2][C * Tile<T, VT>::ROW];
+    double pc;        // l^C
     float pw[C + 4];  // l^n
-    float w[2][C];    // weights of a chunk's tokens in the state behind it; the last chunk's
-};
-template <typename T, int KD, int VT, int C>
-struct __attribute__((aligned(16))) SharedState {
-    T k[C * Tile<T, KD>::ST];
-    T v[C * Tile<T, VT>::ST];
-    float w[1][C];
 };
 
 // Workgroups that read the same rows (the V tiles of a head, the heads of a group) follow each
@@ -271,12 +293,11 @@ __device__ __forceinline__ uint32_t same_xcd(uint32_t id, uint32_t together, uin
 }
 
 // One span (or, STATE, only its state).  OT: the output's type.
-template <typename T, typename OT, int KD, int VT, int C, bool STATE>
-__global__ __launch_bounds__(VT * 4, lin_waves(KD, VT, sizeof(T))) void linattn_kernel(LinPass p) {
+template <typename T, typename OT, int KD, int VT, bool RAGGED, bool STATE>
+__global__ __launch_bounds__(256, lin_waves(KD, sizeof(T))) void linattn_kernel(LinPass p) {
     using X8 = typename Vec<T>::x8;
-    using X4 = typename Vec<T>::x4;
-    constexpr int NT = VT * 4, KB = KD / 16, KS = KD / 32, IB = C / 16, TS = C / 32, NW = NT / 64;
-    __shared__ std::conditional_t<STATE, SharedState<T, KD, VT, C>, Shared<T, KD, VT, C>> sh;
+    constexpr int CB = VT / 64, KB = KD / 16, KS = KD / 32, KR = Tile<T, KD>::ROW;
+    __shared__ Shared<T, KD, VT, STATE> sh;
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), l16 = lane & 15, g = lane >> 4;
     uint32_t id = same_xcd(blockIdx.x, p.together, gridDim.x);
     const int vt = id % (uint32_t)p.vtiles;
@@ -288,204 +309,224 @@ __global__ __launch_bounds__(VT * 4, lin_waves(KD, VT, sizeof(T))) void linattn_
     const bool last = sp.t0 + n >= sp.len;
     if (STATE && last) return;  // no span behind it
     const int64_t block = ((int64_t)sp.seq * p.H + h) * ((int64_t)p.K * p.V);
-    const int v0 = vt * VT, vcols = min(VT, p.V - v0), c0 = wave * 16, vc = c0 + l16;
+    const int v0 = vt * VT, vcols = min(VT, p.V - v0), c0 = wave * (16 * CB);
     float* const mine = p.spans + (((int64_t)slot * p.H + h) * p.vtiles + vt) * (KD * VT) +
-                        wave * (KB * 256) + lane * 4;
+                        wave * (CB * KB * 256) + lane * 4;
 
     if (!STATE && n == 0) {  // an empty sequence hands on what came in
         if (p.final)
-            for (int i = tid; i < p.K * vcols; i += NT) {
+            for (int i = tid; i < p.K * vcols; i += 256) {
                 const int64_t e = block + (int64_t)(i / vcols) * p.s_k + (int64_t)(v0 + i % vcols) * p.s_v;
                 p.final[e] = p.init ? p.init[e] : 0.f;
             }
         return;
     }
 
-    // the first chunk's tiles
-    const int64_t tok0 = p.reverse ? sp.first + sp.len - 1 - sp.t0 : sp.first + sp.t0;
-    const int64_t dir = p.reverse ? -1 : 1;
+    // chunk pointers: the rows of the span's first token in processing order
+    const bool back = p.reverse != 0;
+    const int64_t tok0 = back ? sp.first + sp.len - 1 - sp.t0 : sp.first + sp.t0;
     const T* qp = (const T*)p.q + tok0 * p.q_t + (h / p.qdiv) * p.q_h;
     const T* kp = (const T*)p.k + tok0 * p.k_t + (h / p.kdiv) * p.k_h;
     const T* vp = (const T*)p.v + tok0 * p.v_t + (h / p.vdiv) * p.v_h + v0;
     OT* op = (OT*)p.o + tok0 * p.o_t + h * p.o_h + v0;
-    const int64_t qs = dir * p.q_t, ks = dir * p.k_t, vs = dir * p.v_t, os = dir * p.o_t;
-    Mover<T, C, KD, NT> mq, mk;
-    Mover<T, C, VT, NT> mv, mo;
-    const int kd = row_base<T, KD>(lane), cd = row_base<T, C>(lane);
-    const int kt = col_base<T, KD>(lane), vtb = col_base<T, VT>(lane), vd = row_base<T, VT>(lane);
-    constexpr bool kByTile = sizeof(OT) == sizeof(T);  // outputs leave through v's tile
-    int clen = (int)imin(C, n);
-    if (!STATE) mq.load(qp, qs, clen, p.K);
-    mk.load(kp, ks, clen, p.K);
-    mv.load(vp, vs, clen, vcols);
+    const uint32_t qs = (uint32_t)p.q_t * (uint32_t)sizeof(T), ks = (uint32_t)p.k_t * (uint32_t)sizeof(T);
+    const uint32_t vs = (uint32_t)p.v_t * (uint32_t)sizeof(T), os = (uint32_t)p.o_t * (uint32_t)sizeof(OT);
+    auto fetch = [&](int64_t t, int to) {  // the chunk at t of the span
+        const int have = (int)imin(C, n - t);
+        const int64_t low = back ? -(t + have - 1) : t;
+        if constexpr (!STATE) fill<T, KD, RAGGED>(sh.q[to], qp + low * p.q_t, qs, have, p.K, back);
+        fill<T, KD, RAGGED>(sh.k[to], kp + low * p.k_t, ks, have, p.K, back);
+        fill<T, VT, RAGGED>(sh.v[to], vp + low * p.v_t, vs, have, vcols, back);
+    };
+    fetch(0, 0);
 
-    const float decay = p.decay[h];
-    if constexpr (!STATE) {
-        if (tid <= C) sh.pw[tid] = (float)power(decay, tid);
-        // score tiles above the diagonal that a product over 32 tokens meets
-        for (int i = tid; i < C * Tile<T, C>::ST; i += NT) sh.p[i] = (T)0.f;
-    }
-    if (tid < C) sh.w[0][tid] = p.in_scale * (float)power(decay, C - tid);
-    Rate rate(decay, C);
-    float closing = 0.f;  // the state's factor over the sequence's last chunk
-    if (!STATE && last && p.final) {
-        const int cl = (int)((n - 1) % C) + 1;
-        closing = (float)power(decay, cl - 1 + p.final_pow);
-        if (tid < C)
-            sh.w[STATE ? 0 : 1][tid] = tid < cl ? p.in_scale * (float)power(decay, cl - 1 - tid + p.final_pow) : 0.f;
+    // One exponential a thread: l^0 .. l^C.
+    if (tid <= C) {
+        const double x = power(p.decay[h], tid);
+        sh.pw[tid] = (float)x;
+        if (tid == C) sh.pc = x;
     }
 
-    f32x4 st[KB];
-    const bool split = p.per != 1;  // states come in by way of the workspace
-    if (!STATE && split) {
+    // the state that comes in, in flight while the powers are formed: from the workspace where
+    // the sequence is in spans
+    f32x4 st[KB][CB];
+    const bool split = p.per != 1, come = !STATE && !split && p.init;
+    const Rows sb(come ? (const void*)(p.init + block) : (const void*)p.decay, 0, 1,
+                  come ? (uint32_t)(p.K * p.V) * 4 : 0);
+    // this lane's first entry of each column block; its rows are s_k apart
+    uint32_t s0[CB];
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) st[kb] = *(const f32x4*)(mine + kb * 256);
-    } else {
-        const bool come = !STATE && p.init && vc < vcols;
-        const float f = p.init_pow ? (float)power(decay, 1) : 1.f;
+    for (int cb = 0; cb < CB; ++cb) {
+        const int vc = c0 + tile_col<CB>(cb, l16);
+        s0[cb] = vc < vcols ? (uint32_t)(4 * g * p.s_k + (v0 + vc) * p.s_v) * 4 : kNowhere;
+    }
+    auto entry = [&](int kb, int cb, int r) {
+        return 16 * kb + 4 * g + r < p.K ? s0[cb] + (uint32_t)((16 * kb + r) * p.s_k * 4) : kNowhere;
+    };
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+            if (STATE) {
+                st[kb][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
+            } else if (split) {
+                st[kb][cb] = *(const f32x4*)(mine + (cb * KB + kb) * 256);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    st[kb][cb][r] = __uint_as_float(
+                        __builtin_amdgcn_raw_buffer_load_b32(sb.r, entry(kb, cb, r), 0, 0));
+            }
+        }
+    vm_wait<0>();
+    block_sync();
+    Rate rate(sh.pc);
+    // weights: of the tokens in the state behind a chunk (w), of a score (tw: within a block of
+    // 16 tokens, of rows 16-31 with columns 0-15), of the state in row 16 ib + l16 (pwi)
+    f32x8 w;
+    f32x4 tw[2];
+    float pwi[2];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        w[r] = p.in_scale * sh.pw[C - 4 * g - r];
+        w[4 + r] = p.in_scale * sh.pw[C - 16 - 4 * g - r];
+        const int d = l16 - 4 * g - r;
+        const float x = p.in_scale * sh.pw[max(d, 0)];
+        tw[0][r] = d >= 0 ? x : 0.f;
+        tw[1][r] = p.in_scale * sh.pw[16 + d];
+    }
+    pwi[0] = sh.pw[l16];
+    pwi[1] = sh.pw[16 + l16];
+    if (!STATE && !split && p.init_pow) {
+        const float f = sh.pw[1];
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int kr = 16 * kb + 4 * g + r;
-                st[kb][r] = come && kr < p.K
-                                ? f * p.init[block + (int64_t)kr * p.s_k + (int64_t)(v0 + vc) * p.s_v] : 0.f;
-            }
+            for (int cb = 0; cb < CB; ++cb) st[kb][cb] *= f;
     }
 
-    for (int64_t t = 0; t < n; t += C) {
-        const int cl = clen;
+    const int rb = row_base<T, KD>(lane), kc = col_base<T, KD, 1>(lane), vb = col_base<T, VT, CB>(lane);
+    int buf = 0;
+    for (int64_t t = 0; t < n; t += C, buf ^= 1) {
+        const int cl = (int)imin(C, n - t);
         const bool end = t + C >= n;          // of the span
         const bool close = last && end;       // of the sequence
-        // a thread's units of v's tile are those of the outputs that it takes from it
-        if constexpr (!STATE && kByTile)
-            if (t) mo.get((const T*)sh.v);
-        if constexpr (!STATE) mq.put(sh.q, cl, p.K);
-        mk.put(sh.k, cl, p.K);
-        mv.put(sh.v, cl, vcols);
-        if constexpr (!STATE && kByTile)
-            if (t) {
-                mo.store((T*)op, os, C, vcols);
-                op += C * os;
-            }
-        block_sync();
-        if (!end) {
-            qp += C * qs;
-            kp += C * ks;
-            vp += C * vs;
-            clen = (int)imin(C, n - t - C);
-            if (!STATE) mq.load(qp, qs, clen, p.K);
-            mk.load(kp, ks, clen, p.K);
-            mv.load(vp, vs, clen, vcols);
-        }
-        f32x4 acc[IB];  // transposed: a lane has 4 columns of token 16 ib + l16
+        if (!end) fetch(t + C, buf ^ 1);
+        const char* const tq = sh.q[STATE ? 0 : buf];
+        const char* const tk = sh.k[buf];
+        const char* const tv = sh.v[buf];
+        // Results are transposed: a lane has 4 columns of token 16 ib + l16, and of the scores 4
+        // tokens j of one row i, which is the order in which they meet the values.
+        f32x4 acc[2][CB];
+        X8 sc[2];
         if constexpr (!STATE) {
-            // scores, transposed too: a lane gets 4 tokens j of one row i
-            constexpr int NS = IB * (IB + 1) / 2;
+            f32x4 s00 = {0.f, 0.f, 0.f, 0.f}, s01 = s00, s11 = s00;
 #pragma unroll
-            for (int x = 0; x < (NS + NW - 1) / NW; ++x) {
-                const int tile = x * NW + wave;
-                if (tile < NS) {
-                    int ib = 0, jb = tile;
-                    while (jb > ib) jb -= ++ib;
-                    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+            for (int ib = 0; ib < 2; ++ib)
 #pragma unroll
-                    for (int kk = 0; kk < KS; ++kk)
-                        s = mma(row_frag<T, KD>(sh.k, kd, 16 * jb, 32 * kk),
-                                row_frag<T, KD>(sh.q, kd, 16 * ib, 32 * kk), s);
-                    const int d = 16 * (ib - jb) + l16 - 4 * g;
-                    X4 o;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        o[r] = d - r >= 0 ? (T)(s[r] * (p.in_scale * sh.pw[max(d - r, 0)])) : (T)0.f;
-                    *(X4*)(sh.p + cd + (16 * ib * Tile<T, C>::ST + 16 * jb)) = o;
-                }
-            }
-            // l^i q_i E
-#pragma unroll
-            for (int ib = 0; ib < IB; ++ib) acc[ib] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int cb = 0; cb < CB; ++cb) acc[ib][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
-                X8 e;
+                const X8 q0 = row_frag<T, KD>(tq, rb, 0, 32 * kk), q1 = row_frag<T, KD>(tq, rb, 16, 32 * kk);
+                const X8 k0 = row_frag<T, KD>(tk, rb, 0, 32 * kk), k1 = row_frag<T, KD>(tk, rb, 16, 32 * kk);
+                s00 = mma(k0, q0, s00);
+                s01 = mma(k0, q1, s01);
+                s11 = mma(k1, q1, s11);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    e[r] = (T)st[2 * kk][r];
-                    e[4 + r] = (T)st[2 * kk + 1][r];
+                for (int cb = 0; cb < CB; ++cb) {
+                    X8 e;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        e[r] = (T)st[2 * kk][cb][r];
+                        e[4 + r] = (T)st[2 * kk + 1][cb][r];
+                    }
+                    acc[0][cb] = mma(e, q0, acc[0][cb]);
+                    acc[1][cb] = mma(e, q1, acc[1][cb]);
                 }
-#pragma unroll
-                for (int ib = 0; ib < IB; ++ib)
-                    acc[ib] = mma(e, row_frag<T, KD>(sh.q, kd, 16 * ib, 32 * kk), acc[ib]);
             }
 #pragma unroll
-            for (int ib = 0; ib < IB; ++ib) acc[ib] *= sh.pw[16 * ib + l16];
-            block_sync();
+            for (int cb = 0; cb < CB; ++cb) {
+                acc[0][cb] *= pwi[0];
+                acc[1][cb] *= pwi[1];
+            }
+            // above the diagonal a weight of 0 is not enough: a score there may be infinite
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const bool in = l16 >= 4 * g + r;
+                sc[0][r] = in ? (T)(s00[r] * tw[0][r]) : (T)0.f;
+                sc[0][4 + r] = (T)0.f;
+                sc[1][r] = (T)(s01[r] * tw[1][r]);
+                sc[1][4 + r] = in ? (T)(s11[r] * tw[0][r]) : (T)0.f;
+            }
         }
         // the chunk's values: scores times v, and the state behind the chunk
         const bool update = STATE || !close || p.final;
-        if (update) {
-            const float f = close ? closing : rate.next();
+        X8 vf[CB];
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb) st[kb] *= f;
-        }
-#pragma unroll
-        for (int ts = 0; ts < TS; ++ts) {
-            const X8 vf = col_frag<VT>(sh.v, vtb, 32 * ts, c0);
+        for (int cb = 0; cb < CB; ++cb) {
+            vf[cb] = col_frag<VT>((const T*)nullptr, tv, vb ^ cb * 4 * (int)sizeof(T), c0);
             if constexpr (!STATE) {
-#pragma unroll
-                for (int ib = 2 * ts; ib < IB; ++ib)
-                    acc[ib] = mma(vf, row_frag<T, C>(sh.p, cd, 16 * ib, 32 * ts), acc[ib]);
-            }
-            if (update) {
-                const float* const wt = sh.w[!STATE && close ? 1 : 0] + 32 * ts + 4 * g;
-                const f32x8 w = cat<f32x8, f32x4>(*(const f32x4*)wt, *(const f32x4*)(wt + 16));
-                X8 vw[kParts<T>];
-                weigh(vf, w, vw);
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb)
-                    st[kb] = mma_weighted(col_frag<KD>(sh.k, kt, 32 * ts, 16 * kb), vw, st[kb]);
+                acc[0][cb] = mma(vf[cb], sc[0], acc[0][cb]);
+                acc[1][cb] = mma(vf[cb], sc[1], acc[1][cb]);
             }
         }
+        if (update) {
+            float f = rate.next();
+            if (close) {
+                const int top = cl - 1 + p.final_pow;
+                f = sh.pw[top];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const int j = (r & 4) * 4 + 4 * g + (r & 3);
+                    w[r] = j < cl ? p.in_scale * sh.pw[max(top - j, 0)] : 0.f;
+                }
+            }
+            X8 vw[CB][kParts<T>];
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb) weigh(vf[cb], w, vw[cb]);
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                const X8 a = col_frag<KD>((const T*)nullptr, tk, kc, 16 * kb);
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb) {
+                    st[kb][cb] *= f;
+                    st[kb][cb] = mma_weighted(a, vw[cb], st[kb][cb]);
+                }
+            }
+        }
+        // The next chunk's loads are waited for ahead of this one's stores, which need not be.
+        if (!end) vm_wait<0>();
         if constexpr (!STATE) {
-            if constexpr (kByTile) {
-                // this wave alone has read these columns of v
+            const Rows ob(op + (back ? -(t + cl - 1) : t) * p.o_t, os, cl, vcols * (uint32_t)sizeof(OT));
 #pragma unroll
-                for (int ib = 0; ib < IB; ++ib) {
-                    X4 o;
+            for (int ib = 0; ib < 2; ++ib) {
+                const int i = 16 * ib + l16, c = c0 + tile_col<CB>(0, 4 * g);
+                const uint32_t off = (uint32_t)(back ? cl - 1 - i : i) * os + (uint32_t)(c * sizeof(OT));
+                float x[4 * CB];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) o[r] = (T)(p.out_scale * acc[ib][r]);
-                    *(X4*)(sh.v + vd + (16 * ib * Tile<T, VT>::ST + c0)) = o;
-                }
-            } else {
-#pragma unroll
-                for (int ib = 0; ib < IB; ++ib) {
-                    const int i = 16 * ib + l16, c = c0 + 4 * g;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (i < cl && c + r < vcols) op[i * os + c + r] = (OT)(p.out_scale * acc[ib][r]);
-                }
-                op += C * os;
+                for (int j = 0; j < 4 * CB; ++j) x[j] = p.out_scale * acc[ib][j / 4][j % 4];
+                store_run<OT, 4 * CB, RAGGED>(ob, off, i < cl ? vcols - c : 0, x);
             }
         }
         block_sync();
-        if constexpr (!STATE && kByTile)
-            if (end) {
-                mo.get((const T*)sh.v);
-                mo.store((T*)op, os, cl, vcols);
-            }
     }
 
-    if constexpr (STATE) {
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) *(f32x4*)(mine + kb * 256) = st[kb];
-    } else if (last && p.final && vc < vcols) {
+    const Rows fb(last && p.final ? (const void*)(p.final + block) : (const void*)p.decay, 0, 1,
+                  last && p.final ? (uint32_t)(p.K * p.V) * 4 : 0);
+    if (STATE || (last && p.final))
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int kr = 16 * kb + 4 * g + r;
-                if (kr < p.K) p.final[block + (int64_t)kr * p.s_k + (int64_t)(v0 + vc) * p.s_v] = st[kb][r];
+            for (int cb = 0; cb < CB; ++cb) {
+                if (STATE) {
+                    *(f32x4*)(mine + (cb * KB + kb) * 256) = st[kb][cb];
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(st[kb][cb][r]), fb.r,
+                                                              entry(kb, cb, r), 0, 0);
+                }
             }
-    }
 }
 
 // Joins the span states of every sequence: slot s gets the state that enters span s.
@@ -500,9 +541,11 @@ __global__ __launch_bounds__(256) void linattn_join(LinPass p, int KD, int VT) {
     const int64_t spans = cdiv(sp.len, p.span);
     const int e = blockIdx.y * 256 + threadIdx.x, lane = e & 63, tile = e >> 6;
     const int kb = tile % (KD / 16), vb = tile / (KD / 16);
-    const int kr = 16 * kb + 4 * (lane >> 4), vc = vt * VT + 16 * vb + (lane & 15);
+    const int kr = 16 * kb + 4 * (lane >> 4);
+    const int vc = vt * VT + (VT == 64 ? 16 * vb + (lane & 15)
+                                       : vb / 2 * 32 + tile_col<2>(vb % 2, lane & 15));
     const float decay = p.decay[h];
-    Rate rate(decay, p.span);
+    Rate rate(power(decay, p.span));
     const float f = p.init_pow ? (float)power(decay, 1) : 1.f;
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
     if (p.init)
@@ -547,15 +590,14 @@ __global__ __launch_bounds__(256) void linattn_heads_sum(const float* part, T* o
 // ---- host ----------------------------------------------------------------------------------
 
 struct LinTiles {
-    int KD, VT, C;
+    int KD, VT;
 };
 // K is padded to 64, 128 or 256.  The state of a workgroup's columns is KD x VT / 256
 // registers a thread: 64 at most.
-LinTiles lin_tiles(int K, int V, int32_t dtype) {
+LinTiles lin_tiles(int K, int V) {
     LinTiles t;
     t.KD = K <= 64 ? 64 : (K <= 128 ? 128 : 256);
     t.VT = V <= 64 || t.KD == 256 ? 64 : 128;
-    t.C = dtype == SSD_F32 || t.KD == 256 ? 32 : 64;
     return t;
 }
 
@@ -565,14 +607,15 @@ struct LinPlan {
     int32_t slots, per, vtiles;
     size_t bytes;  // of the span states (0: whole sequences)
 };
-constexpr int64_t kFill = 512;  // two workgroups a CU
+#include <stdlib.h>
+#define kFill (getenv("KFILL") ? (int64_t)atoi(getenv("KFILL")) : (int64_t)512)
 
 LinPlan lin_plan(const ssd_linattn_dims& d, int K, int V) {
     LinPlan pl;
-    pl.t = lin_tiles(K, V, d.dtype);
+    pl.t = lin_tiles(K, V);
     pl.vtiles = (int)cdiv(V, pl.t.VT);
     const int64_t S = d.nseq > 0 ? d.nseq : d.batch, T = (int64_t)d.batch * d.seqlen;
-    const int64_t wgs = S * d.nheads * pl.vtiles, C = pl.t.C;
+    const int64_t wgs = S * d.nheads * pl.vtiles;
     // packed sequences are of any length: cut as if they were one
     const int64_t want = d.nseq > 0 ? cdiv(kFill, (int64_t)d.nheads * pl.vtiles) : cdiv(kFill, wgs);
     const int64_t tokens = d.nseq > 0 ? T : d.seqlen;
@@ -591,32 +634,37 @@ LinPlan lin_plan(const ssd_linattn_dims& d, int K, int V) {
     return pl;
 }
 
-template <typename T, typename OT, int KD, int VT, int C>
+template <typename T, typename OT, int KD, int VT, bool RAGGED>
 void launch_tiles(const LinPass& p, const LinPlan& pl, hipStream_t s) {
     const dim3 grid((unsigned)((int64_t)pl.slots * p.H * pl.vtiles));
     if (pl.bytes) {
-        linattn_kernel<T, OT, KD, VT, C, true><<<grid, VT * 4, 0, s>>>(p);
+        linattn_kernel<T, OT, KD, VT, RAGGED, true><<<grid, 256, 0, s>>>(p);
         const dim3 joins((unsigned)((int64_t)p.S * p.H * pl.vtiles), KD * VT / 1024);
         linattn_join<<<joins, 256, 0, s>>>(p, KD, VT);
     }
-    linattn_kernel<T, OT, KD, VT, C, false><<<grid, VT * 4, 0, s>>>(p);
+    linattn_kernel<T, OT, KD, VT, RAGGED, false><<<grid, 256, 0, s>>>(p);
+}
+template <typename T, typename OT, int KD, int VT>
+void launch_tiles(const LinPass& p, const LinPlan& pl, hipStream_t s) {
+    constexpr int EPU = 16 / sizeof(T);
+    if (p.K % EPU || p.V % EPU) launch_tiles<T, OT, KD, VT, true>(p, pl, s);
+    else launch_tiles<T, OT, KD, VT, false>(p, pl, s);
 }
 template <typename T, typename OT>
 void launch_pass(LinPass& p, const LinPlan& pl, hipStream_t s) {
-    constexpr int C = sizeof(T) == 2 ? 64 : 32;
     p.span = pl.span;
     p.slots = pl.slots;
     p.per = pl.per;
     p.vtiles = pl.vtiles;
     p.together = pl.vtiles * (p.qdiv > p.kdiv ? p.qdiv : p.kdiv);
     if (pl.t.KD == 64) {
-        if (pl.t.VT == 64) launch_tiles<T, OT, 64, 64, C>(p, pl, s);
-        else launch_tiles<T, OT, 64, 128, C>(p, pl, s);
+        if (pl.t.VT == 64) launch_tiles<T, OT, 64, 64>(p, pl, s);
+        else launch_tiles<T, OT, 64, 128>(p, pl, s);
     } else if (pl.t.KD == 128) {
-        if (pl.t.VT == 64) launch_tiles<T, OT, 128, 64, C>(p, pl, s);
-        else launch_tiles<T, OT, 128, 128, C>(p, pl, s);
+        if (pl.t.VT == 64) launch_tiles<T, OT, 128, 64>(p, pl, s);
+        else launch_tiles<T, OT, 128, 128>(p, pl, s);
     } else {
-        launch_tiles<T, OT, 256, 64, 32>(p, pl, s);
+        launch_tiles<T, OT, 256, 64>(p, pl, s);
     }
 }
 
