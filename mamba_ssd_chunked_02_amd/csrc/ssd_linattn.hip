@@ -44,6 +44,11 @@ struct LinPass {
     float in_scale, out_scale;
 };
 
+// Passes of one launch: blockIdx.y's is its own.
+struct LinPasses {
+    LinPass p[3];
+};
+
 // Sequence and span of a slot.  With cu sequence i owns the slots from cu[i] / span + i on:
 // one for every span it can have, and at least one.
 struct Span {
@@ -294,7 +299,9 @@ __device__ __forceinline__ uint32_t same_xcd(uint32_t id, uint32_t together, uin
 
 // One span (or, STATE, only its state).  OT: the output's type.
 template <typename T, typename OT, int KD, int VT, bool RAGGED, bool STATE>
-__global__ __launch_bounds__(256, lin_waves(KD, sizeof(T))) void linattn_kernel(LinPass p) {
+__global__ __launch_bounds__(256, lin_waves(KD, sizeof(T))) void linattn_kernel(LinPasses ps) {
+    const LinPass& p = ps.p[blockIdx.y];
+    touch_args(p);
     using X8 = typename Vec<T>::x8;
     constexpr int CB = VT / 64, KB = KD / 16, KS = KD / 32, KR = Tile<T, KD>::ROW;
     __shared__ Shared<T, KD, VT, STATE> sh;
@@ -427,6 +434,7 @@ __global__ __launch_bounds__(256, lin_waves(KD, sizeof(T))) void linattn_kernel(
                 for (int cb = 0; cb < CB; ++cb) acc[ib][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
+                if (kk && 32 * kk >= p.K) break;  // K is padded to KD: nothing but zeros from here
                 const X8 q0 = row_frag<T, KD>(tq, rb, 0, 32 * kk), q1 = row_frag<T, KD>(tq, rb, 16, 32 * kk);
                 const X8 k0 = row_frag<T, KD>(tk, rb, 0, 32 * kk), k1 = row_frag<T, KD>(tk, rb, 16, 32 * kk);
                 s00 = mma(k0, q0, s00);
@@ -486,6 +494,7 @@ __global__ __launch_bounds__(256, lin_waves(KD, sizeof(T))) void linattn_kernel(
             for (int cb = 0; cb < CB; ++cb) weigh(vf[cb], w, vw[cb]);
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
+                if (kb && 16 * kb >= p.K) break;
                 const X8 a = col_frag<KD>((const T*)nullptr, tk, kc, 16 * kb);
 #pragma unroll
                 for (int cb = 0; cb < CB; ++cb) {
@@ -531,7 +540,9 @@ __global__ __launch_bounds__(256, lin_waves(KD, sizeof(T))) void linattn_kernel(
 
 // Joins the span states of every sequence: slot s gets the state that enters span s.
 // A thread takes 4 entries (one lane's part of a result tile).
-__global__ __launch_bounds__(256) void linattn_join(LinPass p, int KD, int VT) {
+__global__ __launch_bounds__(256) void linattn_join(LinPasses ps, int KD, int VT) {
+    const LinPass& p = ps.p[blockIdx.z];
+    touch_args(p);
     uint32_t id = blockIdx.x;
     const int vt = id % (uint32_t)p.vtiles;
     id /= (uint32_t)p.vtiles;
@@ -544,24 +555,27 @@ __global__ __launch_bounds__(256) void linattn_join(LinPass p, int KD, int VT) {
     const int kr = 16 * kb + 4 * (lane >> 4);
     const int vc = vt * VT + (VT == 64 ? 16 * vb + (lane & 15)
                                        : vb / 2 * 32 + tile_col<2>(vb % 2, lane & 15));
-    const float decay = p.decay[h];
-    Rate rate(power(decay, p.span));
-    const float f = p.init_pow ? (float)power(decay, 1) : 1.f;
-    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    float* at = p.spans + (((int64_t)slot0 * p.H + h) * p.vtiles + vt) * (KD * VT) + e * 4;
+    const int64_t step = (int64_t)p.H * p.vtiles * (KD * VT);
+    constexpr int UN = 16;  // spans in flight
+    f32x4 x[UN], s = {0.f, 0.f, 0.f, 0.f};
+    auto load = [&](int64_t i) {
+#pragma unroll
+        for (int j = 0; j < UN; ++j)
+            if (i + j + 1 < spans) x[j] = *(const f32x4*)(at + j * step);
+    };
+    load(0);
     if (p.init)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             if (kr + r < p.K && vc < p.V)
-                s[r] = f * p.init[((int64_t)seq * p.H + h) * ((int64_t)p.K * p.V) +
-                                  (int64_t)(kr + r) * p.s_k + (int64_t)vc * p.s_v];
-    float* at = p.spans + (((int64_t)slot0 * p.H + h) * p.vtiles + vt) * (KD * VT) + e * 4;
-    const int64_t step = (int64_t)p.H * p.vtiles * (KD * VT);
-    constexpr int UN = 8;  // spans in flight
+                s[r] = p.init[((int64_t)seq * p.H + h) * ((int64_t)p.K * p.V) +
+                              (int64_t)(kr + r) * p.s_k + (int64_t)vc * p.s_v];
+    const float decay = p.decay[h];
+    Rate rate(power(decay, p.span));
+    if (p.init_pow) s *= (float)power(decay, 1);
     for (int64_t i = 0; i < spans; i += UN, at += UN * step) {
-        f32x4 x[UN];
-#pragma unroll
-        for (int j = 0; j < UN; ++j)
-            if (i + j + 1 < spans) x[j] = *(const f32x4*)(at + j * step);
+        if (i) load(i);
 #pragma unroll
         for (int j = 0; j < UN; ++j)
             if (i + j < spans) {
@@ -610,14 +624,14 @@ struct LinPlan {
 #include <stdlib.h>
 #define kFill (getenv("KFILL") ? (int64_t)atoi(getenv("KFILL")) : (int64_t)512)
 
-LinPlan lin_plan(const ssd_linattn_dims& d, int K, int V) {
+LinPlan lin_plan(const ssd_linattn_dims& d, int K, int V, int passes = 1) {
     LinPlan pl;
     pl.t = lin_tiles(K, V);
     pl.vtiles = (int)cdiv(V, pl.t.VT);
     const int64_t S = d.nseq > 0 ? d.nseq : d.batch, T = (int64_t)d.batch * d.seqlen;
-    const int64_t wgs = S * d.nheads * pl.vtiles;
+    const int64_t wgs = S * d.nheads * pl.vtiles * passes;
     // packed sequences are of any length: cut as if they were one
-    const int64_t want = d.nseq > 0 ? cdiv(kFill, (int64_t)d.nheads * pl.vtiles) : cdiv(kFill, wgs);
+    const int64_t want = d.nseq > 0 ? cdiv(kFill, (int64_t)d.nheads * pl.vtiles * passes) : cdiv(kFill, wgs);
     const int64_t tokens = d.nseq > 0 ? T : d.seqlen;
     pl.span = cdiv(cdiv(tokens, want), C) * C;
     if (pl.span < 2 * C) pl.span = 2 * C;
@@ -635,36 +649,43 @@ LinPlan lin_plan(const ssd_linattn_dims& d, int K, int V) {
 }
 
 template <typename T, typename OT, int KD, int VT, bool RAGGED>
-void launch_tiles(const LinPass& p, const LinPlan& pl, hipStream_t s) {
-    const dim3 grid((unsigned)((int64_t)pl.slots * p.H * pl.vtiles));
+void launch_tiles(const LinPasses& ps, int passes, const LinPlan& pl, hipStream_t s) {
+    const LinPass& p = ps.p[0];
+    const dim3 grid((unsigned)((int64_t)pl.slots * p.H * pl.vtiles), passes);
     if (pl.bytes) {
-        linattn_kernel<T, OT, KD, VT, RAGGED, true><<<grid, 256, 0, s>>>(p);
-        const dim3 joins((unsigned)((int64_t)p.S * p.H * pl.vtiles), KD * VT / 1024);
-        linattn_join<<<joins, 256, 0, s>>>(p, KD, VT);
+        linattn_kernel<T, OT, KD, VT, RAGGED, true><<<grid, 256, 0, s>>>(ps);
+        const dim3 joins((unsigned)((int64_t)p.S * p.H * pl.vtiles), KD * VT / 1024, passes);
+        linattn_join<<<joins, 256, 0, s>>>(ps, KD, VT);
     }
-    linattn_kernel<T, OT, KD, VT, RAGGED, false><<<grid, 256, 0, s>>>(p);
+    linattn_kernel<T, OT, KD, VT, RAGGED, false><<<grid, 256, 0, s>>>(ps);
 }
 template <typename T, typename OT, int KD, int VT>
-void launch_tiles(const LinPass& p, const LinPlan& pl, hipStream_t s) {
+void launch_tiles(const LinPasses& ps, int passes, const LinPlan& pl, hipStream_t s) {
     constexpr int EPU = 16 / sizeof(T);
-    if (p.K % EPU || p.V % EPU) launch_tiles<T, OT, KD, VT, true>(p, pl, s);
-    else launch_tiles<T, OT, KD, VT, false>(p, pl, s);
+    if (ps.p[0].K % EPU || ps.p[0].V % EPU) launch_tiles<T, OT, KD, VT, true>(ps, passes, pl, s);
+    else launch_tiles<T, OT, KD, VT, false>(ps, passes, pl, s);
 }
+// Passes of one plan, side by side in each launch: their span states lie behind each other in
+// the workspace (pl.bytes each).
 template <typename T, typename OT>
-void launch_pass(LinPass& p, const LinPlan& pl, hipStream_t s) {
-    p.span = pl.span;
-    p.slots = pl.slots;
-    p.per = pl.per;
-    p.vtiles = pl.vtiles;
-    p.together = pl.vtiles * (p.qdiv > p.kdiv ? p.qdiv : p.kdiv);
+void launch_passes(LinPasses& ps, int passes, const LinPlan& pl, hipStream_t s) {
+    for (int i = 0; i < passes; ++i) {
+        LinPass& p = ps.p[i];
+        p.span = pl.span;
+        p.slots = pl.slots;
+        p.per = pl.per;
+        p.vtiles = pl.vtiles;
+        p.together = pl.vtiles * (p.qdiv > p.kdiv ? p.qdiv : p.kdiv);
+        p.spans = (float*)((char*)p.spans + i * pl.bytes);
+    }
     if (pl.t.KD == 64) {
-        if (pl.t.VT == 64) launch_tiles<T, OT, 64, 64>(p, pl, s);
-        else launch_tiles<T, OT, 64, 128>(p, pl, s);
+        if (pl.t.VT == 64) launch_tiles<T, OT, 64, 64>(ps, passes, pl, s);
+        else launch_tiles<T, OT, 64, 128>(ps, passes, pl, s);
     } else if (pl.t.KD == 128) {
-        if (pl.t.VT == 64) launch_tiles<T, OT, 128, 64>(p, pl, s);
-        else launch_tiles<T, OT, 128, 128>(p, pl, s);
+        if (pl.t.VT == 64) launch_tiles<T, OT, 128, 64>(ps, passes, pl, s);
+        else launch_tiles<T, OT, 128, 128>(ps, passes, pl, s);
     } else {
-        launch_tiles<T, OT, 256, 64>(p, pl, s);
+        launch_tiles<T, OT, 256, 64>(ps, passes, pl, s);
     }
 }
 
@@ -711,18 +732,22 @@ size_t state_bytes(const ssd_linattn_dims& d) {
     return (size_t)(d.nseq > 0 ? d.nseq : d.batch) * d.nheads * d.keydim * d.valuedim * 4;
 }
 
-// The backward's workspace: span states of one pass at a time, and the shares of dk or dv.
+// The backward's plan.  The passes for dq and dk have the same sizes and share their launches
+// (all gradients in the input's type); shares of dk and dv, where heads share keys and values,
+// are float32 and go by themselves.  Workspace: the span states of the passes of a launch, and
+// the shares of dk or dv.
 struct LinBwdPlan {
-    LinPlan dq, dk, dv;
+    LinPlan qk, v;  // dq and dk (dq or dk alone where heads share), dv
+    int together;
     size_t spans, shares;
 };
 LinBwdPlan lin_bwd_plan(const ssd_linattn_dims& d) {
     LinBwdPlan b;
-    b.dq = lin_plan(d, d.valuedim, d.keydim);
-    b.dk = lin_plan(d, d.valuedim, d.keydim);
-    b.dv = lin_plan(d, d.keydim, d.valuedim);
-    b.spans = (size_t)imax(imax(b.dq.bytes, b.dk.bytes), b.dv.bytes);
-    b.shares = d.nheads == d.ngroups ? 0
+    b.together = d.nheads == d.ngroups ? 2 : 1;
+    b.qk = lin_plan(d, d.valuedim, d.keydim, b.together);
+    b.v = lin_plan(d, d.keydim, d.valuedim);
+    b.spans = (size_t)imax(b.together * b.qk.bytes, b.v.bytes);
+    b.shares = b.together == 2 ? 0
                : up256((size_t)d.batch * d.seqlen * d.nheads * imax(d.keydim, d.valuedim) * 4);
     return b;
 }
@@ -761,7 +786,8 @@ int ssd_linattn_fwd(const ssd_linattn_dims* dims, const ssd_linattn_layout* layo
     const LinPlan pl = lin_plan(d, d.keydim, d.valuedim);
     if (pl.bytes && (!workspace || workspace_bytes < pl.bytes)) return SSD_ERR_WORKSPACE;
     if (cu_seqlens && check_cu_env(cu_seqlens, d.nseq, T, (hipStream_t)stream, &st)) return st;
-    LinPass p = lin_common(d, decay, cu_seqlens);
+    LinPasses ps = {};
+    LinPass& p = ps.p[0] = lin_common(d, decay, cu_seqlens);
     p.q = q, p.q_t = l.q_token, p.q_h = l.q_head;
     p.k = k, p.k_t = l.k_token, p.k_h = l.k_group;
     p.v = v, p.v_t = l.v_token, p.v_h = l.v_group;
@@ -771,8 +797,8 @@ int ssd_linattn_fwd(const ssd_linattn_dims* dims, const ssd_linattn_layout* layo
     p.init = init_state, p.final = final_state, p.spans = (float*)workspace;
     p.reverse = reverse != 0, p.init_pow = 1, p.final_pow = 0;
     p.in_scale = 1.f, p.out_scale = d.scale;
-    if (d.dtype == SSD_BF16) launch_pass<bf16, bf16>(p, pl, (hipStream_t)stream);
-    else launch_pass<float, float>(p, pl, (hipStream_t)stream);
+    if (d.dtype == SSD_BF16) launch_passes<bf16, bf16>(ps, 1, pl, (hipStream_t)stream);
+    else launch_passes<float, float>(ps, 1, pl, (hipStream_t)stream);
     return launched();
 }
 
@@ -815,65 +841,64 @@ int ssd_linattn_bwd(const ssd_linattn_dims* dims, const ssd_linattn_layout* layo
     float* const shares = (float*)((char*)workspace + b.spans);
     const bool half = d.dtype == SSD_BF16;
 
-    LinPass p = lin_common(d, decay, cu_seqlens);
-    p.spans = (float*)workspace;
-    if (T > 0) {
-        p.q = dy, p.q_t = l.dy_token, p.q_h = l.dy_head;
-        p.k = v, p.k_t = l.v_token, p.k_h = l.v_group, p.kdiv = R;
-        p.v = k, p.v_t = l.k_token, p.v_h = l.k_group, p.vdiv = R;
-        p.o = dq, p.o_t = l.dq_token, p.o_h = l.dq_head;
-        p.K = d.valuedim, p.V = d.keydim, p.s_k = 1, p.s_v = d.valuedim;
-        p.init = init_state, p.final = nullptr;
-        p.reverse = reverse != 0, p.init_pow = 1, p.final_pow = 0;
-        p.in_scale = 1.f, p.out_scale = d.scale;
-        if (half) launch_pass<bf16, bf16>(p, b.dq, s);
-        else launch_pass<float, float>(p, b.dq, s);
+    LinPass q_ = lin_common(d, decay, cu_seqlens);
+    q_.spans = (float*)workspace;
+    LinPass k_ = q_, v_ = q_;
+    q_.q = dy, q_.q_t = l.dy_token, q_.q_h = l.dy_head;
+    q_.k = v, q_.k_t = l.v_token, q_.k_h = l.v_group, q_.kdiv = R;
+    q_.v = k, q_.v_t = l.k_token, q_.v_h = l.k_group, q_.vdiv = R;
+    q_.o = dq, q_.o_t = l.dq_token, q_.o_h = l.dq_head;
+    q_.K = d.valuedim, q_.V = d.keydim, q_.s_k = 1, q_.s_v = d.valuedim;
+    q_.init = init_state;
+    q_.reverse = reverse != 0, q_.init_pow = 1, q_.final_pow = 0;
+    q_.in_scale = 1.f, q_.out_scale = d.scale;
+
+    k_.q = v, k_.q_t = l.v_token, k_.q_h = l.v_group, k_.qdiv = R;
+    k_.k = dy, k_.k_t = l.dy_token, k_.k_h = l.dy_head;
+    k_.v = q, k_.v_t = l.q_token, k_.v_h = l.q_head;
+    k_.o = R == 1 ? dk : shares;
+    k_.o_t = R == 1 ? l.dk_token : (int64_t)d.nheads * d.keydim;
+    k_.o_h = R == 1 ? l.dk_group : d.keydim;
+    k_.K = d.valuedim, k_.V = d.keydim, k_.s_k = 1, k_.s_v = d.valuedim;
+
+    v_.q = k, v_.q_t = l.k_token, v_.q_h = l.k_group, v_.qdiv = R;
+    v_.k = q, v_.k_t = l.q_token, v_.k_h = l.q_head;
+    v_.v = dy, v_.v_t = l.dy_token, v_.v_h = l.dy_head;
+    v_.o = R == 1 ? dv : shares;
+    v_.o_t = R == 1 ? l.dv_token : (int64_t)d.nheads * d.valuedim;
+    v_.o_h = R == 1 ? l.dv_group : d.valuedim;
+    v_.K = d.keydim, v_.V = d.valuedim, v_.s_k = d.valuedim, v_.s_v = 1;
+    v_.final = dinit_state;
+    for (LinPass* p : {&k_, &v_}) {
+        p->init = d_final;
+        p->reverse = reverse == 0;
+        p->init_pow = 0, p->final_pow = 1;
+        p->in_scale = d.scale, p->out_scale = 1.f;
     }
-    // the passes in the opposite order, dk before dv: dinit may be d_final's buffer
-    p.init = d_final;
-    p.reverse = reverse == 0;
-    p.init_pow = 0, p.final_pow = 1;
-    p.in_scale = d.scale, p.out_scale = 1.f;
-    auto run = [&](const LinPlan& pl) {
-        if (R == 1) {
-            if (half) launch_pass<bf16, bf16>(p, pl, s);
-            else launch_pass<float, float>(p, pl, s);
-        } else {
-            if (half) launch_pass<bf16, float>(p, pl, s);
-            else launch_pass<float, float>(p, pl, s);
-        }
+    auto run = [&](const LinPass& p, bool share, const LinPlan& pl) {
+        LinPasses ps = {{p}};
+        if (!half) launch_passes<float, float>(ps, 1, pl, s);
+        else if (share) launch_passes<bf16, float>(ps, 1, pl, s);
+        else launch_passes<bf16, bf16>(ps, 1, pl, s);
     };
     auto join = [&](void* out, int64_t o_t, int64_t o_g, int D) {
-        if (R == 1) return;
         const int64_t items = T * d.ngroups * D;
         const dim3 grid((unsigned)(items < (1 << 28) ? cdiv(items, 256) : 1 << 20));
         if (half) linattn_heads_sum<bf16><<<grid, 256, 0, s>>>(shares, (bf16*)out, items, D, d.ngroups, R, o_t, o_g);
         else linattn_heads_sum<float><<<grid, 256, 0, s>>>(shares, (float*)out, items, D, d.ngroups, R, o_t, o_g);
     };
-    if (T > 0) {
-        p.q = v, p.q_t = l.v_token, p.q_h = l.v_group, p.qdiv = R;
-        p.k = dy, p.k_t = l.dy_token, p.k_h = l.dy_head, p.kdiv = 1;
-        p.v = q, p.v_t = l.q_token, p.v_h = l.q_head, p.vdiv = 1;
-        p.o = R == 1 ? dk : shares;
-        p.o_t = R == 1 ? l.dk_token : (int64_t)d.nheads * d.keydim;
-        p.o_h = R == 1 ? l.dk_group : d.keydim;
-        p.K = d.valuedim, p.V = d.keydim, p.s_k = 1, p.s_v = d.valuedim;
-        p.final = nullptr;
-        run(b.dk);
+    // dv last: dinit may be d_final's buffer, which the pass for dk reads
+    if (T > 0 && R == 1) {
+        LinPasses ps = {{q_, k_}};
+        if (half) launch_passes<bf16, bf16>(ps, 2, b.qk, s);
+        else launch_passes<float, float>(ps, 2, b.qk, s);
+    } else if (T > 0) {
+        run(q_, false, b.qk);
+        run(k_, true, b.qk);
         join(dk, l.dk_token, l.dk_group, d.keydim);
     }
-    if (T > 0 || dinit_state) {
-        p.q = k, p.q_t = l.k_token, p.q_h = l.k_group, p.qdiv = R;
-        p.k = q, p.k_t = l.q_token, p.k_h = l.q_head, p.kdiv = 1;
-        p.v = dy, p.v_t = l.dy_token, p.v_h = l.dy_head, p.vdiv = 1;
-        p.o = R == 1 ? dv : shares;
-        p.o_t = R == 1 ? l.dv_token : (int64_t)d.nheads * d.valuedim;
-        p.o_h = R == 1 ? l.dv_group : d.valuedim;
-        p.K = d.keydim, p.V = d.valuedim, p.s_k = d.valuedim, p.s_v = 1;
-        p.final = dinit_state;
-        run(b.dv);
-        if (T > 0) join(dv, l.dv_token, l.dv_group, d.valuedim);
-    }
+    if (T > 0 || dinit_state) run(v_, R > 1, b.v);
+    if (T > 0 && R > 1) join(dv, l.dv_token, l.dv_group, d.valuedim);
     return launched();
 }
 
