@@ -14,10 +14,11 @@
 // undecayed) and dinit = l R_0: one kernel serves all four (LinPass::init_pow, final_pow).
 //
 // (C = 32.)  A workgroup walks the chunks of one span of a sequence for one head and VT columns of V,
-// the state in registers: each of its four waves holds all K rows of VT / 4 columns, so no
-// product needs a sum across waves, and what a wave reads from LDS meets all its columns.  Where sequences x heads do not fill the chip a
+// the state in registers: each of its NW waves holds all K rows of its 16 CB columns, so no
+// product needs a sum across waves.  Where sequences x heads do not fill the chip a
 // sequence is cut into spans: their states are formed first (STATE), joined along the
 // sequence (linattn_join) and then every span is walked from its own incoming state.
+#include <stdlib.h>
 #include <type_traits>
 
 #include "ssd_layer.h"
@@ -125,34 +126,37 @@ struct Tile {
     }
 };
 
-// Columns of a wave's 16 CB in the order of its result tiles: with two tiles a lane's 4 rows of
-// each are 8 neighbours in memory.
-template <int CB>
-__device__ __forceinline__ int tile_col(int cb, int m) {
-    return CB == 2 ? 8 * (m >> 2) + 4 * cb + (m & 3) : m;
+// Rows and columns of two result tiles side by side are dealt out so that a lane's 4 entries of
+// each are 8 neighbours in memory: entry m of tile `half` is 8 (m / 4) + 4 half + m % 4 of 32.
+template <int TILES>
+__device__ __forceinline__ int dealt(int half, int m) {
+    return TILES == 2 ? 8 * (m >> 2) + 4 * half + (m & 3) : m;
 }
 
-// MFMA operands over 32 entries of a contraction, in the order in which a pair of result
-// tiles holds them: a lane of group g has entries 4g..4g+3 and 16+4g..16+4g+3.  Multiples of
-// 16 rows and columns move an address by a constant: + r0 ROW, ^ c0 sizeof(T).
+// MFMA operands.  Over 32 keys a lane of group g has keys 8g..8g+7, over 32 tokens tokens
+// 4g..4g+3 and 16+4g..16+4g+3: the orders in which a pair of result tiles holds them (the
+// state's with its keys dealt out, the scores' as they come).  Multiples of 16 rows and columns
+// move an address by a constant: + r0 ROW, ^ c0 sizeof(T).
 template <typename T, int COLS>
 __device__ __forceinline__ int row_base(int lane) {
-    return Tile<T, COLS>::at(lane & 15, 4 * (lane >> 4));
+    return Tile<T, COLS>::at(lane & 15, 8 * (lane >> 4));
 }
 // tile[r0 + l16][c0 ..]
-template <typename T, int COLS>
-__device__ __forceinline__ typename Vec<T>::x8 row_frag(const char* t, int base, int r0, int c0) {
-    using X4 = typename Vec<T>::x4;
-    constexpr int E = sizeof(T);
-    return cat<typename Vec<T>::x8, X4>(*(const X4*)(t + (base ^ c0 * E) + r0 * Tile<T, COLS>::ROW),
-                                        *(const X4*)(t + (base ^ (c0 + 16) * E) + r0 * Tile<T, COLS>::ROW));
+template <int COLS>
+__device__ __forceinline__ bf16x8 row_frag(const bf16*, const char* t, int base, int r0, int c0) {
+    return *(const bf16x8*)(t + (base ^ c0 * 2) + r0 * Tile<bf16, COLS>::ROW);
 }
-// tile[0 ..][c0 + the lane's column]: column m = l16 of result tile cb of CB
-template <typename T, int COLS, int CB>
+template <int COLS>
+__device__ __forceinline__ f32x8 row_frag(const float*, const char* t, int base, int r0, int c0) {
+    return cat<f32x8, f32x4>(*(const f32x4*)(t + (base ^ c0 * 4) + r0 * Tile<float, COLS>::ROW),
+                             *(const f32x4*)(t + (base ^ c0 * 4 ^ 16) + r0 * Tile<float, COLS>::ROW));
+}
+// tile[0 ..][c0 + the lane's column], the first of TILES side by side; ^ 4 sizeof(T) is the second
+template <typename T, int COLS, int TILES>
 __device__ __forceinline__ int col_base(int lane) {
     const int j = lane & 15, r = 4 * (lane >> 4);
-    if (sizeof(T) == 2) return Tile<T, COLS>::at(r + (j >> 2), tile_col<CB>(0, 4 * (j & 3)));
-    return Tile<T, COLS>::at(r, tile_col<CB>(0, j));
+    if (sizeof(T) == 2) return Tile<T, COLS>::at(r + (j >> 2), dealt<TILES>(0, 4 * (j & 3)));
+    return Tile<T, COLS>::at(r, dealt<TILES>(0, j));
 }
 template <int COLS>
 __device__ __forceinline__ bf16x8 col_frag(const bf16*, const char* t, int base, int c0) {
@@ -209,14 +213,14 @@ struct Rows {
 
 // N neighbours of a row at byte offset `off`, of which `left` lie in the row: with whole units
 // all or none.
-template <typename OT, int N, bool RAGGED>
+template <typename OT, int N, bool SINGLY>
 __device__ __forceinline__ void store_run(const Rows& b, uint32_t off, int left, const float (&x)[N]) {
     typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
     typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
     OT o[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) o[j] = (OT)x[j];
-    if constexpr (!RAGGED) {
+    if constexpr (!SINGLY) {
         if (left < N) off = kNowhere;
         if constexpr (sizeof(o) == 8) {
             __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, o), b.r, off, 0, 0);
@@ -241,42 +245,75 @@ __device__ __forceinline__ void store_run(const Rows& b, uint32_t off, int left,
 }
 
 // Waves a SIMD that the kernel is compiled for: two workgroups a CU.
-constexpr int lin_waves(int KD, int size) { return KD * size > 512 ? 1 : 2; }
+constexpr int lin_waves(int KD, int VT, int NW, int size) {
+    return (4 * (KD * 2 + VT) * C * size > 160 * 1024 ? 1 : 2) * NW / 4;
+}
 
 template <typename T> constexpr int kParts = sizeof(T) == 2 ? 3 : 1;
 
-// Fills a tile with the chunk's rows: row r is the chunk's r-th token in processing order (with
-// `back`, memory row have - 1 - r); rows past `have` are zeros, or values of the chunk where
-// its rows lie closer than they are wide, and columns past `cols` zeros.  Each of four waves
-// issues every fourth load of 64 units straight into LDS, nothing passes through registers and
-// nothing is waited for.  RAGGED (rows of no whole units): element by element, waiting.
-template <typename T, int COLS, bool RAGGED>
-__device__ __forceinline__ void fill(char* tile, const void* low, uint32_t step, int have, int cols, bool back) {
+// 16 bytes of each lane, to 1 KB of LDS from `to` on.
+__device__ __forceinline__ void load_unit(const Rows& b, char* to, uint32_t off) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(b.r, (__attribute__((address_space(3))) void*)to, 16, off, 0, 0, 0);
+}
+
+// What a kernel is built for: FULL, K is KD and rows are whole units; PADDED, K is less, and
+// products over nothing but padding are skipped; RAGGED, rows need not be whole units either.
+enum { FULL, PADDED, RAGGED };
+
+// The chunks of one per-token tensor on their way into LDS tiles.  Row r of a tile is the
+// chunk's r-th token in processing order (with `back` the chunks lie in memory from the last
+// to the first, and so do their rows); rows past the chunk's end are zeros, or values of the
+// chunk where its rows lie closer than they are wide, and columns past `cols` zeros.  Each of
+// NW waves issues every NW-th load of 64 units straight into LDS: nothing passes through
+// registers and nothing is waited for.  RAGGED: element by element, waiting.
+template <typename T, int COLS, int NW, int MODE>
+struct Stream {
     using L = Tile<T, COLS>;
-    const int lane = threadIdx.x & 63, wave = wave_id();
-    const Rows b(low, step, have, cols * (uint32_t)sizeof(T));
+    static constexpr int LOADS = C * L::UPR / 64, N = (LOADS + NW - 1) / NW;
+    const char* low;   // lowest row of the next chunk, were it full
+    uint32_t step, width, off[N];
+    int32_t cols;
+    bool back;
+    // `first`: the first token's row
+    __device__ __forceinline__ Stream(const T* first, int64_t stride, int cols_, bool back_)
+        : step((uint32_t)stride * (uint32_t)sizeof(T)), width(cols_ * (uint32_t)sizeof(T)), cols(cols_), back(back_) {
+        low = (const char*)first - (back ? (int64_t)(C - 1) * step : 0);
 #pragma unroll
-    for (int i = 0; i < C * L::UPR / 256; ++i) {
-        const int place = (i * 4 + wave) * 64 + lane, r = place / L::UPR, c = (place % L::UPR ^ L::swap(r)) * L::EPU;
-        const uint32_t off = (uint32_t)(back ? have - 1 - r : r) * step + (uint32_t)(c * sizeof(T));
-        if constexpr (!RAGGED) {
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                b.r, (__attribute__((address_space(3))) void*)(tile + (i * 4 + wave) * 1024), 16,
-                c < cols ? off : kNowhere, 0, 0, 0);
-        } else {
-            T u[L::EPU];
-#pragma unroll
-            for (int j = 0; j < L::EPU; ++j) {
-                const uint32_t at = c + j < cols ? off + j * (uint32_t)sizeof(T) : kNowhere;
-                if constexpr (sizeof(T) == 2)
-                    u[j] = __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(b.r, at, 0, 0));
-                else
-                    u[j] = __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(b.r, at, 0, 0));
-            }
-            __builtin_memcpy(__builtin_assume_aligned(tile + place * 16, 16), u, 16);
+        for (int i = 0; i < N; ++i) {
+            const int place = (i * NW + wave_id()) * 64 + (threadIdx.x & 63), r = place / L::UPR;
+            const int c = (place % L::UPR ^ L::swap(r)) * L::EPU;
+            off[i] = (uint32_t)(back ? C - 1 - r : r) * step + (uint32_t)(c * sizeof(T));
+            if (MODE != RAGGED && c >= cols) off[i] = kNowhere;
         }
     }
-}
+    // the next chunk, of `have` tokens
+    __device__ __forceinline__ void fill(char* tile, int have) {
+        const uint32_t gap = back ? (uint32_t)(C - have) * step : 0;  // kNowhere - gap stays past the rows
+        const Rows b(low + gap, step, have, width);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int load = i * NW + wave_id();
+            if (LOADS % NW && load >= LOADS) break;
+            if constexpr (MODE != RAGGED) {
+                load_unit(b, tile + load * 1024, off[i] - gap);
+            } else {
+                const int place = load * 64 + (threadIdx.x & 63);
+                const int c = (place % L::UPR ^ L::swap(place / L::UPR)) * L::EPU;
+                T u[L::EPU];
+#pragma unroll
+                for (int j = 0; j < L::EPU; ++j) {
+                    const uint32_t at = c + j < cols ? off[i] - gap + j * (uint32_t)sizeof(T) : kNowhere;
+                    if constexpr (sizeof(T) == 2)
+                        u[j] = __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(b.r, at, 0, 0));
+                    else
+                        u[j] = __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(b.r, at, 0, 0));
+                }
+                __builtin_memcpy(__builtin_assume_aligned(tile + place * 16, 16), u, 16);
+            }
+        }
+        low += back ? -(int64_t)C * step : (int64_t)C * step;
+    }
+};
 
 // The chunk being worked on and the next one.
 template <typename T, int KD, int VT, bool STATE>
@@ -286,6 +323,7 @@ struct __attribute__((aligned(1024))) Shared {
     char v[2][C * Tile<T, VT>::ROW];
     double pc;        // l^C
     float pw[C + 4];  // l^n
+    float w[2][C];    // the tokens' weights in the state behind their chunk; behind the last
 };
 
 // Workgroups that read the same rows (the V tiles of a head, the heads of a group) follow each
@@ -298,12 +336,12 @@ __device__ __forceinline__ uint32_t same_xcd(uint32_t id, uint32_t together, uin
 }
 
 // One span (or, STATE, only its state).  OT: the output's type.
-template <typename T, typename OT, int KD, int VT, bool RAGGED, bool STATE>
-__global__ __launch_bounds__(256, lin_waves(KD, sizeof(T))) void linattn_kernel(LinPasses ps) {
+template <typename T, typename OT, int KD, int VT, int NW, int MODE, bool STATE>
+__global__ __launch_bounds__(NW * 64, lin_waves(KD, VT, NW, sizeof(T))) void linattn_kernel(LinPasses ps) {
     const LinPass& p = ps.p[blockIdx.y];
     touch_args(p);
     using X8 = typename Vec<T>::x8;
-    constexpr int CB = VT / 64, KB = KD / 16, KS = KD / 32, KR = Tile<T, KD>::ROW;
+    constexpr int NT = NW * 64, CB = VT / (16 * NW), KB = KD / 16, KS = KD / 32;
     __shared__ Shared<T, KD, VT, STATE> sh;
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), l16 = lane & 15, g = lane >> 4;
     uint32_t id = same_xcd(blockIdx.x, p.together, gridDim.x);
@@ -322,30 +360,24 @@ __global__ __launch_bounds__(256, lin_waves(KD, sizeof(T))) void linattn_kernel(
 
     if (!STATE && n == 0) {  // an empty sequence hands on what came in
         if (p.final)
-            for (int i = tid; i < p.K * vcols; i += 256) {
+            for (int i = tid; i < p.K * vcols; i += NT) {
                 const int64_t e = block + (int64_t)(i / vcols) * p.s_k + (int64_t)(v0 + i % vcols) * p.s_v;
                 p.final[e] = p.init ? p.init[e] : 0.f;
             }
         return;
     }
 
-    // chunk pointers: the rows of the span's first token in processing order
     const bool back = p.reverse != 0;
     const int64_t tok0 = back ? sp.first + sp.len - 1 - sp.t0 : sp.first + sp.t0;
-    const T* qp = (const T*)p.q + tok0 * p.q_t + (h / p.qdiv) * p.q_h;
-    const T* kp = (const T*)p.k + tok0 * p.k_t + (h / p.kdiv) * p.k_h;
-    const T* vp = (const T*)p.v + tok0 * p.v_t + (h / p.vdiv) * p.v_h + v0;
-    OT* op = (OT*)p.o + tok0 * p.o_t + h * p.o_h + v0;
-    const uint32_t qs = (uint32_t)p.q_t * (uint32_t)sizeof(T), ks = (uint32_t)p.k_t * (uint32_t)sizeof(T);
-    const uint32_t vs = (uint32_t)p.v_t * (uint32_t)sizeof(T), os = (uint32_t)p.o_t * (uint32_t)sizeof(OT);
-    auto fetch = [&](int64_t t, int to) {  // the chunk at t of the span
-        const int have = (int)imin(C, n - t);
-        const int64_t low = back ? -(t + have - 1) : t;
-        if constexpr (!STATE) fill<T, KD, RAGGED>(sh.q[to], qp + low * p.q_t, qs, have, p.K, back);
-        fill<T, KD, RAGGED>(sh.k[to], kp + low * p.k_t, ks, have, p.K, back);
-        fill<T, VT, RAGGED>(sh.v[to], vp + low * p.v_t, vs, have, vcols, back);
+    Stream<T, KD, NW, MODE> ks((const T*)p.k + tok0 * p.k_t + (h / p.kdiv) * p.k_h, p.k_t, p.K, back);
+    Stream<T, KD, NW, MODE> qs((const T*)p.q + tok0 * p.q_t + (h / p.qdiv) * p.q_h, p.q_t, p.K, back);
+    Stream<T, VT, NW, MODE> vs((const T*)p.v + tok0 * p.v_t + (h / p.vdiv) * p.v_h + v0, p.v_t, vcols, back);
+    auto fetch = [&](int have, int to) {
+        if constexpr (!STATE) qs.fill(sh.q[to], have);
+        ks.fill(sh.k[to], have);
+        vs.fill(sh.v[to], have);
     };
-    fetch(0, 0);
+    fetch((int)imin(C, n), 0);
 
     // One exponential a thread: l^0 .. l^C.
     if (tid <= C) {
@@ -364,11 +396,12 @@ __global__ __launch_bounds__(256, lin_waves(KD, sizeof(T))) void linattn_kernel(
     uint32_t s0[CB];
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) {
-        const int vc = c0 + tile_col<CB>(cb, l16);
-        s0[cb] = vc < vcols ? (uint32_t)(4 * g * p.s_k + (v0 + vc) * p.s_v) * 4 : kNowhere;
+        const int vc = c0 + dealt<CB>(cb, l16);
+        s0[cb] = vc < vcols ? (uint32_t)(8 * g * p.s_k + (v0 + vc) * p.s_v) * 4 : kNowhere;
     }
     auto entry = [&](int kb, int cb, int r) {
-        return 16 * kb + 4 * g + r < p.K ? s0[cb] + (uint32_t)((16 * kb + r) * p.s_k * 4) : kNowhere;
+        const int k = 32 * (kb / 2) + 4 * (kb % 2) + r;  // and 8 g
+        return 8 * g + k < p.K ? s0[cb] + (uint32_t)(k * p.s_k * 4) : kNowhere;
     };
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb)
@@ -388,44 +421,61 @@ __global__ __launch_bounds__(256, lin_waves(KD, sizeof(T))) void linattn_kernel(
     vm_wait<0>();
     block_sync();
     Rate rate(sh.pc);
-    // weights: of the tokens in the state behind a chunk (w), of a score (tw: within a block of
-    // 16 tokens, of rows 16-31 with columns 0-15), of the state in row 16 ib + l16 (pwi)
-    f32x8 w;
+    // weights of a score: within a block of 16 tokens, and of rows 16-31 with columns 0-15
     f32x4 tw[2];
-    float pwi[2];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        w[r] = p.in_scale * sh.pw[C - 4 * g - r];
-        w[4 + r] = p.in_scale * sh.pw[C - 16 - 4 * g - r];
         const int d = l16 - 4 * g - r;
         const float x = p.in_scale * sh.pw[max(d, 0)];
         tw[0][r] = d >= 0 ? x : 0.f;
         tw[1][r] = p.in_scale * sh.pw[16 + d];
     }
-    pwi[0] = sh.pw[l16];
-    pwi[1] = sh.pw[16 + l16];
-    if (!STATE && !split && p.init_pow) {
-        const float f = sh.pw[1];
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-            for (int cb = 0; cb < CB; ++cb) st[kb][cb] *= f;
+    // the sequence's last chunk, of `tail` tokens, is followed by no decay, or by final_pow
+    const int tail = (int)((n - 1) % C) + 1, top = tail - 1 + p.final_pow;
+    if (tid < C) {
+        sh.w[0][tid] = p.in_scale * sh.pw[C - tid];
+        sh.w[1][tid] = tid < tail ? p.in_scale * sh.pw[max(top - tid, 0)] : 0.f;
     }
+    const float closing = sh.pw[top], out_scale = p.out_scale;
+    block_sync();
+    // The state is st * held: a chunk's factor goes into `held`, and into the entries only once
+    // that has left [1/256, 256] (every sixth chunk at l = 31/32).
+    float held = !STATE && !split && p.init_pow ? sh.pw[1] : 1.f;
 
-    const int rb = row_base<T, KD>(lane), kc = col_base<T, KD, 1>(lane), vb = col_base<T, VT, CB>(lane);
-    int buf = 0;
-    for (int64_t t = 0; t < n; t += C, buf ^= 1) {
-        const int cl = (int)imin(C, n - t);
-        const bool end = t + C >= n;          // of the span
-        const bool close = last && end;       // of the sequence
-        if (!end) fetch(t + C, buf ^ 1);
+    const int rb = row_base<T, KD>(lane), kc = col_base<T, KD, 2>(lane), vb = col_base<T, VT, CB>(lane);
+    // outputs: this lane's 4 CB columns of tokens l16 and 16 + l16
+    const uint32_t os = (uint32_t)p.o_t * (uint32_t)sizeof(OT);
+    const int oc = c0 + dealt<CB>(0, 4 * g);
+    const char* op = (const char*)((OT*)p.o + tok0 * p.o_t + h * p.o_h + v0) - (back ? (int64_t)(C - 1) * os : 0);
+    const uint32_t ooff = (uint32_t)(back ? C - 1 - l16 : l16) * os + (uint32_t)(oc * sizeof(OT));
+    const uint32_t onext = back ? 0u - 16 * os : 16 * os, owidth = vcols * (uint32_t)sizeof(OT);
+    const int keys = p.K;
+    const bool final = p.final != nullptr;
+    int64_t left = n;
+    for (int buf = 0; left > 0; left -= C, buf ^= 1) {
+        const int cl = (int)imin(C, left);
+        const bool end = left <= C, close = last && end;  // of the span, of the sequence
+        if (!end) fetch((int)imin(C, left - C), buf ^ 1);
         const char* const tq = sh.q[STATE ? 0 : buf];
         const char* const tk = sh.k[buf];
         const char* const tv = sh.v[buf];
+        const float come_in = held, now = held * (close ? closing : rate.next());
+        const bool drop = !(now >= 0.00390625f && now <= 256.f);
+        held = drop ? 1.f : now;
+        // v, plain and weighted for the state behind the chunk
+        X8 vf[CB], vw[CB][kParts<T>];
+        {
+            const float* const wt = sh.w[close ? 1 : 0] + 4 * g;
+            const f32x8 w = cat<f32x8, f32x4>(*(const f32x4*)wt, *(const f32x4*)(wt + 16)) * (1.f / held);
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb) {
+                vf[cb] = col_frag<VT>((const T*)nullptr, tv, vb ^ cb * 4 * (int)sizeof(T), c0);
+                weigh(vf[cb], w, vw[cb]);
+            }
+        }
         // Results are transposed: a lane has 4 columns of token 16 ib + l16, and of the scores 4
         // tokens j of one row i, which is the order in which they meet the values.
         f32x4 acc[2][CB];
-        X8 sc[2];
         if constexpr (!STATE) {
             f32x4 s00 = {0.f, 0.f, 0.f, 0.f}, s01 = s00, s11 = s00;
 #pragma unroll
@@ -434,9 +484,11 @@ __global__ __launch_bounds__(256, lin_waves(KD, sizeof(T))) void linattn_kernel(
                 for (int cb = 0; cb < CB; ++cb) acc[ib][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
-                if (kk && 32 * kk >= p.K) break;  // K is padded to KD: nothing but zeros from here
-                const X8 q0 = row_frag<T, KD>(tq, rb, 0, 32 * kk), q1 = row_frag<T, KD>(tq, rb, 16, 32 * kk);
-                const X8 k0 = row_frag<T, KD>(tk, rb, 0, 32 * kk), k1 = row_frag<T, KD>(tk, rb, 16, 32 * kk);
+                if (MODE != FULL && kk && 32 * kk >= keys) break;
+                const X8 q0 = row_frag<KD>((const T*)nullptr, tq, rb, 0, 32 * kk);
+                const X8 q1 = row_frag<KD>((const T*)nullptr, tq, rb, 16, 32 * kk);
+                const X8 k0 = row_frag<KD>((const T*)nullptr, tk, rb, 0, 32 * kk);
+                const X8 k1 = row_frag<KD>((const T*)nullptr, tk, rb, 16, 32 * kk);
                 s00 = mma(k0, q0, s00);
                 s01 = mma(k0, q1, s01);
                 s11 = mma(k1, q1, s11);
@@ -452,12 +504,9 @@ __global__ __launch_bounds__(256, lin_waves(KD, sizeof(T))) void linattn_kernel(
                     acc[1][cb] = mma(e, q1, acc[1][cb]);
                 }
             }
-#pragma unroll
-            for (int cb = 0; cb < CB; ++cb) {
-                acc[0][cb] *= pwi[0];
-                acc[1][cb] *= pwi[1];
-            }
+            const float f0 = come_in * sh.pw[l16], f1 = come_in * sh.pw[16 + l16];
             // above the diagonal a weight of 0 is not enough: a score there may be infinite
+            X8 sc[2];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const bool in = l16 >= 4 * g + r;
@@ -466,55 +515,38 @@ __global__ __launch_bounds__(256, lin_waves(KD, sizeof(T))) void linattn_kernel(
                 sc[1][r] = (T)(s01[r] * tw[1][r]);
                 sc[1][4 + r] = in ? (T)(s11[r] * tw[0][r]) : (T)0.f;
             }
-        }
-        // the chunk's values: scores times v, and the state behind the chunk
-        const bool update = STATE || !close || p.final;
-        X8 vf[CB];
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb) {
-            vf[cb] = col_frag<VT>((const T*)nullptr, tv, vb ^ cb * 4 * (int)sizeof(T), c0);
-            if constexpr (!STATE) {
-                acc[0][cb] = mma(vf[cb], sc[0], acc[0][cb]);
-                acc[1][cb] = mma(vf[cb], sc[1], acc[1][cb]);
+            for (int cb = 0; cb < CB; ++cb) {
+                acc[0][cb] = mma(vf[cb], sc[0], acc[0][cb] * f0);
+                acc[1][cb] = mma(vf[cb], sc[1], acc[1][cb] * f1);
             }
         }
-        if (update) {
-            float f = rate.next();
-            if (close) {
-                const int top = cl - 1 + p.final_pow;
-                f = sh.pw[top];
+        if (drop) {
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    const int j = (r & 4) * 4 + 4 * g + (r & 3);
-                    w[r] = j < cl ? p.in_scale * sh.pw[max(top - j, 0)] : 0.f;
-                }
-            }
-            X8 vw[CB][kParts<T>];
+            for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-            for (int cb = 0; cb < CB; ++cb) weigh(vf[cb], w, vw[cb]);
+                for (int cb = 0; cb < CB; ++cb) st[kb][cb] *= now;
+        }
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                if (kb && 16 * kb >= p.K) break;
-                const X8 a = col_frag<KD>((const T*)nullptr, tk, kc, 16 * kb);
+        for (int kb = 0; kb < KB; ++kb) {
+            if (MODE != FULL && kb >= 2 && 32 * (kb / 2) >= keys) break;
+            const X8 a = col_frag<KD>((const T*)nullptr, tk, kc ^ kb % 2 * 4 * (int)sizeof(T), 32 * (kb / 2));
 #pragma unroll
-                for (int cb = 0; cb < CB; ++cb) {
-                    st[kb][cb] *= f;
-                    st[kb][cb] = mma_weighted(a, vw[cb], st[kb][cb]);
-                }
-            }
+            for (int cb = 0; cb < CB; ++cb) st[kb][cb] = mma_weighted(a, vw[cb], st[kb][cb]);
         }
         // The next chunk's loads are waited for ahead of this one's stores, which need not be.
         if (!end) vm_wait<0>();
         if constexpr (!STATE) {
-            const Rows ob(op + (back ? -(t + cl - 1) : t) * p.o_t, os, cl, vcols * (uint32_t)sizeof(OT));
+            const uint32_t gap = back ? (uint32_t)(C - cl) * os : 0;
+            const Rows ob(op + gap, os, cl, owidth);
+            op += back ? -(int64_t)C * os : (int64_t)C * os;
 #pragma unroll
             for (int ib = 0; ib < 2; ++ib) {
-                const int i = 16 * ib + l16, c = c0 + tile_col<CB>(0, 4 * g);
-                const uint32_t off = (uint32_t)(back ? cl - 1 - i : i) * os + (uint32_t)(c * sizeof(OT));
                 float x[4 * CB];
 #pragma unroll
-                for (int j = 0; j < 4 * CB; ++j) x[j] = p.out_scale * acc[ib][j / 4][j % 4];
-                store_run<OT, 4 * CB, RAGGED>(ob, off, i < cl ? vcols - c : 0, x);
+                for (int j = 0; j < 4 * CB; ++j) x[j] = out_scale * acc[ib][j / 4][j % 4];
+                store_run<OT, 4 * CB, MODE == RAGGED>(ob, ooff + ib * onext - gap,
+                                                      16 * ib + l16 < cl ? vcols - oc : 0, x);
             }
         }
         block_sync();
@@ -522,17 +554,17 @@ __global__ __launch_bounds__(256, lin_waves(KD, sizeof(T))) void linattn_kernel(
 
     const Rows fb(last && p.final ? (const void*)(p.final + block) : (const void*)p.decay, 0, 1,
                   last && p.final ? (uint32_t)(p.K * p.V) * 4 : 0);
-    if (STATE || (last && p.final))
+    if (STATE || (last && final))
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
             for (int cb = 0; cb < CB; ++cb) {
                 if (STATE) {
-                    *(f32x4*)(mine + (cb * KB + kb) * 256) = st[kb][cb];
+                    *(f32x4*)(mine + (cb * KB + kb) * 256) = st[kb][cb] * held;
                 } else {
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(st[kb][cb][r]), fb.r,
+                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(st[kb][cb][r] * held), fb.r,
                                                               entry(kb, cb, r), 0, 0);
                 }
             }
@@ -540,7 +572,7 @@ __global__ __launch_bounds__(256, lin_waves(KD, sizeof(T))) void linattn_kernel(
 
 // Joins the span states of every sequence: slot s gets the state that enters span s.
 // A thread takes 4 entries (one lane's part of a result tile).
-__global__ __launch_bounds__(256) void linattn_join(LinPasses ps, int KD, int VT) {
+__global__ __launch_bounds__(256) void linattn_join(LinPasses ps, int KD, int VT, int CB) {
     const LinPass& p = ps.p[blockIdx.z];
     touch_args(p);
     uint32_t id = blockIdx.x;
@@ -552,9 +584,9 @@ __global__ __launch_bounds__(256) void linattn_join(LinPasses ps, int KD, int VT
     const int64_t spans = cdiv(sp.len, p.span);
     const int e = blockIdx.y * 256 + threadIdx.x, lane = e & 63, tile = e >> 6;
     const int kb = tile % (KD / 16), vb = tile / (KD / 16);
-    const int kr = 16 * kb + 4 * (lane >> 4);
-    const int vc = vt * VT + (VT == 64 ? 16 * vb + (lane & 15)
-                                       : vb / 2 * 32 + tile_col<2>(vb % 2, lane & 15));
+    const int kr = 32 * (kb / 2) + 4 * (kb % 2) + 8 * (lane >> 4);
+    const int vc = vt * VT + (CB == 1 ? 16 * vb + (lane & 15)
+                                       : vb / 2 * 32 + dealt<2>(vb % 2, lane & 15));
     float* at = p.spans + (((int64_t)slot0 * p.H + h) * p.vtiles + vt) * (KD * VT) + e * 4;
     const int64_t step = (int64_t)p.H * p.vtiles * (KD * VT);
     constexpr int UN = 16;  // spans in flight
@@ -608,10 +640,10 @@ struct LinTiles {
 };
 // K is padded to 64, 128 or 256.  The state of a workgroup's columns is KD x VT / 256
 // registers a thread: 64 at most.
-LinTiles lin_tiles(int K, int V) {
+LinTiles lin_tiles(int K, int V, int32_t dtype) {
     LinTiles t;
     t.KD = K <= 64 ? 64 : (K <= 128 ? 128 : 256);
-    t.VT = V <= 64 || t.KD == 256 ? 64 : 128;
+    t.VT = V <= 64 || (t.KD == 256 && dtype == SSD_F32) || getenv("VT64") ? 64 : 128;
     return t;
 }
 
@@ -626,7 +658,7 @@ struct LinPlan {
 
 LinPlan lin_plan(const ssd_linattn_dims& d, int K, int V, int passes = 1) {
     LinPlan pl;
-    pl.t = lin_tiles(K, V);
+    pl.t = lin_tiles(K, V, d.dtype);
     pl.vtiles = (int)cdiv(V, pl.t.VT);
     const int64_t S = d.nseq > 0 ? d.nseq : d.batch, T = (int64_t)d.batch * d.seqlen;
     const int64_t wgs = S * d.nheads * pl.vtiles * passes;
@@ -634,7 +666,7 @@ LinPlan lin_plan(const ssd_linattn_dims& d, int K, int V, int passes = 1) {
     const int64_t want = d.nseq > 0 ? cdiv(kFill, (int64_t)d.nheads * pl.vtiles * passes) : cdiv(kFill, wgs);
     const int64_t tokens = d.nseq > 0 ? T : d.seqlen;
     pl.span = cdiv(cdiv(tokens, want), C) * C;
-    if (pl.span < 2 * C) pl.span = 2 * C;
+    { int ms = getenv("MINSPAN") ? atoi(getenv("MINSPAN")) : 2; if (pl.span < ms * C) pl.span = ms * C; }
     if (pl.span >= tokens) {
         pl.span = (int64_t)1 << 40;  // whole sequences
         pl.per = 1;
@@ -648,22 +680,23 @@ LinPlan lin_plan(const ssd_linattn_dims& d, int K, int V, int passes = 1) {
     return pl;
 }
 
-template <typename T, typename OT, int KD, int VT, bool RAGGED>
+template <typename T, typename OT, int KD, int VT, int NW, int MODE>
 void launch_tiles(const LinPasses& ps, int passes, const LinPlan& pl, hipStream_t s) {
     const LinPass& p = ps.p[0];
     const dim3 grid((unsigned)((int64_t)pl.slots * p.H * pl.vtiles), passes);
     if (pl.bytes) {
-        linattn_kernel<T, OT, KD, VT, RAGGED, true><<<grid, 256, 0, s>>>(ps);
+        linattn_kernel<T, OT, KD, VT, NW, MODE, true><<<grid, NW * 64, 0, s>>>(ps);
         const dim3 joins((unsigned)((int64_t)p.S * p.H * pl.vtiles), KD * VT / 1024, passes);
-        linattn_join<<<joins, 256, 0, s>>>(ps, KD, VT);
+        linattn_join<<<joins, 256, 0, s>>>(ps, KD, VT, VT / (16 * NW));
     }
-    linattn_kernel<T, OT, KD, VT, RAGGED, false><<<grid, 256, 0, s>>>(ps);
+    linattn_kernel<T, OT, KD, VT, NW, MODE, false><<<grid, NW * 64, 0, s>>>(ps);
 }
-template <typename T, typename OT, int KD, int VT>
+template <typename T, typename OT, int KD, int VT, int NW>
 void launch_tiles(const LinPasses& ps, int passes, const LinPlan& pl, hipStream_t s) {
     constexpr int EPU = 16 / sizeof(T);
-    if (ps.p[0].K % EPU || ps.p[0].V % EPU) launch_tiles<T, OT, KD, VT, true>(ps, passes, pl, s);
-    else launch_tiles<T, OT, KD, VT, false>(ps, passes, pl, s);
+    if (ps.p[0].K % EPU || ps.p[0].V % EPU) launch_tiles<T, OT, KD, VT, NW, RAGGED>(ps, passes, pl, s);
+    else if (ps.p[0].K < KD) launch_tiles<T, OT, KD, VT, NW, PADDED>(ps, passes, pl, s);
+    else launch_tiles<T, OT, KD, VT, NW, FULL>(ps, passes, pl, s);
 }
 // Passes of one plan, side by side in each launch: their span states lie behind each other in
 // the workspace (pl.bytes each).
@@ -678,14 +711,18 @@ void launch_passes(LinPasses& ps, int passes, const LinPlan& pl, hipStream_t s) 
         p.together = pl.vtiles * (p.qdiv > p.kdiv ? p.qdiv : p.kdiv);
         p.spans = (float*)((char*)p.spans + i * pl.bytes);
     }
+    static int nw = getenv("NW") ? atoi(getenv("NW")) : 4;
+#define LIN(KD) \
+        if (pl.t.VT == 64 || KD * sizeof(T) > 512) launch_tiles<T, OT, KD, 64, 4>(ps, passes, pl, s); \
+        else if constexpr (KD * sizeof(T) > 512) return; \
+        else if (nw == 8) launch_tiles<T, OT, KD, 128, 8>(ps, passes, pl, s); \
+        else launch_tiles<T, OT, KD, 128, 4>(ps, passes, pl, s)
     if (pl.t.KD == 64) {
-        if (pl.t.VT == 64) launch_tiles<T, OT, 64, 64>(ps, passes, pl, s);
-        else launch_tiles<T, OT, 64, 128>(ps, passes, pl, s);
+        LIN(64);
     } else if (pl.t.KD == 128) {
-        if (pl.t.VT == 64) launch_tiles<T, OT, 128, 64>(ps, passes, pl, s);
-        else launch_tiles<T, OT, 128, 128>(ps, passes, pl, s);
+        LIN(128);
     } else {
-        launch_tiles<T, OT, 256, 64>(ps, passes, pl, s);
+        LIN(256);
     }
 }
 
