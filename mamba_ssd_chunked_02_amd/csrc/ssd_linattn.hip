@@ -204,11 +204,18 @@ __device__ __forceinline__ void weigh(const f32x8& v, const f32x8& w, f32x8 (&o)
 // which kNowhere is past.
 constexpr uint32_t kNowhere = 0x80000000u;
 struct Rows {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     __amdgpu_buffer_rsrc_t r;
+    u32x4 words;  // the same
     // `low`: the lowest row; have rows, `step` bytes apart, of `width` bytes
     __device__ __forceinline__ Rows(const void* low, uint32_t step, int have, uint32_t width)
         : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(low), (short)0,
-                                              (int)((uint32_t)(have - 1) * step + width), 0x00020000)) {}
+                                              (int)((uint32_t)(have - 1) * step + width), 0x00020000)),
+          words{word((uint32_t)(uintptr_t)low), word((uint32_t)((uintptr_t)low >> 32) & 0xffff),
+                word((uint32_t)(have - 1) * step + width), 0x00020000u} {}
+    __device__ static __forceinline__ uint32_t word(uint32_t v) {
+        return (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+    }
 };
 
 // N neighbours of a row at byte offset `off`, of which `left` lie in the row: with whole units
@@ -251,9 +258,15 @@ constexpr int lin_waves(int KD, int VT, int NW, int size) {
 
 template <typename T> constexpr int kParts = sizeof(T) == 2 ? 3 : 1;
 
-// 16 bytes of each lane, to 1 KB of LDS from `to` on.
+// 16 bytes of each lane, to 1 KB of LDS from `to` on.  In assembly, since the compiler has every
+// transposing read of LDS wait for all such loads that it knows of, the next chunk's among them;
+// vm_wait is theirs.  The wait states are those of a scalar register that a vector instruction
+// wrote (5) and of m0 (1), which the compiler does not see to in here.
 __device__ __forceinline__ void load_unit(const Rows& b, char* to, uint32_t off) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(b.r, (__attribute__((address_space(3))) void*)to, 16, off, 0, 0, 0);
+    const uint32_t at = __builtin_amdgcn_readfirstlane(
+        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)to);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 ::"s"(at), "v"(off), "s"(b.words) : "memory", "m0");
 }
 
 // What a kernel is built for: FULL, K is KD and rows are whole units; PADDED, K is less, and
@@ -451,11 +464,18 @@ __global__ __launch_bounds__(NW * 64, lin_waves(KD, VT, NW, sizeof(T))) void lin
     const uint32_t onext = back ? 0u - 16 * os : 16 * os, owidth = vcols * (uint32_t)sizeof(OT);
     const int keys = p.K;
     const bool final = p.final != nullptr;
-    int64_t left = n;
-    for (int buf = 0; left > 0; left -= C, buf ^= 1) {
-        const int cl = (int)imin(C, left);
-        const bool end = left <= C, close = last && end;  // of the span, of the sequence
-        if (!end) fetch((int)imin(C, left - C), buf ^ 1);
+    const int chunks = (int)cdiv(n, C);
+    for (int i = 0; i < chunks; ++i) {
+        const int buf = i & 1;
+        const bool end = i + 1 == chunks, close = last && end;  // of the span, of the sequence
+        const int cl = end ? tail : C;
+        // Tables are read ahead of the loads of the next chunk: the compiler would have a read of
+        // them wait for those loads.
+        const float* const wt = sh.w[close ? 1 : 0] + 4 * g;
+        f32x8 w = cat<f32x8, f32x4>(*(const f32x4*)wt, *(const f32x4*)(wt + 16));
+        float f0 = sh.pw[l16], f1 = sh.pw[16 + l16];
+        asm volatile("" : "+v"(w), "+v"(f0), "+v"(f1));
+        if (!end) fetch(i + 2 == chunks ? tail : C, buf ^ 1);
         const char* const tq = sh.q[STATE ? 0 : buf];
         const char* const tk = sh.k[buf];
         const char* const tv = sh.v[buf];
@@ -464,14 +484,11 @@ __global__ __launch_bounds__(NW * 64, lin_waves(KD, VT, NW, sizeof(T))) void lin
         held = drop ? 1.f : now;
         // v, plain and weighted for the state behind the chunk
         X8 vf[CB], vw[CB][kParts<T>];
-        {
-            const float* const wt = sh.w[close ? 1 : 0] + 4 * g;
-            const f32x8 w = cat<f32x8, f32x4>(*(const f32x4*)wt, *(const f32x4*)(wt + 16)) * (1.f / held);
+        w *= __builtin_amdgcn_rcpf(held);
 #pragma unroll
-            for (int cb = 0; cb < CB; ++cb) {
-                vf[cb] = col_frag<VT>((const T*)nullptr, tv, vb ^ cb * 4 * (int)sizeof(T), c0);
-                weigh(vf[cb], w, vw[cb]);
-            }
+        for (int cb = 0; cb < CB; ++cb) {
+            vf[cb] = col_frag<VT>((const T*)nullptr, tv, vb ^ cb * 4 * (int)sizeof(T), c0);
+            weigh(vf[cb], w, vw[cb]);
         }
         // Results are transposed: a lane has 4 columns of token 16 ib + l16, and of the scores 4
         // tokens j of one row i, which is the order in which they meet the values.
@@ -504,7 +521,8 @@ __global__ __launch_bounds__(NW * 64, lin_waves(KD, VT, NW, sizeof(T))) void lin
                     acc[1][cb] = mma(e, q1, acc[1][cb]);
                 }
             }
-            const float f0 = come_in * sh.pw[l16], f1 = come_in * sh.pw[16 + l16];
+            f0 *= come_in;
+            f1 *= come_in;
             // above the diagonal a weight of 0 is not enough: a score there may be infinite
             X8 sc[2];
 #pragma unroll
@@ -521,6 +539,11 @@ __global__ __launch_bounds__(NW * 64, lin_waves(KD, VT, NW, sizeof(T))) void lin
                 acc[1][cb] = mma(vf[cb], sc[1], acc[1][cb] * f1);
             }
         }
+        // formed here, among the products above, and not behind the branch
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+            for (int j = 0; j < kParts<T>; ++j) asm volatile("" : "+v"(vw[cb][j]));
         if (drop) {
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb)
