@@ -14,11 +14,10 @@
 // undecayed) and dinit = l R_0: one kernel serves all four (LinPass::init_pow, final_pow).
 //
 // (C = 32.)  A workgroup walks the chunks of one span of a sequence for one head and VT columns of V,
-// the state in registers: each of its NW waves holds all K rows of its 16 CB columns, so no
+// the state in registers: each of its four waves holds all K rows of VT / 4 columns, so no
 // product needs a sum across waves.  Where sequences x heads do not fill the chip a
 // sequence is cut into spans: their states are formed first (STATE), joined along the
 // sequence (linattn_join) and then every span is walked from its own incoming state.
-#include <stdlib.h>
 #include <type_traits>
 
 #include "ssd_layer.h"
@@ -252,9 +251,7 @@ __device__ __forceinline__ void store_run(const Rows& b, uint32_t off, int left,
 }
 
 // Waves a SIMD that the kernel is compiled for: two workgroups a CU.
-constexpr int lin_waves(int KD, int VT, int NW, int size) {
-    return (4 * (KD * 2 + VT) * C * size > 160 * 1024 ? 1 : 2) * NW / 4;
-}
+constexpr int lin_waves(int KD, int VT, int size) { return 2 * (2 * KD + VT) * C * size > 80 * 1024 - 1024 ? 1 : 2; }
 
 template <typename T> constexpr int kParts = sizeof(T) == 2 ? 3 : 1;
 
@@ -277,12 +274,12 @@ enum { FULL, PADDED, RAGGED };
 // chunk's r-th token in processing order (with `back` the chunks lie in memory from the last
 // to the first, and so do their rows); rows past the chunk's end are zeros, or values of the
 // chunk where its rows lie closer than they are wide, and columns past `cols` zeros.  Each of
-// NW waves issues every NW-th load of 64 units straight into LDS: nothing passes through
+// four waves issues every fourth load of 64 units straight into LDS: nothing passes through
 // registers and nothing is waited for.  RAGGED: element by element, waiting.
-template <typename T, int COLS, int NW, int MODE>
+template <typename T, int COLS, int MODE>
 struct Stream {
     using L = Tile<T, COLS>;
-    static constexpr int LOADS = C * L::UPR / 64, N = (LOADS + NW - 1) / NW;
+    static constexpr int N = C * L::UPR / 256;
     const char* low;   // lowest row of the next chunk, were it full
     uint32_t step, width, off[N];
     int32_t cols;
@@ -293,7 +290,7 @@ struct Stream {
         low = (const char*)first - (back ? (int64_t)(C - 1) * step : 0);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int place = (i * NW + wave_id()) * 64 + (threadIdx.x & 63), r = place / L::UPR;
+            const int place = (i * 4 + wave_id()) * 64 + (threadIdx.x & 63), r = place / L::UPR;
             const int c = (place % L::UPR ^ L::swap(r)) * L::EPU;
             off[i] = (uint32_t)(back ? C - 1 - r : r) * step + (uint32_t)(c * sizeof(T));
             if (MODE != RAGGED && c >= cols) off[i] = kNowhere;
@@ -305,8 +302,7 @@ struct Stream {
         const Rows b(low + gap, step, have, width);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int load = i * NW + wave_id();
-            if (LOADS % NW && load >= LOADS) break;
+            const int load = i * 4 + wave_id();
             if constexpr (MODE != RAGGED) {
                 load_unit(b, tile + load * 1024, off[i] - gap);
             } else {
@@ -349,12 +345,12 @@ __device__ __forceinline__ uint32_t same_xcd(uint32_t id, uint32_t together, uin
 }
 
 // One span (or, STATE, only its state).  OT: the output's type.
-template <typename T, typename OT, int KD, int VT, int NW, int MODE, bool STATE>
-__global__ __launch_bounds__(NW * 64, lin_waves(KD, VT, NW, sizeof(T))) void linattn_kernel(LinPasses ps) {
+template <typename T, typename OT, int KD, int VT, int MODE, bool STATE>
+__global__ __launch_bounds__(256, lin_waves(KD, VT, sizeof(T))) void linattn_kernel(LinPasses ps) {
     const LinPass& p = ps.p[blockIdx.y];
     touch_args(p);
     using X8 = typename Vec<T>::x8;
-    constexpr int NT = NW * 64, CB = VT / (16 * NW), KB = KD / 16, KS = KD / 32;
+    constexpr int CB = VT / 64, KB = KD / 16, KS = KD / 32;
     __shared__ Shared<T, KD, VT, STATE> sh;
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), l16 = lane & 15, g = lane >> 4;
     uint32_t id = same_xcd(blockIdx.x, p.together, gridDim.x);
@@ -373,7 +369,7 @@ __global__ __launch_bounds__(NW * 64, lin_waves(KD, VT, NW, sizeof(T))) void lin
 
     if (!STATE && n == 0) {  // an empty sequence hands on what came in
         if (p.final)
-            for (int i = tid; i < p.K * vcols; i += NT) {
+            for (int i = tid; i < p.K * vcols; i += 256) {
                 const int64_t e = block + (int64_t)(i / vcols) * p.s_k + (int64_t)(v0 + i % vcols) * p.s_v;
                 p.final[e] = p.init ? p.init[e] : 0.f;
             }
@@ -382,9 +378,9 @@ __global__ __launch_bounds__(NW * 64, lin_waves(KD, VT, NW, sizeof(T))) void lin
 
     const bool back = p.reverse != 0;
     const int64_t tok0 = back ? sp.first + sp.len - 1 - sp.t0 : sp.first + sp.t0;
-    Stream<T, KD, NW, MODE> ks((const T*)p.k + tok0 * p.k_t + (h / p.kdiv) * p.k_h, p.k_t, p.K, back);
-    Stream<T, KD, NW, MODE> qs((const T*)p.q + tok0 * p.q_t + (h / p.qdiv) * p.q_h, p.q_t, p.K, back);
-    Stream<T, VT, NW, MODE> vs((const T*)p.v + tok0 * p.v_t + (h / p.vdiv) * p.v_h + v0, p.v_t, vcols, back);
+    Stream<T, KD, MODE> ks((const T*)p.k + tok0 * p.k_t + (h / p.kdiv) * p.k_h, p.k_t, p.K, back);
+    Stream<T, KD, MODE> qs((const T*)p.q + tok0 * p.q_t + (h / p.qdiv) * p.q_h, p.q_t, p.K, back);
+    Stream<T, VT, MODE> vs((const T*)p.v + tok0 * p.v_t + (h / p.vdiv) * p.v_h + v0, p.v_t, vcols, back);
     auto fetch = [&](int have, int to) {
         if constexpr (!STATE) qs.fill(sh.q[to], have);
         ks.fill(sh.k[to], have);
@@ -439,9 +435,9 @@ __global__ __launch_bounds__(NW * 64, lin_waves(KD, VT, NW, sizeof(T))) void lin
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int d = l16 - 4 * g - r;
-        const float x = p.in_scale * sh.pw[max(d, 0)];
+        const float x = p.in_scale * p.out_scale * sh.pw[max(d, 0)];
         tw[0][r] = d >= 0 ? x : 0.f;
-        tw[1][r] = p.in_scale * sh.pw[16 + d];
+        tw[1][r] = p.in_scale * p.out_scale * sh.pw[16 + d];
     }
     // the sequence's last chunk, of `tail` tokens, is followed by no decay, or by final_pow
     const int tail = (int)((n - 1) % C) + 1, top = tail - 1 + p.final_pow;
@@ -521,8 +517,8 @@ __global__ __launch_bounds__(NW * 64, lin_waves(KD, VT, NW, sizeof(T))) void lin
                     acc[1][cb] = mma(e, q1, acc[1][cb]);
                 }
             }
-            f0 *= come_in;
-            f1 *= come_in;
+            f0 *= come_in * out_scale;
+            f1 *= come_in * out_scale;
             // above the diagonal a weight of 0 is not enough: a score there may be infinite
             X8 sc[2];
 #pragma unroll
@@ -567,7 +563,7 @@ __global__ __launch_bounds__(NW * 64, lin_waves(KD, VT, NW, sizeof(T))) void lin
             for (int ib = 0; ib < 2; ++ib) {
                 float x[4 * CB];
 #pragma unroll
-                for (int j = 0; j < 4 * CB; ++j) x[j] = out_scale * acc[ib][j / 4][j % 4];
+                for (int j = 0; j < 4 * CB; ++j) x[j] = acc[ib][j / 4][j % 4];
                 store_run<OT, 4 * CB, MODE == RAGGED>(ob, ooff + ib * onext - gap,
                                                       16 * ib + l16 < cl ? vcols - oc : 0, x);
             }
@@ -595,7 +591,7 @@ __global__ __launch_bounds__(NW * 64, lin_waves(KD, VT, NW, sizeof(T))) void lin
 
 // Joins the span states of every sequence: slot s gets the state that enters span s.
 // A thread takes 4 entries (one lane's part of a result tile).
-__global__ __launch_bounds__(256) void linattn_join(LinPasses ps, int KD, int VT, int CB) {
+__global__ __launch_bounds__(256) void linattn_join(LinPasses ps, int KD, int VT) {
     const LinPass& p = ps.p[blockIdx.z];
     touch_args(p);
     uint32_t id = blockIdx.x;
@@ -608,7 +604,7 @@ __global__ __launch_bounds__(256) void linattn_join(LinPasses ps, int KD, int VT
     const int e = blockIdx.y * 256 + threadIdx.x, lane = e & 63, tile = e >> 6;
     const int kb = tile % (KD / 16), vb = tile / (KD / 16);
     const int kr = 32 * (kb / 2) + 4 * (kb % 2) + 8 * (lane >> 4);
-    const int vc = vt * VT + (CB == 1 ? 16 * vb + (lane & 15)
+    const int vc = vt * VT + (VT == 64 ? 16 * vb + (lane & 15)
                                        : vb / 2 * 32 + dealt<2>(vb % 2, lane & 15));
     float* at = p.spans + (((int64_t)slot0 * p.H + h) * p.vtiles + vt) * (KD * VT) + e * 4;
     const int64_t step = (int64_t)p.H * p.vtiles * (KD * VT);
@@ -661,12 +657,12 @@ __global__ __launch_bounds__(256) void linattn_heads_sum(const float* part, T* o
 struct LinTiles {
     int KD, VT;
 };
-// K is padded to 64, 128 or 256.  The state of a workgroup's columns is KD x VT / 256
-// registers a thread: 64 at most.
+// K is padded to 64, 128 or 256, V cut into tiles of 128 columns, or 64 where there are no more
+// (and for 256 float32 keys, whose tiles with 128 columns would not fit LDS twice).
 LinTiles lin_tiles(int K, int V, int32_t dtype) {
     LinTiles t;
     t.KD = K <= 64 ? 64 : (K <= 128 ? 128 : 256);
-    t.VT = V <= 64 || (t.KD == 256 && dtype == SSD_F32) || getenv("VT64") ? 64 : 128;
+    t.VT = V <= 64 || (t.KD == 256 && dtype == SSD_F32) ? 64 : 128;
     return t;
 }
 
@@ -676,21 +672,32 @@ struct LinPlan {
     int32_t slots, per, vtiles;
     size_t bytes;  // of the span states (0: whole sequences)
 };
-#include <stdlib.h>
-#define kFill (getenv("KFILL") ? (int64_t)atoi(getenv("KFILL")) : (int64_t)512)
 
+// Workgroups that are resident at once: two a CU, or one where the tiles take more than half of
+// its LDS (lin_waves).
+int64_t lin_resident(const LinTiles& t, int32_t dtype) {
+    return 256 * lin_waves(t.KD, t.VT, (int)elem_size(dtype));
+}
+
+// Spans.  A workgroup takes 1.2 us a chunk by itself (64 x 128 bf16; 3.5 128 x 128 float32), and
+// cutting a sequence takes two more launches and a state written and read for every span:
+// enough spans that every resident workgroup has one, half as many more in a packed batch,
+// whose spans are uneven (65536 tokens x 16 heads in 16 sequences: 512 workgroups 486 us, 768
+// 440, 1536 450; 32768 x 8 heads of 256, one workgroup a CU: 128 578 us, 256 346, 512 358).
+// Short sequences stay whole: 2 x 256 tokens x 12 heads bf16 17 us, cut 22; 2 x 512 27 and 22;
+// float32 2 x 128 39 and 40, 2 x 256 66 and 43.
 LinPlan lin_plan(const ssd_linattn_dims& d, int K, int V, int passes = 1) {
     LinPlan pl;
     pl.t = lin_tiles(K, V, d.dtype);
     pl.vtiles = (int)cdiv(V, pl.t.VT);
     const int64_t S = d.nseq > 0 ? d.nseq : d.batch, T = (int64_t)d.batch * d.seqlen;
-    const int64_t wgs = S * d.nheads * pl.vtiles * passes;
+    const int64_t rows = (int64_t)d.nheads * pl.vtiles * passes;  // workgroups of a sequence in one span
+    const int64_t fill = lin_resident(pl.t, d.dtype) * (d.nseq > 0 ? 3 : 2) / 2;
     // packed sequences are of any length: cut as if they were one
-    const int64_t want = d.nseq > 0 ? cdiv(kFill, (int64_t)d.nheads * pl.vtiles * passes) : cdiv(kFill, wgs);
-    const int64_t tokens = d.nseq > 0 ? T : d.seqlen;
-    pl.span = cdiv(cdiv(tokens, want), C) * C;
-    { int ms = getenv("MINSPAN") ? atoi(getenv("MINSPAN")) : 2; if (pl.span < ms * C) pl.span = ms * C; }
-    if (pl.span >= tokens) {
+    const int64_t tokens = d.nseq > 0 ? T : d.seqlen, want = cdiv(fill, d.nseq > 0 ? rows : S * rows);
+    pl.span = imax(cdiv(cdiv(tokens, want), C), 2) * C;
+    const int64_t least = (d.dtype == SSD_BF16 ? 8 : 4) * C;
+    if (pl.span >= tokens || T <= S * least) {
         pl.span = (int64_t)1 << 40;  // whole sequences
         pl.per = 1;
         pl.slots = (int)S;
@@ -703,23 +710,23 @@ LinPlan lin_plan(const ssd_linattn_dims& d, int K, int V, int passes = 1) {
     return pl;
 }
 
-template <typename T, typename OT, int KD, int VT, int NW, int MODE>
+template <typename T, typename OT, int KD, int VT, int MODE>
 void launch_tiles(const LinPasses& ps, int passes, const LinPlan& pl, hipStream_t s) {
     const LinPass& p = ps.p[0];
     const dim3 grid((unsigned)((int64_t)pl.slots * p.H * pl.vtiles), passes);
     if (pl.bytes) {
-        linattn_kernel<T, OT, KD, VT, NW, MODE, true><<<grid, NW * 64, 0, s>>>(ps);
+        linattn_kernel<T, OT, KD, VT, MODE, true><<<grid, 256, 0, s>>>(ps);
         const dim3 joins((unsigned)((int64_t)p.S * p.H * pl.vtiles), KD * VT / 1024, passes);
-        linattn_join<<<joins, 256, 0, s>>>(ps, KD, VT, VT / (16 * NW));
+        linattn_join<<<joins, 256, 0, s>>>(ps, KD, VT);
     }
-    linattn_kernel<T, OT, KD, VT, NW, MODE, false><<<grid, NW * 64, 0, s>>>(ps);
+    linattn_kernel<T, OT, KD, VT, MODE, false><<<grid, 256, 0, s>>>(ps);
 }
-template <typename T, typename OT, int KD, int VT, int NW>
+template <typename T, typename OT, int KD, int VT>
 void launch_tiles(const LinPasses& ps, int passes, const LinPlan& pl, hipStream_t s) {
     constexpr int EPU = 16 / sizeof(T);
-    if (ps.p[0].K % EPU || ps.p[0].V % EPU) launch_tiles<T, OT, KD, VT, NW, RAGGED>(ps, passes, pl, s);
-    else if (ps.p[0].K < KD) launch_tiles<T, OT, KD, VT, NW, PADDED>(ps, passes, pl, s);
-    else launch_tiles<T, OT, KD, VT, NW, FULL>(ps, passes, pl, s);
+    if (ps.p[0].K % EPU || ps.p[0].V % EPU) launch_tiles<T, OT, KD, VT, RAGGED>(ps, passes, pl, s);
+    else if (ps.p[0].K < KD) launch_tiles<T, OT, KD, VT, PADDED>(ps, passes, pl, s);
+    else launch_tiles<T, OT, KD, VT, FULL>(ps, passes, pl, s);
 }
 // Passes of one plan, side by side in each launch: their span states lie behind each other in
 // the workspace (pl.bytes each).
@@ -734,18 +741,17 @@ void launch_passes(LinPasses& ps, int passes, const LinPlan& pl, hipStream_t s) 
         p.together = pl.vtiles * (p.qdiv > p.kdiv ? p.qdiv : p.kdiv);
         p.spans = (float*)((char*)p.spans + i * pl.bytes);
     }
-    static int nw = getenv("NW") ? atoi(getenv("NW")) : 4;
-#define LIN(KD) \
-        if (pl.t.VT == 64 || KD * sizeof(T) > 512) launch_tiles<T, OT, KD, 64, 4>(ps, passes, pl, s); \
-        else if constexpr (KD * sizeof(T) > 512) return; \
-        else if (nw == 8) launch_tiles<T, OT, KD, 128, 8>(ps, passes, pl, s); \
-        else launch_tiles<T, OT, KD, 128, 4>(ps, passes, pl, s)
     if (pl.t.KD == 64) {
-        LIN(64);
+        if (pl.t.VT == 64) launch_tiles<T, OT, 64, 64>(ps, passes, pl, s);
+        else launch_tiles<T, OT, 64, 128>(ps, passes, pl, s);
     } else if (pl.t.KD == 128) {
-        LIN(128);
+        if (pl.t.VT == 64) launch_tiles<T, OT, 128, 64>(ps, passes, pl, s);
+        else launch_tiles<T, OT, 128, 128>(ps, passes, pl, s);
+    } else if constexpr (sizeof(T) == 4) {  // two tiles of 256 x 128 would not fit LDS
+        launch_tiles<T, OT, 256, 64>(ps, passes, pl, s);
     } else {
-        LIN(256);
+        if (pl.t.VT == 64) launch_tiles<T, OT, 256, 64>(ps, passes, pl, s);
+        else launch_tiles<T, OT, 256, 128>(ps, passes, pl, s);
     }
 }
 
