@@ -690,15 +690,15 @@ def ssd_linattn_step(q, k, v, decay, state, scale=1.0, slots=None, new_state=Non
 
 # ---- group norm ----------------------------------------------------------------------------
 
-def _maps(t, name, shape):
+def _maps(t, name, shape, dense):
     """(sample, position) strides of a [n, ..., C] tensor with contiguous channels whose
-    positions form one stride."""
+    positions form one stride; `dense` are those of a contiguous one."""
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}")
-    n, C = shape[0], shape[-1]
-    P = shape[1:-1].numel()
     if t.is_contiguous() or t.numel() == 0:
-        return P * C, C
+        return dense
+    n, C = shape[0], shape[-1]
+    P = dense[0] // C
     m = t.view(n, P, C)  # raises where the positions do not form one stride
     if C > 1 and m.stride(2) != 1:
         raise ValueError(f"{name} needs contiguous channels")
@@ -722,13 +722,13 @@ def _groupnorm_arguments(x, groups, weight, bias, z, activation, eps, out, dy, s
     _same(x, (z, "z"), (out, "y"), (dy, "dy"))
     _floats(x, (weight, (C,), "weight"), (bias, (C,), "bias"),
             *((t, (shape[0], groups), name) for t, name in stats))
-    P = shape[1:-1].numel()
+    P = 1 if len(shape) == 2 else shape[1:-1].numel()
     dense = (P * C, C)
     act = 2 if z is not None else _ACTIVATIONS[activation]
-    return _struct(SsdGroupnormDims, shape[0], P, *_maps(x, "x", shape),
-                   *(dense if out is None else _maps(out, "y", shape)),
-                   *(dense if z is None else _maps(z, "z", shape)),
-                   *(dense if dy is None else _maps(dy, "dy", shape)), C, groups, code, act,
+    return _struct(SsdGroupnormDims, shape[0], P, *_maps(x, "x", shape, dense),
+                   *(dense if out is None else _maps(out, "y", shape, dense)),
+                   *(dense if z is None else _maps(z, "z", shape, dense)),
+                   *(dense if dy is None else _maps(dy, "dy", shape, dense)), C, groups, code, act,
                    float(eps), 0)
 
 

@@ -9,8 +9,13 @@
 //
 // Both are bound by memory.  P = 1: a group is D consecutive elements, LG lanes take it (64 /
 // LG groups a wave) and hold it in registers between the sums and the output: one pass.
-// P > 1: column statistics of runs of positions (one pass over x), joined per group, and a
-// second pass for the output, which the caches serve as far as they hold x.
+// P > 1: statistics of runs of positions (one pass over x), and a second pass for the output,
+// which joins them first and which the caches serve as far as they hold x.
+//
+// Reached (what a copy of 1 GiB reaches is 5.16 TB/s): 8192 x 16 groups of 128, gated, gradients
+// (168 MB) 34 us, 4.9 TB/s; 4096 x 12 groups of 128, gated (38 MB) 9.3 us in the kernel, 4.1 TB/s;
+// 8 maps of 4096 x 320 (42 MB) 22 us in two launches: 7.6 us, and 14.6 for the second, a third of
+// which is the joining of the runs behind a cold read of what other XCDs wrote.
 #include "ssd_layer.h"
 
 namespace ssd {
@@ -31,7 +36,8 @@ struct GnParams {
     const float* mean_in;
     const float* rstd_in;
     float* part;  // columns' sums of the runs [n][runs][2][C]
-    float* sums;  // backward, P > 1: mean(g), mean(g xh) [n][G][2]
+    float* of_runs;  // groups' sums of the runs [n][runs][2][G], where a workgroup spans the channels
+    float* sums;  // groups' sums over their runs [n][G][2], where it does not
     int64_t n, P;
     int64_t x_n, x_p, z_n, z_p, y_n, y_p, dy_n, dy_p;  // strides of samples and positions
     int64_t runlen;
@@ -248,11 +254,33 @@ struct Grid {
     }
 };
 
-// Columns' means and squared deviations of a run, blocks of UN rows joined as they come
-// (Chan): no squares of values with a large mean are summed.
+constexpr int kWide = 2048;  // channels that a workgroup spans at most (256 vectors)
+
+// Calls f(g) once for each group of the workgroup's channels with a wave's lanes, groups dealt
+// to the waves.
+// Calls f(g, lane, lanes) once for each of G groups with `lanes` neighbouring lanes (a power of
+// two up to 64: as many as the workgroup has for each group, so that one round does).  With g = G there is nothing
+// to do but take part in the lanes' sums.
+template <typename F>
+__device__ __forceinline__ void each_group(int G, F f) {
+    int lanes = 64;
+    while (lanes > 1 && lanes * G > (int)blockDim.x) lanes /= 2;
+    const int at = threadIdx.x / lanes, step = blockDim.x / lanes;
+    // threads behind the last whole set of lanes take no group
+    for (int g0 = 0; g0 < G; g0 += step)
+        f(at < step && g0 + at < G ? g0 + at : G, threadIdx.x % lanes, lanes);
+}
+__device__ __forceinline__ float some_sum(float v, int lanes) {
+    for (int o = 1; o < lanes; o *= 2) v += __shfl_xor(v, o);
+    return v;
+}
+
+// Columns' means and squared deviations of a run.  Sums are of the distances from the column's
+// first value in the run: it is one of them, so the mean's share of their squares is at most
+// (run's length) x the deviations', however large the values are.
 template <typename T, int V>
 __global__ __launch_bounds__(256) void gn_stats(GnParams p, int across) {
-    constexpr int UN = 4;
+    constexpr int UN = 8;
     __shared__ float ex[2][256][V];
     const Grid<V> t(p, across);
     int64_t n;
@@ -260,67 +288,87 @@ __global__ __launch_bounds__(256) void gn_stats(GnParams p, int across) {
     if (n >= p.n) return;
     const int64_t p0 = run * p.runlen, p1 = p0 + p.runlen < p.P ? p0 + p.runlen : p.P;
     const T* x = (const T*)p.x + n * p.x_n + t.c;
-    float mean[V], m2[V], cnt = 0.f;
+    float first[V], s1[V], s2[V];
+    load_vec<T, V>(x + p0 * p.x_p, V, first);
 #pragma unroll
-    for (int j = 0; j < V; ++j) mean[j] = m2[j] = 0.f;
+    for (int j = 0; j < V; ++j) s1[j] = s2[j] = 0.f;
     for (int64_t q = p0 + t.r; q < p1; q += UN * t.R) {
         RawVec<T, V> raw[UN];
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
+            // rows past the run's end are its first: no distance
             const int64_t at = q + i * t.R;
-            load_raw<T, V>(x + (at < p1 ? at : q) * p.x_p, V, raw[i]);
+            load_raw<T, V>(x + (at < p1 ? at : p0) * p.x_p, V, raw[i]);
         }
-        const int64_t rest = (p1 - q + t.R - 1) / t.R;
-        const float k = rest < UN ? (float)rest : (float)UN, all = cnt + k;
-        const float ik = 1.f / k, share = k / all, cross = cnt * share;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float v[UN], s = 0.f, d2 = 0.f;
+        for (int i = 0; i < UN; ++i)
 #pragma unroll
-            for (int i = 0; i < UN; ++i) {
-                v[i] = (float)raw[i].v[j];
-                s += i < rest ? v[i] : 0.f;
+            for (int j = 0; j < V; ++j) {
+                const float d = (float)raw[i].v[j] - first[j];
+                s1[j] += d;
+                s2[j] = fmaf(d, d, s2[j]);
             }
-            s *= ik;
-#pragma unroll
-            for (int i = 0; i < UN; ++i) {
-                const float d = v[i] - s;
-                d2 += i < rest ? d * d : 0.f;
-            }
-            const float d = s - mean[j];
-            mean[j] += d * share;
-            m2[j] += d2 + d * d * cross;
-        }
-        cnt = all;
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        ex[0][threadIdx.x][j] = mean[j];
-        ex[1][threadIdx.x][j] = m2[j];
+        ex[0][threadIdx.x][j] = s1[j];
+        ex[1][threadIdx.x][j] = s2[j];
     }
     __syncthreads();
-    if (t.r) return;
-    const int64_t len = p1 - p0;
-    cnt = 0.f;
+    if (t.r && !p.of_runs) return;
+    const float len = (float)(p1 - p0);
+    float mean[V], m2[V];
+    if (t.r == 0) {
+        for (int r = 1; r < t.R; ++r)
 #pragma unroll
-    for (int j = 0; j < V; ++j) mean[j] = m2[j] = 0.f;
-    for (int r = 0; r < t.R; ++r) {
-        const float k = (float)(len > r ? (len - r + t.R - 1) / t.R : 0);
-        if (k == 0.f) break;
-        const float share = k / (cnt + k), cross = cnt * share;
+            for (int j = 0; j < V; ++j) {
+                s1[j] += ex[0][r * across + t.cl][j];
+                s2[j] += ex[1][r * across + t.cl][j];
+            }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const float d = ex[0][r * across + t.cl][j] - mean[j];
-            mean[j] += d * share;
-            m2[j] += ex[1][r * across + t.cl][j] + d * d * cross;
+            const float d = s1[j] / len;
+            mean[j] = first[j] + d;
+            const float e = fmaf(-d, s1[j], s2[j]);
+            m2[j] = e < 0.f ? 0.f : e;  // a NaN stays
         }
-        cnt += k;
     }
-    if (t.skip < V) {
-        float* part = p.part + (n * p.runs + run) * 2 * p.C + t.c;
-        store_vec<float, V>(part, V, mean);
-        store_vec<float, V>(part + p.C, V, m2);
+    if (!p.of_runs) {
+        if (t.skip < V) {
+            float* part = p.part + (n * p.runs + run) * 2 * p.C + t.c;
+            store_vec<float, V>(part, V, mean);
+            store_vec<float, V>(part + p.C, V, m2);
+        }
+        return;
     }
+    // the run's groups: columns of equal counts
+    __syncthreads();
+    float* const cm = &ex[0][0][0];
+    float* const cs = &ex[1][0][0];
+    if (t.r == 0)
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (j >= t.skip) {
+                cm[t.c + j] = mean[j];
+                cs[t.c + j] = m2[j];
+            }
+    __syncthreads();
+    each_group(p.G, [&](int g, int lane, int lanes) {
+        const int d0 = g < p.G ? g * p.D : 0, D = g < p.G ? p.D : 0;
+        float a = 0.f, b = 0.f;
+        for (int d = lane; d < D; d += lanes) a += cm[d0 + d];
+        a = some_sum(a, lanes) / (float)p.D;
+        for (int d = lane; d < D; d += lanes) {
+            const float e = cm[d0 + d] - a;
+            b += cs[d0 + d] + len * e * e;
+        }
+        b = some_sum(b, lanes);
+        if (D && lane == 0) {
+            float* o = p.of_runs + (n * p.runs + run) * 2 * p.G + g;
+            o[0] = a;
+            o[p.G] = b;
+        }
+    });
 }
 
 // Sum over a workgroup of 256, in every thread.
@@ -332,7 +380,8 @@ __device__ __forceinline__ float group_sum(float v, float* ex) {
     return ex[0] + ex[1] + ex[2] + ex[3];
 }
 
-// One workgroup a sample and group: mean and rstd from its columns' of every run.
+// Where a workgroup does not span the channels, one for each sample and group: mean and rstd
+// from its columns' of every run.
 __global__ __launch_bounds__(256) void gn_stats_join(GnParams p) {
     __shared__ float ex[4];
     const int64_t id = unit();
@@ -369,6 +418,7 @@ __global__ __launch_bounds__(256) void gn_stats_join(GnParams p) {
 template <typename T, int V, int ACT>
 __global__ __launch_bounds__(256) void gn_apply(GnParams p, int across) {
     constexpr int UN = 4;
+    __shared__ float stats[2][kWide];
     const Grid<V> t(p, across);
     int64_t n;
     const int64_t run = divide(unit(), p.runs, &n);
@@ -377,6 +427,17 @@ __global__ __launch_bounds__(256) void gn_apply(GnParams p, int across) {
     const T* x = (const T*)p.x + n * p.x_n + t.c;
     const T* z = (const T*)p.z + n * p.z_n + t.c;
     T* y = (T*)p.out + n * p.y_n + t.c;
+    // the first rows are on their way while the statistics are joined, and each time the next
+    RawVec<T, V> xr[UN], zr[UN];
+    auto fetch = [&](int64_t q) {
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            const int64_t at = q + i * t.R < p1 ? q + i * t.R : p0;
+            load_raw<T, V>(x + at * p.x_p, V, xr[i]);
+            if (ACT == GATE) load_raw<T, V>(z + at * p.z_p, V, zr[i]);
+        }
+    };
+    fetch(p0 + t.r);
     float a[V], m[V], b[V], w[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -385,28 +446,57 @@ __global__ __launch_bounds__(256) void gn_apply(GnParams p, int across) {
     }
     if (p.weight) load_vec<float, V>(p.weight + t.c, V, w);
     if (p.bias) load_vec<float, V>(p.bias + t.c, V, b);
+    if (p.of_runs) {
+        // relative to the first run's mean, so that no squares of large values are summed
+        each_group(p.G, [&](int g, int lane, int lanes) {
+            const float* q = p.of_runs + n * p.runs * 2 * p.G + (g < p.G ? g : 0);
+            const float first = q[0];
+            float shift = 0.f, sq = 0.f;
+#pragma unroll 8
+            for (int i = lane; i < p.runs; i += lanes) {
+                const float len = (float)(i + 1 < p.runs ? p.runlen : p.P - i * p.runlen);
+                const float e = q[(int64_t)i * 2 * p.G] - first;
+                shift += len * e;
+                sq += q[((int64_t)i * 2 + 1) * p.G] + len * (float)p.D * e * e;
+            }
+            shift = some_sum(shift, lanes) / (float)p.P;
+            const float mean = first + shift;
+            const float var = some_sum(sq, lanes) / ((float)p.P * (float)p.D) - shift * shift;
+            const float rstd = 1.f / sqrtf((var < 0.f ? 0.f : var) + p.eps);
+            if (g < p.G && lane == 0) {
+                stats[0][g] = mean;
+                stats[1][g] = rstd;
+                if (run == 0) {
+                    if (p.mean) p.mean[n * p.G + g] = mean;
+                    if (p.rstd) p.rstd[n * p.G + g] = rstd;
+                }
+            }
+        });
+        __syncthreads();
+    }
+    int g = (int)t.c / p.D, at0 = (int)t.c % p.D;  // a group, and the channel in it
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int64_t g = n * p.G + (t.c + j) / p.D;
-        m[j] = p.mean[g];
-        a[j] = p.rstd[g];
+        if (j && ++at0 == p.D) at0 = 0, ++g;
+        m[j] = p.of_runs ? stats[0][g] : p.mean[n * p.G + g];
+        a[j] = p.of_runs ? stats[1][g] : p.rstd[n * p.G + g];
     }
     for (int64_t q = p0 + t.r; q < p1; q += UN * t.R) {
-        RawVec<T, V> xr[UN], zr[UN];
+        float v[UN][V], u[UN][V];
 #pragma unroll
-        for (int i = 0; i < UN; ++i) {
-            const int64_t at = q + i * t.R < p1 ? q + i * t.R : q;
-            load_raw<T, V>(x + at * p.x_p, V, xr[i]);
-            if (ACT == GATE) load_raw<T, V>(z + at * p.z_p, V, zr[i]);
-        }
+        for (int i = 0; i < UN; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                v[i][j] = (float)xr[i].v[j];
+                u[i][j] = ACT == GATE ? (float)zr[i].v[j] : 0.f;
+            }
+        if (q + UN * t.R < p1) fetch(q + UN * t.R);
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
             const int64_t at = q + i * t.R;
             float o[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                o[j] = activate<ACT>(((float)xr[i].v[j] - m[j]) * a[j] * w[j] + b[j],
-                                     ACT == GATE ? (float)zr[i].v[j] : 0.f);
+            for (int j = 0; j < V; ++j) o[j] = activate<ACT>((v[i][j] - m[j]) * a[j] * w[j] + b[j], u[i][j]);
             if (at < p1) store_own<T, V>(y + at * p.y_p, t.skip, o);
         }
     }
@@ -416,7 +506,7 @@ __global__ __launch_bounds__(256) void gn_apply(GnParams p, int across) {
 template <typename T, int V, int ACT, bool DX>
 __global__ __launch_bounds__(256) void gn_bwd(GnParams p, int across) {
     constexpr int UN = 2;
-    __shared__ float ex[DX ? 1 : 2][DX ? 1 : 256][V];
+    __shared__ float ex[2][256][V];  // DX: mean(g) and mean(g xh) of the groups
     const Grid<V> t(p, across);
     int64_t n;
     const int64_t run = divide(unit(), p.runs, &n);
@@ -427,6 +517,18 @@ __global__ __launch_bounds__(256) void gn_bwd(GnParams p, int across) {
     const T* dy = (const T*)p.dy + n * p.dy_n + t.c;
     T* dx = (T*)p.out + n * p.y_n + t.c;
     T* dz = (T*)p.dz + n * p.z_n + t.c;
+    // the first rows are on their way while the groups' sums are joined, and each time the next
+    RawVec<T, V> xr[UN], zr[UN], gr[UN];
+    auto fetch = [&](int64_t q) {
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            const int64_t at = q + i * t.R < p1 ? q + i * t.R : p0;
+            load_raw<T, V>(x + at * p.x_p, V, xr[i]);
+            load_raw<T, V>(dy + at * p.dy_p, V, gr[i]);
+            if (ACT == GATE) load_raw<T, V>(z + at * p.z_p, V, zr[i]);
+        }
+    };
+    fetch(p0 + t.r);
     float m[V], a[V], b[V], w[V], s0[V], s1[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -435,32 +537,62 @@ __global__ __launch_bounds__(256) void gn_bwd(GnParams p, int across) {
     }
     if (p.weight) load_vec<float, V>(p.weight + t.c, V, w);
     if (ACT != PLAIN && p.bias) load_vec<float, V>(p.bias + t.c, V, b);
+    int64_t g = n * p.G + (int)t.c / p.D;  // a group, and the channel in it
+    int at0 = (int)t.c % p.D;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int64_t g = n * p.G + (t.c + j) / p.D;
+        if (j && ++at0 == p.D) at0 = 0, ++g;
         m[j] = p.mean_in[g];
         a[j] = p.rstd_in[g];
-        s0[j] = DX ? p.sums[2 * g] : 0.f;
-        s1[j] = DX ? p.sums[2 * g + 1] : 0.f;
+        s0[j] = DX && !p.of_runs ? p.sums[2 * g] : 0.f;
+        s1[j] = DX && !p.of_runs ? p.sums[2 * g + 1] : 0.f;
+    }
+    if (DX && p.of_runs) {
+        float* const sums = &ex[0][0][0];  // [2][G], G <= 256 V
+        each_group(p.G, [&](int g, int lane, int lanes) {
+            const float* q = p.of_runs + n * p.runs * 2 * p.G + (g < p.G ? g : 0);
+            float x = 0.f, y = 0.f;
+#pragma unroll 8
+            for (int i = lane; i < p.runs; i += lanes) {
+                x += q[(int64_t)i * 2 * p.G];
+                y += q[((int64_t)i * 2 + 1) * p.G];
+            }
+            const float inv = 1.f / ((float)p.P * (float)p.D);
+            x = some_sum(x, lanes) * inv;
+            y = some_sum(y, lanes) * inv;
+            if (g < p.G && lane == 0) {
+                sums[g] = x;
+                sums[p.G + g] = y;
+            }
+        });
+        __syncthreads();
+        int g = (int)t.c / p.D, at0 = (int)t.c % p.D;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            if (j && ++at0 == p.D) at0 = 0, ++g;
+            s0[j] = sums[g];
+            s1[j] = sums[p.G + g];
+        }
     }
     for (int64_t q = p0 + t.r; q < p1; q += UN * t.R) {
-        RawVec<T, V> xr[UN], zr[UN], gr[UN];
+        float xv[UN][V], zv[UN][V], gv[UN][V];
 #pragma unroll
-        for (int i = 0; i < UN; ++i) {
-            const int64_t at = q + i * t.R < p1 ? q + i * t.R : q;
-            load_raw<T, V>(x + at * p.x_p, V, xr[i]);
-            load_raw<T, V>(dy + at * p.dy_p, V, gr[i]);
-            if (ACT == GATE) load_raw<T, V>(z + at * p.z_p, V, zr[i]);
-        }
+        for (int i = 0; i < UN; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                xv[i][j] = (float)xr[i].v[j];
+                zv[i][j] = ACT == GATE ? (float)zr[i].v[j] : 0.f;
+                gv[i][j] = (float)gr[i].v[j];
+            }
+        if (q + UN * t.R < p1) fetch(q + UN * t.R);
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
             const int64_t at = q + i * t.R;
             float o[V], zo[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float xh = ((float)xr[i].v[j] - m[j]) * a[j];
-                const float du = slope<ACT>((float)gr[i].v[j], xh * w[j] + b[j],
-                                            ACT == GATE ? (float)zr[i].v[j] : 0.f, zo[j]);
+                const float xh = (xv[i][j] - m[j]) * a[j];
+                const float du = slope<ACT>(gv[i][j], xh * w[j] + b[j], zv[i][j], zo[j]);
                 if (DX) {
                     o[j] = a[j] * (du * w[j] - s0[j] - xh * s1[j]);
                 } else if (at < p1) {
@@ -481,20 +613,51 @@ __global__ __launch_bounds__(256) void gn_bwd(GnParams p, int across) {
             ex[1][threadIdx.x][j] = s1[j];
         }
         __syncthreads();
-        if (t.r || t.skip >= V) return;
-        for (int r = 1; r < t.R; ++r)
+        if (t.r || t.skip >= V) {
+            if (!p.of_runs) return;
+        } else for (int r = 1; r < t.R; ++r)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 s0[j] += ex[0][r * across + t.cl][j];
                 s1[j] += ex[1][r * across + t.cl][j];
             }
-        float* part = p.part + (n * p.runs + run) * 2 * p.C + t.c;
-        store_vec<float, V>(part, V, s0);
-        store_vec<float, V>(part + p.C, V, s1);
+        if (t.r == 0 && t.skip < V) {
+            float* part = p.part + (n * p.runs + run) * 2 * p.C + t.c;
+            store_vec<float, V>(part, V, s0);
+            store_vec<float, V>(part + p.C, V, s1);
+        }
+        if (!p.of_runs) return;
+        // the run's groups: sums of g = du w and of g xh
+        __syncthreads();
+        float* const cx = &ex[0][0][0];
+        float* const cd = &ex[1][0][0];
+        if (t.r == 0)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (j >= t.skip) {
+                    cx[t.c + j] = s0[j] * w[j];
+                    cd[t.c + j] = s1[j] * w[j];
+                }
+        __syncthreads();
+        each_group(p.G, [&](int g, int lane, int lanes) {
+            const int d0 = g < p.G ? g * p.D : 0, D = g < p.G ? p.D : 0;
+            float x = 0.f, y = 0.f;
+            for (int d = lane; d < D; d += lanes) {
+                x += cd[d0 + d];
+                y += cx[d0 + d];
+            }
+            x = some_sum(x, lanes);
+            y = some_sum(y, lanes);
+            if (D && lane == 0) {
+                float* o = p.of_runs + (n * p.runs + run) * 2 * p.G + g;
+                o[0] = x;
+                o[p.G] = y;
+            }
+        });
     }
 }
 
-// One workgroup a sample and group: mean(g) and mean(g xh) from the columns' sums.
+// Likewise mean(g) and mean(g xh) from the columns' sums.
 __global__ __launch_bounds__(256) void gn_bwd_join(GnParams p) {
     __shared__ float ex[4];
     const int64_t id = unit();
@@ -557,9 +720,10 @@ RunPlan run_plan(const ssd_groupnorm_dims& d) {
     r.blocks = (int)cdiv(vecs, 256);
     r.across = (int)cdiv(vecs, r.blocks);
     const int64_t R = 256 / r.across;
-    // four workgroups a CU, but no fewer than 8 rows a thread
-    const int64_t want = cdiv(1024, imax(1, d.samples) * r.blocks);
-    r.runlen = imax(cdiv(d.positions, want), 8 * R);
+    // Two workgroups a CU, but no fewer than 4 rows a thread: more runs leave more to join (8 x
+    // 4096 x 320 bf16, us: 256 workgroups 23, 512 22, 768 24, 1024 28).
+    const int64_t want = cdiv(512, imax(1, d.samples) * r.blocks);
+    r.runlen = imax(cdiv(d.positions, want), 4 * R);
     r.runs = (int)cdiv(d.positions, r.runlen);
     return r;
 }
@@ -570,9 +734,11 @@ bool by_rows(const ssd_groupnorm_dims& d) {
 
 int32_t row_walkers(const ssd_groupnorm_dims& d) {
     const RowPlan r = row_plan(d);
-    // 2048 workgroups' worth of lanes at most, and no fewer than four rows each
+    // 768 workgroups' worth of lanes (three a CU) at most, and no fewer than four rows each: each
+    // walker writes a row of sums that is read again (8192 x 16 groups of 128 bf16 with a gate,
+    // us: 512 workgroups 34, 768 34, 1024 36, 2048 42).
     const int64_t per = cdiv((int64_t)d.groups * r.LG, 256);
-    int64_t w = imax(1, 2048 / per);
+    int64_t w = imax(1, 768 / per);
     const int64_t most = imax(1, cdiv(d.samples, 4));
     return (int32_t)(w < most ? w : most);
 }
@@ -642,7 +808,7 @@ void launch_runs_fwd(const ssd_groupnorm_dims& d, const GnParams& p, RunPlan r, 
     const dim3 grid = units(p.n * r.runs, r.blocks);
     const dim3 block((unsigned)(256 / r.across * r.across));
     gn_stats<T, V><<<grid, block, 0, s>>>(p, r.across);
-    gn_stats_join<<<units(p.n * p.G), 256, 0, s>>>(p);
+    if (!p.of_runs) gn_stats_join<<<units(p.n * p.G), 256, 0, s>>>(p);
     if (d.activation == PLAIN) gn_apply<T, V, PLAIN><<<grid, block, 0, s>>>(p, r.across);
     else if (d.activation == SILU) gn_apply<T, V, SILU><<<grid, block, 0, s>>>(p, r.across);
     else gn_apply<T, V, GATE><<<grid, block, 0, s>>>(p, r.across);
@@ -652,7 +818,7 @@ void launch_runs_bwd(const GnParams& p, RunPlan r, hipStream_t s) {
     const dim3 grid = units(p.n * r.runs, r.blocks);
     const dim3 block((unsigned)(256 / r.across * r.across));
     gn_bwd<T, V, ACT, false><<<grid, block, 0, s>>>(p, r.across);
-    gn_bwd_join<<<units(p.n * p.G), 256, 0, s>>>(p);
+    if (!p.of_runs) gn_bwd_join<<<units(p.n * p.G), 256, 0, s>>>(p);
     gn_bwd<T, V, ACT, true><<<grid, block, 0, s>>>(p, r.across);
 }
 template <typename T, int V>
@@ -662,8 +828,9 @@ void launch_runs_bwd(const ssd_groupnorm_dims& d, const GnParams& p, RunPlan r, 
     else launch_runs_bwd<T, V, GATE>(p, r, s);
 }
 
-// Workspace: columns' sums of the runs (and what the backward's join leaves), and in the
-// forward the statistics where the caller does not take them.
+// Workspace: columns' sums of the runs, and groups' (of the runs, or where a workgroup does not
+// span the channels joined; in the forward the statistics then, if the caller does not take
+// them).  The forward needs no columns' sums but in that case.
 struct GnSpace {
     size_t part, sums;
 };
@@ -674,8 +841,9 @@ GnSpace gn_space(const ssd_groupnorm_dims& d, bool bwd) {
         return w;
     }
     const RunPlan r = run_plan(d);
-    w.part = up256((size_t)imax(1, d.samples * r.runs) * 2 * d.channels * 4);
-    w.sums = up256((size_t)imax(1, d.samples * d.groups) * 2 * 4);
+    const size_t runs = (size_t)imax(1, d.samples * r.runs), one = r.blocks == 1;
+    w.part = bwd || !one ? up256(runs * 2 * d.channels * 4) : 0;
+    w.sums = up256((one ? runs : (size_t)imax(1, d.samples)) * 2 * d.groups * 4);
     return w;
 }
 
@@ -727,9 +895,13 @@ int ssd_groupnorm_fwd(const ssd_groupnorm_dims* dims, const void* x, const float
     p.part = (float*)workspace;
     p.runs = r.runs;
     p.runlen = r.runlen;
-    float* const stats = (float*)((char*)workspace + w.part);
-    if (!p.mean) p.mean = stats;
-    if (!p.rstd) p.rstd = stats + d.samples * d.groups;
+    float* const sums = (float*)((char*)workspace + w.part);
+    if (r.blocks == 1) {
+        p.of_runs = sums;
+    } else {
+        if (!p.mean) p.mean = sums;
+        if (!p.rstd) p.rstd = sums + d.samples * d.groups;
+    }
     if (d.dtype == SSD_BF16) {
         if (r.V == 1) launch_runs_fwd<bf16, 1>(d, p, r, s);
         else launch_runs_fwd<bf16, 8>(d, p, r, s);
@@ -798,7 +970,7 @@ int ssd_groupnorm_bwd(const ssd_groupnorm_dims* dims, const void* x, const float
         const RunPlan r = run_plan(d);
         p.runs = r.runs;
         p.runlen = r.runlen;
-        p.sums = (float*)((char*)workspace + w.part);
+        (r.blocks == 1 ? p.of_runs : p.sums) = (float*)((char*)workspace + w.part);
         c.rows = d.samples * r.runs;
         if (d.dtype == SSD_BF16) {
             if (r.V == 1) launch_runs_bwd<bf16, 1>(d, p, r, s);
