@@ -217,6 +217,19 @@ struct Rows {
     }
 };
 
+// A score as a bfloat16 operand in two parts, 16 bits: a row of few tokens has few scores, whose
+// roundings its output would take over whole (1.7 times the error of its own rounding, and twice
+// two matrix instructions of 80 to avoid it).
+template <typename T> constexpr int kScoreParts = sizeof(T) == 2 ? 2 : 1;
+__device__ __forceinline__ void split_scores(const f32x8& s, bf16x8 (&o)[2]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        o[0][j] = (bf16)s[j];
+        o[1][j] = (bf16)(s[j] - (float)o[0][j]);
+    }
+}
+__device__ __forceinline__ void split_scores(const f32x8& s, f32x8 (&o)[1]) { o[0] = s; }
+
 // N neighbours of a row at byte offset `off`, of which `left` lie in the row: with whole units
 // all or none.
 template <typename OT, int N, bool SINGLY>
@@ -520,19 +533,27 @@ __global__ __launch_bounds__(256, lin_waves(KD, VT, sizeof(T))) void linattn_ker
             f0 *= come_in * out_scale;
             f1 *= come_in * out_scale;
             // above the diagonal a weight of 0 is not enough: a score there may be infinite
-            X8 sc[2];
+            f32x8 sf[2];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const bool in = l16 >= 4 * g + r;
-                sc[0][r] = in ? (T)(s00[r] * tw[0][r]) : (T)0.f;
-                sc[0][4 + r] = (T)0.f;
-                sc[1][r] = (T)(s01[r] * tw[1][r]);
-                sc[1][4 + r] = in ? (T)(s11[r] * tw[0][r]) : (T)0.f;
+                sf[0][r] = in ? s00[r] * tw[0][r] : 0.f;
+                sf[0][4 + r] = 0.f;
+                sf[1][r] = s01[r] * tw[1][r];
+                sf[1][4 + r] = in ? s11[r] * tw[0][r] : 0.f;
             }
+            X8 sc[2][kScoreParts<T>];
+            split_scores(sf[0], sc[0]);
+            split_scores(sf[1], sc[1]);
 #pragma unroll
             for (int cb = 0; cb < CB; ++cb) {
-                acc[0][cb] = mma(vf[cb], sc[0], acc[0][cb] * f0);
-                acc[1][cb] = mma(vf[cb], sc[1], acc[1][cb] * f1);
+                acc[0][cb] *= f0;
+                acc[1][cb] *= f1;
+#pragma unroll
+                for (int j = 0; j < kScoreParts<T>; ++j) {
+                    acc[0][cb] = mma(vf[cb], sc[0][j], acc[0][cb]);
+                    acc[1][cb] = mma(vf[cb], sc[1][j], acc[1][cb]);
+                }
             }
         }
         // formed here, among the products above, and not behind the branch
