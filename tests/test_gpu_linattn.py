@@ -361,3 +361,61 @@ def test_streams_graphs_and_workspaces():
         assert torch.equal(y2, y3) and all(torch.equal(g2[n], g3[n]) for n in g3)
         if i == 0:
             assert torch.equal(y2, y0) and torch.equal(f2, f0) and all(torch.equal(g2[n], g0[n]) for n in g0)
+
+
+def test_offsets_past_32_bits():
+    """Tokens 2^21 elements apart: 2200 of them span 4.6e9 elements; in and against the order of
+    memory, and a pool of 4.4e9 entries."""
+    L, stride = 2200, 1 << 21
+    wide = torch.empty((1, L, stride), dtype=torch.bfloat16, device=DEV)
+    s = make("bf16", 1, L, 2, 2, 16, 24)
+    at, views = 0, []
+    for n in ("q", "k", "v"):
+        w = s[n].shape[2] * s[n].shape[3]
+        view = wide[..., at:at + w].unflatten(-1, s[n].shape[2:])
+        view.copy_(up(s[n]))
+        views.append(view)
+        at += w
+    y = wide[..., at:at + 48].unflatten(-1, (2, 24))
+    dec = up(s["decay"])
+    for reverse in (False, True):
+        m.ssd_linattn_fwd(*views, dec, reverse=reverse, y=y)
+        want = m.ssd_linattn_fwd(up(s["q"]), up(s["k"]), up(s["v"]), dec, reverse=reverse)[0]
+        assert torch.equal(y, want)
+    del wide, views, view, y
+    nslots = (1 << 32) // (2 * 128 * 128) + 1000
+    pool = torch.empty((nslots, 2, 128, 128), dtype=torch.float32, device=DEV)
+    rows = torch.tensor([nslots - 1, 0], dtype=torch.int32, device=DEV)
+    s = make("f32", 2, 1, 2, 1, 128, 128)
+    pool[rows.long()] = up(s["init"])
+    small = up(s["init"]).clone()
+    q, k, v = (up(s[n])[:, 0] for n in ("q", "k", "v"))
+    a_ = m.ssd_linattn_step(q, k, v, up(s["decay"]), pool, slots=rows)
+    b_ = m.ssd_linattn_step(q, k, v, up(s["decay"]), small)
+    assert torch.equal(a_, b_) and torch.equal(pool[rows.long()], small)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_tokens_closer_than_their_rows(dtype):
+    """Views whose tokens overlap, or are one and the same, are read as they are."""
+    g = torch.Generator().manual_seed(9)
+    line = torch.randn(4000, generator=g).to(TYPES[dtype]).to(DEV)
+    dec = torch.tensor([-0.1, -0.01], device=DEV)
+    for token in (0, 8, 24):
+        q, k, v = (torch.as_strided(line, (1, 45, 2, d), (45 * token, token, 900, 1), o)
+                   for d, o in ((48, 0), (48, 30), (24, 100)))
+        y, f = m.ssd_linattn_fwd(q, k, v, dec)
+        y2, f2 = m.ssd_linattn_fwd(q.contiguous(), k.contiguous(), v.contiguous(), dec)
+        assert torch.equal(y, y2) and torch.equal(f, f2)
+
+
+def test_bfloat16_rows_of_one_token_keep_their_precision():
+    """One token, no state: y is (q . k) v scaled, rounded once.  With scores of 16 bits the
+    product is off by 2^-17 before that: half a step and a 256th of one."""
+    s = make("bf16", 300, 1, 2, 2, 64, 64, carry=False)
+    y, _ = m.ssd_linattn_fwd(up(s["q"]), up(s["k"]), up(s["v"]), up(s["decay"]))
+    ref, _ = lo.linattn(d(s["q"]), d(s["k"]), d(s["v"]), d(s["decay"]))
+    size, _ = lo.linattn(a(s["q"]), a(s["k"]), a(s["v"]), d(s["decay"]))
+    err = (y.double().cpu() - ref).abs()
+    # q . k itself is a float32 sum of 64 terms: 80 2^-24 of their sizes
+    assert (err <= 2.0 ** -9 * 2 * ref.abs() * (0.5 + 2.0 ** -8) * 1.01 + 80 * 2.0 ** -24 * size).all()
