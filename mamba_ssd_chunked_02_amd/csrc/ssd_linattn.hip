@@ -750,8 +750,10 @@ void launch_tiles(const LinPasses& ps, int passes, const LinPlan& pl, hipStream_
 template <typename T, typename OT, int KD, int VT>
 void launch_tiles(const LinPasses& ps, int passes, const LinPlan& pl, hipStream_t s) {
     constexpr int EPU = 16 / sizeof(T);
+    bool full = true;  // the passes' K and V are the same two numbers
+    for (int i = 0; i < passes; ++i) full = full && ps.p[i].K == KD;
     if (ps.p[0].K % EPU || ps.p[0].V % EPU) launch_tiles<T, OT, KD, VT, RAGGED>(ps, passes, pl, s);
-    else if (ps.p[0].K < KD) launch_tiles<T, OT, KD, VT, PADDED>(ps, passes, pl, s);
+    else if (!full) launch_tiles<T, OT, KD, VT, PADDED>(ps, passes, pl, s);
     else launch_tiles<T, OT, KD, VT, FULL>(ps, passes, pl, s);
 }
 // Passes of one plan, side by side in each launch: their span states lie behind each other in
@@ -825,23 +827,27 @@ size_t state_bytes(const ssd_linattn_dims& d) {
     return (size_t)(d.nseq > 0 ? d.nseq : d.batch) * d.nheads * d.keydim * d.valuedim * 4;
 }
 
-// The backward's plan.  The passes for dq and dk have the same sizes and share their launches
-// (all gradients in the input's type); shares of dk and dv, where heads share keys and values,
-// are float32 and go by themselves.  Workspace: the span states of the passes of a launch, and
-// the shares of dk or dv.
+// The backward's plan.  The passes for dq and dk have the same sizes, and where K and V take the
+// same tiles that for dv too: they share their launches, if their outputs have one type (where
+// heads share keys and values, their shares of dk and dv are float32, and added up afterwards).
+// 3001 tokens x 8 heads of 96 and 72, float32: one launch for each pass 203 us, for two 172.
 struct LinBwdPlan {
-    LinPlan qk, v;  // dq and dk (dq or dk alone where heads share), dv
-    int together;
-    size_t spans, shares;
+    LinPlan qk, v;  // dq and dk, dv
+    int together;   // passes of a launch: 1, 2 (dq and dk) or 3
+    size_t spans, dk_shares, dv_shares;
 };
 LinBwdPlan lin_bwd_plan(const ssd_linattn_dims& d) {
     LinBwdPlan b;
-    b.together = d.nheads == d.ngroups ? 2 : 1;
-    b.qk = lin_plan(d, d.valuedim, d.keydim, b.together);
-    b.v = lin_plan(d, d.keydim, d.valuedim);
+    const int K = d.keydim, V = d.valuedim;
+    const LinTiles x = lin_tiles(V, K, d.dtype), y = lin_tiles(K, V, d.dtype);
+    const bool same = x.KD == y.KD && x.VT == y.VT && cdiv(K, x.VT) == cdiv(V, y.VT);
+    b.together = d.nheads != d.ngroups && d.dtype != SSD_F32 ? 1 : (same ? 3 : 2);
+    b.qk = lin_plan(d, V, K, b.together);
+    b.v = b.together == 3 ? b.qk : lin_plan(d, K, V);
     b.spans = (size_t)imax(b.together * b.qk.bytes, b.v.bytes);
-    b.shares = b.together == 2 ? 0
-               : up256((size_t)d.batch * d.seqlen * d.nheads * imax(d.keydim, d.valuedim) * 4);
+    const size_t rows = d.nheads == d.ngroups ? 0 : (size_t)d.batch * d.seqlen * d.nheads;
+    b.dk_shares = up256(rows * K * 4);
+    b.dv_shares = up256(rows * V * 4);
     return b;
 }
 
@@ -898,7 +904,7 @@ int ssd_linattn_fwd(const ssd_linattn_dims* dims, const ssd_linattn_layout* layo
 size_t ssd_linattn_bwd_workspace_bytes(const ssd_linattn_dims* dims) {
     if (lin_check(dims, nullptr) != SSD_OK) return 0;
     const LinBwdPlan b = lin_bwd_plan(*dims);
-    return b.spans + b.shares;
+    return b.spans + b.dk_shares + b.dv_shares;
 }
 
 int ssd_linattn_bwd(const ssd_linattn_dims* dims, const ssd_linattn_layout* layout, const void* q,
@@ -927,11 +933,12 @@ int ssd_linattn_bwd(const ssd_linattn_dims* dims, const ssd_linattn_layout* layo
         return SSD_ERR_OVERLAP;
     if (overlaps(init_state, state_bytes(d), dinit_state, state_bytes(d))) return SSD_ERR_OVERLAP;
     const LinBwdPlan b = lin_bwd_plan(d);
-    if (b.spans + b.shares && (!workspace || workspace_bytes < b.spans + b.shares)) return SSD_ERR_WORKSPACE;
+    if (b.spans + b.dk_shares + b.dv_shares && (!workspace || workspace_bytes < b.spans + b.dk_shares + b.dv_shares)) return SSD_ERR_WORKSPACE;
     if (cu_seqlens && check_cu_env(cu_seqlens, d.nseq, T, (hipStream_t)stream, &st)) return st;
     const hipStream_t s = (hipStream_t)stream;
     const int R = d.nheads / d.ngroups;
-    float* const shares = (float*)((char*)workspace + b.spans);
+    float* const dk_shares = (float*)((char*)workspace + b.spans);
+    float* const dv_shares = (float*)((char*)dk_shares + b.dk_shares);
     const bool half = d.dtype == SSD_BF16;
 
     LinPass q_ = lin_common(d, decay, cu_seqlens);
@@ -949,7 +956,7 @@ int ssd_linattn_bwd(const ssd_linattn_dims* dims, const ssd_linattn_layout* layo
     k_.q = v, k_.q_t = l.v_token, k_.q_h = l.v_group, k_.qdiv = R;
     k_.k = dy, k_.k_t = l.dy_token, k_.k_h = l.dy_head;
     k_.v = q, k_.v_t = l.q_token, k_.v_h = l.q_head;
-    k_.o = R == 1 ? dk : shares;
+    k_.o = R == 1 ? dk : dk_shares;
     k_.o_t = R == 1 ? l.dk_token : (int64_t)d.nheads * d.keydim;
     k_.o_h = R == 1 ? l.dk_group : d.keydim;
     k_.K = d.valuedim, k_.V = d.keydim, k_.s_k = 1, k_.s_v = d.valuedim;
@@ -957,7 +964,7 @@ int ssd_linattn_bwd(const ssd_linattn_dims* dims, const ssd_linattn_layout* layo
     v_.q = k, v_.q_t = l.k_token, v_.q_h = l.k_group, v_.qdiv = R;
     v_.k = q, v_.k_t = l.q_token, v_.k_h = l.q_head;
     v_.v = dy, v_.v_t = l.dy_token, v_.v_h = l.dy_head;
-    v_.o = R == 1 ? dv : shares;
+    v_.o = R == 1 ? dv : dv_shares;
     v_.o_t = R == 1 ? l.dv_token : (int64_t)d.nheads * d.valuedim;
     v_.o_h = R == 1 ? l.dv_group : d.valuedim;
     v_.K = d.keydim, v_.V = d.valuedim, v_.s_k = d.valuedim, v_.s_v = 1;
@@ -974,24 +981,30 @@ int ssd_linattn_bwd(const ssd_linattn_dims* dims, const ssd_linattn_layout* layo
         else if (share) launch_passes<bf16, float>(ps, 1, pl, s);
         else launch_passes<bf16, bf16>(ps, 1, pl, s);
     };
-    auto join = [&](void* out, int64_t o_t, int64_t o_g, int D) {
+    auto join = [&](const float* shares, void* out, int64_t o_t, int64_t o_g, int D) {
         const int64_t items = T * d.ngroups * D;
         const dim3 grid((unsigned)(items < (1 << 28) ? cdiv(items, 256) : 1 << 20));
         if (half) linattn_heads_sum<bf16><<<grid, 256, 0, s>>>(shares, (bf16*)out, items, D, d.ngroups, R, o_t, o_g);
         else linattn_heads_sum<float><<<grid, 256, 0, s>>>(shares, (float*)out, items, D, d.ngroups, R, o_t, o_g);
     };
-    // dv last: dinit may be d_final's buffer, which the pass for dk reads
-    if (T > 0 && R == 1) {
-        LinPasses ps = {{q_, k_}};
-        if (half) launch_passes<bf16, bf16>(ps, 2, b.qk, s);
-        else launch_passes<float, float>(ps, 2, b.qk, s);
-    } else if (T > 0) {
-        run(q_, false, b.qk);
-        run(k_, true, b.qk);
-        join(dk, l.dk_token, l.dk_group, d.keydim);
+    // dinit may be d_final's buffer, which the pass for dk reads: dv's is behind it then
+    const bool apart = dinit_state && dinit_state == d_final;
+    const bool all = b.together == 3 && !apart;
+    if (T > 0) {
+        if (b.together > 1) {
+            LinPasses ps = {{q_, k_, v_}};
+            if (half) launch_passes<bf16, bf16>(ps, all ? 3 : 2, b.qk, s);
+            else launch_passes<float, float>(ps, all ? 3 : 2, b.qk, s);
+        } else {
+            run(q_, false, b.qk);
+            run(k_, true, b.qk);
+        }
     }
-    if (T > 0 || dinit_state) run(v_, R > 1, b.v);
-    if (T > 0 && R > 1) join(dv, l.dv_token, l.dv_group, d.valuedim);
+    if ((T > 0 && !all) || (T == 0 && dinit_state)) run(v_, R > 1, b.v);
+    if (T > 0 && R > 1) {
+        join(dk_shares, dk, l.dk_token, l.dk_group, d.keydim);
+        join(dv_shares, dv, l.dv_token, l.dv_group, d.valuedim);
+    }
     return launched();
 }
 

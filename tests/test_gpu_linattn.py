@@ -420,3 +420,22 @@ def test_bfloat16_rows_of_one_token_keep_their_precision():
     err = (y.double().cpu() - ref).abs()
     # q . k itself is a float32 sum of 64 terms: 80 2^-24 of their sizes
     assert (err <= (2.0 ** -8 + 2.0 ** -15) * ref.abs() + 80 * 2.0 ** -24 * size).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("b,L,H,G,K,V", [(40, 70, 16, 16, 24, 24), (1, 900, 2, 2, 40, 40), (1, 900, 4, 2, 24, 100)])
+def test_gradient_of_the_state_in_place(dtype, b, L, H, G, K, V):
+    """dinit_state written over d_final, in whole sequences and spans, passes together and apart."""
+    s = make(dtype, b, L, H, G, K, V)
+    q, k, v, dec, dy, init = (up(s[n]) for n in ("q", "k", "v", "decay", "dy", "init"))
+    want = m.ssd_linattn_bwd(q, k, v, dec, dy, scale=0.5, init_state=init, d_final=up(s["d_final"]))
+    state = up(s["d_final"])
+    ly = m._layer
+    dims, lay, _, _, _ = ly._linattn_arguments(q, k, v, dec, 0.5, None, None, dy)
+    got = {n: torch.empty_like(t) for n, t in (("dq", q), ("dk", k), ("dv", v))}
+    keep, *ws = ly._workspace("ssd_linattn_bwd_workspace_bytes", dims, q, None)
+    ly._launch("ssd_linattn_bwd", q, dims, lay, q.data_ptr(), k.data_ptr(), v.data_ptr(), dec.data_ptr(),
+               init.data_ptr(), None, 0, dy.data_ptr(), state.data_ptr(), got["dq"].data_ptr(),
+               got["dk"].data_ptr(), got["dv"].data_ptr(), state.data_ptr(), *ws)
+    got["dinit_state"] = state
+    assert all(torch.equal(got[n], want[n]) for n in want)
