@@ -40,7 +40,7 @@ struct LinPass {
     int32_t S, H, K, V, s_k, s_v;
     int32_t qdiv, kdiv, vdiv;  // head h reads head h / div
     int32_t slots, per;        // span slots; spans of a sequence without cu
-    int32_t vtiles, together, kd, reverse, init_pow, final_pow;
+    int32_t vtiles, together, reverse, init_pow, final_pow;
     float in_scale, out_scale;
 };
 
@@ -357,8 +357,7 @@ __device__ __forceinline__ uint32_t same_xcd(uint32_t id, uint32_t together, uin
     return (i / together * 8 + x) * together + i % together;
 }
 
-// One span (or, STATE, only its state).  OT: the output's type.  The state's keys can be dealt to
-// several workgroups (blockIdx.z): with 256 of them a span's state takes two of 128.
+// One span (or, STATE, only its state).  OT: the output's type.
 template <typename T, typename OT, int KD, int VT, int MODE, bool STATE>
 __global__ __launch_bounds__(256, lin_waves(KD, VT, sizeof(T))) void linattn_kernel(LinPasses ps) {
     const LinPass& p = ps.p[blockIdx.y];
@@ -378,10 +377,8 @@ __global__ __launch_bounds__(256, lin_waves(KD, VT, sizeof(T))) void linattn_ker
     if (STATE && last) return;  // no span behind it
     const int64_t block = ((int64_t)sp.seq * p.H + h) * ((int64_t)p.K * p.V);
     const int v0 = vt * VT, vcols = min(VT, p.V - v0), c0 = wave * (16 * CB);
-    const int k0 = STATE ? (int)blockIdx.z * KD : 0, keys = min(KD, p.K - k0);
-    const int kbs = STATE ? p.kd / 16 : KB;  // tiles of a column of the stored state
-    float* const mine = p.spans + (((int64_t)slot * p.H + h) * p.vtiles + vt) * (kbs * 16 * VT) +
-                        (wave * CB * kbs + k0 / 16) * 256 + lane * 4;
+    float* const mine = p.spans + (((int64_t)slot * p.H + h) * p.vtiles + vt) * (KD * VT) +
+                        wave * (CB * KB * 256) + lane * 4;
 
     if (!STATE && n == 0) {  // an empty sequence hands on what came in
         if (p.final)
@@ -394,7 +391,7 @@ __global__ __launch_bounds__(256, lin_waves(KD, VT, sizeof(T))) void linattn_ker
 
     const bool back = p.reverse != 0;
     const int64_t tok0 = back ? sp.first + sp.len - 1 - sp.t0 : sp.first + sp.t0;
-    Stream<T, KD, MODE> ks((const T*)p.k + tok0 * p.k_t + (h / p.kdiv) * p.k_h + k0, p.k_t, keys, back);
+    Stream<T, KD, MODE> ks((const T*)p.k + tok0 * p.k_t + (h / p.kdiv) * p.k_h, p.k_t, p.K, back);
     Stream<T, KD, MODE> qs((const T*)p.q + tok0 * p.q_t + (h / p.qdiv) * p.q_h, p.q_t, p.K, back);
     Stream<T, VT, MODE> vs((const T*)p.v + tok0 * p.v_t + (h / p.vdiv) * p.v_h + v0, p.v_t, vcols, back);
     auto fetch = [&](int have, int to) {
@@ -474,6 +471,7 @@ __global__ __launch_bounds__(256, lin_waves(KD, VT, sizeof(T))) void linattn_ker
     const char* op = (const char*)((OT*)p.o + tok0 * p.o_t + h * p.o_h + v0) - (back ? (int64_t)(C - 1) * os : 0);
     const uint32_t ooff = (uint32_t)(back ? C - 1 - l16 : l16) * os + (uint32_t)(oc * sizeof(OT));
     const uint32_t onext = back ? 0u - 16 * os : 16 * os, owidth = vcols * (uint32_t)sizeof(OT);
+    const int keys = p.K;
     const bool final = p.final != nullptr;
     const int chunks = (int)cdiv(n, C);
     for (int i = 0; i < chunks; ++i) {
@@ -602,7 +600,7 @@ __global__ __launch_bounds__(256, lin_waves(KD, VT, sizeof(T))) void linattn_ker
 #pragma unroll
             for (int cb = 0; cb < CB; ++cb) {
                 if (STATE) {
-                    *(f32x4*)(mine + (cb * kbs + kb) * 256) = st[kb][cb] * held;
+                    *(f32x4*)(mine + (cb * KB + kb) * 256) = st[kb][cb] * held;
                 } else {
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
@@ -738,10 +736,7 @@ void launch_tiles(const LinPasses& ps, int passes, const LinPlan& pl, hipStream_
     const LinPass& p = ps.p[0];
     const dim3 grid((unsigned)((int64_t)pl.slots * p.H * pl.vtiles), passes);
     if (pl.bytes) {
-        // (32768 tokens x 8 heads of 256: 155 us in workgroups of 256 keys, 97 of 128)
-        constexpr int KS = KD > 128 ? 128 : KD;
-        const dim3 states(grid.x, grid.y, KD / KS);
-        linattn_kernel<T, T, KS, VT, MODE, true><<<states, 256, 0, s>>>(ps);
+        linattn_kernel<T, OT, KD, VT, MODE, true><<<grid, 256, 0, s>>>(ps);
         const dim3 joins((unsigned)((int64_t)p.S * p.H * pl.vtiles), KD * VT / 1024, passes);
         linattn_join<<<joins, 256, 0, s>>>(ps, KD, VT);
     }
@@ -766,7 +761,6 @@ void launch_passes(LinPasses& ps, int passes, const LinPlan& pl, hipStream_t s) 
         p.slots = pl.slots;
         p.per = pl.per;
         p.vtiles = pl.vtiles;
-        p.kd = pl.t.KD;
         p.together = pl.vtiles * (p.qdiv > p.kdiv ? p.qdiv : p.kdiv);
         p.spans = (float*)((char*)p.spans + i * pl.bytes);
     }
