@@ -18,6 +18,16 @@
 // product needs a sum across waves.  Where sequences x heads do not fill the chip a
 // sequence is cut into spans: their states are formed first (STATE), joined along the
 // sequence (linattn_join) and then every span is walked from its own incoming state.
+//
+// What bounds it, and figures (one MI355X, whole calls).  65536 packed tokens x 16 heads of 128 x
+// 128, bf16 (1.1 GB): 440 us, where its bytes take 214: the spans' states read k and v a second
+// time, at the memory's rate, and in the scan the two waves of a SIMD do not cover each other's
+// chain of a chunk (load, LDS, products, barrier): vector units 39 % busy, matrix units 31, LDS 32.
+// 32768 x 8 heads of 256 (0.54 GB): 325 us, with one wave a SIMD.  4096 tokens x 12 heads of 64 x
+// 128 34 us and their gradients 76: three and six launches of 9 to 23 us, of which 4 are
+// before the first chunk.  Float32 runs at the matrix units' float32 rate.  More waves of fewer
+// columns wait for LDS (each reads every key and query), a third wave a SIMD spills, and a third
+// buffer of tiles gained nothing.
 #include <type_traits>
 
 #include "ssd_layer.h"
@@ -217,9 +227,8 @@ struct Rows {
     }
 };
 
-// A score as a bfloat16 operand in two parts, 16 bits: a row of few tokens has few scores, whose
-// roundings its output would take over whole (1.7 times the error of its own rounding, and twice
-// two matrix instructions of 80 to avoid it).
+// A score as a bfloat16 operand in two parts, 16 bits.  In one part its rounding is as large as the
+// output's own, and in the first rows of a sequence, which sum few of them, nothing averages it out.
 template <typename T> constexpr int kScoreParts = sizeof(T) == 2 ? 2 : 1;
 __device__ __forceinline__ void split_scores(const f32x8& s, bf16x8 (&o)[2]) {
 #pragma unroll
@@ -702,9 +711,11 @@ int64_t lin_resident(const LinTiles& t, int32_t dtype) {
 
 // Spans.  A workgroup takes 1.2 us a chunk by itself (64 x 128 bf16; 3.5 128 x 128 float32), and
 // cutting a sequence takes two more launches and a state written and read for every span:
-// enough spans that every resident workgroup has one, half as many more in a packed batch,
-// whose spans are uneven (65536 tokens x 16 heads in 16 sequences: 512 workgroups 486 us, 768
-// 440, 1536 450; 32768 x 8 heads of 256, one workgroup a CU: 128 578 us, 256 346, 512 358).
+// enough spans that every resident workgroup has one, two in a packed batch, whose spans are
+// uneven (in the mean of some draws of the lengths: 65536 tokens x 16 heads in 16 sequences, bf16,
+// one for each 482 us, 1.5 451, two 440, three 455; gradients of 3001 x 8 heads of 96 and 72 in 7
+// sequences, float32, 176, 160, 155 and 157.  32768 x 8 heads of 256, one workgroup a CU: 128
+// workgroups 578 us, 256 346, 512 358).
 // Short sequences stay whole: 2 x 256 tokens x 12 heads bf16 17 us, cut 22; 2 x 512 27 and 22;
 // float32 2 x 128 39 and 40, 2 x 256 66 and 43.
 LinPlan lin_plan(const ssd_linattn_dims& d, int K, int V, int passes = 1) {
@@ -713,7 +724,7 @@ LinPlan lin_plan(const ssd_linattn_dims& d, int K, int V, int passes = 1) {
     pl.vtiles = (int)cdiv(V, pl.t.VT);
     const int64_t S = d.nseq > 0 ? d.nseq : d.batch, T = (int64_t)d.batch * d.seqlen;
     const int64_t rows = (int64_t)d.nheads * pl.vtiles * passes;  // workgroups of a sequence in one span
-    const int64_t fill = lin_resident(pl.t, d.dtype) * (d.nseq > 0 ? 3 : 2) / 2;
+    const int64_t fill = lin_resident(pl.t, d.dtype) * (d.nseq > 0 ? 2 : 1);
     // packed sequences are of any length: cut as if they were one
     const int64_t tokens = d.nseq > 0 ? T : d.seqlen, want = cdiv(fill, d.nseq > 0 ? rows : S * rows);
     pl.span = imax(cdiv(cdiv(tokens, want), C), 2) * C;
@@ -824,7 +835,8 @@ size_t state_bytes(const ssd_linattn_dims& d) {
 // The backward's plan.  The passes for dq and dk have the same sizes, and where K and V take the
 // same tiles that for dv too: they share their launches, if their outputs have one type (where
 // heads share keys and values, their shares of dk and dv are float32, and added up afterwards).
-// 3001 tokens x 8 heads of 96 and 72, float32: one launch for each pass 203 us, for two 172.
+// 3001 tokens x 8 heads of 96 and 72, float32: one launch for each pass 203 us, one for two 172,
+// one for all three 155.
 struct LinBwdPlan {
     LinPlan qk, v;  // dq and dk, dv
     int together;   // passes of a launch: 1, 2 (dq and dk) or 3
@@ -927,7 +939,8 @@ int ssd_linattn_bwd(const ssd_linattn_dims* dims, const ssd_linattn_layout* layo
         return SSD_ERR_OVERLAP;
     if (overlaps(init_state, state_bytes(d), dinit_state, state_bytes(d))) return SSD_ERR_OVERLAP;
     const LinBwdPlan b = lin_bwd_plan(d);
-    if (b.spans + b.dk_shares + b.dv_shares && (!workspace || workspace_bytes < b.spans + b.dk_shares + b.dv_shares)) return SSD_ERR_WORKSPACE;
+    const size_t need = b.spans + b.dk_shares + b.dv_shares;
+    if (need && (!workspace || workspace_bytes < need)) return SSD_ERR_WORKSPACE;
     if (cu_seqlens && check_cu_env(cu_seqlens, d.nseq, T, (hipStream_t)stream, &st)) return st;
     const hipStream_t s = (hipStream_t)stream;
     const int R = d.nheads / d.ngroups;
