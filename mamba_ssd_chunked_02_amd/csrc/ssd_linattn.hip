@@ -22,7 +22,8 @@
 // What bounds it, and figures (one MI355X, whole calls).  65536 packed tokens x 16 heads of 128 x
 // 128, bf16 (1.1 GB): 440 us, where its bytes take 214: the spans' states read k and v a second
 // time, at the memory's rate, and in the scan the two waves of a SIMD do not cover each other's
-// chain of a chunk (load, LDS, products, barrier): vector units 39 % busy, matrix units 31, LDS 32.
+// chain of a chunk (load, LDS, products, barrier): matrix units and LDS are a third of the time
+// busy each, vector units a third to 41 %.
 // 32768 x 8 heads of 256 (0.54 GB): 325 us, with one wave a SIMD.  4096 tokens x 12 heads of 64 x
 // 128 34 us and their gradients 76: three and six launches of 9 to 23 us, of which 4 are
 // before the first chunk.  Float32 runs at the matrix units' float32 rate.  More waves of fewer

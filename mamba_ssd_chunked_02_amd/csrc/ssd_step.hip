@@ -273,7 +273,7 @@ struct LinStepParams {
 // A workgroup takes CP value columns of one head: CP / VW lanes across (VW columns each,
 // the last vector moved back to end with the row), the other threads down the state's
 // rows, UN rows in flight each.  Bound by memory: 64 sequences x 32 heads of 128 x 128 (270 MB) 46
-// us where the states are in the 256 MB cache in part, 58 where they are not, 4.7 TB/s.
+// us where the states are in the 256 MB cache in part, 58 where they are not (4.7 TB/s).
 template <typename T, int CP, int VW>
 __global__ __launch_bounds__(256) void linattn_step_kernel(LinStepParams p) {
     constexpr int PL = CP / VW, ROWS = 256 / PL, UN = 8;
