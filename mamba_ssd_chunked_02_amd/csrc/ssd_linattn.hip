@@ -240,8 +240,9 @@ __device__ __forceinline__ void split_scores(const f32x8& s, bf16x8 (&o)[2]) {
 }
 __device__ __forceinline__ void split_scores(const f32x8& s, f32x8 (&o)[1]) { o[0] = s; }
 
-// N neighbours of a row at byte offset `off`, of which `left` lie in the row: with whole units
-// all or none.
+// N neighbours of a row at byte offset `off`, of which `left` lie in the row: whole units of 16
+// bytes (or the one run of 8) lie in it or not, each for itself, since a row of float32 may end
+// between the two units of a run.
 template <typename OT, int N, bool SINGLY>
 __device__ __forceinline__ void store_run(const Rows& b, uint32_t off, int left, const float (&x)[N]) {
     typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
@@ -250,15 +251,16 @@ __device__ __forceinline__ void store_run(const Rows& b, uint32_t off, int left,
 #pragma unroll
     for (int j = 0; j < N; ++j) o[j] = (OT)x[j];
     if constexpr (!SINGLY) {
-        if (left < N) off = kNowhere;
         if constexpr (sizeof(o) == 8) {
-            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, o), b.r, off, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, o), b.r, left >= N ? off : kNowhere,
+                                                  0, 0);
         } else {
+            constexpr int U = 16 / sizeof(OT);
 #pragma unroll
             for (int j = 0; j < (int)sizeof(o) / 16; ++j) {
                 u32x4 v;
                 __builtin_memcpy(&v, (const char*)o + 16 * j, 16);
-                __builtin_amdgcn_raw_buffer_store_b128(v, b.r, off + 16 * j, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b128(v, b.r, left >= (j + 1) * U ? off + 16 * j : kNowhere, 0, 0);
             }
         }
     } else {
