@@ -102,13 +102,15 @@ __device__ __forceinline__ double power(float decay, int64_t n) {
 // Factors l^n, one for each of many steps of n tokens, as floats whose product stays the
 // power: what a float leaves out of l^n (`low`, relative) is gathered and put back whenever
 // it has grown to a unit of the last place.  Over 1000 steps of 32 tokens a fixed factor is
-// up to 3e-5 off.
+// up to 3e-5 off.  A power below 2^-126 has fewer bits than that, and 1 over it may be infinite:
+// what is left out of it, of a state that is gone in two steps, is not gathered.
 struct Rate {
     float rate, low, unrate, owed;
     __device__ __forceinline__ explicit Rate(double exact) {
         rate = (float)exact;
-        low = rate > 0.f ? (float)((exact - (double)rate) / (double)rate) : 0.f;
-        unrate = rate > 0.f ? 1.f / rate : 0.f;
+        const bool normal = rate >= 1.17549435e-38f;
+        low = normal ? (float)((exact - (double)rate) / (double)rate) : 0.f;
+        unrate = normal ? 1.f / rate : 0.f;
         owed = 0.f;
     }
     __device__ __forceinline__ float next() {
