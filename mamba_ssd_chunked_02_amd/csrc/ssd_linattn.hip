@@ -633,9 +633,12 @@ __global__ __launch_bounds__(256) void linattn_join(LinPasses ps, int KD, int VT
     const int vt = id % (uint32_t)p.vtiles;
     id /= (uint32_t)p.vtiles;
     const int h = id % (uint32_t)p.H, seq = id / (uint32_t)p.H;
+    // The sequence's own bounds, not those of whom the first slot would be looked up for: with
+    // cu out of order that may be another, whose spans from here on would leave the workspace.
     const int slot0 = p.cu ? (int)slot_base(p, seq) : seq * p.per;
-    const Span sp = span_of(p, slot0);
-    const int64_t spans = cdiv(sp.len, p.span);
+    int64_t first, end;
+    sequence_span(p.cu, seq, p.L, p.T, &first, &end);
+    const int64_t spans = cdiv(end - first, p.span);
     const int e = blockIdx.y * 256 + threadIdx.x, lane = e & 63, tile = e >> 6;
     const int kb = tile % (KD / 16), vb = tile / (KD / 16);
     const int kr = 32 * (kb / 2) + 4 * (kb % 2) + 8 * (lane >> 4);

@@ -61,3 +61,31 @@ def test_span_powers_below_the_normal_numbers(tokens):
         steps = 8 + 32 + L + 16
         close(y[-1:], ry, ay, steps, "y")
         close(final[-1:], rf, af, steps, "final_state")
+
+
+BAD_CU = [[0, 4096, 0, 4096], [4096, 0, 4096, 0], [4000, 10, 4096, 4096], [-5, 5000, -9, 4096],
+          [0, 2000, 1000, 4096], [1 << 30, -(1 << 30), 1 << 30, 0]]
+
+
+@pytest.mark.parametrize("cu", BAD_CU)
+def test_bounds_out_of_order_stay_in_the_buffers(cu):
+    """Results are unspecified, but nothing behind a buffer is touched."""
+    T, H, K, V = 4096, 2, 16, 24
+    g = torch.Generator().manual_seed(1)
+    q, k, v, dy = (torch.randn((1, T, H, n), generator=g).to(DEV) for n in (K, K, V, V))
+    dec = torch.tensor([-0.1, -0.01], device=DEV)
+    bounds = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    ly = m._layer
+    dims = m.SsdLinattnDims(1, T, H, H, K, V, 3, 0, 1.0, 0)
+    for name in ("fwd", "bwd"):
+        need = ly._entry(f"ssd_linattn_{name}_workspace_bytes")(dims)
+        buf = torch.full((2 * need + (8 << 20),), 7, dtype=torch.uint8, device=DEV)
+        ws = dict(cu_seqlens=bounds, workspace=buf[:need])
+        if name == "fwd":
+            wide = torch.full((3, T, H, V), 5.0, device=DEV)
+            states = torch.full((5, H, K, V), 5.0, device=DEV)
+            m.ssd_linattn_fwd(q, k, v, dec, y=wide[1:2], final_state=states[1:4], **ws)
+            assert (wide[[0, 2]] == 5).all() and (states[[0, 4]] == 5).all()
+        else:
+            m.ssd_linattn_bwd(q, k, v, dec, dy, **ws)
+        assert (buf[need:] == 7).all()
