@@ -675,14 +675,18 @@ __global__ __launch_bounds__(256) void linattn_join(LinPasses ps, int KD, int VT
 }
 
 // out[t][g] = the sum of part[t][g * R .. g * R + R - 1] (rows of D entries): gradients of
-// keys and values that R heads share.
+// keys and values that R heads share.  Tokens outside the sequences have no shares and stay as
+// they are.
 template <typename T>
-__global__ __launch_bounds__(256) void linattn_heads_sum(const float* part, T* out, int64_t items, int D,
-                                                         int G, int R, int64_t o_t, int64_t o_g) {
+__global__ __launch_bounds__(256) void linattn_heads_sum(const float* part, T* out, const int32_t* cu, int S,
+                                                         int64_t items, int D, int G, int R, int64_t o_t,
+                                                         int64_t o_g) {
+    const int64_t first = cu ? cu[0] : 0, end = cu ? cu[S] : (int64_t)1 << 40;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < items; i += (int64_t)gridDim.x * 256) {
         int64_t tg, t;
         const int d = (int)divide(i, D, &tg);
         const int g = (int)divide(tg, G, &t);
+        if (t < first || t >= end) continue;
         const float* q = part + (tg * R) * D + d;
         float s = 0.f;
         for (int r = 0; r < R; ++r) s += q[(int64_t)r * D];
@@ -999,8 +1003,12 @@ int ssd_linattn_bwd(const ssd_linattn_dims* dims, const ssd_linattn_layout* layo
     auto join = [&](const float* shares, void* out, int64_t o_t, int64_t o_g, int D) {
         const int64_t items = T * d.ngroups * D;
         const dim3 grid((unsigned)(items < (1 << 28) ? cdiv(items, 256) : 1 << 20));
-        if (half) linattn_heads_sum<bf16><<<grid, 256, 0, s>>>(shares, (bf16*)out, items, D, d.ngroups, R, o_t, o_g);
-        else linattn_heads_sum<float><<<grid, 256, 0, s>>>(shares, (float*)out, items, D, d.ngroups, R, o_t, o_g);
+        if (half)
+            linattn_heads_sum<bf16><<<grid, 256, 0, s>>>(shares, (bf16*)out, cu_seqlens, d.nseq, items, D,
+                                                         d.ngroups, R, o_t, o_g);
+        else
+            linattn_heads_sum<float><<<grid, 256, 0, s>>>(shares, (float*)out, cu_seqlens, d.nseq, items, D,
+                                                          d.ngroups, R, o_t, o_g);
     };
     // dinit may be d_final's buffer, which the pass for dk reads: dv's is behind it then
     const bool apart = dinit_state && dinit_state == d_final;

@@ -89,3 +89,27 @@ def test_bounds_out_of_order_stay_in_the_buffers(cu):
         else:
             m.ssd_linattn_bwd(q, k, v, dec, dy, **ws)
         assert (buf[need:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,G", [(2, 2), (4, 2), (3, 1)])
+@pytest.mark.parametrize("cu", [[0, 0, 70, 100], [20, 30, 100, 100], [0, 0, 0, 0], [0, 900, 905, 950]])
+def test_tokens_outside_the_sequences_stay(dtype, H, G, cu):
+    """The gradients' rows before the first and behind the last sequence, heads shared or not."""
+    L, K, V = (130, 16, 24) if cu[-1] < 900 else (1000, 16, 24)
+    s = make(dtype, 1, L, H, G, K, V, cu=cu)
+    q, k, v, dec, dy, init, df = (up(s[n]) for n in ("q", "k", "v", "decay", "dy", "init", "d_final"))
+    bounds = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    ly = m._layer
+    dims, lay, c, _, state = ly._linattn_arguments(q, k, v, dec, 0.5, bounds, None, dy)
+    need = ly._entry("ssd_linattn_bwd_workspace_bytes")(dims)
+    ws = torch.full((need // 4 + 1,), float("nan"), device=DEV)
+    g = {n: torch.full_like(t, 5.0) for n, t in (("dq", q), ("dk", k), ("dv", v))}
+    ly._launch("ssd_linattn_bwd", q, dims, lay, *(t.data_ptr() for t in (q, k, v, dec, init, c)), 0,
+               dy.data_ptr(), df.data_ptr(), *(t.data_ptr() for t in g.values()),
+               torch.empty(state, device=DEV).data_ptr(), ws.data_ptr(), need)
+    want = m.ssd_linattn_bwd(q, k, v, dec, dy, scale=0.5, init_state=init, cu_seqlens=bounds, d_final=df)
+    for n in g:
+        assert (g[n][0, :cu[0]] == 5).all() and (g[n][0, cu[-1]:] == 5).all(), n
+        inside = g[n][0, cu[0]:cu[-1]]
+        assert inside.isfinite().all() and torch.equal(inside, want[n][0, cu[0]:cu[-1]]), n
