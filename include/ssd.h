@@ -589,11 +589,11 @@ int ssd_step(const ssd_dims* dims, const ssd_layout* layout,
  * ssd_fwd's.  Element alignment is enough for q, k, v and y; 16-byte aligned
  * rows are faster.  SSD_ERR_SHAPE where y's rows share elements.
  *
- * bf16: the states that q meets are rounded to bf16 once, as operands of
- * their products, and scores to 16 bits (sums in float32); the states
- * themselves and what is added to them keep 24 bits.  A NaN or infinity in a
- * token may make NaN of its whole chunk of 32 tokens of the sequence, and of
- * what follows.
+ * bf16: scores, and the states where q meets them, are rounded to 16 bits as
+ * operands of their products (sums in float32); the states themselves and
+ * what is added to them keep 24 bits.  A NaN or infinity in a token may make
+ * NaN of its whole chunk of 32 tokens of the sequence, and of what follows; an
+ * infinity in a state NaN of what meets it.
  */
 #define SSD_LINATTN_MAX_DIM 256
 typedef struct ssd_linattn_dims {
