@@ -779,7 +779,7 @@ int gn_check(const ssd_groupnorm_dims* d) {
     if (d->dtype != SSD_F32 && d->dtype != SSD_BF16) return SSD_ERR_DTYPE;
     if (d->samples < 0 || d->positions < 1 || d->groups < 1 || d->channels < 1 ||
         d->channels % d->groups || d->channels > kMaxStride ||
-        d->samples > kMaxTokens / d->positions || !(d->eps >= 0.f))
+        d->samples > kMaxTokens / d->positions || !(d->eps >= 0.f) || d->reserved != 0)
         return SSD_ERR_SHAPE;
     if (d->activation < SSD_ACT_NONE || d->activation > SSD_ACT_GATE) return SSD_ERR_UNSUPPORTED;
     if (d->samples * d->groups > kMaxTokens) return SSD_ERR_SHAPE;
