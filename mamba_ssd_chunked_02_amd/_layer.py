@@ -699,9 +699,12 @@ def _maps(t, name, shape, dense):
         return dense
     n, C = shape[0], shape[-1]
     P = dense[0] // C
-    m = t.view(n, P, C)  # raises where the positions do not form one stride
-    if C > 1 and m.stride(2) != 1:
+    if C > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} needs contiguous channels")
+    try:
+        m = t.view(n, P, C)
+    except RuntimeError:
+        raise ValueError(f"{name} needs positions that form one stride (a crop has to be made contiguous)") from None
     row = m.stride(1) if P > 1 else C
     return (m.stride(0) if n > 1 else P * row), row
 
@@ -736,8 +739,8 @@ def ssd_groupnorm_fwd(x, groups, weight=None, bias=None, z=None, activation=None
                       workspace=None):
     """Group norm, channels last, with an activation: x [n, ..., C] (bf16 or fp32;
     the dimensions between are positions, over which a sample's statistics run:
-    [tokens, C] norms every token's groups on their own), weight, bias [C] fp32 or
-    None.  ``activation``: None or "silu"; or ``z``, a gate like x:
+    [tokens, C] norms every token's groups on their own; channels contiguous, and
+    positions that form one stride), weight, bias [C] fp32 or None.  ``activation``: None or "silu"; or ``z``, a gate like x:
     ``y = norm(x) silu(z)``.  ``y`` may be preallocated (x itself for in place).
     Returns (y, mean, rstd) with mean and rstd [n, groups] fp32, for
     ``ssd_groupnorm_bwd``."""
