@@ -740,8 +740,9 @@ def ssd_groupnorm_fwd(x, groups, weight=None, bias=None, z=None, activation=None
     """Group norm, channels last, with an activation: x [n, ..., C] (bf16 or fp32;
     the dimensions between are positions, over which a sample's statistics run:
     [tokens, C] norms every token's groups on their own; channels contiguous, and
-    positions that form one stride), weight, bias [C] fp32 or None.  ``activation``: None or "silu"; or ``z``, a gate like x:
-    ``y = norm(x) silu(z)``.  ``y`` may be preallocated (x itself for in place).
+    positions that form one stride), weight, bias [C] fp32 or None.
+    ``activation``: None or "silu"; or ``z``, a gate like x: ``y = norm(x) silu(z)``.
+    ``y`` may be preallocated (x itself for in place).
     Returns (y, mean, rstd) with mean and rstd [n, groups] fp32, for
     ``ssd_groupnorm_bwd``."""
     dims = _groupnorm_arguments(x, groups, weight, bias, z, activation, eps, y, None, ())

@@ -13,9 +13,11 @@
 // which joins them first and which the caches serve as far as they hold x.
 //
 // Reached (what a copy of 1 GiB reaches is 5.16 TB/s): 8192 x 16 groups of 128, gated, gradients
-// (168 MB) 34 us, 4.9 TB/s; 4096 x 12 groups of 128, gated (38 MB) 9.3 us in the kernel, 4.1 TB/s;
-// 8 maps of 4096 x 320 (42 MB) 22 us in two launches: 7.6 us, and 14.6 for the second, a third of
-// which is the joining of the runs behind a cold read of what other XCDs wrote.
+// (168 MB) 34 us, 4.9 TB/s; 4096 x 12 groups of 128, gated (38 MB) 10 us in the kernel, 3.8 TB/s;
+// 8 maps of 4096 x 320 (42 MB) 23 us in two launches, the second of which joins the runs behind a
+// cold read of what other XCDs wrote, a third of its time.  A group that one wave cannot hold (over
+// 2048 channels in bf16, 1024 in float32) takes the launches of P > 1 with P = 1: 4096 x 4096 in one
+// group, bf16, 121 us, six times what its bytes take.
 #include "ssd_layer.h"
 
 namespace ssd {
@@ -257,8 +259,8 @@ struct Grid {
 constexpr int kWide = 2048;  // channels that a workgroup spans at most (256 vectors)
 
 // Calls f(g, lane, lanes) once for each of G groups with `lanes` neighbouring lanes (a power of
-// two up to 64: as many as the workgroup has for each group, so that one round does).  With g = G there is nothing
-// to do but take part in the lanes' sums.
+// two up to 64: as many as the workgroup has for each group, so that one round does).  With g = G
+// there is nothing to do but take part in the lanes' sums.
 template <typename F>
 __device__ __forceinline__ void each_group(int G, F f) {
     int lanes = 64;
@@ -752,7 +754,7 @@ RunPlan run_plan(const ssd_groupnorm_dims& d) {
     r.across = (int)cdiv(vecs, r.blocks);
     const int64_t R = 256 / r.across;
     // Two workgroups a CU, but no fewer than 4 rows a thread: more runs leave more to join (8 x
-    // 4096 x 320 bf16, us: 256 workgroups 23, 512 22, 768 24, 1024 28).
+    // 4096 x 320 bf16, one call behind the other, us: 256 workgroups 24, 512 24, 768 26, 1024 31).
     const int64_t want = cdiv(512, imax(1, d.samples) * r.blocks);
     r.runlen = imax(cdiv(d.positions, want), 4 * R);
     r.runs = (int)cdiv(d.positions, r.runlen);

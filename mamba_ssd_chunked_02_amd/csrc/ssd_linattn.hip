@@ -20,15 +20,15 @@
 // sequence (linattn_join) and then every span is walked from its own incoming state.
 //
 // What bounds it, and figures (one MI355X, whole calls).  65536 packed tokens x 16 heads of 128 x
-// 128, bf16 (1.1 GB): 440 us, where its bytes take 214: the spans' states read k and v a second
-// time, at the memory's rate, and in the scan the two waves of a SIMD do not cover each other's
-// chain of a chunk (load, LDS, products, barrier): matrix units and LDS are a third of the time
-// busy each, vector units a third to 41 %.
-// 32768 x 8 heads of 256 (0.54 GB): 325 us, with one wave a SIMD.  4096 tokens x 12 heads of 64 x
-// 128 34 us and their gradients 76: three and six launches of 9 to 23 us, of which 4 are
-// before the first chunk.  Float32 runs at the matrix units' float32 rate.  More waves of fewer
-// columns wait for LDS (each reads every key and query), a third wave a SIMD spills, and a third
-// buffer of tiles gained nothing.
+// 128, bf16 (1.1 GB): 452 us, where its bytes take 215: the spans' states read k and v a second
+// time, near the memory's rate, and in the scan the two waves of a SIMD do not cover each other's
+// chain of a chunk (load, LDS, products, barrier): matrix units are busy 33 % of the time, LDS 28,
+// vector units 35 to 44.
+// 32768 x 8 heads of 256 (0.54 GB): 358 us, with one wave a SIMD; forming its states reads 1.9
+// TB/s.  4096 tokens x 12 heads of 64 x 128 34 us and their gradients 78: three and six launches of 8
+// to 26 us, of which 4 are before the first chunk.  Float32 runs at the matrix units' float32 rate.
+// More waves of fewer columns wait for LDS (each reads every key and query), a third wave a SIMD
+// spills, and a third buffer of tiles gained nothing.
 #include <type_traits>
 
 #include "ssd_layer.h"
@@ -244,8 +244,8 @@ struct Rows {
 
 // Scores, and the state where queries meet it, as bfloat16 operands in two parts, 16 bits.  In one
 // part their rounding is as large as the output's own, and where few of them are summed nothing
-// averages it out.  With the state in one part outputs are 2.25e-3 off (root of the mean square), with
-// two 1.66e-3, which is the output's own rounding.  It costs two matrix instructions for 32 keys and
+// averages it out.  With the state in one part outputs are 2.25e-3 off (root of the mean square),
+// with two 1.66e-3, which is the output's own rounding.  It costs two matrix instructions for 32 keys and
 // 16 columns: 65536 tokens x 16 heads of 128 x 128 452 us where one part takes 437, 32768 x 8 of
 // 256 x 256 358 and 328, 4096 x 12 of 64 x 128 34.0 and 33.6, their gradients 78.0 and 75.9.
 template <typename T> constexpr int kSplit = sizeof(T) == 2 ? 2 : 1;
@@ -742,11 +742,11 @@ int64_t lin_resident(const LinTiles& t, int32_t dtype) {
 // cutting a sequence takes two more launches and a state written and read for every span:
 // enough spans that every resident workgroup has one, two in a packed batch, whose spans are
 // uneven (in the mean of some draws of the lengths: 65536 tokens x 16 heads in 16 sequences, bf16,
-// one for each 482 us, 1.5 451, two 440, three 455; gradients of 3001 x 8 heads of 96 and 72 in 7
+// one for each 498 us, 1.5 475, two 459, three 476; gradients of 3001 x 8 heads of 96 and 72 in 7
 // sequences, float32, 176, 160, 155 and 157.  32768 x 8 heads of 256, one workgroup a CU: 128
-// workgroups 578 us, 256 346, 512 358).
-// Short sequences stay whole: 2 x 256 tokens x 12 heads bf16 17 us, cut 22; 2 x 512 27 and 22;
-// float32 2 x 128 39 and 40, 2 x 256 66 and 43.
+// workgroups 635 us, 256 368, 512 386).
+// Short sequences stay whole: 2 x 256 tokens x 12 heads of 64 x 128, bf16, 19 us, cut 20; 2 x 512 30
+// and 22; float32 2 x 128 23 and 26, 2 x 256 39 and 27.
 LinPlan lin_plan(const ssd_linattn_dims& d, int K, int V, int passes = 1) {
     LinPlan pl;
     pl.t = lin_tiles(K, V, d.dtype);
