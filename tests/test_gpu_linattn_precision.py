@@ -66,3 +66,16 @@ def test_spans(K, V):
 def test_state_alone():
     """One token that meets a state: y = q S + (q . k) v."""
     check(3, 1, 4, 4, 128, 128, decay=torch.tensor([0.0, -0.01, -1.0, -5.0]))
+
+
+@pytest.mark.parametrize("K,V,L", [(64, 128, 300), (128, 128, 1000), (256, 100, 200)])
+def test_float32_over_many_entries(K, V, L):
+    """The root of the mean square, where roundings of either sign average out: a score, a state and
+    an output are each sums of at most 2^8 terms in a row, whose roundings of at most 2^-24 add up
+    like sqrt(2^8): 16 2^-24 for each of the three, of the terms' sizes."""
+    s = make("f32", 1, L, 2, 2, K, V)
+    args = [up(s[n]) for n in ("q", "k", "v", "decay")]
+    y, _ = m.ssd_linattn_fwd(*args, init_state=up(s["init"]))
+    f = lambda t: lo.linattn(t(s["q"]), t(s["k"]), t(s["v"]), d(s["decay"]), init=t(s["init"]))[0]
+    ref, size = f(d), f(a)
+    assert (y.double().cpu() - ref).square().mean().sqrt() <= 48 * 2.0 ** -24 * size.square().mean().sqrt()
