@@ -638,7 +638,8 @@ int ssd_linattn_fwd(const ssd_linattn_dims* dims, const ssd_linattn_layout* layo
  * where their rows share elements), dk and dv summed over the heads of a
  * group; dinit_state [S, H, K, V] float32 (the gradient at zeros without an
  * init_state), NULL to skip, or d_final's own buffer; it must not overlap
- * init_state.  workspace as above.
+ * init_state.  Rows of tokens outside the sequences are not written.
+ * workspace as above.
  */
 size_t ssd_linattn_bwd_workspace_bytes(const ssd_linattn_dims* dims);
 

@@ -647,7 +647,8 @@ def ssd_linattn_bwd(q, k, v, decay, dy, scale=1.0, init_state=None, cu_seqlens=N
     """Gradients of ``ssd_linattn_fwd``: a dict with contiguous dq, dk, dv (dk and
     dv summed over the heads of a group) and dinit_state [S, H, K, V] fp32 (the
     gradient at zeros without an init_state).  ``d_final`` is the gradient of
-    final_state or None for zeros.  The decay is a constant: it has none."""
+    final_state or None for zeros.  The decay is a constant: it has none.  Rows of
+    tokens outside every cu_seqlens segment are not written."""
     dims, lay, cu, _, state = _linattn_arguments(q, k, v, decay, scale, cu_seqlens, None, dy)
     _floats(q, (init_state, state, "init_state"), (d_final, state, "d_final"))
     g = {"dq": _output(q), "dk": _output(k), "dv": _output(v),
